@@ -35,8 +35,8 @@ def sources():
 
 
 def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
-        os.path.join(HERE, "..", "include", "gs_splat.h")]
+    include = os.path.join(HERE, "..", "include")
+    return [os.path.join(d, f) for d in (CSRC, include) for f in os.listdir(d)]
 
 
 def _variants(debug):
