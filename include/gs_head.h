@@ -140,7 +140,8 @@ int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* wei
                          int out_features, int dtype, void* ys, int32_t* d_status,
                          void* stream);
 
-/* Bytes of workspace gs_expert_linear_bwd needs. */
+/* Bytes of workspace (16-byte aligned) gs_expert_linear_bwd needs for
+ * grad_weight; may be 0. */
 size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_features,
                                            int out_features, int dtype);
 

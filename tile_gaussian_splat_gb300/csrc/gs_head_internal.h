@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 #include <cuda_runtime.h>
 
 namespace gs {
@@ -61,5 +62,17 @@ void launch_linear_dx(const LinearArgs& a, const void* grad_ys, const void* weig
 void launch_linear_dw(const LinearArgs& a, const void* grad_ys, const void* xs,
                       void* grad_weight, cudaStream_t s);
 void launch_linear_db(const LinearArgs& a, const void* grad_ys, void* grad_bias, cudaStream_t s);
+
+// ---- expert_mma.cu: the same products on the tensor cores.  Each returns a
+// gs_status.
+bool mma_usable(const LinearArgs& a, std::initializer_list<const void*> arrays);
+int launch_mma_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
+                   void* ys, cudaStream_t s);
+int launch_mma_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
+                  cudaStream_t s);
+// Bytes of partial sums (0 when every expert's sum is taken in one piece).
+size_t mma_dw_workspace(const LinearArgs& a);
+int launch_mma_dw(const LinearArgs& a, const void* grad_ys, const void* xs, void* grad_weight,
+                  void* workspace, cudaStream_t s);
 
 }  // namespace gs

@@ -186,15 +186,23 @@ int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* wei
     if (!array_ok(xs, dtype) || !array_ok(weight, dtype) || (bias && !array_ok(bias, dtype)) ||
         !array_ok(ys, dtype))
         return GS_ERR_INVALID_ARG;
-    launch_linear_fwd(LinearArgs{offsets, rows, experts, in_features, out_features, dtype,
-                                 d_status},
-                      xs, weight, bias, ys, static_cast<cudaStream_t>(stream));
+    const LinearArgs a{offsets, rows, experts, in_features, out_features, dtype, d_status};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (mma_usable(a, {xs, weight, bias, ys})) {
+        const int rc = launch_mma_fwd(a, xs, weight, bias, ys, s);
+        if (rc != GS_OK) return rc;
+    } else {
+        launch_linear_fwd(a, xs, weight, bias, ys, s);
+    }
     return check_launch();
 }
 
 size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_features,
                                            int out_features, int dtype) {
-    return 0;
+    int32_t dummy = 0;
+    if (!linear_ok(&dummy, rows, experts, in_features, out_features, dtype)) return 0;
+    return align_up(mma_dw_workspace(
+        LinearArgs{nullptr, rows, experts, in_features, out_features, dtype, nullptr}));
 }
 
 int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* offsets,
@@ -210,10 +218,29 @@ int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* off
     if (grad_weight && (!array_ok(grad_weight, dtype) || (rows > 0 && !array_ok(xs, dtype))))
         return GS_ERR_INVALID_ARG;
     if (grad_bias && !array_ok(grad_bias, dtype)) return GS_ERR_INVALID_ARG;
+    const size_t need = gs_expert_linear_bwd_workspace_size(rows, experts, in_features,
+                                                            out_features, dtype);
+    if (grad_weight && need &&
+        (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need))
+        return GS_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LinearArgs a{offsets, rows, experts, in_features, out_features, dtype, d_status};
-    if (grad_xs && rows > 0) launch_linear_dx(a, grad_ys, weight, grad_xs, s);
-    if (grad_weight) launch_linear_dw(a, grad_ys, xs, grad_weight, s);
+    if (grad_xs && rows > 0) {
+        if (mma_usable(a, {grad_ys, weight, grad_xs})) {
+            const int rc = launch_mma_dx(a, grad_ys, weight, grad_xs, s);
+            if (rc != GS_OK) return rc;
+        } else {
+            launch_linear_dx(a, grad_ys, weight, grad_xs, s);
+        }
+    }
+    if (grad_weight) {
+        if (rows > 0 && mma_usable(a, {grad_ys, xs, grad_weight})) {
+            const int rc = launch_mma_dw(a, grad_ys, xs, grad_weight, workspace, s);
+            if (rc != GS_OK) return rc;
+        } else {
+            launch_linear_dw(a, grad_ys, xs, grad_weight, s);
+        }
+    }
     if (grad_bias) launch_linear_db(a, grad_ys, grad_bias, s);
     return check_launch();
 }
