@@ -1,4 +1,13 @@
 // Layer norm over the channels of each row, forward and backward.
+//
+// Both directions read each input once and write each output once, so they
+// are bound by memory bandwidth.  Up to 1024 channels a row lives in the
+// registers of kLanes lanes (the mean, the variance about it and the output
+// come from one read), a lane owns the same channels of every row it meets --
+// weight and bias are loaded once, the sums of their gradients stay in
+// registers -- and several rows are loaded before the first is used.  Longer
+// rows take one block each and are read again from the cache.
+#include <algorithm>
 #include <cstdint>
 
 #include "gs_head_internal.h"
@@ -9,158 +18,488 @@ namespace gs {
 namespace {
 
 constexpr int kNormThreads = 128;
-constexpr int kNormWarps = kNormThreads / 32;
-constexpr int kMaxSlices = 1216;
+constexpr int kLongThreads = 256;
+constexpr int kRegisterChannels = 1024;
+constexpr int kMaxSlices = 152 * 16;  // blocks that leave partial parameter gradients
 
-// One warp a row, three passes over the row.
-template <typename T, typename P>
-__global__ void __launch_bounds__(kNormThreads)
-    k_norm_fwd(const T* __restrict__ x, int64_t ldx, const P* __restrict__ w,
-               const P* __restrict__ b, int64_t rows, int channels, float eps, T* __restrict__ y,
-               int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t r = blockIdx.x * (int64_t)kNormWarps + threadIdx.x / 32; r < rows;
-         r += (int64_t)gridDim.x * kNormWarps) {
-        const T* xr = x + r * ldx;
+struct NormFwd {
+    const void *x, *weight, *bias;
+    void* y;
+    float *mean, *rstd;
+    int64_t ldx, ldy, rows;
+    int channels, param_dtype;
+    float eps;
+};
+
+struct NormBwd {
+    const void *gy, *x, *weight;
+    const float *mean, *rstd;
+    void* gx;
+    float* partial;  // or null
+    int64_t ldgy, ldx, ldgx, rows;
+    int channels, param_dtype;
+};
+
+// Sums over the kLanes lanes of a row of each of kCount values, in every lane.
+// A row of the whole block exchanges its warps' sums through `scratch` (two
+// halves used in turn, so one barrier a call is enough).
+struct RowScratch {
+    float part[2][kNormThreads / 32][8];
+};
+
+template <int kLanes, int kCount>
+__device__ __forceinline__ void row_sums(float* v, RowScratch& scratch, int& half) {
+    constexpr int kIn = kLanes < 32 ? kLanes : 32;
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) v[k] = group_sum<kIn>(v[k]);
+    if constexpr (kLanes > 32) {
+        static_assert(kLanes == kNormThreads && kCount <= 8, "a row is the block's");
+        float(*part)[8] = scratch.part[half];
+        half ^= 1;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int k = 0; k < kCount; ++k) part[threadIdx.x / 32][k] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kCount; ++k) {
+            v[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kNormThreads / 32; ++w) v[k] += part[w][k];
+        }
+    }
+}
+
+// kVec elements per access, kLanes lanes a row, kItems accesses a lane and
+// row, kRows rows of a lane in flight.
+template <typename T, int kVec, int kLanes, int kItems, int kRows>
+__global__ void __launch_bounds__(kNormThreads) k_norm_fwd(NormFwd a) {
+    constexpr int kGroups = kNormThreads / kLanes;
+    __shared__ RowScratch scratch;
+    int half = 0;
+    const int at = threadIdx.x % kLanes;
+    float w[kItems][kVec], b[kItems][kVec];
+    bool in[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int c = (i * kLanes + at) * kVec;
+        in[i] = c < a.channels;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            w[i][j] = in[i] && a.weight ? load_any(a.weight, a.param_dtype, c + j) : 1.f;
+            b[i][j] = in[i] && a.bias ? load_any(a.bias, a.param_dtype, c + j) : 0.f;
+        }
+    }
+    const float n = (float)a.channels;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.rows; r0 += step * kRows) {
+        RawVec<T, kVec> raw[kRows][kItems];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
+            const T* x = static_cast<const T*>(a.x) + r * a.ldx + at * kVec;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                raw[u][i] = r < a.rows && in[i] ? load_raw<T, kVec>(x + i * kLanes * kVec)
+                                                : RawVec<T, kVec>{};
+        }
+        float mu[kRows], rs[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            mu[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                float v[kVec];
+                unpack<T, kVec>(raw[u][i], v);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) mu[u] += v[j];
+            }
+        }
+        row_sums<kLanes, kRows>(mu, scratch, half);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            mu[u] /= n;
+            rs[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                float v[kVec];
+                unpack<T, kVec>(raw[u][i], v);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    const float d = in[i] ? v[j] - mu[u] : 0.f;
+                    rs[u] += d * d;
+                }
+            }
+        }
+        row_sums<kLanes, kRows>(rs, scratch, half);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
+            if (r >= a.rows) continue;
+            rs[u] = 1.0f / sqrtf(rs[u] / n + a.eps);
+            T* y = static_cast<T*>(a.y) + r * a.ldy + at * kVec;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                float v[kVec];
+                unpack<T, kVec>(raw[u][i], v);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) v[j] = (v[j] - mu[u]) * rs[u] * w[i][j] + b[i][j];
+                if (in[i]) store_vec<T, kVec>(y + i * kLanes * kVec, v);
+            }
+            if (a.mean && at == 0) {
+                a.mean[r] = mu[u];
+                a.rstd[r] = rs[u];
+            }
+        }
+    }
+}
+
+// grad_x, and per block the sums over its rows of grad_y * xh and grad_y.
+template <typename T, int kVec, int kLanes, int kItems, int kRows>
+__global__ void __launch_bounds__(kNormThreads) k_norm_bwd(NormBwd a) {
+    constexpr int kGroups = kNormThreads / kLanes;
+    extern __shared__ float sums[];  // [kGroups - 1][2][channels]
+    __shared__ RowScratch scratch;
+    int half = 0;
+    const int at = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    float w[kItems][kVec], gw[kItems][kVec], gb[kItems][kVec];
+    bool in[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int c = (i * kLanes + at) * kVec;
+        in[i] = c < a.channels;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            w[i][j] = in[i] && a.weight ? load_any(a.weight, a.param_dtype, c + j) : 1.f;
+            gw[i][j] = gb[i][j] = 0.f;
+        }
+    }
+    const float n = (float)a.channels;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.rows; r0 += step * kRows) {
+        RawVec<T, kVec> rx[kRows][kItems], rg[kRows][kItems];
+        float mu[kRows], rs[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = r0 + u * step + group;
+            const bool here = r < a.rows;
+            const T* x = static_cast<const T*>(a.x) + r * a.ldx + at * kVec;
+            const T* g = static_cast<const T*>(a.gy) + r * a.ldgy + at * kVec;
+            mu[u] = here ? a.mean[r] : 0.f;
+            rs[u] = here ? a.rstd[r] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const bool take = here && in[i];
+                rx[u][i] = take ? load_raw<T, kVec>(x + i * kLanes * kVec) : RawVec<T, kVec>{};
+                rg[u][i] = take ? load_raw<T, kVec>(g + i * kLanes * kVec) : RawVec<T, kVec>{};
+            }
+        }
+        float s01[2 * kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                float x[kVec], g[kVec];
+                unpack<T, kVec>(rx[u][i], x);
+                unpack<T, kVec>(rg[u][i], g);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    const float xh = in[i] ? (x[j] - mu[u]) * rs[u] : 0.f;
+                    gw[i][j] += g[j] * xh;
+                    gb[i][j] += g[j];
+                    const float gn = g[j] * w[i][j];
+                    s0 += gn;
+                    s1 += gn * xh;
+                }
+            }
+            s01[2 * u] = s0;
+            s01[2 * u + 1] = s1;
+        }
+        if (!a.gx) continue;
+        row_sums<kLanes, 2 * kRows>(s01, scratch, half);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = r0 + u * step + group;
+            const float s0 = s01[2 * u] / n, s1 = s01[2 * u + 1] / n;
+            if (r >= a.rows) continue;
+            T* out = static_cast<T*>(a.gx) + r * a.ldgx + at * kVec;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                float x[kVec], g[kVec];
+                unpack<T, kVec>(rx[u][i], x);
+                unpack<T, kVec>(rg[u][i], g);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    x[j] = rs[u] * (g[j] * w[i][j] - s0 - (x[j] - mu[u]) * rs[u] * s1);
+                if (in[i]) store_vec<T, kVec>(out + i * kLanes * kVec, x);
+            }
+        }
+    }
+    if (!a.partial) return;
+    if (group > 0) {
+        float* mine = sums + (int64_t)(group - 1) * 2 * a.channels;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (in[i]) {
+                    const int c = (i * kLanes + at) * kVec + j;
+                    mine[c] = gw[i][j];
+                    mine[a.channels + c] = gb[i][j];
+                }
+    }
+    __syncthreads();
+    if (group > 0) return;
+    float* out = a.partial + (int64_t)blockIdx.x * 2 * a.channels;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (in[i]) {
+                const int c = (i * kLanes + at) * kVec + j;
+                for (int q = 0; q < kGroups - 1; ++q) {
+                    gw[i][j] += sums[q * 2 * a.channels + c];
+                    gb[i][j] += sums[q * 2 * a.channels + a.channels + c];
+                }
+                out[c] = gw[i][j];
+                out[a.channels + c] = gb[i][j];
+            }
+}
+
+// The block's sum of v, in every thread.  `scratch`: one float a warp.
+__device__ __forceinline__ float block_sum(float v, float* scratch) {
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLongThreads / 32; ++i) v += scratch[i];
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads) k_norm_fwd_long(NormFwd a) {
+    __shared__ float scratch[kLongThreads / 32];
+    const float n = (float)a.channels;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + r * a.ldx;
         float s = 0.f;
-        for (int c = lane; c < channels; c += 32) s += to_f(xr[c]);
-        const float mu = warp_sum(s) / (float)channels;
+        for (int c = threadIdx.x; c < a.channels; c += kLongThreads) s += to_f(x[c]);
+        const float mu = block_sum(s, scratch) / n;
         s = 0.f;
-        for (int c = lane; c < channels; c += 32) {
-            const float d = to_f(xr[c]) - mu;
+        for (int c = threadIdx.x; c < a.channels; c += kLongThreads) {
+            const float d = to_f(x[c]) - mu;
             s += d * d;
         }
-        const float rs = 1.0f / sqrtf(warp_sum(s) / (float)channels + eps);
-        for (int c = lane; c < channels; c += 32) {
-            float v = (to_f(xr[c]) - mu) * rs;
-            if (w) v *= to_f(w[c]);
-            if (b) v += to_f(b[c]);
-            y[r * ldy + c] = from_f<T>(v);
+        const float rs = 1.0f / sqrtf(block_sum(s, scratch) / n + a.eps);
+        T* y = static_cast<T*>(a.y) + r * a.ldy;
+        for (int c = threadIdx.x; c < a.channels; c += kLongThreads) {
+            float v = (to_f(x[c]) - mu) * rs;
+            if (a.weight) v *= load_any(a.weight, a.param_dtype, c);
+            if (a.bias) v += load_any(a.bias, a.param_dtype, c);
+            y[c] = from_f<T>(v);
         }
-        if (mean && lane == 0) {
-            mean[r] = mu;
-            rstd[r] = rs;
-        }
-    }
-}
-
-template <typename T, typename P>
-__global__ void __launch_bounds__(kNormThreads)
-    k_norm_bwd_x(const T* __restrict__ gy, int64_t ldgy, const T* __restrict__ x, int64_t ldx,
-                 const P* __restrict__ w, const float* __restrict__ mean,
-                 const float* __restrict__ rstd, int64_t rows, int channels, T* __restrict__ gx,
-                 int64_t ldgx) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t r = blockIdx.x * (int64_t)kNormWarps + threadIdx.x / 32; r < rows;
-         r += (int64_t)gridDim.x * kNormWarps) {
-        const float mu = mean[r], rs = rstd[r];
-        float s0 = 0.f, s1 = 0.f;
-        for (int c = lane; c < channels; c += 32) {
-            const float g = to_f(gy[r * ldgy + c]) * (w ? to_f(w[c]) : 1.0f);
-            s0 += g;
-            s1 += g * ((to_f(x[r * ldx + c]) - mu) * rs);
-        }
-        s0 = warp_sum(s0) / (float)channels;
-        s1 = warp_sum(s1) / (float)channels;
-        for (int c = lane; c < channels; c += 32) {
-            const float g = to_f(gy[r * ldgy + c]) * (w ? to_f(w[c]) : 1.0f);
-            const float xh = (to_f(x[r * ldx + c]) - mu) * rs;
-            gx[r * ldgx + c] = from_f<T>(rs * (g - s0 - xh * s1));
+        if (a.mean && threadIdx.x == 0) {
+            a.mean[r] = mu;
+            a.rstd[r] = rs;
         }
     }
 }
 
-// Partial column sums of grad_y * xh and grad_y over one slice of rows.
 template <typename T>
-__global__ void __launch_bounds__(kNormThreads)
-    k_norm_bwd_params(const T* __restrict__ gy, int64_t ldgy, const T* __restrict__ x,
-                      int64_t ldx, const float* __restrict__ mean,
-                      const float* __restrict__ rstd, int64_t rows, int channels,
-                      float* __restrict__ partial) {
+__global__ void __launch_bounds__(kLongThreads) k_norm_bwd_long(NormBwd a) {
+    __shared__ float scratch[kLongThreads / 32];
+    const float n = (float)a.channels;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+        const T* gy = static_cast<const T*>(a.gy) + r * a.ldgy;
+        const float mu = a.mean[r], rs = a.rstd[r];
+        float s0 = 0.f, s1 = 0.f;
+        for (int c = threadIdx.x; c < a.channels; c += kLongThreads) {
+            const float g =
+                to_f(gy[c]) * (a.weight ? load_any(a.weight, a.param_dtype, c) : 1.f);
+            s0 += g;
+            s1 += g * ((to_f(x[c]) - mu) * rs);
+        }
+        s0 = block_sum(s0, scratch) / n;
+        s1 = block_sum(s1, scratch) / n;
+        T* gx = static_cast<T*>(a.gx) + r * a.ldgx;
+        for (int c = threadIdx.x; c < a.channels; c += kLongThreads) {
+            const float g =
+                to_f(gy[c]) * (a.weight ? load_any(a.weight, a.param_dtype, c) : 1.f);
+            gx[c] = from_f<T>(rs * (g - s0 - (to_f(x[c]) - mu) * rs * s1));
+        }
+    }
+}
+
+// Long rows' parameter sums: a thread a channel, a block a slice of the rows.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) k_norm_params_long(NormBwd a) {
     const int c = blockIdx.x * kNormThreads + threadIdx.x;
-    if (c >= channels) return;
-    const int64_t per = (rows + gridDim.y - 1) / gridDim.y;
-    const int64_t r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
+    if (c >= a.channels) return;
+    const int64_t per = (a.rows + gridDim.y - 1) / gridDim.y;
+    const int64_t r0 = blockIdx.y * per, r1 = min(a.rows, r0 + per);
     float sw = 0.f, sb = 0.f;
+#pragma unroll 4
     for (int64_t r = r0; r < r1; ++r) {
-        const float g = to_f(gy[r * ldgy + c]);
-        sw += g * ((to_f(x[r * ldx + c]) - mean[r]) * rstd[r]);
+        const float g = to_f(static_cast<const T*>(a.gy)[r * a.ldgy + c]);
+        const float x = to_f(static_cast<const T*>(a.x)[r * a.ldx + c]);
+        sw += g * ((x - a.mean[r]) * a.rstd[r]);
         sb += g;
     }
-    float* out = partial + (int64_t)blockIdx.y * 2 * channels;
+    float* out = a.partial + (int64_t)blockIdx.y * 2 * a.channels;
     out[c] = sw;
-    out[channels + c] = sb;
+    out[a.channels + c] = sb;
 }
 
-template <typename P>
-__global__ void __launch_bounds__(kNormThreads)
-    k_norm_bwd_reduce(const float* __restrict__ partial, int slices, int channels,
-                      P* __restrict__ gw, P* __restrict__ gb) {
-    const int c = blockIdx.x * kNormThreads + threadIdx.x;
-    if (c >= channels) return;
+// The slices' partial sums added up: 32 channels a block, eight threads a
+// channel.
+__global__ void __launch_bounds__(256)
+    k_norm_params_sum(const float* __restrict__ partial, int slices, int channels,
+                      int param_dtype, void* gw, void* gb) {
+    __shared__ float part[8][2][32];
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
     float sw = 0.f, sb = 0.f;
-    for (int i = 0; i < slices; ++i) {
-        sw += partial[(int64_t)i * 2 * channels + c];
-        sb += partial[(int64_t)i * 2 * channels + channels + c];
+    if (c < channels) {
+#pragma unroll 4
+        for (int i = g; i < slices; i += 8) {
+            sw += partial[(int64_t)i * 2 * channels + c];
+            sb += partial[(int64_t)i * 2 * channels + channels + c];
+        }
     }
-    if (gw) gw[c] = from_f<P>(sw);
-    if (gb) gb[c] = from_f<P>(sb);
+    part[g][0][threadIdx.x % 32] = sw;
+    part[g][1][threadIdx.x % 32] = sb;
+    __syncthreads();
+    if (g > 1 || c >= channels) return;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[i][g][threadIdx.x % 32];
+    void* out = g == 0 ? gw : gb;
+    if (out) store_any(out, param_dtype, c, s);
 }
 
-int norm_blocks(int64_t rows) {
-    const int64_t b = (rows + kNormWarps - 1) / kNormWarps;
-    return (int)(b < 152 * 64 ? b : 152 * 64);
+// Calls f with the form for rows of `channels` elements.  Few lanes a row
+// with several accesses each keep the instructions spent on sums across lanes
+// and on addresses small beside those on elements (with 32 lanes and two
+// elements a lane the forward over 64 channels was bound by instruction issue:
+// 279 us for 2 M rows, against 162 us for its bytes); a lane still holds at
+// most 16 elements, so that many rows are in flight.
+template <int kVec_, int kLanes_, int kItems_, int kRows_>
+struct Form {
+    static constexpr int kVec = kVec_, kLanes = kLanes_, kItems = kItems_, kRows = kRows_;
+};
+
+template <typename T, int kVec, typename F>
+void with_form(int channels, F&& f) {
+    const int n = (channels + kVec - 1) / kVec;
+    if constexpr (kVec == 1) {
+        if (n <= 32) return f(Form<1, 8, 4, 4>{});
+        if (n <= 64) return f(Form<1, 8, 8, 2>{});
+        if (n <= 128) return f(Form<1, 32, 4, 4>{});
+        if (n <= 256) return f(Form<1, 32, 8, 2>{});
+        if (n <= 512) return f(Form<1, 128, 4, 4>{});
+        return f(Form<1, 128, 8, 2>{});
+    } else {
+        if (n <= 8) return f(Form<kVec, 8, 1, 4>{});
+        if (n <= 16) return f(Form<kVec, 8, 2, 2>{});
+        if (n <= 32) return f(Form<kVec, 32, 1, 4>{});
+        if (n <= 64) return f(Form<kVec, 32, 2, 2>{});
+        if (n <= 128) return f(Form<kVec, 128, 1, 4>{});
+        if constexpr (kVec * 128 < kRegisterChannels) return f(Form<kVec, 128, 2, 2>{});
+    }
 }
 
-template <typename F>
-void with_types(int dtype, int param_dtype, F&& f) {
-    with_dtype(dtype, [&](auto t) {
-        if (param_dtype == dtype)
-            f(t, t);
-        else
-            f(t, float{});
-    });
+int blocks_for(int64_t rows, int groups, int cap) {
+    return (int)std::min<int64_t>((rows + groups - 1) / groups, cap);
+}
+
+// Blocks of a kernel that are resident at once: a walk over the rows in equal
+// shares needs exactly those (a second, part-filled wave costs a whole one).
+template <typename K>
+int resident_blocks(K kernel, size_t smem) {
+    int per = 0, dev = 0, sms = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kNormThreads, smem) !=
+            cudaSuccess ||
+        cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 152;
+    return std::max(1, per) * sms;
 }
 
 }  // namespace
 
 int norm_bwd_slices(int64_t rows, int channels) {
-    int64_t s = (rows + 63) / 64;
-    if (s > kMaxSlices) s = kMaxSlices;
-    return (int)(s < 1 ? 1 : s);
+    return (int)std::min<int64_t>(std::max<int64_t>((rows + 3) / 4, 1), kMaxSlices);
 }
 
-void launch_norm_fwd(const NormArgs& a, const void* bias, float eps, void* y, int64_t ldy,
+void launch_norm_fwd(const NormArgs& n, const void* bias, float eps, void* y, int64_t ldy,
                      float* mean, float* rstd, cudaStream_t s) {
-    with_types(a.dtype, a.param_dtype, [&](auto t, auto p) {
+    const NormFwd a{n.x, n.weight, bias, y, mean, rstd, n.ldx, ldy, n.rows, n.channels,
+                    n.param_dtype, eps};
+    with_dtype(n.dtype, [&](auto t) {
         using T = decltype(t);
-        using P = decltype(p);
-        k_norm_fwd<T, P><<<norm_blocks(a.rows), kNormThreads, 0, s>>>(
-            (const T*)a.x, a.ldx, (const P*)a.weight, (const P*)bias, a.rows, a.channels, eps,
-            (T*)y, ldy, mean, rstd);
+        constexpr int kWhole = 16 / (int)sizeof(T);
+        if (n.channels > kRegisterChannels) {
+            k_norm_fwd_long<T><<<blocks_for(n.rows, 1, 152 * 8), kLongThreads, 0, s>>>(a);
+            return;
+        }
+        const auto go = [&](auto form) {
+            using F = decltype(form);
+            const int groups = kNormThreads / F::kLanes;
+            const auto kernel = k_norm_fwd<T, F::kVec, F::kLanes, F::kItems, F::kRows>;
+            static const int resident = resident_blocks(kernel, 0);
+            kernel<<<blocks_for(n.rows, groups, resident), kNormThreads, 0, s>>>(a);
+        };
+        if (n.channels % kWhole == 0 && rows_aligned<T>(n.x, n.ldx) && rows_aligned<T>(y, ldy))
+            with_form<T, kWhole>(n.channels, go);
+        else
+            with_form<T, 1>(n.channels, go);
     });
 }
 
-void launch_norm_bwd(const NormArgs& a, const void* grad_y, int64_t ldgy, const float* mean,
+void launch_norm_bwd(const NormArgs& n, const void* grad_y, int64_t ldgy, const float* mean,
                      const float* rstd, void* grad_x, int64_t ldgx, void* grad_weight,
                      void* grad_bias, float* partial, cudaStream_t s) {
-    with_types(a.dtype, a.param_dtype, [&](auto t, auto p) {
+    const bool params = grad_weight || grad_bias;
+    const NormBwd a{grad_y, n.x, n.weight, mean, rstd, grad_x, params ? partial : nullptr, ldgy,
+                    n.ldx, ldgx, n.rows, n.channels, n.param_dtype};
+    int slices = 0;
+    if (n.rows > 0) with_dtype(n.dtype, [&](auto t) {
         using T = decltype(t);
-        using P = decltype(p);
-        if (grad_x && a.rows > 0)
-            k_norm_bwd_x<T, P><<<norm_blocks(a.rows), kNormThreads, 0, s>>>(
-                (const T*)grad_y, ldgy, (const T*)a.x, a.ldx, (const P*)a.weight, mean, rstd,
-                a.rows, a.channels, (T*)grad_x, ldgx);
-        if (grad_weight || grad_bias) {
-            const int cb = (a.channels + kNormThreads - 1) / kNormThreads;
-            const int slices = norm_bwd_slices(a.rows, a.channels);
-            k_norm_bwd_params<T><<<dim3(cb, slices), kNormThreads, 0, s>>>(
-                (const T*)grad_y, ldgy, (const T*)a.x, a.ldx, mean, rstd, a.rows, a.channels,
-                partial);
-            k_norm_bwd_reduce<P><<<cb, kNormThreads, 0, s>>>(partial, slices, a.channels,
-                                                             (P*)grad_weight, (P*)grad_bias);
+        constexpr int kWhole = 16 / (int)sizeof(T);
+        if (n.channels > kRegisterChannels) {
+            if (grad_x)
+                k_norm_bwd_long<T><<<blocks_for(n.rows, 1, 152 * 8), kLongThreads, 0, s>>>(a);
+            if (params) {
+                slices = blocks_for(n.rows, 64, norm_bwd_slices(n.rows, n.channels));
+                k_norm_params_long<T>
+                    <<<dim3((n.channels + kNormThreads - 1) / kNormThreads, slices),
+                       kNormThreads, 0, s>>>(a);
+            }
+            return;
         }
+        const auto go = [&](auto form) {
+            using F = decltype(form);
+            const int groups = kNormThreads / F::kLanes;
+            const size_t smem = params ? (groups - 1) * 2 * n.channels * sizeof(float) : 0;
+            const auto kernel = k_norm_bwd<T, F::kVec, F::kLanes, F::kItems, F::kRows>;
+            static const int resident = resident_blocks(
+                kernel, (groups - 1) * 2 * F::kVec * F::kLanes * F::kItems * sizeof(float));
+            slices = blocks_for(n.rows, groups,
+                                std::min(norm_bwd_slices(n.rows, n.channels), resident));
+            kernel<<<slices, kNormThreads, smem, s>>>(a);
+        };
+        if (n.channels % kWhole == 0 && rows_aligned<T>(n.x, n.ldx) &&
+            rows_aligned<T>(grad_y, ldgy) && (!grad_x || rows_aligned<T>(grad_x, ldgx)))
+            with_form<T, kWhole>(n.channels, go);
+        else
+            with_form<T, 1>(n.channels, go);
     });
+    if (params)
+        k_norm_params_sum<<<(n.channels + 31) / 32, 256, 0, s>>>(partial, slices, n.channels,
+                                                                 n.param_dtype, grad_weight,
+                                                                 grad_bias);
 }
 
 }  // namespace gs
