@@ -76,7 +76,7 @@ int gs_layer_norm_bwd(const void* grad_y, int64_t ldgy, const void* x, int64_t l
                       void* grad_weight, void* grad_bias, void* workspace,
                       size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace gs_expert_sort needs. */
+/* Bytes of workspace gs_expert_sort needs (0 for a few thousand pairs). */
 size_t gs_expert_sort_workspace_size(int64_t tokens, int topk, int experts);
 
 /*
@@ -141,7 +141,7 @@ int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* wei
                          void* stream);
 
 /* Bytes of workspace (16-byte aligned) gs_expert_linear_bwd needs for
- * grad_weight; may be 0. */
+ * grad_weight and grad_bias. */
 size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_features,
                                            int out_features, int dtype);
 

@@ -51,9 +51,9 @@ def test_expert_sort(lib):
                 dict(experts=1025), dict(off=0), dict(order=0), dict(slots=0), dict(ids=6),
                 dict(tokens=1 << 30)):
         assert sort(**bad) == 1, bad
-    assert sort(ws=0) == 4 and sort(n=0) == 4
+    assert sort(tokens=100000, ws=0) == 4 and sort(tokens=100000, n=100) == 4
     assert lib.gs_expert_sort_workspace_size(4, 0, 8) == 0
-    assert lib.gs_expert_sort_workspace_size(4, 2, 8) > 0
+    assert lib.gs_expert_sort_workspace_size(100000, 2, 8) > 0
 
 
 def test_rows(lib):
@@ -102,3 +102,4 @@ def test_expert_linear(lib):
     for bad in (dict(gys=0), dict(xs=0), dict(off=0), dict(w=0), dict(gx=1), dict(gw=1),
                 dict(gb=1), dict(rows=-1)):
         assert bwd(**bad) == 1, bad
+    assert bwd(ws=0) == 4 and bwd(ws=8) == 4 and bwd(n=16) == 4  # missing, misaligned, small

@@ -461,8 +461,12 @@ def gs_rasterize_bwd_steps(means2d, conics, colors, opacities, backgrounds, mask
 
 
 # ---- the feature head (include/gs_head.h) ------------------------------------
+#
+# A call on one token is over in a few microseconds on the GPU, so the checks
+# build no message before they fail and the stream is read as its raw handle.
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _dtype(t, what):
@@ -472,35 +476,51 @@ def _dtype(t, what):
     return code
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _refuse(what):
+    raise ValueError(what)
 
 
 def _rows(t, what):
     """(data pointer, row distance) of a (..., channels) tensor whose rows lie
     at one distance, such as a channel slice of a contiguous image."""
-    _need(t.is_cuda, f"{what}: expected a CUDA tensor")
-    ch, shape, stride = t.shape[-1], t.shape, t.stride()
+    if not t.is_cuda:
+        _refuse(f"{what}: expected a CUDA tensor")
+    if t.dim() == 0:
+        _refuse(f"{what}: at least one dimension expected")
+    ch = t.shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr() or None, ch
+    shape, stride = t.shape, t.stride()
     ld, rows = None, 1
     for d in range(t.dim() - 2, -1, -1):
         if shape[d] == 1:
             continue
         if ld is None:
             ld = stride[d]
-        _need(stride[d] == ld * rows, f"{what}: the rows must lie at one distance")
+        if stride[d] != ld * rows:
+            _refuse(f"{what}: the rows must lie at one distance")
         rows *= shape[d]
-    _need(ch <= 1 or stride[-1] == 1, f"{what}: the channels of a row must be contiguous")
+    if ch > 1 and stride[-1] != 1:
+        _refuse(f"{what}: the channels of a row must be contiguous")
     ld = ch if ld is None else ld
-    _need(t.numel() == 0 or ld >= ch, f"{what}: rows must not overlap")
+    if t.numel() and ld < ch:
+        _refuse(f"{what}: rows must not overlap")
     return t.data_ptr() or None, ld
+
+
+def _on(stream, like):
+    """The call's stream as a raw handle: `stream`, or the current one of the
+    device that `like` is on."""
+    if not like.is_cuda:
+        _refuse("expected a CUDA tensor")
+    return _raw_stream(like.get_device()) if stream is None else stream.cuda_stream
 
 
 def _new(shape, dtype, like, stream):
     """An output or workspace the call's stream uses: when that is not the
     current one, the allocator is told."""
-    t = _empty(shape, dtype, like.device)
-    if stream is not None and stream != torch.cuda.current_stream(like.device):
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None and stream.cuda_stream != _raw_stream(like.get_device()):
         t.record_stream(stream)
     return t
 
@@ -511,26 +531,20 @@ def _workspace(workspace, n_bytes, like, stream):
     return _new((n_bytes,), torch.uint8, like, stream)
 
 
-def _vector(t, n, dtypes, what):
-    if t is not None:
-        _need(tuple(t.shape) == (n,) and t.dtype in dtypes,
-              f"{what}: shape ({n},) and type {' or '.join(map(str, dtypes))} expected")
-    return t
-
-
 def _same(t, shape, dtype, what):
-    _need(tuple(t.shape) == tuple(shape) and t.dtype == dtype,
-          f"{what}: shape {tuple(shape)} and type {dtype} expected")
+    if t.shape != shape or t.dtype != dtype:
+        _refuse(f"{what}: shape {tuple(shape)} and type {dtype} expected")
     return t
 
 
 def _norm_params(x, weight, bias):
     """The common type of weight and bias: float32 or x's."""
-    p = next((t.dtype for t in (weight, bias) if t is not None), torch.float32)
-    _need(p in (torch.float32, x.dtype), "weight, bias: float32 or the type of x expected")
-    ch = x.shape[-1]
-    _vector(weight, ch, (p,), "weight")
-    _vector(bias, ch, (p,), "bias")
+    p = weight.dtype if weight is not None else bias.dtype if bias is not None else torch.float32
+    if p is not torch.float32 and p != x.dtype:
+        _refuse("weight, bias: float32 or the type of x expected")
+    for t in (weight, bias):
+        if t is not None:
+            _same(t, x.shape[-1:], p, "weight, bias")
     return p
 
 
@@ -540,19 +554,23 @@ def gs_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stats=True,
     of float32 or x's type, or None.  Returns (y, mean, rstd) with mean and
     rstd float32 of x's leading shape (None without stats)."""
     dt = _dtype(x, "x")
-    _need(x.dim() >= 1, "x: at least one dimension expected")
-    ch = x.shape[-1]
-    rows = x.numel() // ch if ch else 0
-    p = _norm_params(x, weight, bias)
     xp, ldx = _rows(x, "x")
-    y = out if out is not None else _new(x.shape, x.dtype, x, stream)
-    _same(y, x.shape, x.dtype, "out")
-    yp, ldy = _rows(y, "out")
-    mean = _new(x.shape[:-1], torch.float32, x, stream) if stats else None
-    rstd = _new(x.shape[:-1], torch.float32, x, stream) if stats else None
-    _check(lib().gs_layer_norm_fwd(xp, ldx, _ptr(weight), _ptr(bias), rows, ch, dt, _DTYPES[p],
-                                   float(eps), yp, ldy, _ptr(mean), _ptr(rstd), _stream(stream)),
-           "gs_layer_norm_fwd")
+    shape = x.shape
+    ch = shape[-1]
+    p = _norm_params(x, weight, bias)
+    if out is None:
+        y = _new(shape, x.dtype, x, stream)
+        yp, ldy = y.data_ptr() or None, ch
+    else:
+        y = _same(out, shape, x.dtype, "out")
+        yp, ldy = _rows(y, "out")
+    mean = rstd = None
+    if stats:
+        mean = _new(shape[:-1], torch.float32, x, stream)
+        rstd = _new(shape[:-1], torch.float32, x, stream)
+    _check(lib().gs_layer_norm_fwd(xp, ldx, _ptr(weight), _ptr(bias),
+                                   x.numel() // ch if ch else 0, ch, dt, _DTYPES[p], eps, yp, ldy,
+                                   _ptr(mean), _ptr(rstd), _on(stream, x)), "gs_layer_norm_fwd")
     return y, mean, rstd
 
 
@@ -563,28 +581,33 @@ def gs_layer_norm_bwd(grad_y, x, weight, mean, rstd, out=None, params=True, para
     weight), or None without params.  out: where grad_x goes, such as the
     channel slice of a wider gradient image."""
     dt = _dtype(x, "x")
-    _same(grad_y, x.shape, x.dtype, "grad_y")
-    ch = x.shape[-1]
+    xp, ldx = _rows(x, "x")
+    shape = x.shape
+    gp, ldg = _rows(_same(grad_y, shape, x.dtype, "grad_y"), "grad_y")
+    ch = shape[-1]
     rows = x.numel() // ch if ch else 0
     p = _norm_params(x, weight, None) if weight is not None else param_dtype or torch.float32
-    _need(p in (torch.float32, x.dtype), "param_dtype: float32 or the type of x expected")
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _need(t.numel() == rows and t.dtype == torch.float32,
-              f"{name}: one float32 per row expected")
-    xp, ldx = _rows(x, "x")
-    gp, ldg = _rows(grad_y, "grad_y")
-    gx = out if out is not None else _new(x.shape, x.dtype, x, stream)
-    _same(gx, x.shape, x.dtype, "out")
-    op, ldo = _rows(gx, "out")
+    if p is not torch.float32 and p != x.dtype:
+        _refuse("param_dtype: float32 or the type of x expected")
+    for t in (mean, rstd):
+        if t.numel() != rows or t.dtype != torch.float32:
+            _refuse("mean, rstd: one float32 per row expected")
+    if out is None:
+        gx = _new(shape, x.dtype, x, stream)
+        op, ldo = gx.data_ptr() or None, ch
+    else:
+        gx = _same(out, shape, x.dtype, "out")
+        op, ldo = _rows(gx, "out")
     gw = gb = ws = None
     n_bytes = 0
+    L = lib()
     if params:
         gw, gb = _new((ch,), p, x, stream), _new((ch,), p, x, stream)
-        n_bytes = int(lib().gs_layer_norm_bwd_workspace_size(rows, ch))
+        n_bytes = L.gs_layer_norm_bwd_workspace_size(rows, ch)
         ws = _workspace(workspace, n_bytes, x, stream)
-    _check(lib().gs_layer_norm_bwd(gp, ldg, xp, ldx, _ptr(weight), _ptr(mean), _ptr(rstd), rows,
-                                   ch, dt, _DTYPES[p], op, ldo, _ptr(gw), _ptr(gb), _ptr(ws),
-                                   n_bytes, _stream(stream)), "gs_layer_norm_bwd")
+    _check(L.gs_layer_norm_bwd(gp, ldg, xp, ldx, _ptr(weight), _ptr(mean), _ptr(rstd), rows, ch,
+                               dt, _DTYPES[p], op, ldo, _ptr(gw), _ptr(gb), _ptr(ws), n_bytes,
+                               _on(stream, x)), "gs_layer_norm_bwd")
     return gx, gw, gb
 
 
@@ -593,53 +616,57 @@ def gs_expert_sort(expert_ids, experts, workspace=None, stream=None):
     expert; an id outside [0, experts) drops its pair.  Returns (offsets
     int32 (experts + 1,), order int32 (tokens * topk,), slots int32
     (tokens, topk))."""
-    _need(expert_ids.dim() == 2 and expert_ids.dtype == torch.int32,
-          "expert_ids: int32 (tokens, topk) expected")
+    if expert_ids.dim() != 2 or expert_ids.dtype != torch.int32:
+        _refuse("expert_ids: int32 (tokens, topk) expected")
     T, k = expert_ids.shape
+    if experts < 0:
+        _refuse("experts: a count expected")
     offsets = _new((experts + 1,), torch.int32, expert_ids, stream)
     order = _new((T * k,), torch.int32, expert_ids, stream)
     slots = _new((T, k), torch.int32, expert_ids, stream)
-    n_bytes = int(lib().gs_expert_sort_workspace_size(T, k, experts))
-    ws = _workspace(workspace, n_bytes, expert_ids, stream)
-    _check(lib().gs_expert_sort(_ptr(expert_ids), T, k, experts, _ptr(offsets), _ptr(order),
-                                _ptr(slots), _ptr(ws), n_bytes, _stream(stream)),
+    L = lib()
+    n_bytes = L.gs_expert_sort_workspace_size(T, k, experts)
+    ws = _workspace(workspace, n_bytes, expert_ids, stream) if n_bytes else None
+    _check(L.gs_expert_sort(_ptr(expert_ids), T, k, experts, _ptr(offsets), _ptr(order),
+                            _ptr(slots), _ptr(ws), n_bytes, _on(stream, expert_ids)),
            "gs_expert_sort")
     return offsets, order, slots
 
 
-def _plan(slots, offsets=None):
-    _need(slots.dim() == 2 and slots.dtype == torch.int32, "slots: int32 (tokens, topk) expected")
-    if offsets is not None:
-        _offsets(offsets)
+def _pairs(slots):
+    if slots.dim() != 2 or slots.dtype != torch.int32:
+        _refuse("slots: int32 (tokens, topk) expected")
     return slots.shape
 
 
-def _offsets(offsets):
-    _need(offsets.dim() == 1 and offsets.numel() >= 2 and offsets.dtype == torch.int32,
-          "offsets: int32 (experts + 1,) expected")
+def _experts(offsets):
+    if offsets.dim() != 1 or offsets.numel() < 2 or offsets.dtype != torch.int32:
+        _refuse("offsets: int32 (experts + 1,) expected")
     return offsets.numel() - 1
+
+
+def _pair_weights(weights, slots):
+    if weights is not None:
+        _same(weights, slots.shape, torch.float32, "weights")
+    return _ptr(weights)
 
 
 def gs_expert_dispatch(x, slots, offsets, d_status=None, out=None, stream=None):
     """x's rows (tokens, channels) in expert order: (tokens * topk, channels),
     zero rows behind the kept pairs."""
     dt = _dtype(x, "x")
-    T, k = _plan(slots, offsets)
-    _need(x.dim() == 2 and x.shape[0] == T, "x: (tokens, channels) expected")
+    T, k = _pairs(slots)
+    E = _experts(offsets)
+    if x.dim() != 2 or x.shape[0] != T:
+        _refuse("x: (tokens, channels) expected")
     ch = x.shape[1]
     xp, ldx = _rows(x, "x")
-    xs = out if out is not None else _new((T * k, ch), x.dtype, x, stream)
-    _same(xs, (T * k, ch), x.dtype, "out")
-    _check(lib().gs_expert_dispatch(xp, ldx, _ptr(slots), _ptr(offsets), T, k,
-                                    offsets.numel() - 1, ch, dt, _ptr(xs), _ptr(d_status),
-                                    _stream(stream)), "gs_expert_dispatch")
+    xs = _new((T * k, ch), x.dtype, x, stream) if out is None else \
+        _same(out, (T * k, ch), x.dtype, "out")
+    _check(lib().gs_expert_dispatch(xp, ldx, _ptr(slots), _ptr(offsets), T, k, E, ch, dt,
+                                    _ptr(xs), _ptr(d_status), _on(stream, x)),
+           "gs_expert_dispatch")
     return xs
-
-
-def _pair_weights(weights, slots):
-    if weights is not None:
-        _same(weights, slots.shape, torch.float32, "weights")
-    return weights
 
 
 def gs_expert_combine(ys, slots, weights=None, d_status=None, out=None, stream=None):
@@ -647,14 +674,18 @@ def gs_expert_combine(ys, slots, weights=None, d_status=None, out=None, stream=N
     (tokens, channels).  weights float32 (tokens, topk), None for ones (the
     gradient of gs_expert_dispatch)."""
     dt = _dtype(ys, "ys")
-    T, k = _plan(slots)
-    _need(ys.dim() == 2 and ys.shape[0] == T * k, "ys: (tokens * topk, channels) expected")
+    T, k = _pairs(slots)
+    if ys.dim() != 2 or ys.shape[0] != T * k:
+        _refuse("ys: (tokens * topk, channels) expected")
     ch = ys.shape[1]
-    y = out if out is not None else _new((T, ch), ys.dtype, ys, stream)
-    _same(y, (T, ch), ys.dtype, "out")
-    yp, ldy = _rows(y, "out")
-    _check(lib().gs_expert_combine(_ptr(ys), _ptr(slots), _ptr(_pair_weights(weights, slots)), T,
-                                   k, ch, dt, yp, ldy, _ptr(d_status), _stream(stream)),
+    if out is None:
+        y = _new((T, ch), ys.dtype, ys, stream)
+        yp, ldy = y.data_ptr() or None, ch
+    else:
+        y = _same(out, (T, ch), ys.dtype, "out")
+        yp, ldy = _rows(y, "out")
+    _check(lib().gs_expert_combine(_ptr(ys), _ptr(slots), _pair_weights(weights, slots), T, k, ch,
+                                   dt, yp, ldy, _ptr(d_status), _on(stream, ys)),
            "gs_expert_combine")
     return y
 
@@ -663,28 +694,29 @@ def gs_expert_combine_bwd(grad_y, ys, slots, weights, offsets, d_status=None, st
     """Gradients of gs_expert_combine: (grad_ys (tokens * topk, channels),
     grad_weights float32 (tokens, topk), None without weights)."""
     dt = _dtype(ys, "ys")
-    T, k = _plan(slots, offsets)
-    _need(ys.dim() == 2 and ys.shape[0] == T * k, "ys: (tokens * topk, channels) expected")
+    T, k = _pairs(slots)
+    E = _experts(offsets)
+    if ys.dim() != 2 or ys.shape[0] != T * k:
+        _refuse("ys: (tokens * topk, channels) expected")
     ch = ys.shape[1]
-    _same(grad_y, (T, ch), ys.dtype, "grad_y")
-    gp, ldg = _rows(grad_y, "grad_y")
+    gp, ldg = _rows(_same(grad_y, (T, ch), ys.dtype, "grad_y"), "grad_y")
     gys = _new((T * k, ch), ys.dtype, ys, stream)
     gw = _new((T, k), torch.float32, ys, stream) if weights is not None else None
     _check(lib().gs_expert_combine_bwd(gp, ldg, _ptr(ys), _ptr(slots),
-                                       _ptr(_pair_weights(weights, slots)), _ptr(offsets), T, k,
-                                       offsets.numel() - 1, ch, dt, _ptr(gys), _ptr(gw),
-                                       _ptr(d_status), _stream(stream)),
+                                       _pair_weights(weights, slots), _ptr(offsets), T, k, E, ch,
+                                       dt, _ptr(gys), _ptr(gw), _ptr(d_status), _on(stream, ys)),
            "gs_expert_combine_bwd")
     return gys, gw
 
 
-def _linear_shapes(rows, offsets, weight, width):
-    E = _offsets(offsets)
-    _need(weight.dim() == 3 and weight.shape[0] == E and weight.dtype == rows.dtype,
-          "weight: (experts, out_features, in_features) of the rows' type expected")
-    _need(rows.dim() == 2 and rows.shape[1] == weight.shape[width],
-          "rows of the weight's width expected")
-    return E, weight.shape[2], weight.shape[1]
+def _linear_shapes(xs, offsets, weight):
+    E = _experts(offsets)
+    if weight.dim() != 3 or weight.shape[0] != E or weight.dtype != xs.dtype:
+        _refuse("weight: (experts, out_features, in_features) of the rows' type expected")
+    _, o, i = weight.shape
+    if xs.dim() != 2 or xs.shape[1] != i:
+        _refuse("xs: (rows, in_features) expected")
+    return E, i, o
 
 
 def gs_expert_linear_fwd(xs, offsets, weight, bias=None, d_status=None, out=None, stream=None):
@@ -693,14 +725,15 @@ def gs_expert_linear_fwd(xs, offsets, weight, bias=None, d_status=None, out=None
     or None.  Returns ys (rows, out_features), zero rows behind the last
     expert's."""
     dt = _dtype(xs, "xs")
-    E, i, o = _linear_shapes(xs, offsets, weight, 2)
+    E, i, o = _linear_shapes(xs, offsets, weight)
+    R = xs.shape[0]
     if bias is not None:
         _same(bias, (E, o), xs.dtype, "bias")
-    ys = out if out is not None else _new((xs.shape[0], o), xs.dtype, xs, stream)
-    _same(ys, (xs.shape[0], o), xs.dtype, "out")
-    _check(lib().gs_expert_linear_fwd(_ptr(xs), _ptr(offsets), _ptr(weight), _ptr(bias),
-                                      xs.shape[0], E, i, o, dt, _ptr(ys), _ptr(d_status),
-                                      _stream(stream)), "gs_expert_linear_fwd")
+    ys = _new((R, o), xs.dtype, xs, stream) if out is None else \
+        _same(out, (R, o), xs.dtype, "out")
+    _check(lib().gs_expert_linear_fwd(_ptr(xs), _ptr(offsets), _ptr(weight), _ptr(bias), R, E, i,
+                                      o, dt, _ptr(ys), _ptr(d_status), _on(stream, xs)),
+           "gs_expert_linear_fwd")
     return ys
 
 
@@ -709,15 +742,16 @@ def gs_expert_linear_bwd(grad_ys, xs, offsets, weight, bias=True, input=True, d_
     """Gradients of gs_expert_linear_fwd: (grad_xs, grad_weight, grad_bias),
     the first None without `input`, the last None without `bias`."""
     dt = _dtype(xs, "xs")
-    E, i, o = _linear_shapes(xs, offsets, weight, 2)
+    E, i, o = _linear_shapes(xs, offsets, weight)
     R = xs.shape[0]
     _same(grad_ys, (R, o), xs.dtype, "grad_ys")
     gx = _new((R, i), xs.dtype, xs, stream) if input else None
     gw = _new((E, o, i), xs.dtype, xs, stream)
     gb = _new((E, o), xs.dtype, xs, stream) if bias else None
-    n_bytes = int(lib().gs_expert_linear_bwd_workspace_size(R, E, i, o, dt))
-    ws = _workspace(workspace, n_bytes, xs, stream)
-    _check(lib().gs_expert_linear_bwd(_ptr(grad_ys), _ptr(xs), _ptr(offsets), _ptr(weight), R, E,
-                                      i, o, dt, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), n_bytes,
-                                      _ptr(d_status), _stream(stream)), "gs_expert_linear_bwd")
+    L = lib()
+    n_bytes = L.gs_expert_linear_bwd_workspace_size(R, E, i, o, dt)
+    ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
+    _check(L.gs_expert_linear_bwd(_ptr(grad_ys), _ptr(xs), _ptr(offsets), _ptr(weight), R, E, i,
+                                  o, dt, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), n_bytes,
+                                  _ptr(d_status), _on(stream, xs)), "gs_expert_linear_bwd")
     return gx, gw, gb

@@ -1,6 +1,7 @@
 // Every expert's matrix product over its sorted rows, and its gradients.
 #include <cstdint>
 
+#include "expert_rows.cuh"
 #include "gs_device.cuh"
 #include "gs_head_internal.h"
 #include "gs_types.cuh"
@@ -138,17 +139,72 @@ __global__ void __launch_bounds__(kTileThreads)
         }
 }
 
+// Column sums of the rows of one piece (an expert's next kBiasRows rows):
+// 32 lanes take kVec * kItems columns each, eight warps every eighth row.
+constexpr int kBiasRows = 512;
+
+template <typename T, int kVec, int kItems>
+__global__ void __launch_bounds__(256)
+    k_bias_pieces(LinearArgs g, const T* __restrict__ gys, float* __restrict__ partial) {
+    extern __shared__ int32_t begin[];  // [experts + 1], then prefix [experts + 1]
+    __shared__ float part[8][32 * kVec * kItems];
+    int32_t* prefix = begin + g.experts + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (warp == 0)
+        expert_pieces(g.offsets, g.experts, g.rows, kBiasRows, begin, prefix, g.d_status);
+    __syncthreads();
+    const int piece = blockIdx.y;
+    if (piece >= prefix[g.experts]) return;
+    const int e = expert_of(prefix, g.experts, piece);
+    const int r0 = begin[e] + (piece - prefix[e]) * kBiasRows;
+    const int r1 = min(begin[e + 1], r0 + kBiasRows);
+    const int m0 = blockIdx.x * 32 * kVec * kItems + lane * kVec;
+    float sum[kItems][kVec] = {};
+#pragma unroll 4
+    for (int r = r0 + warp; r < r1; r += 8) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int m = m0 + i * 32 * kVec;
+            if (m >= g.out) continue;
+            float v[kVec];
+            unpack<T, kVec>(load_raw<T, kVec>(gys + (int64_t)r * g.out + m), v);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) sum[i][k] += v[k];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) part[warp][(i * 32 + lane) * kVec + k] = sum[i][k];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 32 * kVec * kItems; c += 256) {
+        const int m = blockIdx.x * 32 * kVec * kItems + c;
+        if (m >= g.out) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += part[w][c];
+        partial[(int64_t)piece * g.out + m] = v;
+    }
+}
+
+// grad_bias[e] = the sum of the expert's pieces.
 template <typename T>
-__global__ void __launch_bounds__(kTileThreads)
-    k_bias_grad(LinearArgs g, const T* __restrict__ gys, T* __restrict__ gb) {
-    const int e = blockIdx.y, m = blockIdx.x * kTileThreads + threadIdx.x;
-    int64_t r0, r1;
-    expert_rows(g.offsets, g.experts, g.rows, e, &r0, &r1, g.d_status);
+__global__ void __launch_bounds__(256)
+    k_bias_sum(LinearArgs g, const float* __restrict__ partial, T* __restrict__ gb) {
+    extern __shared__ int32_t begin[];
+    int32_t* prefix = begin + g.experts + 1;
+    if (threadIdx.x < 32)
+        expert_pieces(g.offsets, g.experts, g.rows, kBiasRows, begin, prefix, nullptr);
+    __syncthreads();
+    const int e = blockIdx.y, m = blockIdx.x * 256 + threadIdx.x;
     if (m >= g.out) return;
     float sum = 0.f;
-    for (int64_t r = r0; r < r1; ++r) sum += to_f(gys[r * g.out + m]);
+#pragma unroll 4
+    for (int q = prefix[e]; q < prefix[e + 1]; ++q) sum += partial[(int64_t)q * g.out + m];
     gb[(int64_t)e * g.out + m] = from_f<T>(sum);
 }
+
+int64_t bias_pieces(const LinearArgs& a) { return a.rows / kBiasRows + a.experts; }
 
 dim3 rows_grid(const LinearArgs& a, int width) {
     // each expert (and the rows of none) can leave one tile part-filled
@@ -186,11 +242,29 @@ void launch_linear_dw(const LinearArgs& a, const void* grad_ys, const void* xs,
     });
 }
 
-void launch_linear_db(const LinearArgs& a, const void* grad_ys, void* grad_bias, cudaStream_t s) {
+size_t linear_db_workspace(const LinearArgs& a) {
+    return (size_t)bias_pieces(a) * a.out * sizeof(float);
+}
+
+void launch_linear_db(const LinearArgs& a, const void* grad_ys, void* grad_bias, void* workspace,
+                      cudaStream_t s) {
+    float* partial = static_cast<float*>(workspace);
+    const size_t smem = 2 * sizeof(int32_t) * (a.experts + 1);
     with_dtype(a.dtype, [&](auto t) {
         using T = decltype(t);
-        k_bias_grad<T><<<dim3((a.out + kTileThreads - 1) / kTileThreads, a.experts),
-                         kTileThreads, 0, s>>>(a, (const T*)grad_ys, (T*)grad_bias);
+        constexpr int kWhole = 16 / (int)sizeof(T);
+        const T* gys = static_cast<const T*>(grad_ys);
+        const auto grid = [&](int columns) {
+            return dim3((a.out + columns - 1) / columns, (unsigned)bias_pieces(a));
+        };
+        if (a.rows > 0) {
+            if (a.out % kWhole == 0 && rows_aligned<T>(grad_ys, a.out))
+                k_bias_pieces<T, kWhole, 1><<<grid(32 * kWhole), 256, smem, s>>>(a, gys, partial);
+            else
+                k_bias_pieces<T, 1, 4><<<grid(128), 256, smem, s>>>(a, gys, partial);
+        }
+        k_bias_sum<T><<<dim3((a.out + 255) / 256, a.experts), 256, smem, s>>>(
+            a, partial, static_cast<T*>(grad_bias));
     });
 }
 

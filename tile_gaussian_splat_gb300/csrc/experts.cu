@@ -1,6 +1,8 @@
 // Pairs sorted by expert (a stable counting sort), rows copied into that
 // order, and rows summed back with their weights.
+#include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include "gs_device.cuh"
 #include "gs_head_internal.h"
@@ -10,12 +12,12 @@ namespace gs {
 
 namespace {
 
-constexpr int kSortUnitThreads = 128;
-constexpr int kSortUnitWarps = kSortUnitThreads / 32;
+constexpr int kSortThreads = 256;
+constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxUnits = 152 * 16;
 constexpr int kScanThreads = 256;
-constexpr int kRowThreads = 128;
-constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kSmallSort = 4096;  // most pairs of the one-block sort
+constexpr int kAhead = 4;  // groups of 32 ids a warp has in flight
 
 // Range of pairs of one unit (a warp): whole groups of 32.
 __device__ __forceinline__ void unit_range(int64_t n, int units, int unit, int64_t* i0,
@@ -26,96 +28,48 @@ __device__ __forceinline__ void unit_range(int64_t n, int units, int unit, int64
     *i1 = min(n, (unit + 1) * per * 32);
 }
 
-// counts[unit][e] = pairs of expert e in the unit's range.
-__global__ void __launch_bounds__(kSortUnitThreads)
-    k_expert_count(const int32_t* __restrict__ ids, int64_t n, int experts, int units,
-                   int32_t* __restrict__ counts) {
-    extern __shared__ int32_t sm[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int unit = blockIdx.x * kSortUnitWarps + warp;
-    int32_t* own = sm + warp * experts;
-    for (int e = lane; e < experts; e += 32) own[e] = 0;
-    __syncwarp();
-    if (unit >= units) return;
-    int64_t i0, i1;
-    unit_range(n, units, unit, &i0, &i1);
-    for (int64_t i = i0 + lane; i < i1; i += 32) {
-        const int e = ids[i];
-        if (e >= 0 && e < experts) atomicAdd(&own[e], 1);
-    }
-    __syncwarp();
-    for (int e = lane; e < experts; e += 32) counts[(int64_t)unit * experts + e] = own[e];
-}
-
-// Exclusive prefix over the units of one expert's counts (block e), in place,
-// and its total.
-__global__ void __launch_bounds__(kScanThreads)
-    k_expert_scan(int32_t* __restrict__ counts, int units, int experts,
-                  int32_t* __restrict__ totals) {
-    __shared__ int32_t part[kScanThreads];
-    const int e = blockIdx.x, t = threadIdx.x;
-    const int per = (units + kScanThreads - 1) / kScanThreads;
-    const int u0 = min(units, t * per), u1 = min(units, u0 + per);
-    int32_t sum = 0;
-    for (int u = u0; u < u1; ++u) sum += counts[(int64_t)u * experts + e];
-    part[t] = sum;
-    __syncthreads();
-    for (int o = 1; o < kScanThreads; o <<= 1) {
-        const int32_t v = t >= o ? part[t - o] : 0;
-        __syncthreads();
-        part[t] += v;
-        __syncthreads();
-    }
-    int32_t run = part[t] - sum;
-    for (int u = u0; u < u1; ++u) {
-        const int32_t c = counts[(int64_t)u * experts + e];
-        counts[(int64_t)u * experts + e] = run;
-        run += c;
-    }
-    if (t == kScanThreads - 1) totals[e] = part[t];
-}
-
-// offsets from the totals.
-__global__ void k_expert_offsets(const int32_t* __restrict__ totals, int experts,
-                                 int32_t* __restrict__ offsets) {
-    if (threadIdx.x == 0) {
-        int32_t run = 0;
-        for (int e = 0; e < experts; ++e) {
-            offsets[e] = run;
-            run += totals[e];
+// Calls f(i, e) for the unit's pairs, 32 at a time in order; e = -1 for a
+// dropped pair and beyond the range.
+template <typename F>
+__device__ __forceinline__ void walk_pairs(const int32_t* __restrict__ ids, int64_t i0,
+                                           int64_t i1, int experts, F&& f) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t g = i0; g < i1; g += 32 * kAhead) {
+        int e[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const int64_t i = g + q * 32 + lane;
+            e[q] = i < i1 ? ids[i] : -1;
+            if (e[q] >= experts) e[q] = -1;
         }
-        offsets[experts] = run;
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            if (g + q * 32 < i1) f(g + q * 32 + lane, e[q] < 0 ? -1 : e[q]);
     }
 }
 
-// Each unit walks its range in order, 32 pairs at a time; a pair's row is its
-// expert's start plus the pairs of that expert before it.
-__global__ void __launch_bounds__(kSortUnitThreads)
-    k_expert_place(const int32_t* __restrict__ ids, int64_t n, int experts, int units,
-                   const int32_t* __restrict__ counts, const int32_t* __restrict__ offsets,
-                   int32_t* __restrict__ order, int32_t* __restrict__ slots) {
-    extern __shared__ int32_t sm[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int unit = blockIdx.x * kSortUnitWarps + warp;
-    const int64_t kept = offsets[experts];
-    for (int64_t i = kept + (int64_t)blockIdx.x * kSortUnitThreads + threadIdx.x; i < n;
-         i += (int64_t)gridDim.x * kSortUnitThreads)
-        order[i] = -1;
-    if (unit >= units) return;
-    int32_t* own = sm + warp * experts;
-    for (int e = lane; e < experts; e += 32)
-        own[e] = offsets[e] + counts[(int64_t)unit * experts + e];
+// own[e] = the unit's pairs of expert e.
+__device__ __forceinline__ void count_unit(const int32_t* __restrict__ ids, int64_t i0,
+                                           int64_t i1, int experts, int32_t* own) {
+    for (int e = threadIdx.x & 31; e < experts; e += 32) own[e] = 0;
     __syncwarp();
-    int64_t i0, i1;
-    unit_range(n, units, unit, &i0, &i1);
-    for (int64_t g = i0; g < i1; g += 32) {
-        const int64_t i = g + lane;
-        int e = i < i1 ? ids[i] : -1;
-        if (e < 0 || e >= experts) e = -1;
+    walk_pairs(ids, i0, i1, experts, [&](int64_t, int e) {
+        if (e >= 0) atomicAdd(&own[e], 1);
+    });
+    __syncwarp();
+}
+
+// Places the unit's pairs; own[e]: the row of its first pair of expert e.  A
+// pair's row is that plus the pairs of its expert before it in the unit.
+__device__ __forceinline__ void place_unit(const int32_t* __restrict__ ids, int64_t i0,
+                                           int64_t i1, int experts, int32_t* own,
+                                           int32_t* __restrict__ order,
+                                           int32_t* __restrict__ slots) {
+    __syncwarp();
+    walk_pairs(ids, i0, i1, experts, [&](int64_t i, int e) {
         const unsigned same = __match_any_sync(0xffffffffu, e);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        int32_t at = -1;
-        if (e >= 0) at = own[e] + before;
+        const int before = __popc(same & lanemask_lt());
+        const int32_t at = e >= 0 ? own[e] + before : -1;
         __syncwarp();
         if (e >= 0 && before == 0) own[e] += __popc(same);
         __syncwarp();
@@ -123,7 +77,123 @@ __global__ void __launch_bounds__(kSortUnitThreads)
             slots[i] = at;
             if (at >= 0) order[at] = (int32_t)i;
         }
+    });
+}
+
+// Exclusive prefix of v[0 .. experts) into out[0 .. experts], by one warp.
+__device__ __forceinline__ void warp_prefix(const int32_t* v, int experts, int32_t* out) {
+    const int lane = threadIdx.x & 31;
+    int run = 0;
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+        const int n = e0 + lane < experts ? v[e0 + lane] : 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        if (e0 + lane < experts) out[e0 + lane] = run + sum - n;
+        run += __shfl_sync(0xffffffffu, sum, 31);
     }
+    if (lane == 0) out[experts] = run;
+}
+
+// The whole sort in one block, for few pairs: one launch in place of three.
+__global__ void __launch_bounds__(kSortThreads)
+    k_expert_sort_small(const int32_t* __restrict__ ids, int64_t n, int experts,
+                        int32_t* __restrict__ offsets, int32_t* __restrict__ order,
+                        int32_t* __restrict__ slots) {
+    extern __shared__ int32_t sm[];  // counts [warps][experts], totals, first [experts + 1]
+    int32_t* totals = sm + kSortWarps * experts;
+    int32_t* first = totals + experts;
+    const int warp = threadIdx.x / 32;
+    int32_t* own = sm + warp * experts;
+    int64_t i0, i1;
+    unit_range(n, kSortWarps, warp, &i0, &i1);
+    count_unit(ids, i0, i1, experts, own);
+    __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += kSortThreads) {
+        int32_t run = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int32_t c = sm[w * experts + e];
+            sm[w * experts + e] = run;
+            run += c;
+        }
+        totals[e] = run;
+    }
+    __syncthreads();
+    if (warp == 0) warp_prefix(totals, experts, first);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= experts; e += kSortThreads) offsets[e] = first[e];
+    for (int64_t i = first[experts] + threadIdx.x; i < n; i += kSortThreads) order[i] = -1;
+    for (int e = threadIdx.x & 31; e < experts; e += 32) own[e] += first[e];
+    place_unit(ids, i0, i1, experts, own, order, slots);
+}
+
+// counts[unit][e] = pairs of expert e in the unit's range.
+__global__ void __launch_bounds__(kSortThreads)
+    k_expert_count(const int32_t* __restrict__ ids, int64_t n, int experts, int units,
+                   int32_t* __restrict__ counts) {
+    extern __shared__ int32_t sm[];
+    const int unit = blockIdx.x * kSortWarps + threadIdx.x / 32;
+    int32_t* own = sm + threadIdx.x / 32 * experts;
+    if (unit >= units) return;
+    int64_t i0, i1;
+    unit_range(n, units, unit, &i0, &i1);
+    count_unit(ids, i0, i1, experts, own);
+    for (int e = threadIdx.x & 31; e < experts; e += 32)
+        counts[(int64_t)unit * experts + e] = own[e];
+}
+
+// Exclusive prefix over the units of one expert's counts (block e), in place,
+// and its total.
+__global__ void __launch_bounds__(kScanThreads)
+    k_expert_scan(int32_t* __restrict__ counts, int units, int experts,
+                  int32_t* __restrict__ totals) {
+    __shared__ int64_t scratch[32];
+    constexpr int kEach = (kMaxUnits + kScanThreads - 1) / kScanThreads;
+    const int e = blockIdx.x, t = threadIdx.x;
+    int32_t c[kEach];
+    int64_t sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int u = t * kEach + i;
+        c[i] = u < units ? counts[(int64_t)u * experts + e] : 0;
+        sum += c[i];
+    }
+    int32_t run = (int32_t)block_exclusive_scan<kScanThreads>(sum, scratch, &total);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int u = t * kEach + i;
+        if (u < units) counts[(int64_t)u * experts + e] = run;
+        run += c[i];
+    }
+    if (t == 0) totals[e] = (int32_t)total;
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    k_expert_place(const int32_t* __restrict__ ids, int64_t n, int experts, int units,
+                   const int32_t* __restrict__ counts, const int32_t* __restrict__ totals,
+                   int32_t* __restrict__ offsets, int32_t* __restrict__ order,
+                   int32_t* __restrict__ slots) {
+    extern __shared__ int32_t sm[];  // first row of the pairs [warps][experts], first [experts + 1]
+    int32_t* first = sm + kSortWarps * experts;
+    const int unit = blockIdx.x * kSortWarps + threadIdx.x / 32;
+    if (threadIdx.x < 32) warp_prefix(totals, experts, first);
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= experts; e += kSortThreads) offsets[e] = first[e];
+    for (int64_t i = first[experts] + (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * kSortThreads)
+        order[i] = -1;
+    if (unit >= units) return;
+    int32_t* own = sm + threadIdx.x / 32 * experts;
+    for (int e = threadIdx.x & 31; e < experts; e += 32)
+        own[e] = first[e] + counts[(int64_t)unit * experts + e];
+    int64_t i0, i1;
+    unit_range(n, units, unit, &i0, &i1);
+    place_unit(ids, i0, i1, experts, own, order, slots);
 }
 
 // A slot read from the caller's array: -1 unless it names one of n rows.
@@ -139,128 +209,294 @@ __device__ __forceinline__ int64_t checked_kept(const int32_t* offsets, int expe
     return min(max(k, (int64_t)0), n);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
-    k_dispatch(RowArgs a, const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slots,
-               const int32_t* __restrict__ offsets, T* __restrict__ xs) {
-    const int lane = threadIdx.x & 31;
-    const int64_t first = blockIdx.x * (int64_t)kRowWarps + threadIdx.x / 32;
-    const int64_t step = (int64_t)gridDim.x * kRowWarps;
-    const int64_t n = a.tokens * a.topk;
-    for (int64_t t = first; t < a.tokens; t += step)
-        for (int j = 0; j < a.topk; ++j) {
-            const int64_t s = checked_slot(slots[t * a.topk + j], n, a.d_status);
-            if (s < 0) continue;
-            for (int c = lane; c < a.channels; c += 32)
-                xs[s * a.channels + c] = x[t * ldx + c];
-        }
-    for (int64_t r = checked_kept(offsets, a.experts, n, a.d_status) + first; r < n; r += step)
-        for (int c = lane; c < a.channels; c += 32) xs[r * a.channels + c] = from_f<T>(0.f);
+// Rows [kept, n) of out are 0, shared among all the grid's row groups.
+template <typename Word, int kLanes>
+__device__ __forceinline__ void zero_rows(Word* out, int words, int64_t kept, int64_t n) {
+    constexpr int kGroups = kRowThreads / kLanes;
+    for (int64_t r = kept + (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes; r < n;
+         r += (int64_t)gridDim.x * kGroups)
+        for (int c = threadIdx.x % kLanes; c < words; c += kLanes) out[r * words + c] = Word{};
 }
 
-template <typename T>
+// A row is moved in words of 16, 4 or 2 bytes, whatever its type: read once,
+// written topk times.  kRows tokens of a lane in flight.
+template <typename Word, int kLanes, int kItems, int kRows>
+__global__ void __launch_bounds__(kRowThreads)
+    k_dispatch(RowArgs a, const Word* __restrict__ x, int64_t ldx, int words,
+               const int32_t* __restrict__ slots, const int32_t* __restrict__ offsets,
+               Word* __restrict__ xs) {
+    constexpr int kGroups = kRowThreads / kLanes;
+    const int64_t n = a.tokens * a.topk, step = (int64_t)gridDim.x * kGroups;
+    const int at = threadIdx.x % kLanes;
+    for (int64_t t0 = (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes; t0 < a.tokens;
+         t0 += step * kRows)
+        for (int c0 = at; c0 < words; c0 += kLanes * kItems) {
+            Word v[kRows][kItems];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int64_t t = t0 + u * step;
+                    const int c = c0 + i * kLanes;
+                    v[u][i] = t < a.tokens && c < words ? x[t * ldx + c] : Word{};
+                }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int64_t t = t0 + u * step;
+                if (t >= a.tokens) break;
+                for (int j = 0; j < a.topk; ++j) {
+                    const int64_t s = checked_slot(slots[t * a.topk + j], n, a.d_status);
+                    if (s < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        const int c = c0 + i * kLanes;
+                        if (c < words) xs[s * words + c] = v[u][i];
+                    }
+                }
+            }
+        }
+    zero_rows<Word, kLanes>(xs, words, checked_kept(offsets, a.experts, n, a.d_status), n);
+}
+
+constexpr int kChoices = 4;  // of a token's rows in flight
+
+// y[t] = sum over j of w[t, j] * ys[slots[t, j]], j ascending.
+template <typename T, int kVec, int kLanes, int kItems>
 __global__ void __launch_bounds__(kRowThreads)
     k_combine(RowArgs a, const T* __restrict__ ys, const int32_t* __restrict__ slots,
               const float* __restrict__ weights, T* __restrict__ y, int64_t ldy) {
-    const int lane = threadIdx.x & 31;
+    constexpr int kGroups = kRowThreads / kLanes;
     const int64_t n = a.tokens * a.topk;
-    for (int64_t t = blockIdx.x * (int64_t)kRowWarps + threadIdx.x / 32; t < a.tokens;
-         t += (int64_t)gridDim.x * kRowWarps)
-        for (int c = lane; c < a.channels; c += 32) {
-            float sum = 0.f;
-            for (int j = 0; j < a.topk; ++j) {
-                const int64_t s = checked_slot(slots[t * a.topk + j], n, a.d_status);
-                if (s < 0) continue;
-                const float v = to_f(ys[s * a.channels + c]);
-                sum += weights ? weights[t * a.topk + j] * v : v;
+    for (int64_t t = (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes; t < a.tokens;
+         t += (int64_t)gridDim.x * kGroups)
+        for (int c0 = threadIdx.x % kLanes * kVec; c0 < a.channels;
+             c0 += kLanes * kVec * kItems) {
+            float sum[kItems][kVec] = {};
+            for (int j0 = 0; j0 < a.topk; j0 += kChoices) {
+                int64_t s[kChoices];
+                float w[kChoices];
+                RawVec<T, kVec> raw[kChoices][kItems];
+#pragma unroll
+                for (int q = 0; q < kChoices; ++q) {
+                    const int64_t p = t * a.topk + j0 + q;
+                    s[q] = j0 + q < a.topk ? checked_slot(slots[p], n, a.d_status) : -1;
+                    w[q] = weights && s[q] >= 0 ? weights[p] : 1.f;
+                }
+#pragma unroll
+                for (int q = 0; q < kChoices; ++q)
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        const int c = c0 + i * kLanes * kVec;
+                        if (s[q] >= 0 && c < a.channels)
+                            raw[q][i] = load_raw<T, kVec>(ys + s[q] * a.channels + c);
+                    }
+#pragma unroll
+                for (int q = 0; q < kChoices; ++q) {
+                    if (s[q] < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        float v[kVec];
+                        unpack<T, kVec>(raw[q][i], v);
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k) sum[i][k] += w[q] * v[k];
+                    }
+                }
             }
-            y[t * ldy + c] = from_f<T>(sum);
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int c = c0 + i * kLanes * kVec;
+                if (c < a.channels) store_vec<T, kVec>(y + t * ldy + c, sum[i]);
+            }
         }
 }
 
-template <typename T>
+// Per pair: grad_ys[s] = w grad_y[t] and grad_weights = <grad_y[t], ys[s]>.
+// grad_y[t] is read once for the pairs in flight.
+template <typename T, int kVec, int kLanes, int kItems>
 __global__ void __launch_bounds__(kRowThreads)
     k_combine_bwd(RowArgs a, const T* __restrict__ gy, int64_t ldgy, const T* __restrict__ ys,
                   const int32_t* __restrict__ slots, const float* __restrict__ weights,
                   const int32_t* __restrict__ offsets, T* __restrict__ gys,
                   float* __restrict__ gw) {
-    const int lane = threadIdx.x & 31;
-    const int64_t first = blockIdx.x * (int64_t)kRowWarps + threadIdx.x / 32;
-    const int64_t step = (int64_t)gridDim.x * kRowWarps;
+    constexpr int kGroups = kRowThreads / kLanes;
+    __shared__ RowScratch scratch;
+    int half = 0;
     const int64_t n = a.tokens * a.topk;
-    for (int64_t t = first; t < a.tokens; t += step)
-        for (int j = 0; j < a.topk; ++j) {
-            const int64_t p = t * a.topk + j;
-            const int64_t s = checked_slot(slots[p], n, a.d_status);
-            float sum = 0.f;
-            if (s >= 0) {
-                const float w = weights ? weights[p] : 1.0f;
-                for (int c = lane; c < a.channels; c += 32) {
-                    const float g = to_f(gy[t * ldgy + c]);
-                    gys[s * a.channels + c] = from_f<T>(w * g);
-                    if (gw) sum += g * to_f(ys[s * a.channels + c]);
+    const int at = threadIdx.x % kLanes;
+    // whole rounds: the lanes of a row stay together for its sums
+    for (int64_t t0 = (int64_t)blockIdx.x * kGroups; t0 < a.tokens;
+         t0 += (int64_t)gridDim.x * kGroups) {
+        const int64_t t = t0 + threadIdx.x / kLanes;
+        for (int j0 = 0; j0 < a.topk; j0 += kChoices) {
+            int64_t s[kChoices];
+            float w[kChoices], dot[kChoices];
+#pragma unroll
+            for (int q = 0; q < kChoices; ++q) {
+                const int64_t p = t * a.topk + j0 + q;
+                s[q] = t < a.tokens && j0 + q < a.topk ? checked_slot(slots[p], n, a.d_status)
+                                                       : -1;
+                w[q] = weights && s[q] >= 0 ? weights[p] : 1.f;
+                dot[q] = 0.f;
+            }
+            for (int c0 = at * kVec; t < a.tokens && c0 < a.channels;
+                 c0 += kLanes * kVec * kItems) {
+                RawVec<T, kVec> rg[kItems], ry[kChoices][kItems];
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int c = c0 + i * kLanes * kVec;
+                    rg[i] = c < a.channels ? load_raw<T, kVec>(gy + t * ldgy + c)
+                                           : RawVec<T, kVec>{};
+#pragma unroll
+                    for (int q = 0; q < kChoices; ++q)
+                        ry[q][i] = gw && s[q] >= 0 && c < a.channels
+                                       ? load_raw<T, kVec>(ys + s[q] * a.channels + c)
+                                       : RawVec<T, kVec>{};
+                }
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int c = c0 + i * kLanes * kVec;
+                    float g[kVec];
+                    unpack<T, kVec>(rg[i], g);
+#pragma unroll
+                    for (int q = 0; q < kChoices; ++q) {
+                        if (s[q] < 0 || c >= a.channels) continue;
+                        float v[kVec], o[kVec];
+                        unpack<T, kVec>(ry[q][i], v);
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k) {
+                            dot[q] += g[k] * v[k];
+                            o[k] = w[q] * g[k];
+                        }
+                        store_vec<T, kVec>(gys + s[q] * a.channels + c, o);
+                    }
                 }
             }
-            if (gw) {
-                sum = warp_sum(sum);
-                if (lane == 0) gw[p] = sum;
-            }
+            if (!gw) continue;
+            row_sums<kLanes, kChoices>(dot, scratch, half);
+#pragma unroll
+            for (int q = 0; q < kChoices; ++q)
+                if (at == q && t < a.tokens && j0 + q < a.topk) gw[t * a.topk + j0 + q] = dot[q];
         }
-    for (int64_t r = checked_kept(offsets, a.experts, n, a.d_status) + first; r < n; r += step)
-        for (int c = lane; c < a.channels; c += 32) gys[r * a.channels + c] = from_f<T>(0.f);
+    }
+    constexpr int kBytes = kVec * (int)sizeof(T);
+    zero_rows<typename Raw<kBytes>::type, kLanes>(
+        reinterpret_cast<typename Raw<kBytes>::type*>(gys), a.channels / kVec,
+        checked_kept(offsets, a.experts, n, a.d_status), n);
 }
 
-int row_blocks(int64_t rows) {
-    const int64_t b = (rows + kRowWarps - 1) / kRowWarps;
-    return (int)(b < 152 * 64 ? b : 152 * 64);
+// Calls f with the form for rows of n accesses of kVec elements: as few lanes
+// as hold a row with two accesses each (four of single elements).
+template <int kVec, typename F>
+void with_row_form(int n, F&& f) {
+    constexpr int kItems = kVec == 1 ? 4 : 2;
+    if (n <= 8) return f(Form<kVec, 8, 1, 4>{});
+    if (n <= 8 * kItems) return f(Form<kVec, 8, kItems, 2>{});
+    if (n <= 64 * kItems) return f(Form<kVec, 32, kItems, 2>{});
+    return f(Form<kVec, 128, kItems, 2>{});
+}
+
+// Blocks for `tokens` rows, `groups` a block: never more than are resident.
+int row_blocks(int64_t tokens, int groups, int resident) {
+    return (int)std::min<int64_t>((tokens + groups - 1) / groups, resident);
 }
 
 }  // namespace
 
 int sort_units(int64_t n) {
+    if (n <= kSmallSort) return 0;
     const int64_t u = (n + 255) / 256;
-    return (int)(u < 1 ? 1 : u > kMaxUnits ? kMaxUnits : u);
+    return (int)std::min<int64_t>(u, kMaxUnits);
 }
 
 void launch_expert_sort(const int32_t* ids, int64_t n, int experts, int32_t* offsets,
                         int32_t* order, int32_t* slots, int32_t* counts, int32_t* totals,
                         cudaStream_t s) {
     const int units = sort_units(n);
-    const int blocks = (units + kSortUnitWarps - 1) / kSortUnitWarps;
-    const size_t smem = (size_t)kSortUnitWarps * experts * sizeof(int32_t);
-    k_expert_count<<<blocks, kSortUnitThreads, smem, s>>>(ids, n, experts, units, counts);
+    const size_t word = sizeof(int32_t), own = (size_t)kSortWarps * experts * word;
+    if (units == 0) {
+        k_expert_sort_small<<<1, kSortThreads, own + (2 * experts + 1) * word, s>>>(
+            ids, n, experts, offsets, order, slots);
+        return;
+    }
+    const int blocks = (units + kSortWarps - 1) / kSortWarps;
+    k_expert_count<<<blocks, kSortThreads, own, s>>>(ids, n, experts, units, counts);
     k_expert_scan<<<experts, kScanThreads, 0, s>>>(counts, units, experts, totals);
-    k_expert_offsets<<<1, 32, 0, s>>>(totals, experts, offsets);
-    k_expert_place<<<blocks, kSortUnitThreads, smem, s>>>(ids, n, experts, units, counts, offsets,
-                                                          order, slots);
+    k_expert_place<<<blocks, kSortThreads, own + (experts + 1) * word, s>>>(
+        ids, n, experts, units, counts, totals, offsets, order, slots);
 }
 
 void launch_dispatch(const RowArgs& a, const void* x, int64_t ldx, const int32_t* slots,
                      const int32_t* offsets, void* xs, cudaStream_t s) {
+    const int size = (int)dtype_size(a.dtype);
+    const auto run = [&](auto word) {
+        using Word = decltype(word);
+        const int per = (int)sizeof(Word) / size;
+        const int words = a.channels / per;
+        with_row_form<sizeof(Word) == 16 ? 8 : 1>(words, [&](auto form) {
+            using F = decltype(form);
+            const auto kernel = k_dispatch<Word, F::kLanes, F::kItems, F::kRows>;
+            static const int resident = resident_blocks(kernel, 0);
+            kernel<<<row_blocks(a.tokens, kRowThreads / F::kLanes, resident), kRowThreads, 0,
+                     s>>>(a, static_cast<const Word*>(x), ldx / per, words, slots, offsets,
+                          static_cast<Word*>(xs));
+        });
+    };
+    const auto whole = [&](int bytes) {
+        return ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xs)) & (bytes - 1)) ==
+                   0 &&
+               ldx * size % bytes == 0 && a.channels * size % bytes == 0;
+    };
+    if (whole(16))
+        run(uint4{});
+    else if (whole(4))
+        run(uint32_t{});
+    else
+        run(uint16_t{});
+}
+
+namespace {
+
+// f(element, form) for rows whose arrays are all readable in 16-byte vectors,
+// or in single elements.
+template <typename F>
+void with_rows(const RowArgs& a, std::initializer_list<const void*> arrays, int64_t ld, F&& f) {
     with_dtype(a.dtype, [&](auto t) {
         using T = decltype(t);
-        k_dispatch<T><<<row_blocks(a.tokens), kRowThreads, 0, s>>>(a, (const T*)x, ldx, slots,
-                                                                   offsets, (T*)xs);
+        constexpr int kWhole = 16 / (int)sizeof(T);
+        bool whole = a.channels % kWhole == 0 && ld % kWhole == 0;
+        for (const void* p : arrays) whole = whole && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+        if (whole)
+            with_row_form<kWhole>(a.channels / kWhole, [&](auto form) { f(t, form); });
+        else
+            with_row_form<1>(a.channels, [&](auto form) { f(t, form); });
     });
 }
 
+}  // namespace
+
 void launch_combine(const RowArgs& a, const void* ys, const int32_t* slots, const float* weights,
                     void* y, int64_t ldy, cudaStream_t s) {
-    with_dtype(a.dtype, [&](auto t) {
+    with_rows(a, {ys, y}, ldy, [&](auto t, auto form) {
         using T = decltype(t);
-        k_combine<T><<<row_blocks(a.tokens), kRowThreads, 0, s>>>(a, (const T*)ys, slots, weights,
-                                                                  (T*)y, ldy);
+        using F = decltype(form);
+        const auto kernel = k_combine<T, F::kVec, F::kLanes, F::kItems>;
+        static const int resident = resident_blocks(kernel, 0);
+        kernel<<<row_blocks(a.tokens, kRowThreads / F::kLanes, resident), kRowThreads, 0, s>>>(
+            a, static_cast<const T*>(ys), slots, weights, static_cast<T*>(y), ldy);
     });
 }
 
 void launch_combine_bwd(const RowArgs& a, const void* grad_y, int64_t ldgy, const void* ys,
                         const int32_t* slots, const float* weights, const int32_t* offsets,
                         void* grad_ys, float* grad_weights, cudaStream_t s) {
-    with_dtype(a.dtype, [&](auto t) {
+    with_rows(a, {grad_y, ys, grad_ys}, ldgy, [&](auto t, auto form) {
         using T = decltype(t);
-        k_combine_bwd<T><<<row_blocks(a.tokens), kRowThreads, 0, s>>>(
-            a, (const T*)grad_y, ldgy, (const T*)ys, slots, weights, offsets, (T*)grad_ys,
-            grad_weights);
+        using F = decltype(form);
+        const auto kernel = k_combine_bwd<T, F::kVec, F::kLanes, F::kItems>;
+        static const int resident = resident_blocks(kernel, 0);
+        kernel<<<row_blocks(a.tokens, kRowThreads / F::kLanes, resident), kRowThreads, 0, s>>>(
+            a, static_cast<const T*>(grad_y), ldgy, static_cast<const T*>(ys), slots, weights,
+            offsets, static_cast<T*>(grad_ys), grad_weights);
     });
 }
 

@@ -29,7 +29,7 @@ void launch_norm_bwd(const NormArgs& a, const void* grad_y, int64_t ldgy, const 
 
 // ---- experts.cu
 // Contiguous ranges of pairs that gs_expert_sort counts and places one warp
-// each.
+// each; 0 when one block sorts them all and needs no workspace.
 int sort_units(int64_t n);
 // counts: sort_units * experts words; totals: experts words.
 void launch_expert_sort(const int32_t* ids, int64_t n, int experts, int32_t* offsets,
@@ -61,7 +61,10 @@ void launch_linear_dx(const LinearArgs& a, const void* grad_ys, const void* weig
                       cudaStream_t s);
 void launch_linear_dw(const LinearArgs& a, const void* grad_ys, const void* xs,
                       void* grad_weight, cudaStream_t s);
-void launch_linear_db(const LinearArgs& a, const void* grad_ys, void* grad_bias, cudaStream_t s);
+// Bytes of partial sums.
+size_t linear_db_workspace(const LinearArgs& a);
+void launch_linear_db(const LinearArgs& a, const void* grad_ys, void* grad_bias, void* workspace,
+                      cudaStream_t s);
 
 // ---- expert_mma.cu: the same products on the tensor cores.  Each returns a
 // gs_status.

@@ -2,6 +2,7 @@
 // and 16-byte vectors.
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -98,6 +99,58 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// Threads of a block that works on rows, each row by kLanes of them.
+constexpr int kRowThreads = 128;
+
+// Sums over the kLanes lanes of a row of each of kCount values, in every lane.
+// A row of the whole block exchanges its warps' sums through `scratch` (two
+// halves used in turn, so one barrier a call is enough).
+struct RowScratch {
+    float part[2][kRowThreads / 32][8];
+};
+
+template <int kLanes, int kCount>
+__device__ __forceinline__ void row_sums(float* v, RowScratch& scratch, int& half) {
+    constexpr int kIn = kLanes < 32 ? kLanes : 32;
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) v[k] = group_sum<kIn>(v[k]);
+    if constexpr (kLanes > 32) {
+        static_assert(kLanes == kRowThreads && kCount <= 8, "a row is the block's");
+        float(*part)[8] = scratch.part[half];
+        half ^= 1;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int k = 0; k < kCount; ++k) part[threadIdx.x / 32][k] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kCount; ++k) {
+            v[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kRowThreads / 32; ++w) v[k] += part[w][k];
+        }
+    }
+}
+
+// How a kernel works on rows: accesses of kVec elements, kLanes lanes a row,
+// kItems accesses a lane, kRows rows of a lane in flight.
+template <int kVec_, int kLanes_, int kItems_, int kRows_>
+struct Form {
+    static constexpr int kVec = kVec_, kLanes = kLanes_, kItems = kItems_, kRows = kRows_;
+};
+
+// Blocks of a kernel that are resident at once: a walk over the rows in equal
+// shares needs exactly those (a second, part-filled wave costs a whole one).
+template <typename K>
+int resident_blocks(K kernel, size_t smem) {
+    int per = 0, dev = 0, sms = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kRowThreads, smem) !=
+            cudaSuccess ||
+        cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 152;
+    return std::max(1, per) * sms;
 }
 
 // Whether rows at distance ld from p can be read in 16-byte vectors.

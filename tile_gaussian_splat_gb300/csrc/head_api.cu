@@ -111,6 +111,7 @@ int gs_layer_norm_bwd(const void* grad_y, int64_t ldgy, const void* x, int64_t l
 
 size_t gs_expert_sort_workspace_size(int64_t tokens, int topk, int experts) {
     if (!pairs_ok(tokens, topk, experts)) return 0;
+    if (sort_units(tokens * topk) == 0) return 0;
     return sort_counts_bytes(tokens * topk, experts) +
            align_up((size_t)experts * sizeof(int32_t));
 }
@@ -121,9 +122,8 @@ int gs_expert_sort(const int32_t* expert_ids, int64_t tokens, int topk, int expe
     if (!pairs_ok(tokens, topk, experts) || !words_ok(offsets)) return GS_ERR_INVALID_ARG;
     if (tokens > 0 && (!words_ok(expert_ids) || !words_ok(order) || !words_ok(slots)))
         return GS_ERR_INVALID_ARG;
-    if (!words_ok(workspace) ||
-        workspace_bytes < gs_expert_sort_workspace_size(tokens, topk, experts))
-        return GS_ERR_WORKSPACE;
+    const size_t need = gs_expert_sort_workspace_size(tokens, topk, experts);
+    if (need && (!words_ok(workspace) || workspace_bytes < need)) return GS_ERR_WORKSPACE;
     int32_t* counts = static_cast<int32_t*>(workspace);
     int32_t* totals = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) +
                                                  sort_counts_bytes(tokens * topk, experts));
@@ -201,8 +201,8 @@ size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_fea
                                            int out_features, int dtype) {
     int32_t dummy = 0;
     if (!linear_ok(&dummy, rows, experts, in_features, out_features, dtype)) return 0;
-    return align_up(mma_dw_workspace(
-        LinearArgs{nullptr, rows, experts, in_features, out_features, dtype, nullptr}));
+    const LinearArgs a{nullptr, rows, experts, in_features, out_features, dtype, nullptr};
+    return align_up(linear_db_workspace(a)) + align_up(mma_dw_workspace(a));
 }
 
 int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* offsets,
@@ -220,7 +220,7 @@ int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* off
     if (grad_bias && !array_ok(grad_bias, dtype)) return GS_ERR_INVALID_ARG;
     const size_t need = gs_expert_linear_bwd_workspace_size(rows, experts, in_features,
                                                             out_features, dtype);
-    if (grad_weight && need &&
+    if ((grad_weight || grad_bias) &&
         (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need))
         return GS_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -235,13 +235,15 @@ int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* off
     }
     if (grad_weight) {
         if (rows > 0 && mma_usable(a, {grad_ys, xs, grad_weight})) {
-            const int rc = launch_mma_dw(a, grad_ys, xs, grad_weight, workspace, s);
+            const int rc = launch_mma_dw(
+                a, grad_ys, xs, grad_weight,
+                static_cast<char*>(workspace) + align_up(linear_db_workspace(a)), s);
             if (rc != GS_OK) return rc;
         } else {
             launch_linear_dw(a, grad_ys, xs, grad_weight, s);
         }
     }
-    if (grad_bias) launch_linear_db(a, grad_ys, grad_bias, s);
+    if (grad_bias) launch_linear_db(a, grad_ys, grad_bias, workspace, s);
     return check_launch();
 }
 

@@ -17,7 +17,7 @@ namespace gs {
 
 namespace {
 
-constexpr int kNormThreads = 128;
+constexpr int kNormThreads = kRowThreads;
 constexpr int kLongThreads = 256;
 constexpr int kRegisterChannels = 1024;
 constexpr int kMaxSlices = 152 * 16;  // blocks that leave partial parameter gradients
@@ -39,35 +39,6 @@ struct NormBwd {
     int64_t ldgy, ldx, ldgx, rows;
     int channels, param_dtype;
 };
-
-// Sums over the kLanes lanes of a row of each of kCount values, in every lane.
-// A row of the whole block exchanges its warps' sums through `scratch` (two
-// halves used in turn, so one barrier a call is enough).
-struct RowScratch {
-    float part[2][kNormThreads / 32][8];
-};
-
-template <int kLanes, int kCount>
-__device__ __forceinline__ void row_sums(float* v, RowScratch& scratch, int& half) {
-    constexpr int kIn = kLanes < 32 ? kLanes : 32;
-#pragma unroll
-    for (int k = 0; k < kCount; ++k) v[k] = group_sum<kIn>(v[k]);
-    if constexpr (kLanes > 32) {
-        static_assert(kLanes == kNormThreads && kCount <= 8, "a row is the block's");
-        float(*part)[8] = scratch.part[half];
-        half ^= 1;
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int k = 0; k < kCount; ++k) part[threadIdx.x / 32][k] = v[k];
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kCount; ++k) {
-            v[k] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kNormThreads / 32; ++w) v[k] += part[w][k];
-        }
-    }
-}
 
 // kVec elements per access, kLanes lanes a row, kItems accesses a lane and
 // row, kRows rows of a lane in flight.
@@ -385,11 +356,6 @@ __global__ void __launch_bounds__(256)
 // elements a lane the forward over 64 channels was bound by instruction issue:
 // 279 us for 2 M rows, against 162 us for its bytes); a lane still holds at
 // most 16 elements, so that many rows are in flight.
-template <int kVec_, int kLanes_, int kItems_, int kRows_>
-struct Form {
-    static constexpr int kVec = kVec_, kLanes = kLanes_, kItems = kItems_, kRows = kRows_;
-};
-
 template <typename T, int kVec, typename F>
 void with_form(int channels, F&& f) {
     const int n = (channels + kVec - 1) / kVec;
@@ -412,19 +378,6 @@ void with_form(int channels, F&& f) {
 
 int blocks_for(int64_t rows, int groups, int cap) {
     return (int)std::min<int64_t>((rows + groups - 1) / groups, cap);
-}
-
-// Blocks of a kernel that are resident at once: a walk over the rows in equal
-// shares needs exactly those (a second, part-filled wave costs a whole one).
-template <typename K>
-int resident_blocks(K kernel, size_t smem) {
-    int per = 0, dev = 0, sms = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kNormThreads, smem) !=
-            cudaSuccess ||
-        cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 152;
-    return std::max(1, per) * sms;
 }
 
 }  // namespace
