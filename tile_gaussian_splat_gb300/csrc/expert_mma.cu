@@ -10,9 +10,10 @@
 //
 // One block per SM walks output tiles of 128 x kWide: a warp copies 64-term
 // slices of A and B into a ring of shared-memory stages (tiled bulk copies),
-// a second one issues the matrix instructions, four more move the finished
+// a second one issues the matrix instructions, eight more move the finished
 // accumulators from tensor memory to the output while the next tile is
-// computed in the other half of it.
+// computed in the other half of it (with four, the forward of 262144 rows,
+// 512 -> 1024, was bound by them: 235 us).
 #include <cstdint>
 #include <type_traits>
 
@@ -32,8 +33,8 @@ enum Product { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 
 constexpr int kHigh = 128;        // rows of an output tile
 constexpr int kSlice = 64;        // terms of the sum per stage: 128 bytes
-constexpr int kMmaThreads = 256;  // warps: copy, products, 2 idle, 4 output
-constexpr int kOutWarps = 4;
+constexpr int kOutWarps = 8;      // two for each quarter of the tile's rows
+constexpr int kMmaThreads = 32 * (4 + kOutWarps);  // warps: copy, products, 2 idle, output
 constexpr int kAccumulators = 2;
 
 struct ProductArgs {
@@ -53,7 +54,7 @@ struct Shape {
     static constexpr int kBytesB = kWide * kSlice * 2;
     static constexpr int kStageBytes = kBytesA + kBytesB;
     static constexpr int kStages = kWide == 256 ? 4 : 6;
-    static constexpr int kStaging = kOutWarps * 32 * 128;
+    static constexpr int kStaging = kOutWarps * 32 * 64;
     static constexpr int kColumns = kAccumulators * kWide;
 };
 
@@ -122,23 +123,23 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 rows x 128 bytes of output held one row a lane (eight 16-byte vectors),
-// turned through shared memory so that eight lanes write one row's 128
+// 32 rows x 64 bytes of output held one row a lane (four 16-byte vectors),
+// turned through shared memory so that four lanes write one row's 64
 // contiguous bytes.  valid_rows of the rows and valid_vectors of a row's
 // vectors are inside the output.
 __device__ __forceinline__ void write_block(char* staging, const uint4* v, char* out,
                                             int64_t pitch, int valid_rows, int valid_vectors) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4*>(staging + lane * 128 + ((j ^ (lane & 7)) << 4)) = v[j];
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(staging + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = v[j];
     __syncwarp();
-    const int j = lane & 7;
+    const int j = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + lane / 8;
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4;
         const uint4 x =
-            *reinterpret_cast<const uint4*>(staging + r * 128 + ((j ^ (r & 7)) << 4));
+            *reinterpret_cast<const uint4*>(staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4));
         if (r < valid_rows && j < valid_vectors)
             *reinterpret_cast<uint4*>(out + r * pitch + j * 16) = x;
     }
@@ -291,20 +292,26 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             mbar_wait_limited(&bars.drain, 0, &none);
         }
     } else if (warp >= 4) {
-        const int q = warp - 4;  // tensor-memory lanes [32 q, 32 q + 32)
-        char* mine = staging + q * 32 * 128;
-        constexpr int kVec = 16 / sizeof(Out);      // outputs per 16 bytes
-        constexpr int kBlock = 128 / sizeof(Out);   // columns per block of 128 bytes
+        const int q = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
+        constexpr int kSpan = kWide / (kOutWarps / 4);  // columns of this warp
+        const int first = (warp - 4) / 4 * kSpan;
+        char* mine = staging + (warp - 4) * 32 * 64;
+        constexpr int kVec = 16 / sizeof(Out);  // outputs per 16 bytes
         uint32_t done = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const Tile c = tile_at<kProduct, kWide>(g, begin, prefix, t);
             const int acc = done % kAccumulators;
+            const uint32_t from =
+                tmem + ((uint32_t)(q * 32) << 16) + acc * kWide + first;
+            uint32_t u[2][32] = {};
             if (c.slices > 0) {
                 ok = warp_wait(&bars.acc_full[acc], (done / kAccumulators) & 1, abort);
                 if (!ok) break;
                 ++done;
                 tmem_fence_after();
+                tmem_load32(from, u[0]);
+                tmem_wait_loads();
             }
             char* out;
             int rows;
@@ -319,47 +326,53 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 rows = c.row1 - c.row0 - q * 32;
             }
 #pragma unroll
-            for (int n = 0; n < kWide; n += kBlock) {
-                if (c.n0 + n >= g.width) break;
-                uint4 v[8];
-#pragma unroll
-                for (int h = 0; h < kBlock / 32; ++h) {
-                    uint32_t u[32];
-                    if (c.slices > 0) {
-                        tmem_load32(tmem + ((uint32_t)(q * 32) << 16) + acc * kWide + n + h * 32,
-                                    u);
-                        tmem_wait_loads();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) u[i] = 0;
-                    }
+            for (int b = 0; b < kSpan / 32; ++b) {
+                const int n = first + b * 32;
+                // the next 32 columns come in while these go out
+                if (c.slices > 0 && b + 1 < kSpan / 32)
+                    tmem_load32(from + (b + 1) * 32, u[(b + 1) & 1]);
+                const uint32_t* w = u[b & 1];
+                const int left = g.width - c.n0 - n;  // columns from here on
+                if (left > 0) {
                     if constexpr (std::is_same<Out, float>::value) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            v[i] = uint4{u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]};
+                        for (int h = 0; h < 2; ++h) {
+                            uint4 v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                v[i] = uint4{w[16 * h + 4 * i], w[16 * h + 4 * i + 1],
+                                             w[16 * h + 4 * i + 2], w[16 * h + 4 * i + 3]};
+                            write_block(mine, v, out + (n + 16 * h) * sizeof(Out),
+                                        (int64_t)g.width * sizeof(Out), rows,
+                                        (left - 16 * h + kVec - 1) / kVec);
+                        }
                     } else {
+                        uint4 v[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             float f[8];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(u[8 * i + j]);
-                            const int col = c.n0 + n + h * 32 + i * 8;
-                            if (kProduct == kForward && g.bias && col < g.width)
+                            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[8 * i + j]);
+                            if (kProduct == kForward && g.bias && i * 8 < left)
                                 add_bias(f, static_cast<const T*>(g.bias) +
-                                                (int64_t)c.expert * g.width + col);
-                            v[h * 4 + i] = uint4{pack2<Out>(f[0], f[1]), pack2<Out>(f[2], f[3]),
-                                                 pack2<Out>(f[4], f[5]), pack2<Out>(f[6], f[7])};
+                                                (int64_t)c.expert * g.width + c.n0 + n + i * 8);
+                            v[i] = uint4{pack2<Out>(f[0], f[1]), pack2<Out>(f[2], f[3]),
+                                         pack2<Out>(f[4], f[5]), pack2<Out>(f[6], f[7])};
                         }
+                        write_block(mine, v, out + n * sizeof(Out),
+                                    (int64_t)g.width * sizeof(Out), rows,
+                                    (left + kVec - 1) / kVec);
                     }
                 }
-                if (c.slices > 0 && n + kBlock >= min(kWide, g.width - c.n0)) {
-                    // the accumulator is read: its next product may begin
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.acc_empty[acc]);
+                if (c.slices > 0) {
+                    tmem_wait_loads();
+                    if (b + 2 == kSpan / 32 || kSpan == 32) {
+                        // the accumulator is read: its next product may begin
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.acc_empty[acc]);
+                    }
                 }
-                write_block(mine, v, out + n * sizeof(Out), (int64_t)g.width * sizeof(Out), rows,
-                            (g.width - c.n0 - n + kVec - 1) / kVec);
             }
         }
         if (kProduct != kWeightGrad) {

@@ -385,14 +385,21 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // Calls f with the form for rows of n accesses of kVec elements: as few lanes
-// as hold a row with two accesses each (four of single elements).
+// as hold a row with two accesses each (eight of single elements).
 template <int kVec, typename F>
 void with_row_form(int n, F&& f) {
-    constexpr int kItems = kVec == 1 ? 4 : 2;
-    if (n <= 8) return f(Form<kVec, 8, 1, 4>{});
-    if (n <= 8 * kItems) return f(Form<kVec, 8, kItems, 2>{});
-    if (n <= 64 * kItems) return f(Form<kVec, 32, kItems, 2>{});
-    return f(Form<kVec, 128, kItems, 2>{});
+    if constexpr (kVec == 1) {
+        if (n <= 32) return f(Form<1, 8, 4, 2>{});
+        if (n <= 64) return f(Form<1, 8, 8, 1>{});
+        if (n <= 128) return f(Form<1, 32, 4, 2>{});
+        if (n <= 256) return f(Form<1, 32, 8, 1>{});
+        return f(Form<1, 128, 4, 2>{});
+    } else {
+        if (n <= 8) return f(Form<kVec, 8, 1, 4>{});
+        if (n <= 16) return f(Form<kVec, 8, 2, 2>{});
+        if (n <= 128) return f(Form<kVec, 32, 2, 2>{});
+        return f(Form<kVec, 128, 2, 2>{});
+    }
 }
 
 // Blocks for `tokens` rows, `groups` a block: never more than are resident.
