@@ -8,12 +8,25 @@
 // The operand whose sum index is not contiguous in memory is handed to the
 // matrix instruction as it lies (MN-major), so nothing is transposed.
 //
-// One block per SM walks output tiles of 128 x kWide: a warp copies 64-term
-// slices of A and B into a ring of shared-memory stages (tiled bulk copies),
-// a second one issues the matrix instructions, eight more move the finished
-// accumulators from tensor memory to the output while the next tile is
-// computed in the other half of it (with four, the forward of 262144 rows,
-// 512 -> 1024, was bound by them: 235 us).
+// Two neighbouring blocks work as one on output tiles of 256 x 256 (each
+// block holds half of the rows of A and of B, so every byte copied into shared
+// memory serves twice the products; a single block on tiles of 128 x 256 was
+// bound by those copies: 15 TB/s out of the L2).  Narrow outputs and few rows
+// take one block and 128-row tiles.  In every block a warp copies 64-term
+// slices into a ring of shared-memory stages (tiled bulk copies, counted on
+// the first block's barrier), one warp of the first block issues the matrix
+// instructions, and eight warps move finished accumulators from tensor memory
+// to the output while the next tile is computed in the other half of it.
+//
+// The weight gradient's sums run over an expert's rows, of which there are
+// many for few output tiles.  The rows of all experts, end to end, are cut
+// into g.groups equal shares; a share's tiles (one per tile of a weight
+// matrix) walk it side by side, so the rows are read from memory once.  An
+// expert that lies within one share is written at once; one that crosses a
+// cut leaves partial sums, added up in the order of the shares afterwards.
+// Two helper warps take the bias gradient's column sums from the same stages,
+// and clear the rows of the next expert in an expert's last slice.
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -42,73 +55,133 @@ struct ProductArgs {
     int64_t rows;
     int experts;
     int high, width, depth;  // extents: high of the weight gradient, depth of the others
-    int chunk;               // weight gradient: rows of a partial sum (0: all of an expert's)
-    const void* bias;
+    int groups;              // weight gradient: shares of the rows
+    const void* bias;        // kForward
     void* out;
+    void* bias_grad;         // kWeightGrad, or null
+    float* partial;          // kWeightGrad: two tiles an item (see Walk)
+    float* bias_partial;     // two tile heights an item
     int32_t* d_status;
 };
 
-template <int kWide>
+// kBlocks blocks share a tile of kHigh * kBlocks rows and kWide columns.
+template <int kBlocks, int kWide>
 struct Shape {
+    static constexpr int kTileHigh = kHigh * kBlocks;
     static constexpr int kBytesA = kHigh * kSlice * 2;
-    static constexpr int kBytesB = kWide * kSlice * 2;
+    static constexpr int kPartB = kWide / kBlocks;  // columns of B a block holds
+    static constexpr int kBytesB = kPartB * kSlice * 2;
     static constexpr int kStageBytes = kBytesA + kBytesB;
-    static constexpr int kStages = kWide == 256 ? 4 : 6;
+    static constexpr int kStages = kStageBytes > 32768 ? 4 : 6;
     static constexpr int kStaging = kOutWarps * 32 * 64;
     static constexpr int kColumns = kAccumulators * kWide;
 };
 
 struct Bars {
-    uint64_t full[8], empty[8], acc_full[kAccumulators], acc_empty[kAccumulators], drain;
+    // of the first block: a stage's data is there (in all blocks), its rows of
+    // another expert are cleared, the accumulators may be overwritten
+    uint64_t full[6], cleared, acc_empty[kAccumulators];
+    // of each block: the helpers may read a stage, it may be overwritten, the
+    // accumulators are finished
+    uint64_t landed[6], empty[6], acc_full[kAccumulators], drain;
     uint32_t tmem;
     int abort;
 };
 
-template <int kWide>
+template <int kBlocks, int kWide>
 constexpr size_t smem_bytes(int experts) {
-    using S = Shape<kWide>;
+    using S = Shape<kBlocks, kWide>;
     return 1024 + (size_t)S::kStages * S::kStageBytes + S::kStaging + sizeof(Bars) +
            2 * sizeof(int32_t) * (size_t)(experts + 1);
 }
 
-// One output tile of the walk.
+// A place in a ring of kCount stages, and how often it has gone round.
+template <int kCount>
+struct Ring {
+    uint32_t stage = 0, turn = 0;
+    __device__ __forceinline__ void advance() {
+        if (++stage == kCount) {
+            stage = 0;
+            ++turn;
+        }
+    }
+};
+
+// One output tile, or one expert's part of it (kWeightGrad).
 struct Tile {
-    int expert, piece;
+    int expert;
     int row0, row1;  // rows of the output (of the sum, for kWeightGrad)
     int m0, n0;      // first row (kWeightGrad only) and column of the tile
     int slices;      // 64-term slices of the sum
+    bool whole;      // kWeightGrad: all of the expert's rows
+    int64_t slot;    // kWeightGrad: where a partial sum goes
 };
 
-template <int kProduct, int kWide>
-__device__ __forceinline__ int tiles_per_piece(const ProductArgs& g) {
-    const int across = (g.width + kWide - 1) / kWide;
-    return kProduct == kWeightGrad ? across * ((g.high + kHigh - 1) / kHigh) : across;
+__device__ __forceinline__ int64_t share_begin(int64_t total, int groups, int group) {
+    return total * group / groups;
 }
 
-template <int kProduct, int kWide>
-__device__ __forceinline__ Tile tile_at(const ProductArgs& g, const int32_t* begin,
-                                        const int32_t* prefix, int64_t t) {
-    const int per = tiles_per_piece<kProduct, kWide>(g);
-    const int across = (g.width + kWide - 1) / kWide;
-    Tile r;
-    r.piece = (int)(t / per);
-    const int in = (int)(t - (int64_t)r.piece * per);
-    r.n0 = in % across * kWide;
-    r.m0 = in / across * kHigh;
-    r.expert = expert_of(prefix, g.experts, r.piece);
-    const int height = kProduct == kWeightGrad ? g.chunk : kHigh;
-    const int b = begin[r.expert], e = begin[r.expert + 1];
-    if (height == 0) {
-        r.row0 = b;
-        r.row1 = e;
-    } else {
-        r.row0 = b + (r.piece - prefix[r.expert]) * height;
-        r.row1 = min(e, r.row0 + height);
+// The tiles of one pair of blocks (or block), in order; every warp of it walks
+// the same ones.  kForward, kInputGrad: item = (piece of an expert's rows,
+// column tile).  kWeightGrad: item = (share of the rows, tile of the weight
+// matrix), its experts one after the other; begin and prefix count slices.
+template <int kProduct, int kBlocks, int kWide>
+struct Walk {
+    using S = Shape<kBlocks, kWide>;
+    const ProductArgs& g;
+    const int32_t *begin, *prefix;
+    int64_t item, items, mine = 0, pos = 0, end = 0;
+    int step, across, per;
+
+    __device__ __forceinline__ Walk(const ProductArgs& g_, const int32_t* begin_,
+                                    const int32_t* prefix_)
+        : g(g_), begin(begin_), prefix(prefix_) {
+        item = blockIdx.x / kBlocks;
+        step = gridDim.x / kBlocks;
+        across = (g.width + kWide - 1) / kWide;
+        per = kProduct == kWeightGrad ? across * ((g.high + S::kTileHigh - 1) / S::kTileHigh)
+                                      : across;
+        items = (int64_t)(kProduct == kWeightGrad ? g.groups : prefix[g.experts]) * per;
     }
-    const int terms = kProduct == kWeightGrad ? r.row1 - r.row0 : g.depth;
-    r.slices = (terms + kSlice - 1) / kSlice;
-    return r;
-}
+
+    __device__ __forceinline__ bool next(Tile& c) {
+        if constexpr (kProduct == kWeightGrad) {
+            const int64_t total = prefix[g.experts];
+            while (pos >= end) {
+                if (item >= items) return false;
+                mine = item;
+                item += step;
+                pos = share_begin(total, g.groups, (int)(mine / per));
+                end = share_begin(total, g.groups, (int)(mine / per) + 1);
+            }
+            const int in = (int)(mine % per);
+            c.m0 = in / across * S::kTileHigh;
+            c.n0 = in % across * kWide;
+            c.expert = expert_of(prefix, g.experts, (int)pos);
+            const int first = prefix[c.expert], count = prefix[c.expert + 1] - first;
+            const int k0 = (int)pos - first, k1 = (int)min(end - first, (int64_t)count);
+            c.row0 = begin[c.expert] + k0 * kSlice;
+            c.row1 = min(begin[c.expert + 1], begin[c.expert] + k1 * kSlice);
+            c.slices = k1 - k0;
+            c.whole = c.slices == count;
+            c.slot = mine * 2 + (k0 > 0 ? 0 : 1);
+            pos += c.slices;
+        } else {
+            if (item >= items) return false;
+            const int piece = (int)(item / per);
+            c.m0 = 0;
+            c.n0 = (int)(item - (int64_t)piece * per) * kWide;
+            c.expert = expert_of(prefix, g.experts, piece);
+            c.row0 = begin[c.expert] + (piece - prefix[c.expert]) * S::kTileHigh;
+            c.row1 = min(begin[c.expert + 1], c.row0 + S::kTileHigh);
+            c.slices = (g.depth + kSlice - 1) / kSlice;
+            c.whole = true;
+            c.slot = 0;
+            item += step;
+        }
+        return true;
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -155,13 +228,11 @@ __device__ __forceinline__ void add_bias(float* v, const T* bias) {
     for (int i = 0; i < 8; ++i) v[i] += to_f(p[i]);
 }
 
-// T: element type of the operands; Out: of the output (float for partial sums
-// of the weight gradient).
-template <typename T, typename Out, int kProduct, int kWide>
+template <typename T, int kProduct, int kBlocks, int kWide>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const __grid_constant__ ProductArgs g) {
-    using S = Shape<kWide>;
+    using S = Shape<kBlocks, kWide>;
     constexpr bool kMnA = kProduct == kWeightGrad;
     constexpr bool kMnB = kProduct != kForward;
     extern __shared__ char smem_raw[];
@@ -171,247 +242,327 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     int32_t* begin = reinterpret_cast<int32_t*>(&bars + 1);
     int32_t* prefix = begin + g.experts + 1;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int rank = kBlocks == 2 ? (int)cluster_rank() : 0;
+    // the helpers read the stages too where the bias gradient is asked for
+    const bool columns = kProduct == kWeightGrad && g.bias_grad;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch(&map_a);
         tma_prefetch(&map_b);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 1);
+            mbar_init(&bars.landed[i], 1);
+            mbar_init(&bars.empty[i], kProduct == kWeightGrad ? (columns ? 3 : 2) : 1);
         }
         for (int i = 0; i < kAccumulators; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], kOutWarps);
+            mbar_init(&bars.acc_empty[i], kOutWarps * kBlocks);
         }
+        mbar_init(&bars.cleared, kBlocks);
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
     }
-    if (warp == 1) tmem_alloc(&bars.tmem, S::kColumns);
+    if (warp == 1) tmem_alloc<kBlocks>(&bars.tmem, S::kColumns);
     if (warp == 2)
-        expert_pieces(g.offsets, g.experts, g.rows, kProduct == kWeightGrad ? g.chunk : kHigh,
-                      begin, prefix, blockIdx.x == 0 ? g.d_status : nullptr);
+        expert_pieces(g.offsets, g.experts, g.rows,
+                      kProduct == kWeightGrad ? kSlice : S::kTileHigh, begin, prefix,
+                      blockIdx.x == 0 ? g.d_status : nullptr);
     tmem_fence_before();
     __syncthreads();
+    if (kBlocks == 2) cluster_sync();
     tmem_fence_after();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = bars.tmem, base = smem_u32(smem);
     volatile int* abort = &bars.abort;
-    const int64_t tiles = (int64_t)prefix[g.experts] * tiles_per_piece<kProduct, kWide>(g);
+    Walk<kProduct, kBlocks, kWide> walk(g, begin, prefix);
+    Tile c;
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const Tile c = tile_at<kProduct, kWide>(g, begin, prefix, t);
-                for (int k = 0; k < c.slices; ++k, ++it) {
-                    const int s = it % S::kStages;
-                    if (it >= S::kStages &&
-                        !mbar_wait_limited(&bars.empty[s], (it / S::kStages + 1) & 1, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t a = smem_u32(smem + s * S::kStageBytes);
-                    const uint32_t b = a + S::kBytesA;
-                    uint64_t* full = &bars.full[s];
-                    mbar_expect_tx(full, S::kStageBytes);
+        Ring<S::kStages> at;
+        bool ok = true;
+        while (ok && walk.next(c)) {
+            const int n0 = c.n0 + rank * S::kPartB;
+            for (int k = 0; k < c.slices; ++k, at.advance()) {
+                ok = at.turn == 0 || warp_wait(&bars.empty[at.stage], (at.turn + 1) & 1, abort);
+                if (!ok) break;
+                const uint32_t a = base + at.stage * S::kStageBytes;
+                const uint32_t b = a + S::kBytesA;
+                const uint32_t full = kBlocks == 2 ? mbar_at(&bars.full[at.stage], 0)
+                                                   : smem_u32(&bars.full[at.stage]);
+                if (elect_one()) {
+                    if (rank == 0)
+                        mbar_expect_tx(&bars.full[at.stage], S::kStageBytes * kBlocks);
                     if (kProduct == kWeightGrad) {
+                        const int m0 = c.m0 + rank * kHigh, row = c.row0 + k * kSlice;
+#pragma unroll
                         for (int i = 0; i < kHigh / 64; ++i)
-                            tma_load_2d(a + i * 64 * 128, &map_a, c.m0 + i * 64,
-                                        c.row0 + k * kSlice, full);
-                        for (int i = 0; i < kWide / 64; ++i)
-                            tma_load_2d(b + i * 64 * 128, &map_b, c.n0 + i * 64,
-                                        c.row0 + k * kSlice, full);
+                            tma_load_2d<kBlocks>(a + i * 64 * 128, &map_a, m0 + i * 64, row, full);
+#pragma unroll
+                        for (int i = 0; i < S::kPartB / 64; ++i)
+                            tma_load_2d<kBlocks>(b + i * 64 * 128, &map_b, n0 + i * 64, row, full);
                     } else {
-                        tma_load_2d(a, &map_a, k * kSlice, c.row0, full);
+                        tma_load_2d<kBlocks>(a, &map_a, k * kSlice, c.row0 + rank * kHigh, full);
                         if (kProduct == kForward) {
-                            tma_load_3d(b, &map_b, k * kSlice, c.n0, c.expert, full);
+                            tma_load_3d<kBlocks>(b, &map_b, k * kSlice, n0, c.expert, full);
                         } else {
-                            for (int i = 0; i < kWide / 64; ++i)
-                                tma_load_3d(b + i * 64 * 128, &map_b, c.n0 + i * 64, k * kSlice,
-                                            c.expert, full);
+#pragma unroll
+                            for (int i = 0; i < S::kPartB / 64; ++i)
+                                tma_load_3d<kBlocks>(b + i * 64 * 128, &map_b, n0 + i * 64,
+                                                     k * kSlice, c.expert, full);
                         }
                     }
-                }
-            }
-            if (!ok)  // let the copies in flight land before the block goes
-                for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i) {
-                    int none = 0;
-                    mbar_wait_limited(&bars.full[i % S::kStages], (i / S::kStages) & 1, &none);
-                }
-        }
-    } else if (warp == 1) {
-        constexpr uint32_t word =
-            mma_word(kHigh, kWide, std::is_same<T, __nv_bfloat16>::value, kMnA, kMnB);
-        uint32_t it = 0, done = 0;
-        bool ok = true;
-        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile c = tile_at<kProduct, kWide>(g, begin, prefix, t);
-            if (c.slices == 0) continue;
-            const int acc = done % kAccumulators;
-            if (done >= kAccumulators)
-                ok = warp_wait(&bars.acc_empty[acc], (done / kAccumulators + 1) & 1, abort);
-            ++done;
-            tmem_fence_after();
-            for (int k = 0; k < c.slices && ok; ++k, ++it) {
-                const int s = it % S::kStages;
-                ok = warp_wait(&bars.full[s], (it / S::kStages) & 1, abort);
-                if (!ok) break;
-                const uint32_t a = smem_u32(smem + s * S::kStageBytes);
-                const uint32_t b = a + S::kBytesA;
-                if (kProduct == kWeightGrad && c.row0 + (k + 1) * kSlice > c.row1) {
-                    // rows of the next expert in the last slice count as 0,
-                    // in both operands: they may hold anything
-                    const int first = c.row1 - c.row0 - k * kSlice;
-                    for (int i = first * 8 + lane; i < kSlice * 8; i += 32)
-                        for (int q = 0; q < (kHigh + kWide) / 64; ++q)
-                            *reinterpret_cast<uint4*>(smem + s * S::kStageBytes + q * 64 * 128 +
-                                                      i * 16) = uint4{0, 0, 0, 0};
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
-                if (lane == 0) {
-                    tmem_fence_after();
-#pragma unroll
-                    for (int j = 0; j < kSlice / 16; ++j) {
-                        const uint64_t da = kMnA ? smem_operand(a + j * 2048, 64 * 128, 1024)
-                                                 : smem_operand(a + j * 32, 16, 1024);
-                        const uint64_t db = kMnB ? smem_operand(b + j * 2048, 64 * 128, 1024)
-                                                 : smem_operand(b + j * 32, 16, 1024);
-                        mma_f16(tmem + acc * kWide, da, db, word, k > 0 || j > 0);
-                    }
-                    mma_commit(&bars.empty[s]);
-                    if (k + 1 == c.slices) mma_commit(&bars.acc_full[acc]);
                 }
                 __syncwarp();
             }
         }
-        // nothing of this block is still writing tensor memory when it is freed
-        if (lane == 0) {
-            mma_commit(&bars.drain);
+        if (!ok && rank == 0)  // let the copies in flight land before the blocks go
+            for (int i = 0; i < S::kStages; ++i) {
+                // stages [stage, ...) were last filled one turn ago
+                const uint32_t turn = i < (int)at.stage ? at.turn : at.turn - 1;
+                int none = 0;
+                if (turn != ~0u) mbar_wait_limited(&bars.full[i], turn & 1, &none);
+            }
+    } else if (warp == 1) {
+        constexpr uint32_t word = mma_word(S::kTileHigh, kWide,
+                                           std::is_same<T, __nv_bfloat16>::value, kMnA, kMnB);
+        const uint64_t from_a =
+            kMnA ? smem_operand(base, 64 * 128, 1024) : smem_operand(base, 16, 1024);
+        const uint64_t from_b = kMnB ? smem_operand(base + S::kBytesA, 64 * 128, 1024)
+                                     : smem_operand(base + S::kBytesA, 16, 1024);
+        Ring<S::kStages> at;
+        Ring<kAccumulators> acc;
+        uint32_t cut = 0;
+        bool ok = rank == 0;
+        while (ok && walk.next(c)) {
+            if (acc.turn > 0) ok = warp_wait(&bars.acc_empty[acc.stage], (acc.turn + 1) & 1, abort);
+            tmem_fence_after();
+            const uint32_t d = tmem + acc.stage * kWide;
+            for (int k = 0; k < c.slices && ok; ++k, at.advance()) {
+                ok = warp_wait(&bars.full[at.stage], at.turn & 1, abort);
+                if (!ok) break;
+                if (kProduct == kWeightGrad) {
+                    if (lane < kBlocks) mbar_arrive_at(&bars.landed[at.stage], lane);
+                    if (c.row1 - c.row0 < (k + 1) * kSlice) {
+                        ok = warp_wait(&bars.cleared, cut++ & 1, abort);
+                        if (!ok) break;
+                    }
+                    __syncwarp();
+                }
+                const uint64_t da = from_a + at.stage * (S::kStageBytes >> 4);
+                const uint64_t db = from_b + at.stage * (S::kStageBytes >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < kSlice / 16; ++j)
+                        mma_f16<kBlocks>(d, da + j * ((kMnA ? 2048 : 32) >> 4),
+                                         db + j * ((kMnB ? 2048 : 32) >> 4), word,
+                                         k > 0 || j > 0);
+                    mma_commit<kBlocks>(&bars.empty[at.stage]);
+                    if (k + 1 == c.slices) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
+                }
+                __syncwarp();
+            }
+            acc.advance();
+        }
+        // nothing is still writing tensor memory when it is freed
+        if (rank == 0) {
+            if (elect_one()) mma_commit<kBlocks>(&bars.drain);
+            __syncwarp();
             int none = 0;
             mbar_wait_limited(&bars.drain, 0, &none);
+        }
+    } else if (kProduct == kWeightGrad && (warp == 2 || (warp == 3 && columns))) {
+        Ring<S::kStages> at;
+        bool ok = true;
+        while (ok && walk.next(c)) {
+            float low = 0.f, top = 0.f;  // sums of this lane's two columns of A
+            for (int k = 0; k < c.slices; ++k, at.advance()) {
+                ok = warp_wait(&bars.landed[at.stage], at.turn & 1, abort);
+                if (!ok) break;
+                char* a = smem + at.stage * S::kStageBytes;
+                const int valid = min(kSlice, c.row1 - c.row0 - k * kSlice);
+                if (warp == 2 && valid < kSlice) {
+                    // rows of the next expert count as 0, in both operands:
+                    // they may hold anything
+                    for (int i = valid * 8 + lane; i < kSlice * 8; i += 32)
+                        for (int q = 0; q < S::kStageBytes / (64 * 128); ++q)
+                            *reinterpret_cast<uint4*>(a + q * 64 * 128 + i * 16) =
+                                uint4{0, 0, 0, 0};
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_release_at(&bars.cleared, 0);
+                }
+                if (columns && c.n0 == 0) {
+                    const char* p = a + (warp - 2) * 64 * 128 + (lane & 3) * 4;
+#pragma unroll 8
+                    for (int r = 0; r < valid; ++r) {
+                        const uint32_t v = *reinterpret_cast<const uint32_t*>(
+                            p + r * 128 + ((lane / 4 ^ (r & 7)) << 4));
+                        const T* e = reinterpret_cast<const T*>(&v);
+                        low += to_f(e[0]);
+                        top += to_f(e[1]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(&bars.empty[at.stage], rank);
+            }
+            if (ok && columns && c.n0 == 0) {
+                const int in = rank * kHigh + (warp - 2) * 64 + lane * 2, m = c.m0 + in;
+                if (!c.whole)
+                    *reinterpret_cast<float2*>(g.bias_partial + c.slot * S::kTileHigh + in) =
+                        float2{low, top};
+                else if (m < g.high)
+                    *reinterpret_cast<uint32_t*>(static_cast<T*>(g.bias_grad) +
+                                                 (int64_t)c.expert * g.high + m) =
+                        pack2<T>(low, top);
+            }
         }
     } else if (warp >= 4) {
         const int q = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
         constexpr int kSpan = kWide / (kOutWarps / 4);  // columns of this warp
         const int first = (warp - 4) / 4 * kSpan;
         char* mine = staging + (warp - 4) * 32 * 64;
-        constexpr int kVec = 16 / sizeof(Out);  // outputs per 16 bytes
-        uint32_t done = 0;
+        Ring<kAccumulators> acc;
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile c = tile_at<kProduct, kWide>(g, begin, prefix, t);
-            const int acc = done % kAccumulators;
+        for (; ok && walk.next(c); acc.advance()) {
             const uint32_t from =
-                tmem + ((uint32_t)(q * 32) << 16) + acc * kWide + first;
-            uint32_t u[2][32] = {};
-            if (c.slices > 0) {
-                ok = warp_wait(&bars.acc_full[acc], (done / kAccumulators) & 1, abort);
-                if (!ok) break;
-                ++done;
-                tmem_fence_after();
-                tmem_load32(from, u[0]);
-                tmem_wait_loads();
-            }
+                tmem + ((uint32_t)(q * 32) << 16) + acc.stage * kWide + first;
+            uint32_t u[2][32];
+            ok = warp_wait(&bars.acc_full[acc.stage], acc.turn & 1, abort);
+            if (!ok) break;
+            tmem_fence_after();
+            tmem_load32(from, u[0]);
+            tmem_wait_loads();
+            const int row = rank * kHigh + q * 32;  // first row in the tile
+            const bool partial = kProduct == kWeightGrad && !c.whole;
             char* out;
             int rows;
-            if (kProduct == kWeightGrad) {
-                const int64_t at = std::is_same<T, Out>::value ? c.expert : c.piece;
+            if (partial) {
+                out = reinterpret_cast<char*>(g.partial +
+                                              (c.slot * S::kTileHigh + row) * kWide);
+                rows = 32;
+            } else if (kProduct == kWeightGrad) {
                 out = static_cast<char*>(g.out) +
-                      ((at * g.high + c.m0 + q * 32) * g.width + c.n0) * sizeof(Out);
-                rows = g.high - c.m0 - q * 32;
+                      (((int64_t)c.expert * g.high + c.m0 + row) * g.width + c.n0) * sizeof(T);
+                rows = g.high - c.m0 - row;
             } else {
                 out = static_cast<char*>(g.out) +
-                      (((int64_t)c.row0 + q * 32) * g.width + c.n0) * sizeof(Out);
-                rows = c.row1 - c.row0 - q * 32;
+                      (((int64_t)c.row0 + row) * g.width + c.n0) * sizeof(T);
+                rows = c.row1 - c.row0 - row;
             }
 #pragma unroll
             for (int b = 0; b < kSpan / 32; ++b) {
                 const int n = first + b * 32;
                 // the next 32 columns come in while these go out
-                if (c.slices > 0 && b + 1 < kSpan / 32)
-                    tmem_load32(from + (b + 1) * 32, u[(b + 1) & 1]);
+                if (b + 1 < kSpan / 32) tmem_load32(from + (b + 1) * 32, u[(b + 1) & 1]);
                 const uint32_t* w = u[b & 1];
                 const int left = g.width - c.n0 - n;  // columns from here on
-                if (left > 0) {
-                    if constexpr (std::is_same<Out, float>::value) {
+                if (partial) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint4 v[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                v[i] = uint4{w[16 * h + 4 * i], w[16 * h + 4 * i + 1],
-                                             w[16 * h + 4 * i + 2], w[16 * h + 4 * i + 3]};
-                            write_block(mine, v, out + (n + 16 * h) * sizeof(Out),
-                                        (int64_t)g.width * sizeof(Out), rows,
-                                        (left - 16 * h + kVec - 1) / kVec);
-                        }
-                    } else {
+                    for (int h = 0; h < 2; ++h) {
                         uint4 v[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float f[8];
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = uint4{w[16 * h + 4 * i], w[16 * h + 4 * i + 1],
+                                         w[16 * h + 4 * i + 2], w[16 * h + 4 * i + 3]};
+                        write_block(mine, v, out + (n + 16 * h) * 4, kWide * 4, rows, 4);
+                    }
+                } else if (left > 0) {
+                    uint4 v[4];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[8 * i + j]);
-                            if (kProduct == kForward && g.bias && i * 8 < left)
-                                add_bias(f, static_cast<const T*>(g.bias) +
-                                                (int64_t)c.expert * g.width + c.n0 + n + i * 8);
-                            v[i] = uint4{pack2<Out>(f[0], f[1]), pack2<Out>(f[2], f[3]),
-                                         pack2<Out>(f[4], f[5]), pack2<Out>(f[6], f[7])};
-                        }
-                        write_block(mine, v, out + n * sizeof(Out),
-                                    (int64_t)g.width * sizeof(Out), rows,
-                                    (left + kVec - 1) / kVec);
+                    for (int i = 0; i < 4; ++i) {
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[8 * i + j]);
+                        if (kProduct == kForward && g.bias && i * 8 < left)
+                            add_bias(f, static_cast<const T*>(g.bias) +
+                                            (int64_t)c.expert * g.width + c.n0 + n + i * 8);
+                        v[i] = uint4{pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
+                                     pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])};
                     }
+                    write_block(mine, v, out + n * sizeof(T), (int64_t)g.width * sizeof(T), rows,
+                                (left + 7) / 8);
                 }
-                if (c.slices > 0) {
-                    tmem_wait_loads();
-                    if (b + 2 == kSpan / 32 || kSpan == 32) {
-                        // the accumulator is read: its next product may begin
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars.acc_empty[acc]);
-                    }
+                tmem_wait_loads();
+                if (b + 2 == kSpan / 32) {
+                    // the accumulator is read: its next product may begin
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_at(&bars.acc_empty[acc.stage], 0);
                 }
             }
         }
+        // rows of no expert, and the gradients of experts without rows, are 0
+        const int64_t at = (int64_t)blockIdx.x * (kOutWarps * 32) + threadIdx.x - 128;
+        const int64_t stride = (int64_t)gridDim.x * (kOutWarps * 32);
         if (kProduct != kWeightGrad) {
-            // rows of no expert are 0
-            const int64_t per = (int64_t)g.width * sizeof(Out) / 16;
-            const int64_t first = (int64_t)begin[g.experts] * per, last = g.rows * per;
-            for (int64_t i = first + (int64_t)blockIdx.x * (kOutWarps * 32) + threadIdx.x - 128;
-                 i < last; i += (int64_t)gridDim.x * (kOutWarps * 32))
-                reinterpret_cast<uint4*>(g.out)[i] = uint4{0, 0, 0, 0};
+            const int64_t per = (int64_t)g.width * sizeof(T) / 16;
+            for (int64_t i = begin[g.experts] * per + at; i < g.rows * per; i += stride)
+                static_cast<uint4*>(g.out)[i] = uint4{0, 0, 0, 0};
+        } else {
+            const int64_t per = (int64_t)g.high * g.width * sizeof(T) / 16;
+            for (int e = 0; e < g.experts; ++e) {
+                if (prefix[e] != prefix[e + 1]) continue;
+                for (int64_t i = at; i < per; i += stride)
+                    static_cast<uint4*>(g.out)[e * per + i] = uint4{0, 0, 0, 0};
+                if (g.bias_grad)
+                    for (int64_t i = at; i < g.high; i += stride)
+                        static_cast<T*>(g.bias_grad)[(int64_t)e * g.high + i] = from_f<T>(0.f);
+            }
         }
     }
     __syncthreads();
-    if (warp == 1) tmem_free(tmem, S::kColumns);
+    if (kBlocks == 2) cluster_sync();  // the other block's arrivals and products are over too
+    if (warp == 1) tmem_free<kBlocks>(tmem, S::kColumns);
     if (threadIdx.x == 0 && *abort) report(g.d_status, GS_ERR_TIMEOUT);
 }
 
-// grad_weight[e] = sum over the expert's pieces of their partial sums.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    k_sum_pieces(ProductArgs g, const float* __restrict__ partial, T* __restrict__ out) {
-    extern __shared__ int32_t pieces[];
-    int32_t* prefix = pieces + g.experts + 1;
+// The experts whose rows cross a cut between shares: grad_weight[e] (and
+// grad_bias[e]) = their partial sums in the order of the shares.
+template <typename T, int kBlocks, int kWide>
+__global__ void __launch_bounds__(256) k_sum_shares(const __grid_constant__ ProductArgs g) {
+    using S = Shape<kBlocks, kWide>;
+    constexpr int kSlab = S::kTileHigh / 8;
+    extern __shared__ int32_t begin[];
+    int32_t* prefix = begin + g.experts + 1;
     if (threadIdx.x < 32)
-        expert_pieces(g.offsets, g.experts, g.rows, g.chunk, pieces, prefix, nullptr);
+        expert_pieces(g.offsets, g.experts, g.rows, kSlice, begin, prefix, nullptr);
     __syncthreads();
-    const int e = blockIdx.y;
-    const int64_t size = (int64_t)g.high * g.width / 4;
-    const float4* p = reinterpret_cast<const float4*>(partial);
-    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
+    const int e = blockIdx.y, in = blockIdx.x, per = gridDim.x;
+    const int64_t total = prefix[g.experts];
+    if (prefix[e] == prefix[e + 1]) return;
+    const auto share_of = [&](int64_t pos) {
+        int s = (int)(pos * g.groups / total);
+        while (share_begin(total, g.groups, s) > pos) --s;
+        while (share_begin(total, g.groups, s + 1) <= pos) ++s;
+        return s;
+    };
+    const int s0 = share_of(prefix[e]), s1 = share_of((int64_t)prefix[e + 1] - 1);
+    if (s0 == s1) return;
+    const auto slot = [&](int s) { return ((int64_t)s * per + in) * 2 + (s == s0 ? 1 : 0); };
+    const int across = (g.width + kWide - 1) / kWide;
+    const int m0 = in / across * S::kTileHigh, n0 = in % across * kWide;
+    for (int i = threadIdx.x; i < kSlab * kWide / 4; i += 256) {
+        const int row = blockIdx.z * kSlab + i / (kWide / 4), col = i % (kWide / 4) * 4;
+        if (m0 + row >= g.high || n0 + col >= g.width) continue;
         float4 sum{0.f, 0.f, 0.f, 0.f};
-        for (int q = prefix[e]; q < prefix[e + 1]; ++q) {
-            const float4 v = p[q * size + i];
+        for (int s = s0; s <= s1; ++s) {
+            const float4 v = *reinterpret_cast<const float4*>(
+                g.partial + (slot(s) * S::kTileHigh + row) * kWide + col);
             sum.x += v.x;
             sum.y += v.y;
             sum.z += v.z;
             sum.w += v.w;
         }
-        reinterpret_cast<uint2*>(out)[e * size + i] =
+        *reinterpret_cast<uint2*>(static_cast<T*>(g.out) +
+                                  ((int64_t)e * g.high + m0 + row) * g.width + n0 + col) =
             uint2{pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w)};
+    }
+    if (!g.bias_grad || n0 != 0) return;
+    for (int i = threadIdx.x; i < kSlab; i += 256) {
+        const int row = blockIdx.z * kSlab + i;
+        if (m0 + row >= g.high) continue;
+        float sum = 0.f;
+        for (int s = s0; s <= s1; ++s) sum += g.bias_partial[slot(s) * S::kTileHigh + row];
+        static_cast<T*>(g.bias_grad)[(int64_t)e * g.high + m0 + row] = from_f<T>(sum);
     }
 }
 
@@ -457,52 +608,123 @@ int sm_count() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 1;
+        return 152;
     return n;
 }
 
-template <typename T, typename Out, int kProduct, int kWide>
-int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int64_t max_tiles,
+template <typename T, int kProduct, int kBlocks, int kWide>
+int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int64_t max_items,
            cudaStream_t s) {
-    const auto kernel = k_product<T, Out, kProduct, kWide>;
-    const size_t smem = smem_bytes<kWide>(g.experts);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-        return GS_ERR_CUDA;
-    const int64_t sms = sm_count();
-    kernel<<<(unsigned)(max_tiles < sms ? max_tiles : sms), kMmaThreads, smem, s>>>(a, b, g);
-    return GS_OK;
-}
-
-template <typename T, typename Out, int kProduct>
-int launch_wide(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int64_t pieces,
-                cudaStream_t s) {
-    const int64_t down = kProduct == kWeightGrad ? (g.high + kHigh - 1) / kHigh : 1;
-    const auto tiles = [&](int wide) { return pieces * down * ((g.width + wide - 1) / wide); };
-    return g.width > 128 ? launch<T, Out, kProduct, 256>(a, b, g, tiles(256), s)
-                         : launch<T, Out, kProduct, 128>(a, b, g, tiles(128), s);
+    const auto kernel = k_product<T, kProduct, kBlocks, kWide>;
+    const size_t smem = smem_bytes<kBlocks, kWide>(g.experts);
+    static const bool raised =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem_bytes<kBlocks, kWide>(GS_MAX_EXPERTS)) == cudaSuccess;
+    if (!raised) return GS_ERR_CUDA;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(kBlocks);
+    config.blockDim = dim3(kMmaThreads);
+    config.dynamicSmemBytes = smem;
+    config.stream = s;
+    cudaLaunchAttribute cluster = {};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = kBlocks;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    config.attrs = &cluster;
+    config.numAttrs = 1;
+    // as many pairs as are resident at once (an SM without a partner in its
+    // cluster's reach stays free)
+    static const int resident = [&] {
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, kernel, &config) == cudaSuccess && n > 0
+                   ? n
+                   : sm_count() / kBlocks;
+    }();
+    config.gridDim = dim3((unsigned)(std::min<int64_t>(max_items, resident) * kBlocks));
+    return cudaLaunchKernelEx(&config, kernel, a, b, g) == cudaSuccess ? GS_OK : GS_ERR_CUDA;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int64_t row_tiles(const LinearArgs& a) {
-    return (a.rows + kHigh - 1) / kHigh + a.experts;  // at most one part-filled tile an expert
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Two blocks a tile of 256 x 256 where the output is wide enough and the
+// experts have rows enough on average to fill 256 of them.
+bool use_pairs(const LinearArgs& a, int width) {
+    return width > 128 && a.rows >= (int64_t)256 * a.experts;
 }
 
-// Rows of one partial sum of the weight gradient, 0 for one sum per expert:
-// split when the experts' tiles alone would leave SMs idle.
-int weight_grad_chunk(const LinearArgs& a) {
-    const int64_t wide = a.in > 128 ? 256 : 128;
-    const int64_t tiles = (int64_t)a.experts * ((a.out + kHigh - 1) / kHigh) *
-                          ((a.in + wide - 1) / wide);
-    if (tiles >= 2 * 152 || a.rows < 2048) return 0;
-    const int64_t want = (3 * 152 + tiles - 1) / tiles * a.experts;  // pieces of all experts
-    const int64_t chunk = (a.rows / want + kSlice) / kSlice * kSlice;
-    return (int)(chunk < 512 ? 512 : chunk);
+// Columns of B in one box of a tiled copy.
+int box_b(bool pairs, int width) { return !pairs && width > 128 ? 256 : 128; }
+
+template <typename T, int kProduct>
+int launch_rows(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, bool pairs,
+                cudaStream_t s) {
+    // at most one part-filled tile an expert
+    const int64_t pieces = g.rows / (pairs ? 256 : 128) + g.experts;
+    if (pairs) return launch<T, kProduct, 2, 256>(a, b, g, pieces * ceil_div(g.width, 256), s);
+    if (g.width > 128)
+        return launch<T, kProduct, 1, 256>(a, b, g, pieces * ceil_div(g.width, 256), s);
+    return launch<T, kProduct, 1, 128>(a, b, g, pieces, s);
 }
 
-int64_t weight_grad_pieces(const LinearArgs& a, int chunk) {
-    return chunk ? a.rows / chunk + a.experts : a.experts;
+// How the weight gradient is cut up.
+struct GradPlan {
+    bool pairs;
+    int high, wide;    // of a tile
+    int64_t tiles;     // of a weight matrix
+    int groups;        // shares of the rows
+};
+
+GradPlan grad_plan(const LinearArgs& a) {
+    GradPlan p{};
+    p.pairs = a.out > 128 && a.in > 128;
+    p.high = p.pairs ? 256 : 128;
+    p.wide = a.in > 128 ? 256 : 128;
+    p.tiles = ceil_div(a.out, p.high) * ceil_div(a.in, p.wide);
+    const int64_t units = sm_count() / (p.pairs ? 2 : 1);
+    // shares that fill whole rounds of the units best, of at least 512 rows;
+    // each costs partial sums, weighed here as 1 % of a round
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(a.rows / 512, 64));
+    double best = 0.0;
+    p.groups = 1;
+    for (int64_t g = 1; g <= most; ++g) {
+        const double full = (double)(g * p.tiles) / (double)(units * ceil_div(g * p.tiles, units));
+        const double score = full - 0.01 * (double)ceil_div(g * p.tiles, units);
+        if (score > best) {
+            best = score;
+            p.groups = (int)g;
+        }
+    }
+    return p;
+}
+
+size_t partial_floats(const GradPlan& p) {
+    return p.groups > 1 ? (size_t)(2 * p.groups * p.tiles) * p.high * p.wide : 0;
+}
+
+size_t bias_floats(const GradPlan& p) {
+    return p.groups > 1 ? (size_t)(2 * p.groups * p.tiles) * p.high : 0;
+}
+
+template <typename T, int kBlocks, int kWide>
+int launch_weight_grad(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g,
+                       const GradPlan& p, cudaStream_t s) {
+    const int rc =
+        launch<T, kWeightGrad, kBlocks, kWide>(a, b, g, (int64_t)p.groups * p.tiles, s);
+    if (rc == GS_OK && p.groups > 1)
+        k_sum_shares<T, kBlocks, kWide>
+            <<<dim3((unsigned)p.tiles, g.experts, 8), 256,
+               2 * sizeof(int32_t) * (g.experts + 1), s>>>(g);
+    return rc;
+}
+
+template <typename T>
+int weight_grad_of(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g,
+                   const GradPlan& p, cudaStream_t s) {
+    if (p.pairs) return launch_weight_grad<T, 2, 256>(a, b, g, p, s);
+    if (p.wide == 256) return launch_weight_grad<T, 1, 256>(a, b, g, p, s);
+    return launch_weight_grad<T, 1, 128>(a, b, g, p, s);
 }
 
 }  // namespace
@@ -516,65 +738,70 @@ bool mma_usable(const LinearArgs& a, std::initializer_list<const void*> arrays) 
 
 int launch_mma_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
                    void* ys, cudaStream_t s) {
+    const bool pairs = use_pairs(a, a.out);
     CUtensorMap ma, mb;
     if (!make_map(&ma, a.dtype, xs, a.rows, a.in, 0, kHigh) ||
-        !make_map(&mb, a.dtype, weight, a.out, a.in, a.experts, a.out > 128 ? 256 : 128))
+        !make_map(&mb, a.dtype, weight, a.out, a.in, a.experts, box_b(pairs, a.out)))
         return GS_ERR_CUDA;
-    const ProductArgs g{a.offsets, a.rows, a.experts, 0, a.out, a.in, 0, bias, ys, a.d_status};
-    return a.dtype == GS_F16
-               ? launch_wide<__half, __half, kForward>(ma, mb, g, row_tiles(a), s)
-               : launch_wide<__nv_bfloat16, __nv_bfloat16, kForward>(ma, mb, g, row_tiles(a), s);
+    ProductArgs g{};
+    g.offsets = a.offsets;
+    g.rows = a.rows;
+    g.experts = a.experts;
+    g.width = a.out;
+    g.depth = a.in;
+    g.bias = bias;
+    g.out = ys;
+    g.d_status = a.d_status;
+    return a.dtype == GS_F16 ? launch_rows<__half, kForward>(ma, mb, g, pairs, s)
+                             : launch_rows<__nv_bfloat16, kForward>(ma, mb, g, pairs, s);
 }
 
 int launch_mma_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
                   cudaStream_t s) {
+    const bool pairs = use_pairs(a, a.in);
     CUtensorMap ma, mb;
     if (!make_map(&ma, a.dtype, grad_ys, a.rows, a.out, 0, kHigh) ||
         !make_map(&mb, a.dtype, weight, a.out, a.in, a.experts, kSlice))
         return GS_ERR_CUDA;
-    const ProductArgs g{a.offsets, a.rows, a.experts, 0, a.in, a.out, 0, nullptr, grad_xs,
-                        a.d_status};
-    return a.dtype == GS_F16
-               ? launch_wide<__half, __half, kInputGrad>(ma, mb, g, row_tiles(a), s)
-               : launch_wide<__nv_bfloat16, __nv_bfloat16, kInputGrad>(ma, mb, g, row_tiles(a),
-                                                                       s);
+    ProductArgs g{};
+    g.offsets = a.offsets;
+    g.rows = a.rows;
+    g.experts = a.experts;
+    g.width = a.in;
+    g.depth = a.out;
+    g.out = grad_xs;
+    g.d_status = a.d_status;
+    return a.dtype == GS_F16 ? launch_rows<__half, kInputGrad>(ma, mb, g, pairs, s)
+                             : launch_rows<__nv_bfloat16, kInputGrad>(ma, mb, g, pairs, s);
 }
 
 size_t mma_dw_workspace(const LinearArgs& a) {
-    const int chunk = weight_grad_chunk(a);
-    return chunk ? (size_t)weight_grad_pieces(a, chunk) * a.out * a.in * sizeof(float) : 0;
+    if (a.dtype == GS_F32 || a.in % 8 || a.out % 8) return 0;
+    const GradPlan p = grad_plan(a);
+    return (partial_floats(p) + bias_floats(p)) * sizeof(float);
 }
 
 int launch_mma_dw(const LinearArgs& a, const void* grad_ys, const void* xs, void* grad_weight,
-                  void* workspace, cudaStream_t s) {
+                  void* grad_bias, void* workspace, cudaStream_t s) {
     CUtensorMap ma, mb;
     if (!make_map(&ma, a.dtype, grad_ys, a.rows, a.out, 0, kSlice) ||
         !make_map(&mb, a.dtype, xs, a.rows, a.in, 0, kSlice))
         return GS_ERR_CUDA;
-    const int chunk = weight_grad_chunk(a);
-    const int64_t pieces = weight_grad_pieces(a, chunk);
-    const ProductArgs g{a.offsets, a.rows, a.experts, a.out, a.in, 0, chunk, nullptr,
-                        chunk ? workspace : grad_weight, a.d_status};
-    int rc = GS_OK;
-    const auto run = [&](auto t) {
-        using T = decltype(t);
-        if (!chunk) {
-            rc = launch_wide<T, T, kWeightGrad>(ma, mb, g, pieces, s);
-            return;
-        }
-        rc = launch_wide<T, float, kWeightGrad>(ma, mb, g, pieces, s);
-        if (rc != GS_OK) return;
-        const int64_t vectors = (int64_t)a.out * a.in / 4;
-        k_sum_pieces<T><<<dim3((unsigned)((vectors + 255) / 256 < 64 ? (vectors + 255) / 256 : 64),
-                               a.experts),
-                          256, 2 * sizeof(int32_t) * (a.experts + 1), s>>>(
-            g, static_cast<const float*>(workspace), static_cast<T*>(grad_weight));
-    };
-    if (a.dtype == GS_F16)
-        run(__half{});
-    else
-        run(__nv_bfloat16{});
-    return rc;
+    const GradPlan p = grad_plan(a);
+    ProductArgs g{};
+    g.offsets = a.offsets;
+    g.rows = a.rows;
+    g.experts = a.experts;
+    g.high = a.out;
+    g.width = a.in;
+    g.groups = p.groups;
+    g.out = grad_weight;
+    g.bias_grad = grad_bias;
+    g.partial = static_cast<float*>(workspace);
+    g.bias_partial = g.partial + partial_floats(p);
+    g.d_status = a.d_status;
+    return a.dtype == GS_F16 ? weight_grad_of<__half>(ma, mb, g, p, s)
+                             : weight_grad_of<__nv_bfloat16>(ma, mb, g, p, s);
 }
 
 }  // namespace gs

@@ -73,9 +73,10 @@ int launch_mma_fwd(const LinearArgs& a, const void* xs, const void* weight, cons
                    void* ys, cudaStream_t s);
 int launch_mma_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
                   cudaStream_t s);
-// Bytes of partial sums (0 when every expert's sum is taken in one piece).
+// Bytes of partial sums.
 size_t mma_dw_workspace(const LinearArgs& a);
+// grad_bias may be null.
 int launch_mma_dw(const LinearArgs& a, const void* grad_ys, const void* xs, void* grad_weight,
-                  void* workspace, cudaStream_t s);
+                  void* grad_bias, void* workspace, cudaStream_t s);
 
 }  // namespace gs

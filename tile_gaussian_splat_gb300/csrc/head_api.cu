@@ -233,16 +233,12 @@ int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* off
             launch_linear_dx(a, grad_ys, weight, grad_xs, s);
         }
     }
-    if (grad_weight) {
-        if (rows > 0 && mma_usable(a, {grad_ys, xs, grad_weight})) {
-            const int rc = launch_mma_dw(
-                a, grad_ys, xs, grad_weight,
-                static_cast<char*>(workspace) + align_up(linear_db_workspace(a)), s);
-            if (rc != GS_OK) return rc;
-        } else {
-            launch_linear_dw(a, grad_ys, xs, grad_weight, s);
-        }
+    if (grad_weight && rows > 0 && mma_usable(a, {grad_ys, xs, grad_weight, grad_bias})) {
+        return launch_mma_dw(
+            a, grad_ys, xs, grad_weight, grad_bias,
+            static_cast<char*>(workspace) + align_up(linear_db_workspace(a)), s);
     }
+    if (grad_weight) launch_linear_dw(a, grad_ys, xs, grad_weight, s);
     if (grad_bias) launch_linear_db(a, grad_ys, grad_bias, workspace, s);
     return check_launch();
 }
