@@ -24,8 +24,11 @@
 // matrix) walk it side by side, so the rows are read from memory once.  An
 // expert that lies within one share is written at once; one that crosses a
 // cut leaves partial sums, added up in the order of the shares afterwards.
-// Two helper warps take the bias gradient's column sums from the same stages,
-// and clear the rows of the next expert in an expert's last slice.
+// Four helper warps take the bias gradient's column sums from the same stages,
+// each of a weight matrix' column tiles those of its part of the slices: the
+// copies and the products alone keep shared memory busy, and one tile in two
+// taking all of the sums cost 38 us on 95.  One of them also clears the rows
+// of the next expert in an expert's last slice.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -47,7 +50,10 @@ enum Product { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 constexpr int kHigh = 128;        // rows of an output tile
 constexpr int kSlice = 64;        // terms of the sum per stage: 128 bytes
 constexpr int kOutWarps = 8;      // two for each quarter of the tile's rows
-constexpr int kMmaThreads = 32 * (4 + kOutWarps);  // warps: copy, products, 2 idle, output
+// Warps: 0 copies, 1 issues products, 2 and 3 (and two after the output warps)
+// help with the weight gradient, from 4 on they write the output.
+template <int kProduct>
+constexpr int kMmaThreads = 32 * (4 + kOutWarps + (kProduct == kWeightGrad ? 2 : 0));
 constexpr int kAccumulators = 2;
 
 struct ProductArgs {
@@ -60,7 +66,7 @@ struct ProductArgs {
     void* out;
     void* bias_grad;         // kWeightGrad, or null
     float* partial;          // kWeightGrad: two tiles an item (see Walk)
-    float* bias_partial;     // two tile heights an item
+    float* bias_partial;     // two tile heights an item, then one per expert and tile
     int32_t* d_status;
 };
 
@@ -74,6 +80,8 @@ struct Shape {
     static constexpr int kStageBytes = kBytesA + kBytesB;
     static constexpr int kStages = kStageBytes > 32768 ? 4 : 6;
     static constexpr int kStaging = kOutWarps * 32 * 64;
+    static constexpr int kSpan = kWide / (kOutWarps / 4);  // columns an output warp writes
+    static constexpr int kBias = kOutWarps * kSpan * 4;     // their biases as float32
     static constexpr int kColumns = kAccumulators * kWide;
 };
 
@@ -91,7 +99,8 @@ struct Bars {
 template <int kBlocks, int kWide>
 constexpr size_t smem_bytes(int experts) {
     using S = Shape<kBlocks, kWide>;
-    return 1024 + (size_t)S::kStages * S::kStageBytes + S::kStaging + sizeof(Bars) +
+    return 1024 + (size_t)S::kStages * S::kStageBytes + S::kStaging + S::kBias +
+           sizeof(Bars) +
            2 * sizeof(int32_t) * (size_t)(experts + 1);
 }
 
@@ -113,6 +122,7 @@ struct Tile {
     int row0, row1;  // rows of the output (of the sum, for kWeightGrad)
     int m0, n0;      // first row (kWeightGrad only) and column of the tile
     int slices;      // 64-term slices of the sum
+    int tile;        // kWeightGrad: which tile of the weight matrix
     bool whole;      // kWeightGrad: all of the expert's rows
     int64_t slot;    // kWeightGrad: where a partial sum goes
 };
@@ -154,7 +164,7 @@ struct Walk {
                 pos = share_begin(total, g.groups, (int)(mine / per));
                 end = share_begin(total, g.groups, (int)(mine / per) + 1);
             }
-            const int in = (int)(mine % per);
+            const int in = c.tile = (int)(mine % per);
             c.m0 = in / across * S::kTileHigh;
             c.n0 = in % across * kWide;
             c.expert = expert_of(prefix, g.experts, (int)pos);
@@ -175,6 +185,7 @@ struct Walk {
             c.row0 = begin[c.expert] + (piece - prefix[c.expert]) * S::kTileHigh;
             c.row1 = min(begin[c.expert + 1], c.row0 + S::kTileHigh);
             c.slices = (g.depth + kSlice - 1) / kSlice;
+            c.tile = 0;
             c.whole = true;
             c.slot = 0;
             item += step;
@@ -219,17 +230,8 @@ __device__ __forceinline__ void write_block(char* staging, const uint4* v, char*
     __syncwarp();
 }
 
-// Adds the bias of columns [n, n + 8) to eight sums.
-template <typename T>
-__device__ __forceinline__ void add_bias(float* v, const T* bias) {
-    const uint4 b = *reinterpret_cast<const uint4*>(bias);
-    const T* p = reinterpret_cast<const T*>(&b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += to_f(p[i]);
-}
-
 template <typename T, int kProduct, int kBlocks, int kWide>
-__global__ void __launch_bounds__(kMmaThreads, 1)
+__global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const __grid_constant__ ProductArgs g) {
     using S = Shape<kBlocks, kWide>;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     char* staging = smem + S::kStages * S::kStageBytes;
-    Bars& bars = *reinterpret_cast<Bars*>(staging + S::kStaging);
+    Bars& bars = *reinterpret_cast<Bars*>(staging + S::kStaging + S::kBias);
     int32_t* begin = reinterpret_cast<int32_t*>(&bars + 1);
     int32_t* prefix = begin + g.experts + 1;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.landed[i], 1);
-            mbar_init(&bars.empty[i], kProduct == kWeightGrad ? (columns ? 3 : 2) : 1);
+            mbar_init(&bars.empty[i], kProduct == kWeightGrad ? (columns ? 5 : 2) : 1);
         }
         for (int i = 0; i < kAccumulators; ++i) {
             mbar_init(&bars.acc_full[i], 1);
@@ -369,11 +371,16 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             int none = 0;
             mbar_wait_limited(&bars.drain, 0, &none);
         }
-    } else if (kProduct == kWeightGrad && (warp == 2 || (warp == 3 && columns))) {
+    } else if (kProduct == kWeightGrad && (warp == 2 || (columns && (warp == 3 || warp > 11)))) {
+        const int helper = warp < 4 ? warp - 2 : warp - 10;  // 32 columns each
+        // of eight rows, lanes that read together take rows four apart: their
+        // halves of the swizzled 128 bytes differ
+        const int row8 = (lane >> 3) | (lane >> 2 & 1) << 2, unit = (helper & 1) * 4 + (lane & 3);
         Ring<S::kStages> at;
         bool ok = true;
         while (ok && walk.next(c)) {
-            float low = 0.f, top = 0.f;  // sums of this lane's two columns of A
+            // sums of eight columns of A over every eighth row
+            float sum[8] = {};
             for (int k = 0; k < c.slices; ++k, at.advance()) {
                 ok = warp_wait(&bars.landed[at.stage], at.turn & 1, abort);
                 if (!ok) break;
@@ -390,34 +397,43 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_release_at(&bars.cleared, 0);
                 }
-                if (columns && c.n0 == 0) {
-                    const char* p = a + (warp - 2) * 64 * 128 + (lane & 3) * 4;
-#pragma unroll 8
-                    for (int r = 0; r < valid; ++r) {
-                        const uint32_t v = *reinterpret_cast<const uint32_t*>(
-                            p + r * 128 + ((lane / 4 ^ (r & 7)) << 4));
-                        const T* e = reinterpret_cast<const T*>(&v);
-                        low += to_f(e[0]);
-                        top += to_f(e[1]);
+                if (columns && (c.row0 / kSlice + k) % walk.across == c.n0 / kWide) {
+                    const char* p = a + helper / 2 * 64 * 128;
+#pragma unroll
+                    for (int r = row8; r < kSlice; r += 8) {
+                        if (r >= valid) break;
+                        float v[8];
+                        unpack<T, 8>(*reinterpret_cast<const uint4*>(
+                                         p + r * 128 + ((unit ^ (r & 7)) << 4)),
+                                     v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sum[i] += v[i];
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_at(&bars.empty[at.stage], rank);
             }
-            if (ok && columns && c.n0 == 0) {
-                const int in = rank * kHigh + (warp - 2) * 64 + lane * 2, m = c.m0 + in;
-                if (!c.whole)
-                    *reinterpret_cast<float2*>(g.bias_partial + c.slot * S::kTileHigh + in) =
-                        float2{low, top};
-                else if (m < g.high)
-                    *reinterpret_cast<uint32_t*>(static_cast<T*>(g.bias_grad) +
-                                                 (int64_t)c.expert * g.high + m) =
-                        pack2<T>(low, top);
+            if (ok && columns) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 4);
+                    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
+                    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
+                }
+                const int in = rank * kHigh + helper * 32 + lane * 8;
+                const int64_t slot =
+                    c.whole ? 2 * walk.items + (int64_t)c.expert * walk.per + c.tile : c.slot;
+                float4* p = reinterpret_cast<float4*>(g.bias_partial + slot * S::kTileHigh + in);
+                if (lane < 4) {
+                    p[0] = float4{sum[0], sum[1], sum[2], sum[3]};
+                    p[1] = float4{sum[4], sum[5], sum[6], sum[7]};
+                }
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 4 + kOutWarps) {
         const int q = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
-        constexpr int kSpan = kWide / (kOutWarps / 4);  // columns of this warp
+        constexpr int kSpan = S::kSpan;
+        float* bias = reinterpret_cast<float*>(staging + S::kStaging) + (warp - 4) * kSpan;
         const int first = (warp - 4) / 4 * kSpan;
         char* mine = staging + (warp - 4) * 32 * 64;
         Ring<kAccumulators> acc;
@@ -426,6 +442,17 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const uint32_t from =
                 tmem + ((uint32_t)(q * 32) << 16) + acc.stage * kWide + first;
             uint32_t u[2][32];
+            if (kProduct == kForward && g.bias) {
+                const T* p = static_cast<const T*>(g.bias) + (int64_t)c.expert * g.width;
+#pragma unroll
+                for (int i = lane * 4; i < kSpan; i += 128) {
+                    const int n = c.n0 + first + i;
+                    float v[4] = {};
+                    if (n < g.width) unpack<T, 4>(load_raw<T, 4>(p + n), v);
+                    *reinterpret_cast<float4*>(bias + i) = float4{v[0], v[1], v[2], v[3]};
+                }
+                __syncwarp();
+            }
             ok = warp_wait(&bars.acc_full[acc.stage], acc.turn & 1, abort);
             if (!ok) break;
             tmem_fence_after();
@@ -472,9 +499,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         float f[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[8 * i + j]);
-                        if (kProduct == kForward && g.bias && i * 8 < left)
-                            add_bias(f, static_cast<const T*>(g.bias) +
-                                            (int64_t)c.expert * g.width + c.n0 + n + i * 8);
+                        if (kProduct == kForward && g.bias) {
+                            const float4* p = reinterpret_cast<const float4*>(bias + b * 32) + 2 * i;
+                            const float4 lo = p[0], hi = p[1];
+                            f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
+                            f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+                        }
                         v[i] = uint4{pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
                                      pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])};
                     }
@@ -503,9 +533,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (prefix[e] != prefix[e + 1]) continue;
                 for (int64_t i = at; i < per; i += stride)
                     static_cast<uint4*>(g.out)[e * per + i] = uint4{0, 0, 0, 0};
-                if (g.bias_grad)
-                    for (int64_t i = at; i < g.high; i += stride)
-                        static_cast<T*>(g.bias_grad)[(int64_t)e * g.high + i] = from_f<T>(0.f);
             }
         }
     }
@@ -515,55 +542,86 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (threadIdx.x == 0 && *abort) report(g.d_status, GS_ERR_TIMEOUT);
 }
 
-// The experts whose rows cross a cut between shares: grad_weight[e] (and
-// grad_bias[e]) = their partial sums in the order of the shares.
+constexpr int kSlabs = 16;  // blocks that add up a tile of partial sums
+
+// What was left in parts.  For every cut between shares, kSlabs blocks per
+// tile: the expert that it (and no cut before it) cuts, grad_weight[e] = its
+// partial sums in the order of the shares.  Then for every expert ceil(high /
+// 256) blocks: grad_bias[e] = the sums of its column tiles and shares.
 template <typename T, int kBlocks, int kWide>
-__global__ void __launch_bounds__(256) k_sum_shares(const __grid_constant__ ProductArgs g) {
+__global__ void __launch_bounds__(256)
+    k_sum_parts(const __grid_constant__ ProductArgs g, int tiles) {
     using S = Shape<kBlocks, kWide>;
-    constexpr int kSlab = S::kTileHigh / 8;
+    constexpr int kSlab = S::kTileHigh / kSlabs;
     extern __shared__ int32_t begin[];
     int32_t* prefix = begin + g.experts + 1;
     if (threadIdx.x < 32)
         expert_pieces(g.offsets, g.experts, g.rows, kSlice, begin, prefix, nullptr);
     __syncthreads();
-    const int e = blockIdx.y, in = blockIdx.x, per = gridDim.x;
     const int64_t total = prefix[g.experts];
-    if (prefix[e] == prefix[e + 1]) return;
+    const int across = (g.width + kWide - 1) / kWide;
     const auto share_of = [&](int64_t pos) {
         int s = (int)(pos * g.groups / total);
         while (share_begin(total, g.groups, s) > pos) --s;
         while (share_begin(total, g.groups, s + 1) <= pos) ++s;
         return s;
     };
-    const int s0 = share_of(prefix[e]), s1 = share_of((int64_t)prefix[e + 1] - 1);
-    if (s0 == s1) return;
-    const auto slot = [&](int s) { return ((int64_t)s * per + in) * 2 + (s == s0 ? 1 : 0); };
-    const int across = (g.width + kWide - 1) / kWide;
-    const int m0 = in / across * S::kTileHigh, n0 = in % across * kWide;
-    for (int i = threadIdx.x; i < kSlab * kWide / 4; i += 256) {
-        const int row = blockIdx.z * kSlab + i / (kWide / 4), col = i % (kWide / 4) * 4;
-        if (m0 + row >= g.high || n0 + col >= g.width) continue;
-        float4 sum{0.f, 0.f, 0.f, 0.f};
-        for (int s = s0; s <= s1; ++s) {
-            const float4 v = *reinterpret_cast<const float4*>(
-                g.partial + (slot(s) * S::kTileHigh + row) * kWide + col);
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
+    // an expert's part in share s, of the shares s0 .. that it lies in
+    const auto slot = [&](int s, int s0, int tile) {
+        return ((int64_t)s * tiles + tile) * 2 + (s == s0 ? 1 : 0);
+    };
+    int block = blockIdx.x;
+    const int cut_blocks = (g.groups - 1) * tiles * kSlabs;
+    if (block < cut_blocks) {
+        const int cut = block / (tiles * kSlabs) + 1, tile = block / kSlabs % tiles;
+        const int64_t pos = share_begin(total, g.groups, cut);
+        if (total == 0 || pos >= total) return;
+        const int e = expert_of(prefix, g.experts, (int)pos);
+        if (prefix[e] == pos) return;  // between two experts
+        const int s0 = share_of(prefix[e]);
+        if (cut != s0 + 1) return;  // an earlier cut's blocks do this expert
+        const int s1 = share_of((int64_t)prefix[e + 1] - 1);
+        const int m0 = tile / across * S::kTileHigh + block % kSlabs * kSlab;
+        const int n0 = tile % across * kWide;
+        for (int i = threadIdx.x; i < kSlab * kWide / 4; i += 256) {
+            const int row = i / (kWide / 4), col = i % (kWide / 4) * 4;
+            if (m0 + row >= g.high || n0 + col >= g.width) continue;
+            float4 sum{0.f, 0.f, 0.f, 0.f};
+            for (int s = s0; s <= s1; ++s) {
+                if (share_begin(total, g.groups, s) == share_begin(total, g.groups, s + 1))
+                    continue;
+                const float4 v = *reinterpret_cast<const float4*>(
+                    g.partial + (slot(s, s0, tile) * S::kTileHigh + block % kSlabs * kSlab + row) *
+                                    kWide + col);
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+            *reinterpret_cast<uint2*>(static_cast<T*>(g.out) +
+                                      ((int64_t)e * g.high + m0 + row) * g.width + n0 + col) =
+                uint2{pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w)};
         }
-        *reinterpret_cast<uint2*>(static_cast<T*>(g.out) +
-                                  ((int64_t)e * g.high + m0 + row) * g.width + n0 + col) =
-            uint2{pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w)};
+        return;
     }
-    if (!g.bias_grad || n0 != 0) return;
-    for (int i = threadIdx.x; i < kSlab; i += 256) {
-        const int row = blockIdx.z * kSlab + i;
-        if (m0 + row >= g.high) continue;
-        float sum = 0.f;
-        for (int s = s0; s <= s1; ++s) sum += g.bias_partial[slot(s) * S::kTileHigh + row];
-        static_cast<T*>(g.bias_grad)[(int64_t)e * g.high + m0 + row] = from_f<T>(sum);
+    block -= cut_blocks;
+    const int per = (g.high + 255) / 256, e = block / per;
+    const int m = block % per * 256 + threadIdx.x;
+    if (m >= g.high) return;
+    float sum = 0.f;
+    if (prefix[e] < prefix[e + 1]) {
+        const int s0 = share_of(prefix[e]), s1 = share_of((int64_t)prefix[e + 1] - 1);
+        const int row = m % S::kTileHigh, tile0 = m / S::kTileHigh * across;
+        for (int s = s0; s <= s1; ++s) {
+            if (share_begin(total, g.groups, s) == share_begin(total, g.groups, s + 1)) continue;
+            for (int n = tile0; n < tile0 + across; ++n) {
+                const int64_t at = s0 == s1 ? 2 * (int64_t)g.groups * tiles + e * tiles + n
+                                            : slot(s, s0, n);
+                sum += g.bias_partial[at * S::kTileHigh + row];
+            }
+        }
     }
+    static_cast<T*>(g.bias_grad)[(int64_t)e * g.high + m] = from_f<T>(sum);
 }
 
 // cuTensorMapEncodeTiled, found through the runtime (the library does not
@@ -623,7 +681,7 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int
     if (!raised) return GS_ERR_CUDA;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(kBlocks);
-    config.blockDim = dim3(kMmaThreads);
+    config.blockDim = dim3(kMmaThreads<kProduct>);
     config.dynamicSmemBytes = smem;
     config.stream = s;
     cudaLaunchAttribute cluster = {};
@@ -683,16 +741,21 @@ GradPlan grad_plan(const LinearArgs& a) {
     p.wide = a.in > 128 ? 256 : 128;
     p.tiles = ceil_div(a.out, p.high) * ceil_div(a.in, p.wide);
     const int64_t units = sm_count() / (p.pairs ? 2 : 1);
-    // shares that fill whole rounds of the units best, of at least 512 rows;
-    // each costs partial sums, weighed here as 1 % of a round
+    // Shares: more of them fill the last round of the units better, but each
+    // leaves partial sums (two tiles an item, written and read).  The least
+    // time at 1.6 PFLOP/s on all units and 5 TB/s; 16 experts of 8192 rows,
+    // 1024 x 512: 9 shares 102 us of products and 12 us of sums, 19 shares
+    // 169 and 24.
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(a.rows / 512, 64));
+    const double work = 2.0 * a.rows * p.tiles * p.high * p.wide / 1.6e15;
     double best = 0.0;
-    p.groups = 1;
     for (int64_t g = 1; g <= most; ++g) {
-        const double full = (double)(g * p.tiles) / (double)(units * ceil_div(g * p.tiles, units));
-        const double score = full - 0.01 * (double)ceil_div(g * p.tiles, units);
-        if (score > best) {
-            best = score;
+        const int64_t items = g * p.tiles;
+        const double used = (double)items / (double)(units * ceil_div(items, units));
+        const double sums = g > 1 ? 16.0 * items * p.high * p.wide / 5e12 : 0.0;
+        const double time = work / used + sums;
+        if (g == 1 || time < best) {
+            best = time;
             p.groups = (int)g;
         }
     }
@@ -703,8 +766,8 @@ size_t partial_floats(const GradPlan& p) {
     return p.groups > 1 ? (size_t)(2 * p.groups * p.tiles) * p.high * p.wide : 0;
 }
 
-size_t bias_floats(const GradPlan& p) {
-    return p.groups > 1 ? (size_t)(2 * p.groups * p.tiles) * p.high : 0;
+size_t bias_floats(const GradPlan& p, int experts) {
+    return (size_t)((2 * p.groups + experts) * p.tiles) * p.high;
 }
 
 template <typename T, int kBlocks, int kWide>
@@ -712,10 +775,12 @@ int launch_weight_grad(const CUtensorMap& a, const CUtensorMap& b, const Product
                        const GradPlan& p, cudaStream_t s) {
     const int rc =
         launch<T, kWeightGrad, kBlocks, kWide>(a, b, g, (int64_t)p.groups * p.tiles, s);
-    if (rc == GS_OK && p.groups > 1)
-        k_sum_shares<T, kBlocks, kWide>
-            <<<dim3((unsigned)p.tiles, g.experts, 8), 256,
-               2 * sizeof(int32_t) * (g.experts + 1), s>>>(g);
+    const int64_t blocks = (int64_t)(p.groups - 1) * p.tiles * kSlabs +
+                           (g.bias_grad ? g.experts * ceil_div(g.high, 256) : 0);
+    if (rc == GS_OK && blocks > 0)
+        k_sum_parts<T, kBlocks, kWide>
+            <<<(unsigned)blocks, 256, 2 * sizeof(int32_t) * (g.experts + 1), s>>>(g,
+                                                                                 (int)p.tiles);
     return rc;
 }
 
@@ -778,7 +843,7 @@ int launch_mma_dx(const LinearArgs& a, const void* grad_ys, const void* weight, 
 size_t mma_dw_workspace(const LinearArgs& a) {
     if (a.dtype == GS_F32 || a.in % 8 || a.out % 8) return 0;
     const GradPlan p = grad_plan(a);
-    return (partial_floats(p) + bias_floats(p)) * sizeof(float);
+    return (partial_floats(p) + bias_floats(p, a.experts)) * sizeof(float);
 }
 
 int launch_mma_dw(const LinearArgs& a, const void* grad_ys, const void* xs, void* grad_weight,
