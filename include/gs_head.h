@@ -127,31 +127,40 @@ int gs_expert_combine_bwd(const void* grad_y, int64_t ldgy, const void* ys,
                           int64_t tokens, int topk, int experts, int channels, int dtype,
                           void* grad_ys, float* grad_weights, int32_t* d_status, void* stream);
 
+/* Bytes of workspace gs_expert_linear_fwd and _bwd need.  aligned != 0: every
+ * array begins on a 16-byte boundary.  float32 operands, and rows that are not
+ * whole 16-byte vectors, are laid out there for the tensor cores; the backward
+ * keeps partial sums there. */
+size_t gs_expert_linear_fwd_workspace_size(int64_t rows, int experts, int in_features,
+                                           int out_features, int dtype, int aligned);
+size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_features,
+                                           int out_features, int dtype, int aligned);
+
 /*
  * gs_expert_linear_fwd -- for the rows r of expert e (offsets as
  * gs_expert_sort wrote them):
  *   ys[r] = weight[e] xs[r] + bias[e];  rows of no expert are 0.
  * xs (rows, in_features), weight (experts, out_features, in_features), bias
  * (experts, out_features) or NULL, ys (rows, out_features), all of dtype.
- * Limits: 0 <= rows < 2^31, 1 <= in_features, out_features <= 65536.
+ * workspace (16-byte aligned): as the size call says, or NULL where that is 0.
+ * float32 products keep 24 bits (error as of float32 sums); an infinity in
+ * them makes the results it enters infinite or NaN.
+ * Limits: 0 <= rows < 2^31 (a third of it for float32), 1 <= in_features,
+ * out_features <= 65536.
  */
 int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* weight,
                          const void* bias, int64_t rows, int experts, int in_features,
-                         int out_features, int dtype, void* ys, int32_t* d_status,
-                         void* stream);
-
-/* Bytes of workspace (16-byte aligned) gs_expert_linear_bwd needs for
- * grad_weight and grad_bias. */
-size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_features,
-                                           int out_features, int dtype);
+                         int out_features, int dtype, void* ys, void* workspace,
+                         size_t workspace_bytes, int32_t* d_status, void* stream);
 
 /*
  * gs_expert_linear_bwd -- gradients of gs_expert_linear_fwd:
  *   grad_xs[r] = weight[e]^T grad_ys[r]   (rows of no expert 0)
  *   grad_weight[e] = sum over the expert's rows of grad_ys[r] xs[r]^T
  *   grad_bias[e] = sum over the expert's rows of grad_ys[r]
- * (0 for an expert without rows).  Each output may be NULL; weight is read
- * for grad_xs, xs for grad_weight.
+ * (0 for an expert without rows).  grad_xs may be NULL (weight is then not
+ * read), grad_bias may be NULL, and grad_weight where grad_bias is (xs is then
+ * not read).
  */
 int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* offsets,
                          const void* weight, int64_t rows, int experts, int in_features,

@@ -87,7 +87,7 @@ def test_rows(lib):
 def test_expert_linear(lib):
     def fwd(xs=16, off=8, w=16, b=16, rows=4, experts=2, i=8, o=8, dt=BF16, ys=16):
         return lib.gs_expert_linear_fwd(P(xs), P(off), P(w), P(b), rows, experts, i, o, dt, P(ys),
-                                        None, None)
+                                        None, 0, None, None)
 
     for bad in (dict(xs=0), dict(off=0), dict(off=6), dict(w=0), dict(b=1), dict(rows=-1),
                 dict(rows=1 << 31), dict(experts=0), dict(experts=1025), dict(i=0), dict(o=0),
@@ -99,7 +99,14 @@ def test_expert_linear(lib):
         return lib.gs_expert_linear_bwd(P(gys), P(xs), P(off), P(w), rows, 2, 8, 8, BF16, P(gx),
                                         P(gw), P(gb), P(ws), n, None, None)
 
-    for bad in (dict(gys=0), dict(xs=0), dict(off=0), dict(w=0), dict(gx=1), dict(gw=1),
+    for bad in (dict(gys=0), dict(xs=0), dict(off=0), dict(w=0), dict(gx=1), dict(gw=1), dict(gw=0),
                 dict(gb=1), dict(rows=-1)):
         assert bwd(**bad) == 1, bad
     assert bwd(ws=0) == 4 and bwd(ws=8) == 4 and bwd(n=16) == 4  # missing, misaligned, small
+    # float32 and rows of odd length are laid out in the workspace
+    size = lib.gs_expert_linear_fwd_workspace_size
+    assert size(100, 2, 64, 32, BF16, 1) == 0 and size(100, 2, 64, 32, BF16, 0) > 0
+    assert size(100, 2, 63, 32, F16, 1) > 0 and size(100, 2, 64, 32, F32, 1) > 0
+    assert size(100, 0, 64, 32, F32, 1) == 0
+    assert fwd(dt=F32) == 4 and fwd(i=7) == 4 and fwd(xs=18) == 4
+    assert fwd(dt=F32, rows=(1 << 31) // 3 + 1) == 1

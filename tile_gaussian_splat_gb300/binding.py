@@ -65,8 +65,9 @@ SIGNATURES = {
     "gs_expert_dispatch": (I32, [P, I64, P, P, I64, I32, I32, I32, I32, P, P, P]),
     "gs_expert_combine": (I32, [P, P, P, I64, I32, I32, I32, P, I64, P, P]),
     "gs_expert_combine_bwd": (I32, [P, I64, P, P, P, P, I64, I32, I32, I32, I32, P, P, P, P]),
-    "gs_expert_linear_fwd": (I32, [P, P, P, P, I64, I32, I32, I32, I32, P, P, P]),
-    "gs_expert_linear_bwd_workspace_size": (SZ, [I64, I32, I32, I32, I32]),
+    "gs_expert_linear_fwd_workspace_size": (SZ, [I64, I32, I32, I32, I32, I32]),
+    "gs_expert_linear_fwd": (I32, [P, P, P, P, I64, I32, I32, I32, I32, P, P, SZ, P, P]),
+    "gs_expert_linear_bwd_workspace_size": (SZ, [I64, I32, I32, I32, I32, I32]),
     "gs_expert_linear_bwd": (I32, [P, P, P, P, I64, I32, I32, I32, I32, P, P, P, P, SZ, P, P]),
 }
 
@@ -719,7 +720,13 @@ def _linear_shapes(xs, offsets, weight):
     return E, i, o
 
 
-def gs_expert_linear_fwd(xs, offsets, weight, bias=None, d_status=None, out=None, stream=None):
+def _aligned(*tensors):
+    """Whether every one of the tensors begins on a 16-byte boundary."""
+    return int(all(t.data_ptr() % 16 == 0 for t in tensors))
+
+
+def gs_expert_linear_fwd(xs, offsets, weight, bias=None, d_status=None, out=None, workspace=None,
+                         stream=None):
     """Every expert's product over its sorted rows: xs (rows, in_features),
     weight (experts, out_features, in_features), bias (experts, out_features)
     or None.  Returns ys (rows, out_features), zero rows behind the last
@@ -731,9 +738,12 @@ def gs_expert_linear_fwd(xs, offsets, weight, bias=None, d_status=None, out=None
         _same(bias, (E, o), xs.dtype, "bias")
     ys = _new((R, o), xs.dtype, xs, stream) if out is None else \
         _same(out, (R, o), xs.dtype, "out")
-    _check(lib().gs_expert_linear_fwd(_ptr(xs), _ptr(offsets), _ptr(weight), _ptr(bias), R, E, i,
-                                      o, dt, _ptr(ys), _ptr(d_status), _on(stream, xs)),
-           "gs_expert_linear_fwd")
+    L = lib()
+    n_bytes = L.gs_expert_linear_fwd_workspace_size(R, E, i, o, dt, _aligned(xs, weight))
+    ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
+    _check(L.gs_expert_linear_fwd(_ptr(xs), _ptr(offsets), _ptr(weight), _ptr(bias), R, E, i, o,
+                                  dt, _ptr(ys), _ptr(ws), n_bytes, _ptr(d_status),
+                                  _on(stream, xs)), "gs_expert_linear_fwd")
     return ys
 
 
@@ -749,7 +759,8 @@ def gs_expert_linear_bwd(grad_ys, xs, offsets, weight, bias=True, input=True, d_
     gw = _new((E, o, i), xs.dtype, xs, stream)
     gb = _new((E, o), xs.dtype, xs, stream) if bias else None
     L = lib()
-    n_bytes = L.gs_expert_linear_bwd_workspace_size(R, E, i, o, dt)
+    n_bytes = L.gs_expert_linear_bwd_workspace_size(R, E, i, o, dt,
+                                                    _aligned(grad_ys, xs, weight))
     ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
     _check(L.gs_expert_linear_bwd(_ptr(grad_ys), _ptr(xs), _ptr(offsets), _ptr(weight), R, E, i,
                                   o, dt, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), n_bytes,

@@ -1,5 +1,4 @@
-// The experts' products on the tensor cores (float16 and bfloat16, widths in
-// whole 16-byte vectors).
+// The experts' products on the tensor cores.
 //
 // Three products share one kernel, out[m, n] = sum_k A[m, k] B[n, k]:
 //   kForward     A = xs (rows x in),   B = weight[e] (out x in)     sum over in
@@ -7,6 +6,12 @@
 //   kWeightGrad  A = grad_ys^T (out x rows), B = xs^T (in x rows)   over rows
 // The operand whose sum index is not contiguous in memory is handed to the
 // matrix instruction as it lies (MN-major), so nothing is transposed.
+//
+// float32 operands are first written as three bfloat16 planes, a = a0 + a1 +
+// a2 with eight bits of the fraction each (exact), and a product is six sums,
+// a2 b0 + a0 b2 + a1 b1 + a1 b0 + a0 b1 + a0 b0 in one accumulator; the terms
+// left out are below 2^-22 of |a b|.  Half-type operands whose rows are not
+// whole 16-byte vectors are copied to rows that are (one plane).
 //
 // Two neighbouring blocks work as one on output tiles of 256 x 256 (each
 // block holds half of the rows of A and of B, so every byte copied into shared
@@ -62,6 +67,8 @@ struct ProductArgs {
     int experts;
     int high, width, depth;  // extents: high of the weight gradient, depth of the others
     int groups;              // weight gradient: shares of the rows
+    int pairs;               // sums over plane pairs: 1, or 6 for float32
+    int vectors;             // output rows are whole 16-byte vectors
     const void* bias;        // kForward
     void* out;
     void* bias_grad;         // kWeightGrad, or null
@@ -104,6 +111,14 @@ constexpr size_t smem_bytes(int experts) {
            2 * sizeof(int32_t) * (size_t)(experts + 1);
 }
 
+// Planes of A and B in sum number `sum` of g.pairs, small terms first.
+__device__ __forceinline__ int plane_a(int pairs, int sum) {
+    return 0x001102 >> 4 * (6 - pairs + sum) & 15;  // 2, 0, 1, 1, 0, 0
+}
+__device__ __forceinline__ int plane_b(int pairs, int sum) {
+    return 0x010120 >> 4 * (6 - pairs + sum) & 15;  // 0, 2, 1, 0, 1, 0
+}
+
 // A place in a ring of kCount stages, and how often it has gone round.
 template <int kCount>
 struct Ring {
@@ -121,7 +136,8 @@ struct Tile {
     int expert;
     int row0, row1;  // rows of the output (of the sum, for kWeightGrad)
     int m0, n0;      // first row (kWeightGrad only) and column of the tile
-    int slices;      // 64-term slices of the sum
+    int count;       // 64-term slices of the sum
+    int slices;      // of all the sums over plane pairs
     int tile;        // kWeightGrad: which tile of the weight matrix
     bool whole;      // kWeightGrad: all of the expert's rows
     int64_t slot;    // kWeightGrad: where a partial sum goes
@@ -172,10 +188,11 @@ struct Walk {
             const int k0 = (int)pos - first, k1 = (int)min(end - first, (int64_t)count);
             c.row0 = begin[c.expert] + k0 * kSlice;
             c.row1 = min(begin[c.expert + 1], begin[c.expert] + k1 * kSlice);
-            c.slices = k1 - k0;
-            c.whole = c.slices == count;
+            c.count = k1 - k0;
+            c.slices = c.count * g.pairs;
+            c.whole = c.count == count;
             c.slot = mine * 2 + (k0 > 0 ? 0 : 1);
-            pos += c.slices;
+            pos += c.count;
         } else {
             if (item >= items) return false;
             const int piece = (int)(item / per);
@@ -184,7 +201,8 @@ struct Walk {
             c.expert = expert_of(prefix, g.experts, piece);
             c.row0 = begin[c.expert] + (piece - prefix[c.expert]) * S::kTileHigh;
             c.row1 = min(begin[c.expert + 1], c.row0 + S::kTileHigh);
-            c.slices = (g.depth + kSlice - 1) / kSlice;
+            c.count = (g.depth + kSlice - 1) / kSlice;
+            c.slices = c.count * g.pairs;
             c.tile = 0;
             c.whole = true;
             c.slot = 0;
@@ -207,30 +225,70 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Eight results of the output's type in 16 (half types) or 32 bytes.
+template <typename Out>
+__device__ __forceinline__ void pack8(const float* f, uint4* v) {
+    if constexpr (sizeof(Out) == 4) {
+        v[0] = uint4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                     __float_as_uint(f[3])};
+        v[1] = uint4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                     __float_as_uint(f[7])};
+    } else {
+        v[0] = uint4{pack2<Out>(f[0], f[1]), pack2<Out>(f[2], f[3]), pack2<Out>(f[4], f[5]),
+                     pack2<Out>(f[6], f[7])};
+    }
+}
+
 // 32 rows x 64 bytes of output held one row a lane (four 16-byte vectors),
 // turned through shared memory so that four lanes write one row's 64
-// contiguous bytes.  valid_rows of the rows and valid_vectors of a row's
-// vectors are inside the output.
-__device__ __forceinline__ void write_block(char* staging, const uint4* v, char* out,
-                                            int64_t pitch, int valid_rows, int valid_vectors) {
+// contiguous bytes (or, where rows of the output are not whole vectors, single
+// elements).  valid_rows of the rows and `left` of a row's elements are inside
+// the output.
+template <typename Out>
+__device__ __forceinline__ void write_block(char* staging, const uint4* v, Out* out,
+                                            int64_t pitch, int valid_rows, int left,
+                                            bool vectors) {
     const int lane = threadIdx.x & 31;
+    constexpr int kVec = 16 / sizeof(Out), kRow = 64 / sizeof(Out);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         *reinterpret_cast<uint4*>(staging + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = v[j];
     __syncwarp();
-    const int j = lane & 3;
+    if (vectors) {
+        const int j = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4;
-        const uint4 x =
-            *reinterpret_cast<const uint4*>(staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4));
-        if (r < valid_rows && j < valid_vectors)
-            *reinterpret_cast<uint4*>(out + r * pitch + j * 16) = x;
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + lane / 4;
+            const uint4 x =
+                *reinterpret_cast<const uint4*>(staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4));
+            if (r < valid_rows && j * kVec < left)
+                *reinterpret_cast<uint4*>(out + r * pitch + j * kVec) = x;
+        }
+    } else {
+        const int e = lane % kRow, j = e / kVec;
+        for (int r = lane / kRow; r < min(32, valid_rows); r += 32 / kRow) {
+            const Out x = *reinterpret_cast<const Out*>(
+                staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4) + e % kVec * sizeof(Out));
+            if (e < left) out[r * pitch + e] = x;
+        }
     }
     __syncwarp();
 }
 
-template <typename T, int kProduct, int kBlocks, int kWide>
+// By the output warps: n elements from `out` on are 0; `at` and `stride`: this
+// thread's place among all of them.
+template <typename Out>
+__device__ __forceinline__ void zero_range(Out* out, int64_t n, int64_t at, int64_t stride,
+                                           bool vectors) {
+    if (vectors)
+        for (int64_t i = at; i < n * (int64_t)sizeof(Out) / 16; i += stride)
+            reinterpret_cast<uint4*>(out)[i] = uint4{0, 0, 0, 0};
+    else
+        for (int64_t i = at; i < n; i += stride) out[i] = from_f<Out>(0.f);
+}
+
+// T: type of the planes; Out: of the output and of bias.
+template <typename T, typename Out, int kProduct, int kBlocks, int kWide>
 __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const __grid_constant__ ProductArgs g) {
@@ -283,7 +341,10 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
         bool ok = true;
         while (ok && walk.next(c)) {
             const int n0 = c.n0 + rank * S::kPartB;
-            for (int k = 0; k < c.slices; ++k, at.advance()) {
+            for (int q = 0, sum = 0, k = 0; q < c.slices; ++q, at.advance()) {
+                const int row_a = plane_a(g.pairs, sum) * (int)g.rows + c.row0;
+                const int row_b = plane_b(g.pairs, sum) * (int)g.rows + c.row0;
+                const int matrix = plane_b(g.pairs, sum) * g.experts + c.expert;
                 ok = at.turn == 0 || warp_wait(&bars.empty[at.stage], (at.turn + 1) & 1, abort);
                 if (!ok) break;
                 const uint32_t a = base + at.stage * S::kStageBytes;
@@ -294,26 +355,32 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                     if (rank == 0)
                         mbar_expect_tx(&bars.full[at.stage], S::kStageBytes * kBlocks);
                     if (kProduct == kWeightGrad) {
-                        const int m0 = c.m0 + rank * kHigh, row = c.row0 + k * kSlice;
+                        const int m0 = c.m0 + rank * kHigh;
 #pragma unroll
                         for (int i = 0; i < kHigh / 64; ++i)
-                            tma_load_2d<kBlocks>(a + i * 64 * 128, &map_a, m0 + i * 64, row, full);
+                            tma_load_2d<kBlocks>(a + i * 64 * 128, &map_a, m0 + i * 64,
+                                                 row_a + k * kSlice, full);
 #pragma unroll
                         for (int i = 0; i < S::kPartB / 64; ++i)
-                            tma_load_2d<kBlocks>(b + i * 64 * 128, &map_b, n0 + i * 64, row, full);
+                            tma_load_2d<kBlocks>(b + i * 64 * 128, &map_b, n0 + i * 64,
+                                                 row_b + k * kSlice, full);
                     } else {
-                        tma_load_2d<kBlocks>(a, &map_a, k * kSlice, c.row0 + rank * kHigh, full);
+                        tma_load_2d<kBlocks>(a, &map_a, k * kSlice, row_a + rank * kHigh, full);
                         if (kProduct == kForward) {
-                            tma_load_3d<kBlocks>(b, &map_b, k * kSlice, n0, c.expert, full);
+                            tma_load_3d<kBlocks>(b, &map_b, k * kSlice, n0, matrix, full);
                         } else {
 #pragma unroll
                             for (int i = 0; i < S::kPartB / 64; ++i)
                                 tma_load_3d<kBlocks>(b + i * 64 * 128, &map_b, n0 + i * 64,
-                                                     k * kSlice, c.expert, full);
+                                                     k * kSlice, matrix, full);
                         }
                     }
                 }
                 __syncwarp();
+                if (++k == c.count) {
+                    k = 0;
+                    ++sum;
+                }
             }
         }
         if (!ok && rank == 0)  // let the copies in flight land before the blocks go
@@ -338,7 +405,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
             if (acc.turn > 0) ok = warp_wait(&bars.acc_empty[acc.stage], (acc.turn + 1) & 1, abort);
             tmem_fence_after();
             const uint32_t d = tmem + acc.stage * kWide;
-            for (int k = 0; k < c.slices && ok; ++k, at.advance()) {
+            for (int q = 0, k = 0; q < c.slices && ok; ++q, at.advance()) {
                 ok = warp_wait(&bars.full[at.stage], at.turn & 1, abort);
                 if (!ok) break;
                 if (kProduct == kWeightGrad) {
@@ -356,11 +423,12 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                     for (int j = 0; j < kSlice / 16; ++j)
                         mma_f16<kBlocks>(d, da + j * ((kMnA ? 2048 : 32) >> 4),
                                          db + j * ((kMnB ? 2048 : 32) >> 4), word,
-                                         k > 0 || j > 0);
+                                         q > 0 || j > 0);
                     mma_commit<kBlocks>(&bars.empty[at.stage]);
-                    if (k + 1 == c.slices) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
+                    if (q + 1 == c.slices) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
                 }
                 __syncwarp();
+                if (kProduct == kWeightGrad && ++k == c.count) k = 0;
             }
             acc.advance();
         }
@@ -381,7 +449,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
         while (ok && walk.next(c)) {
             // sums of eight columns of A over every eighth row
             float sum[8] = {};
-            for (int k = 0; k < c.slices; ++k, at.advance()) {
+            for (int q = 0, sums = 0, k = 0; q < c.slices; ++q, at.advance()) {
                 ok = warp_wait(&bars.landed[at.stage], at.turn & 1, abort);
                 if (!ok) break;
                 char* a = smem + at.stage * S::kStageBytes;
@@ -397,7 +465,9 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                     __syncwarp();
                     if (lane == 0) mbar_release_at(&bars.cleared, 0);
                 }
-                if (columns && (c.row0 / kSlice + k) % walk.across == c.n0 / kWide) {
+                // every plane of A once: where it meets plane 0 of B
+                if (columns && plane_b(g.pairs, sums) == 0 &&
+                    (c.row0 / kSlice + k) % walk.across == c.n0 / kWide) {
                     const char* p = a + helper / 2 * 64 * 128;
 #pragma unroll
                     for (int r = row8; r < kSlice; r += 8) {
@@ -412,6 +482,10 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_at(&bars.empty[at.stage], rank);
+                if (++k == c.count) {
+                    k = 0;
+                    ++sums;
+                }
             }
             if (ok && columns) {
 #pragma unroll
@@ -443,13 +517,11 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                 tmem + ((uint32_t)(q * 32) << 16) + acc.stage * kWide + first;
             uint32_t u[2][32];
             if (kProduct == kForward && g.bias) {
-                const T* p = static_cast<const T*>(g.bias) + (int64_t)c.expert * g.width;
+                const Out* p = static_cast<const Out*>(g.bias) + (int64_t)c.expert * g.width;
 #pragma unroll
-                for (int i = lane * 4; i < kSpan; i += 128) {
+                for (int i = lane; i < kSpan; i += 32) {
                     const int n = c.n0 + first + i;
-                    float v[4] = {};
-                    if (n < g.width) unpack<T, 4>(load_raw<T, 4>(p + n), v);
-                    *reinterpret_cast<float4*>(bias + i) = float4{v[0], v[1], v[2], v[3]};
+                    bias[i] = n < g.width ? to_f(p[n]) : 0.f;
                 }
                 __syncwarp();
             }
@@ -460,19 +532,17 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
             tmem_wait_loads();
             const int row = rank * kHigh + q * 32;  // first row in the tile
             const bool partial = kProduct == kWeightGrad && !c.whole;
-            char* out;
+            float* part = nullptr;
+            Out* out = static_cast<Out*>(g.out);
             int rows;
             if (partial) {
-                out = reinterpret_cast<char*>(g.partial +
-                                              (c.slot * S::kTileHigh + row) * kWide);
+                part = g.partial + (c.slot * S::kTileHigh + row) * kWide;
                 rows = 32;
             } else if (kProduct == kWeightGrad) {
-                out = static_cast<char*>(g.out) +
-                      (((int64_t)c.expert * g.high + c.m0 + row) * g.width + c.n0) * sizeof(T);
+                out += ((int64_t)c.expert * g.high + c.m0 + row) * g.width + c.n0;
                 rows = g.high - c.m0 - row;
             } else {
-                out = static_cast<char*>(g.out) +
-                      (((int64_t)c.row0 + row) * g.width + c.n0) * sizeof(T);
+                out += ((int64_t)c.row0 + row) * g.width + c.n0;
                 rows = c.row1 - c.row0 - row;
             }
 #pragma unroll
@@ -490,26 +560,31 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                         for (int i = 0; i < 4; ++i)
                             v[i] = uint4{w[16 * h + 4 * i], w[16 * h + 4 * i + 1],
                                          w[16 * h + 4 * i + 2], w[16 * h + 4 * i + 3]};
-                        write_block(mine, v, out + (n + 16 * h) * 4, kWide * 4, rows, 4);
+                        write_block<float>(mine, v, part + n + 16 * h, kWide, rows, 16, true);
                     }
                 } else if (left > 0) {
-                    uint4 v[4];
+                    constexpr int kRow = 64 / (int)sizeof(Out);  // columns written at a time
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float f[8];
+                    for (int h = 0; h < 32 / kRow; ++h) {
+                        uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[8 * i + j]);
-                        if (kProduct == kForward && g.bias) {
-                            const float4* p = reinterpret_cast<const float4*>(bias + b * 32) + 2 * i;
-                            const float4 lo = p[0], hi = p[1];
-                            f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
-                            f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+                        for (int i = 0; i < kRow / 8; ++i) {
+                            float f[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                f[j] = __uint_as_float(w[kRow * h + 8 * i + j]);
+                            if (kProduct == kForward && g.bias) {
+                                const float4* p = reinterpret_cast<const float4*>(
+                                    bias + b * 32 + kRow * h + 8 * i);
+                                const float4 lo = p[0], hi = p[1];
+                                f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
+                                f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+                            }
+                            pack8<Out>(f, v + i * (int)sizeof(Out) / 2);
                         }
-                        v[i] = uint4{pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
-                                     pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])};
+                        write_block<Out>(mine, v, out + n + kRow * h, g.width, rows,
+                                         left - kRow * h, g.vectors);
                     }
-                    write_block(mine, v, out + n * sizeof(T), (int64_t)g.width * sizeof(T), rows,
-                                (left + 7) / 8);
                 }
                 tmem_wait_loads();
                 if (b + 2 == kSpan / 32) {
@@ -523,17 +598,15 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
         // rows of no expert, and the gradients of experts without rows, are 0
         const int64_t at = (int64_t)blockIdx.x * (kOutWarps * 32) + threadIdx.x - 128;
         const int64_t stride = (int64_t)gridDim.x * (kOutWarps * 32);
+        Out* out = static_cast<Out*>(g.out);
         if (kProduct != kWeightGrad) {
-            const int64_t per = (int64_t)g.width * sizeof(T) / 16;
-            for (int64_t i = begin[g.experts] * per + at; i < g.rows * per; i += stride)
-                static_cast<uint4*>(g.out)[i] = uint4{0, 0, 0, 0};
+            const int64_t kept = begin[g.experts];
+            zero_range(out + kept * g.width, (g.rows - kept) * g.width, at, stride, g.vectors);
         } else {
-            const int64_t per = (int64_t)g.high * g.width * sizeof(T) / 16;
-            for (int e = 0; e < g.experts; ++e) {
-                if (prefix[e] != prefix[e + 1]) continue;
-                for (int64_t i = at; i < per; i += stride)
-                    static_cast<uint4*>(g.out)[e * per + i] = uint4{0, 0, 0, 0};
-            }
+            const int64_t size = (int64_t)g.high * g.width;
+            for (int e = 0; e < g.experts; ++e)
+                if (prefix[e] == prefix[e + 1])
+                    zero_range(out + e * size, size, at, stride, g.vectors);
         }
     }
     __syncthreads();
@@ -548,7 +621,7 @@ constexpr int kSlabs = 16;  // blocks that add up a tile of partial sums
 // tile: the expert that it (and no cut before it) cuts, grad_weight[e] = its
 // partial sums in the order of the shares.  Then for every expert ceil(high /
 // 256) blocks: grad_bias[e] = the sums of its column tiles and shares.
-template <typename T, int kBlocks, int kWide>
+template <typename Out, int kBlocks, int kWide>
 __global__ void __launch_bounds__(256)
     k_sum_parts(const __grid_constant__ ProductArgs g, int tiles) {
     using S = Shape<kBlocks, kWide>;
@@ -598,9 +671,14 @@ __global__ void __launch_bounds__(256)
                 sum.z += v.z;
                 sum.w += v.w;
             }
-            *reinterpret_cast<uint2*>(static_cast<T*>(g.out) +
-                                      ((int64_t)e * g.high + m0 + row) * g.width + n0 + col) =
-                uint2{pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w)};
+            Out* out = static_cast<Out*>(g.out) + ((int64_t)e * g.high + m0 + row) * g.width +
+                       n0 + col;
+            const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+            if (g.vectors) {
+                store_vec<Out, 4>(out, v);
+            } else {
+                for (int j = 0; j < min(4, g.width - n0 - col); ++j) out[j] = from_f<Out>(v[j]);
+            }
         }
         return;
     }
@@ -621,7 +699,55 @@ __global__ void __launch_bounds__(256)
             }
         }
     }
-    static_cast<T*>(g.bias_grad)[(int64_t)e * g.high + m] = from_f<T>(sum);
+    static_cast<Out*>(g.bias_grad)[(int64_t)e * g.high + m] = from_f<Out>(sum);
+}
+
+// A (rows x columns) matrix as planes of rows of `pitch` elements (a multiple
+// of 8): float32 as three of bfloat16, each cutting off the next eight bits of
+// the fraction, half types copied.  Reads once, writes once.
+constexpr int kPlaneRows = 8;
+
+template <typename T, typename Plane>
+__global__ void __launch_bounds__(32 * kPlaneRows)
+    k_planes(const T* __restrict__ x, int64_t rows, int columns, int pitch, bool vectors,
+             Plane* __restrict__ out) {
+    const int c = (blockIdx.x * 32 + threadIdx.x) * 8;
+    if (c >= columns) return;
+    for (int64_t r = (int64_t)blockIdx.y * kPlaneRows + threadIdx.y; r < rows;
+         r += (int64_t)gridDim.y * kPlaneRows) {
+        const T* from = x + r * columns + c;
+        __align__(16) T v[8];
+        if (vectors && c + 8 <= columns) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+                reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(from)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c + i < columns ? from[i] : from_f<T>(0.f);
+        }
+        if constexpr (sizeof(T) == 4) {
+            __align__(16) uint16_t p[3][8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t a0 = __float_as_uint(v[i]) & 0xffff0000u;
+                // an infinity or NaN is all in the first plane
+                const bool finite = (a0 & 0x7f800000u) != 0x7f800000u;
+                const float r1 = finite ? v[i] - __uint_as_float(a0) : 0.f;
+                const uint32_t a1 = __float_as_uint(r1) & 0xffff0000u;
+                const uint32_t a2 = __float_as_uint(r1 - __uint_as_float(a1));
+                // a NaN whose upper half alone would read as an infinity stays one
+                p[0][i] = (uint16_t)(a0 >> 16 | (v[i] != v[i] ? 0x40u : 0u));
+                p[1][i] = (uint16_t)(a1 >> 16);
+                p[2][i] = (uint16_t)(a2 >> 16);
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint4*>(out + ((int64_t)k * rows + r) * pitch + c) =
+                    *reinterpret_cast<const uint4*>(p[k]);
+        } else {
+            *reinterpret_cast<uint4*>(out + r * pitch + c) = *reinterpret_cast<const uint4*>(v);
+        }
+    }
 }
 
 // cuTensorMapEncodeTiled, found through the runtime (the library does not
@@ -644,19 +770,61 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// A (rows x columns) matrix, or `count` of them one after the other, copied
-// in boxes of box_rows x 64 elements (128 bytes, swizzled).
-bool make_map(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64_t columns,
-              int count, int box_rows) {
+// An operand as the tiled copies read it.
+struct Planes {
+    const void* base;
+    int64_t rows;  // of one plane
+    int columns, pitch, count;
+};
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Whether rows of `columns` elements from p on can be copied as they lie.
+bool copyable(int dtype, const void* p, int columns) {
+    return dtype != GS_F32 && columns % 8 == 0 && aligned16(p);
+}
+
+size_t plane_bytes(int dtype, int64_t rows, int columns) {
+    const size_t bytes = (size_t)(dtype == GS_F32 ? 3 : 1) * rows * ceil_div(columns, 8) * 16;
+    return (bytes + 255) / 256 * 256;
+}
+
+// The operand itself, or its planes at *workspace (which moves behind them).
+Planes prepare(int dtype, const void* x, int64_t rows, int columns, char** workspace,
+               cudaStream_t s) {
+    if (copyable(dtype, x, columns)) return Planes{x, rows, columns, columns, 1};
+    const int pitch = (int)ceil_div(columns, 8) * 8, count = dtype == GS_F32 ? 3 : 1;
+    void* out = *workspace;
+    *workspace += plane_bytes(dtype, rows, columns);
+    const dim3 grid((unsigned)ceil_div(columns, 256),
+                    (unsigned)std::min<int64_t>(ceil_div(rows, kPlaneRows), 152 * 64));
+    const dim3 block(32, kPlaneRows);
+    with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        using Plane = typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type;
+        k_planes<T, Plane><<<grid, block, 0, s>>>(
+            static_cast<const T*>(x), rows, columns, pitch,
+            aligned16(x) && columns * sizeof(T) % 16 == 0, static_cast<Plane*>(out));
+    });
+    return Planes{out, rows, columns, pitch, count};
+}
+
+// A matrix (experts = 0), or one matrix an expert, copied in boxes of
+// box_rows x 64 elements (128 bytes, swizzled).
+bool make_map(CUtensorMap* map, int dtype, const Planes& p, int experts, int box_rows) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)columns, (cuuint64_t)rows, (cuuint64_t)count};
-    const cuuint64_t strides[2] = {(cuuint64_t)columns * 2, (cuuint64_t)columns * rows * 2};
+    const int64_t all = p.rows * p.count, one = experts ? p.rows / experts : all;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.columns, (cuuint64_t)one,
+                                (cuuint64_t)(experts * p.count)};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.pitch * 2, (cuuint64_t)p.pitch * one * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
     return encode(map,
-                  dtype == GS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                  count > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, unit,
+                  dtype == GS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  experts > 0 ? 3 : 2, const_cast<void*>(p.base), dims, strides, box, unit,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -670,10 +838,10 @@ int sm_count() {
     return n;
 }
 
-template <typename T, int kProduct, int kBlocks, int kWide>
+template <typename T, typename Out, int kProduct, int kBlocks, int kWide>
 int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int64_t max_items,
            cudaStream_t s) {
-    const auto kernel = k_product<T, kProduct, kBlocks, kWide>;
+    const auto kernel = k_product<T, Out, kProduct, kBlocks, kWide>;
     const size_t smem = smem_bytes<kBlocks, kWide>(g.experts);
     static const bool raised =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -702,10 +870,6 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int
     return cudaLaunchKernelEx(&config, kernel, a, b, g) == cudaSuccess ? GS_OK : GS_ERR_CUDA;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Two blocks a tile of 256 x 256 where the output is wide enough and the
 // experts have rows enough on average to fill 256 of them.
 bool use_pairs(const LinearArgs& a, int width) {
@@ -715,15 +879,15 @@ bool use_pairs(const LinearArgs& a, int width) {
 // Columns of B in one box of a tiled copy.
 int box_b(bool pairs, int width) { return !pairs && width > 128 ? 256 : 128; }
 
-template <typename T, int kProduct>
+template <typename T, typename Out, int kProduct>
 int launch_rows(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, bool pairs,
                 cudaStream_t s) {
     // at most one part-filled tile an expert
     const int64_t pieces = g.rows / (pairs ? 256 : 128) + g.experts;
-    if (pairs) return launch<T, kProduct, 2, 256>(a, b, g, pieces * ceil_div(g.width, 256), s);
+    if (pairs) return launch<T, Out, kProduct, 2, 256>(a, b, g, pieces * ceil_div(g.width, 256), s);
     if (g.width > 128)
-        return launch<T, kProduct, 1, 256>(a, b, g, pieces * ceil_div(g.width, 256), s);
-    return launch<T, kProduct, 1, 128>(a, b, g, pieces, s);
+        return launch<T, Out, kProduct, 1, 256>(a, b, g, pieces * ceil_div(g.width, 256), s);
+    return launch<T, Out, kProduct, 1, 128>(a, b, g, pieces, s);
 }
 
 // How the weight gradient is cut up.
@@ -747,7 +911,8 @@ GradPlan grad_plan(const LinearArgs& a) {
     // 1024 x 512: 9 shares 102 us of products and 12 us of sums, 19 shares
     // 169 and 24.
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(a.rows / 512, 64));
-    const double work = 2.0 * a.rows * p.tiles * p.high * p.wide / 1.6e15;
+    const double work =
+        2.0 * (a.dtype == GS_F32 ? 6 : 1) * a.rows * p.tiles * p.high * p.wide / 1.6e15;
     double best = 0.0;
     for (int64_t g = 1; g <= most; ++g) {
         const int64_t items = g * p.tiles;
@@ -770,103 +935,131 @@ size_t bias_floats(const GradPlan& p, int experts) {
     return (size_t)((2 * p.groups + experts) * p.tiles) * p.high;
 }
 
-template <typename T, int kBlocks, int kWide>
+template <typename T, typename Out, int kBlocks, int kWide>
 int launch_weight_grad(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g,
                        const GradPlan& p, cudaStream_t s) {
     const int rc =
-        launch<T, kWeightGrad, kBlocks, kWide>(a, b, g, (int64_t)p.groups * p.tiles, s);
+        launch<T, Out, kWeightGrad, kBlocks, kWide>(a, b, g, (int64_t)p.groups * p.tiles, s);
     const int64_t blocks = (int64_t)(p.groups - 1) * p.tiles * kSlabs +
                            (g.bias_grad ? g.experts * ceil_div(g.high, 256) : 0);
     if (rc == GS_OK && blocks > 0)
-        k_sum_parts<T, kBlocks, kWide>
+        k_sum_parts<Out, kBlocks, kWide>
             <<<(unsigned)blocks, 256, 2 * sizeof(int32_t) * (g.experts + 1), s>>>(g,
                                                                                  (int)p.tiles);
     return rc;
 }
 
-template <typename T>
+template <typename T, typename Out>
 int weight_grad_of(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g,
                    const GradPlan& p, cudaStream_t s) {
-    if (p.pairs) return launch_weight_grad<T, 2, 256>(a, b, g, p, s);
-    if (p.wide == 256) return launch_weight_grad<T, 1, 256>(a, b, g, p, s);
-    return launch_weight_grad<T, 1, 128>(a, b, g, p, s);
+    if (p.pairs) return launch_weight_grad<T, Out, 2, 256>(a, b, g, p, s);
+    if (p.wide == 256) return launch_weight_grad<T, Out, 1, 256>(a, b, g, p, s);
+    return launch_weight_grad<T, Out, 1, 128>(a, b, g, p, s);
+}
+
+ProductArgs product_args(const LinearArgs& a, void* out, int width) {
+    ProductArgs g{};
+    g.offsets = a.offsets;
+    g.rows = a.rows;
+    g.experts = a.experts;
+    g.width = width;
+    g.pairs = a.dtype == GS_F32 ? 6 : 1;
+    g.vectors = aligned16(out) && (size_t)width * dtype_size(a.dtype) % 16 == 0;
+    g.out = out;
+    g.d_status = a.d_status;
+    return g;
+}
+
+// f(type of the planes, type of the output)
+template <typename F>
+int with_types(int dtype, F&& f) {
+    if (dtype == GS_F32) return f(__nv_bfloat16{}, float{});
+    if (dtype == GS_F16) return f(__half{}, __half{});
+    return f(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
 }  // namespace
 
-bool mma_usable(const LinearArgs& a, std::initializer_list<const void*> arrays) {
-    if (a.dtype == GS_F32 || a.in % 8 || a.out % 8) return false;
-    for (const void* p : arrays)
-        if (!aligned16(p)) return false;
-    return true;
+size_t linear_fwd_workspace(const LinearArgs& a, const void* xs, const void* weight) {
+    size_t n = 0;
+    if (!copyable(a.dtype, xs, a.in)) n += plane_bytes(a.dtype, a.rows, a.in);
+    if (!copyable(a.dtype, weight, a.in))
+        n += plane_bytes(a.dtype, (int64_t)a.experts * a.out, a.in);
+    return n;
 }
 
-int launch_mma_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
-                   void* ys, cudaStream_t s) {
+int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
+                      void* ys, void* workspace, cudaStream_t s) {
     const bool pairs = use_pairs(a, a.out);
+    char* ws = static_cast<char*>(workspace);
+    const Planes pa = prepare(a.dtype, xs, a.rows, a.in, &ws, s);
+    const Planes pb = prepare(a.dtype, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
     CUtensorMap ma, mb;
-    if (!make_map(&ma, a.dtype, xs, a.rows, a.in, 0, kHigh) ||
-        !make_map(&mb, a.dtype, weight, a.out, a.in, a.experts, box_b(pairs, a.out)))
+    if (!make_map(&ma, a.dtype, pa, 0, kHigh) ||
+        !make_map(&mb, a.dtype, pb, a.experts, box_b(pairs, a.out)))
         return GS_ERR_CUDA;
-    ProductArgs g{};
-    g.offsets = a.offsets;
-    g.rows = a.rows;
-    g.experts = a.experts;
-    g.width = a.out;
+    ProductArgs g = product_args(a, ys, a.out);
     g.depth = a.in;
     g.bias = bias;
-    g.out = ys;
-    g.d_status = a.d_status;
-    return a.dtype == GS_F16 ? launch_rows<__half, kForward>(ma, mb, g, pairs, s)
-                             : launch_rows<__nv_bfloat16, kForward>(ma, mb, g, pairs, s);
+    return with_types(a.dtype, [&](auto t, auto o) {
+        return launch_rows<decltype(t), decltype(o), kForward>(ma, mb, g, pairs, s);
+    });
 }
 
-int launch_mma_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
-                  cudaStream_t s) {
-    const bool pairs = use_pairs(a, a.in);
-    CUtensorMap ma, mb;
-    if (!make_map(&ma, a.dtype, grad_ys, a.rows, a.out, 0, kHigh) ||
-        !make_map(&mb, a.dtype, weight, a.out, a.in, a.experts, kSlice))
-        return GS_ERR_CUDA;
-    ProductArgs g{};
-    g.offsets = a.offsets;
-    g.rows = a.rows;
-    g.experts = a.experts;
-    g.width = a.in;
-    g.depth = a.out;
-    g.out = grad_xs;
-    g.d_status = a.d_status;
-    return a.dtype == GS_F16 ? launch_rows<__half, kInputGrad>(ma, mb, g, pairs, s)
-                             : launch_rows<__nv_bfloat16, kInputGrad>(ma, mb, g, pairs, s);
-}
+namespace {
 
-size_t mma_dw_workspace(const LinearArgs& a) {
-    if (a.dtype == GS_F32 || a.in % 8 || a.out % 8) return 0;
+size_t grad_sums_bytes(const LinearArgs& a) {
     const GradPlan p = grad_plan(a);
-    return (partial_floats(p) + bias_floats(p, a.experts)) * sizeof(float);
+    const size_t n = (partial_floats(p) + bias_floats(p, a.experts)) * sizeof(float);
+    return (n + 255) / 256 * 256;
 }
 
-int launch_mma_dw(const LinearArgs& a, const void* grad_ys, const void* xs, void* grad_weight,
-                  void* grad_bias, void* workspace, cudaStream_t s) {
+}  // namespace
+
+size_t linear_bwd_workspace(const LinearArgs& a, const void* grad_ys, const void* xs,
+                            const void* weight) {
+    size_t n = grad_sums_bytes(a);
+    if (!copyable(a.dtype, grad_ys, a.out)) n += plane_bytes(a.dtype, a.rows, a.out);
+    if (!copyable(a.dtype, xs, a.in)) n += plane_bytes(a.dtype, a.rows, a.in);
+    if (!copyable(a.dtype, weight, a.in))
+        n += plane_bytes(a.dtype, (int64_t)a.experts * a.out, a.in);
+    return n;
+}
+
+int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
+                      const void* weight, void* grad_xs, void* grad_weight, void* grad_bias,
+                      void* workspace, cudaStream_t s) {
+    char* ws = static_cast<char*>(workspace);
+    float* sums = reinterpret_cast<float*>(ws);
+    ws += grad_sums_bytes(a);
+    const Planes gy = prepare(a.dtype, grad_ys, a.rows, a.out, &ws, s);
     CUtensorMap ma, mb;
-    if (!make_map(&ma, a.dtype, grad_ys, a.rows, a.out, 0, kSlice) ||
-        !make_map(&mb, a.dtype, xs, a.rows, a.in, 0, kSlice))
+    if (grad_xs) {
+        const bool pairs = use_pairs(a, a.in);
+        const Planes w = prepare(a.dtype, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
+        if (!make_map(&ma, a.dtype, gy, 0, kHigh) || !make_map(&mb, a.dtype, w, a.experts, kSlice))
+            return GS_ERR_CUDA;
+        ProductArgs g = product_args(a, grad_xs, a.in);
+        g.depth = a.out;
+        const int rc = with_types(a.dtype, [&](auto t, auto o) {
+            return launch_rows<decltype(t), decltype(o), kInputGrad>(ma, mb, g, pairs, s);
+        });
+        if (rc != GS_OK) return rc;
+    }
+    if (!grad_weight) return GS_OK;
+    const Planes x = prepare(a.dtype, xs, a.rows, a.in, &ws, s);
+    if (!make_map(&ma, a.dtype, gy, 0, kSlice) || !make_map(&mb, a.dtype, x, 0, kSlice))
         return GS_ERR_CUDA;
     const GradPlan p = grad_plan(a);
-    ProductArgs g{};
-    g.offsets = a.offsets;
-    g.rows = a.rows;
-    g.experts = a.experts;
+    ProductArgs g = product_args(a, grad_weight, a.in);
     g.high = a.out;
-    g.width = a.in;
     g.groups = p.groups;
-    g.out = grad_weight;
     g.bias_grad = grad_bias;
-    g.partial = static_cast<float*>(workspace);
-    g.bias_partial = g.partial + partial_floats(p);
-    g.d_status = a.d_status;
-    return a.dtype == GS_F16 ? weight_grad_of<__half>(ma, mb, g, p, s)
-                             : weight_grad_of<__nv_bfloat16>(ma, mb, g, p, s);
+    g.partial = sums;
+    g.bias_partial = sums + partial_floats(p);
+    return with_types(a.dtype, [&](auto t, auto o) {
+        return weight_grad_of<decltype(t), decltype(o)>(ma, mb, g, p, s);
+    });
 }
 
 }  // namespace gs

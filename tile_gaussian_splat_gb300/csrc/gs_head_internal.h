@@ -4,7 +4,6 @@
 
 #include <cstddef>
 #include <cstdint>
-#include <initializer_list>
 #include <cuda_runtime.h>
 
 namespace gs {
@@ -48,35 +47,21 @@ void launch_combine_bwd(const RowArgs& a, const void* grad_y, int64_t ldgy, cons
                         const int32_t* slots, const float* weights, const int32_t* offsets,
                         void* grad_ys, float* grad_weights, cudaStream_t s);
 
-// ---- expert_linear.cu
+// ---- expert_mma.cu: each returns a gs_status.
 struct LinearArgs {
     const int32_t* offsets;
     int64_t rows;
     int experts, in, out, dtype;
     int32_t* d_status;
 };
-void launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
-                       void* ys, cudaStream_t s);
-void launch_linear_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
-                      cudaStream_t s);
-void launch_linear_dw(const LinearArgs& a, const void* grad_ys, const void* xs,
-                      void* grad_weight, cudaStream_t s);
-// Bytes of partial sums.
-size_t linear_db_workspace(const LinearArgs& a);
-void launch_linear_db(const LinearArgs& a, const void* grad_ys, void* grad_bias, void* workspace,
-                      cudaStream_t s);
-
-// ---- expert_mma.cu: the same products on the tensor cores.  Each returns a
-// gs_status.
-bool mma_usable(const LinearArgs& a, std::initializer_list<const void*> arrays);
-int launch_mma_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
-                   void* ys, cudaStream_t s);
-int launch_mma_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
-                  cudaStream_t s);
-// Bytes of partial sums.
-size_t mma_dw_workspace(const LinearArgs& a);
-// grad_bias may be null.
-int launch_mma_dw(const LinearArgs& a, const void* grad_ys, const void* xs, void* grad_weight,
-                  void* grad_bias, void* workspace, cudaStream_t s);
+size_t linear_fwd_workspace(const LinearArgs& a, const void* xs, const void* weight);
+int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
+                      void* ys, void* workspace, cudaStream_t s);
+size_t linear_bwd_workspace(const LinearArgs& a, const void* grad_ys, const void* xs,
+                            const void* weight);
+// grad_xs, or grad_weight and with it grad_bias, may be null.
+int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
+                      const void* weight, void* grad_xs, void* grad_weight, void* grad_bias,
+                      void* workspace, cudaStream_t s);
 
 }  // namespace gs

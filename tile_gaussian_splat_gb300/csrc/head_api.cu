@@ -50,7 +50,17 @@ bool linear_ok(const int32_t* offsets, int64_t rows, int experts, int in, int ou
         return false;
     if (in < 1 || in > kMaxFeatures || out < 1 || out > kMaxFeatures || !dtype_ok(dtype))
         return false;
+    // the three planes of float32 rows are numbered in 32 bits
+    if (dtype == GS_F32 && 3 * rows >= ((int64_t)1 << 31)) return false;
     return words_ok(offsets);
+}
+
+const int32_t kSomeOffsets = 0;  // stands for the offsets where only sizes are checked
+
+size_t dtype_size(int dtype) { return dtype == GS_F32 ? 4 : 2; }
+
+bool workspace_ok(const void* p, size_t bytes, size_t need) {
+    return need == 0 || (p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && bytes >= need);
 }
 
 size_t sort_counts_bytes(int64_t n, int experts) {
@@ -176,10 +186,18 @@ int gs_expert_combine_bwd(const void* grad_y, int64_t ldgy, const void* ys, cons
     return check_launch();
 }
 
+size_t gs_expert_linear_fwd_workspace_size(int64_t rows, int experts, int in_features,
+                                           int out_features, int dtype, int aligned) {
+    if (!linear_ok(&kSomeOffsets, rows, experts, in_features, out_features, dtype)) return 0;
+    const void* p = reinterpret_cast<const void*>((uintptr_t)(aligned ? 16 : 2));
+    return linear_fwd_workspace(
+        LinearArgs{nullptr, rows, experts, in_features, out_features, dtype, nullptr}, p, p);
+}
+
 int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* weight,
                          const void* bias, int64_t rows, int experts, int in_features,
-                         int out_features, int dtype, void* ys, int32_t* d_status,
-                         void* stream) {
+                         int out_features, int dtype, void* ys, void* workspace,
+                         size_t workspace_bytes, int32_t* d_status, void* stream) {
     if (!linear_ok(offsets, rows, experts, in_features, out_features, dtype))
         return GS_ERR_INVALID_ARG;
     if (rows == 0) return GS_OK;
@@ -187,22 +205,19 @@ int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* wei
         !array_ok(ys, dtype))
         return GS_ERR_INVALID_ARG;
     const LinearArgs a{offsets, rows, experts, in_features, out_features, dtype, d_status};
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (mma_usable(a, {xs, weight, bias, ys})) {
-        const int rc = launch_mma_fwd(a, xs, weight, bias, ys, s);
-        if (rc != GS_OK) return rc;
-    } else {
-        launch_linear_fwd(a, xs, weight, bias, ys, s);
-    }
-    return check_launch();
+    if (!workspace_ok(workspace, workspace_bytes, linear_fwd_workspace(a, xs, weight)))
+        return GS_ERR_WORKSPACE;
+    const int rc = launch_linear_fwd(a, xs, weight, bias, ys, workspace,
+                                     static_cast<cudaStream_t>(stream));
+    return rc == GS_OK ? check_launch() : rc;
 }
 
 size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_features,
-                                           int out_features, int dtype) {
-    int32_t dummy = 0;
-    if (!linear_ok(&dummy, rows, experts, in_features, out_features, dtype)) return 0;
-    const LinearArgs a{nullptr, rows, experts, in_features, out_features, dtype, nullptr};
-    return align_up(linear_db_workspace(a)) + align_up(mma_dw_workspace(a));
+                                           int out_features, int dtype, int aligned) {
+    if (!linear_ok(&kSomeOffsets, rows, experts, in_features, out_features, dtype)) return 0;
+    const void* p = reinterpret_cast<const void*>((uintptr_t)(aligned ? 16 : 2));
+    return linear_bwd_workspace(
+        LinearArgs{nullptr, rows, experts, in_features, out_features, dtype, nullptr}, p, p, p);
 }
 
 int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* offsets,
@@ -217,30 +232,22 @@ int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* off
         return GS_ERR_INVALID_ARG;
     if (grad_weight && (!array_ok(grad_weight, dtype) || (rows > 0 && !array_ok(xs, dtype))))
         return GS_ERR_INVALID_ARG;
-    if (grad_bias && !array_ok(grad_bias, dtype)) return GS_ERR_INVALID_ARG;
-    const size_t need = gs_expert_linear_bwd_workspace_size(rows, experts, in_features,
-                                                            out_features, dtype);
-    if ((grad_weight || grad_bias) &&
-        (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need))
-        return GS_ERR_WORKSPACE;
+    if (grad_bias && (!array_ok(grad_bias, dtype) || !grad_weight)) return GS_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LinearArgs a{offsets, rows, experts, in_features, out_features, dtype, d_status};
-    if (grad_xs && rows > 0) {
-        if (mma_usable(a, {grad_ys, weight, grad_xs})) {
-            const int rc = launch_mma_dx(a, grad_ys, weight, grad_xs, s);
-            if (rc != GS_OK) return rc;
-        } else {
-            launch_linear_dx(a, grad_ys, weight, grad_xs, s);
-        }
+    if (!workspace_ok(workspace, workspace_bytes, linear_bwd_workspace(a, grad_ys, xs, weight)))
+        return GS_ERR_WORKSPACE;
+    if (rows == 0) {  // sums over nothing
+        const size_t row = (size_t)experts * out_features * dtype_size(dtype);
+        if ((grad_weight && cudaMemsetAsync(grad_weight, 0, row * in_features, s) != cudaSuccess) ||
+            (grad_bias && cudaMemsetAsync(grad_bias, 0, row, s) != cudaSuccess))
+            return GS_ERR_CUDA;
+        return GS_OK;
     }
-    if (grad_weight && rows > 0 && mma_usable(a, {grad_ys, xs, grad_weight, grad_bias})) {
-        return launch_mma_dw(
-            a, grad_ys, xs, grad_weight, grad_bias,
-            static_cast<char*>(workspace) + align_up(linear_db_workspace(a)), s);
-    }
-    if (grad_weight) launch_linear_dw(a, grad_ys, xs, grad_weight, s);
-    if (grad_bias) launch_linear_db(a, grad_ys, grad_bias, workspace, s);
-    return check_launch();
+    if (!grad_xs && !grad_weight) return GS_OK;
+    const int rc = launch_linear_bwd(a, grad_ys, xs, weight, grad_xs, grad_weight, grad_bias,
+                                     workspace, s);
+    return rc == GS_OK ? check_launch() : rc;
 }
 
 }  // extern "C"
