@@ -9,8 +9,12 @@
 //
 // float32 operands are first written as three bfloat16 planes, a = a0 + a1 +
 // a2 with eight bits of the fraction each (exact), and a product is six sums,
-// a2 b0 + a0 b2 + a1 b1 + a1 b0 + a0 b1 + a0 b0 in one accumulator; the terms
-// left out are below 2^-22 of |a b|.  Half-type operands whose rows are not
+// a2 b0 + a0 b2 + a1 b1 + a1 b0 + a0 b1 + a0 b0, small ones first; the terms
+// left out are below 2^-22 of |a b|.  The accumulators cut off where float32
+// sums round (1.2e-8 of the result per 16 terms on random data: 3.8e-6 over
+// 5000), so every kRound slices of a0 b0 they are added to a running sum, kept
+// in the other half of tensor memory, and start anew.  (Added to the output
+// itself, that traffic took as long as the products.)  Half-type operands whose rows are not
 // whole 16-byte vectors are copied to rows that are (one plane).
 //
 // Two neighbouring blocks work as one on output tiles of 256 x 256 (each
@@ -68,6 +72,7 @@ struct ProductArgs {
     int high, width, depth;  // extents: high of the weight gradient, depth of the others
     int groups;              // weight gradient: shares of the rows
     int pairs;               // sums over plane pairs: 1, or 6 for float32
+    int rounds;              // float32: some sums take several rounds
     int vectors;             // output rows are whole 16-byte vectors
     const void* bias;        // kForward
     void* out;
@@ -111,6 +116,8 @@ constexpr size_t smem_bytes(int experts) {
            2 * sizeof(int32_t) * (size_t)(experts + 1);
 }
 
+constexpr int kRound = 8;  // slices of a0 b0 summed before they are added to the running sum
+
 // Planes of A and B in sum number `sum` of g.pairs, small terms first.
 __device__ __forceinline__ int plane_a(int pairs, int sum) {
     return 0x001102 >> 4 * (6 - pairs + sum) & 15;  // 2, 0, 1, 1, 0, 0
@@ -123,8 +130,8 @@ __device__ __forceinline__ int plane_b(int pairs, int sum) {
 template <int kCount>
 struct Ring {
     uint32_t stage = 0, turn = 0;
-    __device__ __forceinline__ void advance() {
-        if (++stage == kCount) {
+    __device__ __forceinline__ void advance(int count = kCount) {
+        if ((int)++stage == count) {
             stage = 0;
             ++turn;
         }
@@ -137,7 +144,7 @@ struct Tile {
     int row0, row1;  // rows of the output (of the sum, for kWeightGrad)
     int m0, n0;      // first row (kWeightGrad only) and column of the tile
     int count;       // 64-term slices of the sum
-    int slices;      // of all the sums over plane pairs
+    int q0, q1;      // of the slices of all sums over plane pairs, this round's
     int tile;        // kWeightGrad: which tile of the weight matrix
     bool whole;      // kWeightGrad: all of the expert's rows
     int64_t slot;    // kWeightGrad: where a partial sum goes
@@ -170,7 +177,17 @@ struct Walk {
         items = (int64_t)(kProduct == kWeightGrad ? g.groups : prefix[g.experts]) * per;
     }
 
+    // The slices of the next round of a tile; false after the last.
+    __device__ __forceinline__ bool next_round(Tile& c) const {
+        const int all = c.count * g.pairs;
+        c.q0 = c.q1;
+        c.q1 = g.pairs == 1 ? all : min(all, max(c.q0, all - c.count) + kRound);
+        return c.q0 < all;
+    }
+
+    // c: as the call before left it (count and q1 0 before the first).
     __device__ __forceinline__ bool next(Tile& c) {
+        if (next_round(c)) return true;
         if constexpr (kProduct == kWeightGrad) {
             const int64_t total = prefix[g.experts];
             while (pos >= end) {
@@ -189,7 +206,6 @@ struct Walk {
             c.row0 = begin[c.expert] + k0 * kSlice;
             c.row1 = min(begin[c.expert + 1], begin[c.expert] + k1 * kSlice);
             c.count = k1 - k0;
-            c.slices = c.count * g.pairs;
             c.whole = c.count == count;
             c.slot = mine * 2 + (k0 > 0 ? 0 : 1);
             pos += c.count;
@@ -202,13 +218,13 @@ struct Walk {
             c.row0 = begin[c.expert] + (piece - prefix[c.expert]) * S::kTileHigh;
             c.row1 = min(begin[c.expert + 1], c.row0 + S::kTileHigh);
             c.count = (g.depth + kSlice - 1) / kSlice;
-            c.slices = c.count * g.pairs;
             c.tile = 0;
             c.whole = true;
             c.slot = 0;
             item += step;
         }
-        return true;
+        c.q1 = 0;
+        return next_round(c);
     }
 };
 
@@ -334,14 +350,17 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
     const uint32_t tmem = bars.tmem, base = smem_u32(smem);
     volatile int* abort = &bars.abort;
     Walk<kProduct, kBlocks, kWide> walk(g, begin, prefix);
-    Tile c;
+    Tile c{};
+    // where a running sum takes the second accumulator's place
+    const int accumulators = sizeof(Out) == 4 && g.rounds ? 1 : kAccumulators;
 
     if (warp == 0) {
         Ring<S::kStages> at;
         bool ok = true;
         while (ok && walk.next(c)) {
             const int n0 = c.n0 + rank * S::kPartB;
-            for (int q = 0, sum = 0, k = 0; q < c.slices; ++q, at.advance()) {
+            int sum = c.q0 / c.count, k = c.q0 % c.count;
+            for (int q = c.q0; q < c.q1; ++q, at.advance()) {
                 const int row_a = plane_a(g.pairs, sum) * (int)g.rows + c.row0;
                 const int row_b = plane_b(g.pairs, sum) * (int)g.rows + c.row0;
                 const int matrix = plane_b(g.pairs, sum) * g.experts + c.expert;
@@ -405,7 +424,8 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
             if (acc.turn > 0) ok = warp_wait(&bars.acc_empty[acc.stage], (acc.turn + 1) & 1, abort);
             tmem_fence_after();
             const uint32_t d = tmem + acc.stage * kWide;
-            for (int q = 0, k = 0; q < c.slices && ok; ++q, at.advance()) {
+            int k = kProduct == kWeightGrad ? c.q0 % c.count : 0;
+            for (int q = c.q0; q < c.q1 && ok; ++q, at.advance()) {
                 ok = warp_wait(&bars.full[at.stage], at.turn & 1, abort);
                 if (!ok) break;
                 if (kProduct == kWeightGrad) {
@@ -423,14 +443,14 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                     for (int j = 0; j < kSlice / 16; ++j)
                         mma_f16<kBlocks>(d, da + j * ((kMnA ? 2048 : 32) >> 4),
                                          db + j * ((kMnB ? 2048 : 32) >> 4), word,
-                                         q > 0 || j > 0);
+                                         q > c.q0 || j > 0);
                     mma_commit<kBlocks>(&bars.empty[at.stage]);
-                    if (q + 1 == c.slices) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
+                    if (q + 1 == c.q1) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
                 }
                 __syncwarp();
                 if (kProduct == kWeightGrad && ++k == c.count) k = 0;
             }
-            acc.advance();
+            acc.advance(accumulators);
         }
         // nothing is still writing tensor memory when it is freed
         if (rank == 0) {
@@ -446,10 +466,10 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
         const int row8 = (lane >> 3) | (lane >> 2 & 1) << 2, unit = (helper & 1) * 4 + (lane & 3);
         Ring<S::kStages> at;
         bool ok = true;
+        float sum[8] = {};  // of eight columns of A over every eighth row
         while (ok && walk.next(c)) {
-            // sums of eight columns of A over every eighth row
-            float sum[8] = {};
-            for (int q = 0, sums = 0, k = 0; q < c.slices; ++q, at.advance()) {
+            int sums = c.q0 / c.count, k = c.q0 % c.count;
+            for (int q = c.q0; q < c.q1; ++q, at.advance()) {
                 ok = warp_wait(&bars.landed[at.stage], at.turn & 1, abort);
                 if (!ok) break;
                 char* a = smem + at.stage * S::kStageBytes;
@@ -487,7 +507,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                     ++sums;
                 }
             }
-            if (ok && columns) {
+            if (ok && columns && c.q1 == c.count * g.pairs) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 4);
@@ -502,20 +522,25 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                     p[0] = float4{sum[0], sum[1], sum[2], sum[3]};
                     p[1] = float4{sum[4], sum[5], sum[6], sum[7]};
                 }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = 0.f;
             }
         }
     } else if (warp >= 4 && warp < 4 + kOutWarps) {
         const int q = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
         constexpr int kSpan = S::kSpan;
+        // half types: the next 32 columns come in while these go out (float32
+        // has six times the products to hide behind and sums to hold)
+        constexpr int kAhead = sizeof(Out) == 4 ? 0 : 1;
         float* bias = reinterpret_cast<float*>(staging + S::kStaging) + (warp - 4) * kSpan;
         const int first = (warp - 4) / 4 * kSpan;
         char* mine = staging + (warp - 4) * 32 * 64;
         Ring<kAccumulators> acc;
         bool ok = true;
-        for (; ok && walk.next(c); acc.advance()) {
+        for (; ok && walk.next(c); acc.advance(accumulators)) {
             const uint32_t from =
                 tmem + ((uint32_t)(q * 32) << 16) + acc.stage * kWide + first;
-            uint32_t u[2][32];
+            uint32_t u[1 + kAhead][32];
             if (kProduct == kForward && g.bias) {
                 const Out* p = static_cast<const Out*>(g.bias) + (int64_t)c.expert * g.width;
 #pragma unroll
@@ -528,8 +553,10 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
             ok = warp_wait(&bars.acc_full[acc.stage], acc.turn & 1, abort);
             if (!ok) break;
             tmem_fence_after();
-            tmem_load32(from, u[0]);
-            tmem_wait_loads();
+            if (kAhead) {
+                tmem_load32(from, u[0]);
+                tmem_wait_loads();
+            }
             const int row = rank * kHigh + q * 32;  // first row in the tile
             const bool partial = kProduct == kWeightGrad && !c.whole;
             float* part = nullptr;
@@ -548,11 +575,31 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
 #pragma unroll
             for (int b = 0; b < kSpan / 32; ++b) {
                 const int n = first + b * 32;
-                // the next 32 columns come in while these go out
-                if (b + 1 < kSpan / 32) tmem_load32(from + (b + 1) * 32, u[(b + 1) & 1]);
-                const uint32_t* w = u[b & 1];
+                if (b + kAhead < kSpan / 32)
+                    tmem_load32(from + (b + kAhead) * 32, u[(b + 1) & kAhead]);
+                if (!kAhead) tmem_wait_loads();
+                uint32_t* w = u[b & kAhead];
+                const bool last = c.q1 == c.count * g.pairs;
+                if constexpr (sizeof(Out) == 4) {
+                    const uint32_t sum = from + kWide + b * 32;
+                    if (c.q0 > 0) {
+                        uint32_t was[32];
+                        tmem_load32(sum, was);
+                        tmem_wait_loads();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            w[i] = __float_as_uint(__uint_as_float(was[i]) +
+                                                   __uint_as_float(w[i]));
+                    }
+                    if (!last) {
+                        tmem_store32(sum, w);
+                        tmem_wait_stores();
+                    }
+                }
                 const int left = g.width - c.n0 - n;  // columns from here on
-                if (partial) {
+                if (!last) {
+                    // kept in tensor memory
+                } else if (partial) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint4 v[4];
@@ -587,7 +634,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                     }
                 }
                 tmem_wait_loads();
-                if (b + 2 == kSpan / 32) {
+                if (b + 1 + kAhead == kSpan / 32) {
                     // the accumulator is read: its next product may begin
                     tmem_fence_before();
                     __syncwarp();
@@ -905,20 +952,21 @@ GradPlan grad_plan(const LinearArgs& a) {
     p.wide = a.in > 128 ? 256 : 128;
     p.tiles = ceil_div(a.out, p.high) * ceil_div(a.in, p.wide);
     const int64_t units = sm_count() / (p.pairs ? 2 : 1);
-    // Shares: more of them fill the last round of the units better, but each
-    // leaves partial sums (two tiles an item, written and read).  The least
-    // time at 1.6 PFLOP/s on all units and 5 TB/s; 16 experts of 8192 rows,
-    // 1024 x 512: 9 shares 102 us of products and 12 us of sums, 19 shares
-    // 169 and 24.
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(a.rows / 512, 64));
-    const double work =
-        2.0 * (a.dtype == GS_F32 ? 6 : 1) * a.rows * p.tiles * p.high * p.wide / 1.6e15;
+    // Shares: more of them occupy more units and fill the last round of them
+    // better, but each leaves partial sums (two tiles an item, written and
+    // read).  The least time by this estimate of a unit's walk: 0.35 us a
+    // slice (of each of a float32 product's six sums), 2 us for an expert's
+    // part to come out, and the sums at 5 TB/s.  16 experts of 8192 rows, 1024
+    // x 512: 9 shares measured 131 us and 18 us of sums, 19 shares 169 and 24.
+    const double slices = a.rows / (double)kSlice + 0.5 * a.experts;
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>((int64_t)slices, 2 * units));
     double best = 0.0;
     for (int64_t g = 1; g <= most; ++g) {
         const int64_t items = g * p.tiles;
-        const double used = (double)items / (double)(units * ceil_div(items, units));
-        const double sums = g > 1 ? 16.0 * items * p.high * p.wide / 5e12 : 0.0;
-        const double time = work / used + sums;
+        const double walk = slices / g * 0.35 * (a.dtype == GS_F32 ? 6 : 1) +
+                            2.0 * (a.experts / (double)g + 1);
+        const double sums = g > 1 ? 3.0 + 16.0 * items * p.high * p.wide / 5e6 : 0.0;
+        const double time = walk * ceil_div(items, units) + sums;
         if (g == 1 || time < best) {
             best = time;
             p.groups = (int)g;
@@ -1000,6 +1048,7 @@ int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, c
         return GS_ERR_CUDA;
     ProductArgs g = product_args(a, ys, a.out);
     g.depth = a.in;
+    g.rounds = ceil_div(a.in, kSlice) > kRound;
     g.bias = bias;
     return with_types(a.dtype, [&](auto t, auto o) {
         return launch_rows<decltype(t), decltype(o), kForward>(ma, mb, g, pairs, s);
@@ -1041,6 +1090,7 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
             return GS_ERR_CUDA;
         ProductArgs g = product_args(a, grad_xs, a.in);
         g.depth = a.out;
+        g.rounds = ceil_div(a.out, kSlice) > kRound;
         const int rc = with_types(a.dtype, [&](auto t, auto o) {
             return launch_rows<decltype(t), decltype(o), kInputGrad>(ma, mb, g, pairs, s);
         });
@@ -1053,6 +1103,7 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
     const GradPlan p = grad_plan(a);
     ProductArgs g = product_args(a, grad_weight, a.in);
     g.high = a.out;
+    g.rounds = ceil_div(a.rows, kSlice) > kRound;
     g.groups = p.groups;
     g.bias_grad = grad_bias;
     g.partial = sums;
