@@ -752,16 +752,19 @@ __global__ void __launch_bounds__(256)
 // A (rows x columns) matrix as planes of rows of `pitch` elements (a multiple
 // of 8): float32 as three of bfloat16, each cutting off the next eight bits of
 // the fraction, half types copied.  Reads once, writes once.
-constexpr int kPlaneRows = 8;
+constexpr int kPlaneThreads = 256;
 
+// 2^lanes threads a row (of 8 elements each, at most 32), so that narrow rows
+// leave none idle.
 template <typename T, typename Plane>
-__global__ void __launch_bounds__(32 * kPlaneRows)
-    k_planes(const T* __restrict__ x, int64_t rows, int columns, int pitch, bool vectors,
-             Plane* __restrict__ out) {
-    const int c = (blockIdx.x * 32 + threadIdx.x) * 8;
+__global__ void __launch_bounds__(kPlaneThreads)
+    k_planes(const T* __restrict__ x, int64_t rows, int columns, int pitch, int lanes,
+             bool vectors, Plane* __restrict__ out) {
+    const int c = (blockIdx.x * 32 + (threadIdx.x & ((1 << lanes) - 1))) * 8;
+    const int height = kPlaneThreads >> lanes;
     if (c >= columns) return;
-    for (int64_t r = (int64_t)blockIdx.y * kPlaneRows + threadIdx.y; r < rows;
-         r += (int64_t)gridDim.y * kPlaneRows) {
+    for (int64_t r = (int64_t)blockIdx.y * height + (threadIdx.x >> lanes); r < rows;
+         r += (int64_t)gridDim.y * height) {
         const T* from = x + r * columns + c;
         __align__(16) T v[8];
         if (vectors && c + 8 <= columns) {
@@ -845,14 +848,15 @@ Planes prepare(int dtype, const void* x, int64_t rows, int columns, char** works
     const int pitch = (int)ceil_div(columns, 8) * 8, count = dtype == GS_F32 ? 3 : 1;
     void* out = *workspace;
     *workspace += plane_bytes(dtype, rows, columns);
+    int lanes = 0;
+    while (lanes < 5 && (8 << lanes) < columns) ++lanes;
     const dim3 grid((unsigned)ceil_div(columns, 256),
-                    (unsigned)std::min<int64_t>(ceil_div(rows, kPlaneRows), 152 * 64));
-    const dim3 block(32, kPlaneRows);
+                    (unsigned)std::min<int64_t>(ceil_div(rows, kPlaneThreads >> lanes), 152 * 64));
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         using Plane = typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type;
-        k_planes<T, Plane><<<grid, block, 0, s>>>(
-            static_cast<const T*>(x), rows, columns, pitch,
+        k_planes<T, Plane><<<grid, kPlaneThreads, 0, s>>>(
+            static_cast<const T*>(x), rows, columns, pitch, lanes,
             aligned16(x) && columns * sizeof(T) % 16 == 0, static_cast<Plane*>(out));
     });
     return Planes{out, rows, columns, pitch, count};
@@ -956,7 +960,8 @@ GradPlan grad_plan(const LinearArgs& a) {
     // better, but each leaves partial sums (two tiles an item, written and
     // read).  The least time by this estimate of a unit's walk: 0.35 us a
     // slice (of each of a float32 product's six sums), 2 us for an expert's
-    // part to come out, and the sums at 5 TB/s.  16 experts of 8192 rows, 1024
+    // part to come out, and the sums at 5 TB/s (where experts are longer than a
+    // slice, so that a cut falls inside one).  16 experts of 8192 rows, 1024
     // x 512: 9 shares measured 131 us and 18 us of sums, 19 shares 169 and 24.
     const double slices = a.rows / (double)kSlice + 0.5 * a.experts;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>((int64_t)slices, 2 * units));
@@ -965,7 +970,8 @@ GradPlan grad_plan(const LinearArgs& a) {
         const int64_t items = g * p.tiles;
         const double walk = slices / g * 0.35 * (a.dtype == GS_F32 ? 6 : 1) +
                             2.0 * (a.experts / (double)g + 1);
-        const double sums = g > 1 ? 3.0 + 16.0 * items * p.high * p.wide / 5e6 : 0.0;
+        const double inside = std::max(0.0, 1.0 - a.experts / slices);
+        const double sums = g > 1 ? 3.0 + inside * 16.0 * items * p.high * p.wide / 5e6 : 0.0;
         const double time = walk * ceil_div(items, units) + sums;
         if (g == 1 || time < best) {
             best = time;
@@ -1030,6 +1036,7 @@ int with_types(int dtype, F&& f) {
 
 size_t linear_fwd_workspace(const LinearArgs& a, const void* xs, const void* weight) {
     size_t n = 0;
+    if (few_rows(a)) return n;
     if (!copyable(a.dtype, xs, a.in)) n += plane_bytes(a.dtype, a.rows, a.in);
     if (!copyable(a.dtype, weight, a.in))
         n += plane_bytes(a.dtype, (int64_t)a.experts * a.out, a.in);
@@ -1038,6 +1045,10 @@ size_t linear_fwd_workspace(const LinearArgs& a, const void* xs, const void* wei
 
 int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
                       void* ys, void* workspace, cudaStream_t s) {
+    if (few_rows(a)) {
+        launch_few_fwd(a, xs, weight, bias, ys, s);
+        return GS_OK;
+    }
     const bool pairs = use_pairs(a, a.out);
     char* ws = static_cast<char*>(workspace);
     const Planes pa = prepare(a.dtype, xs, a.rows, a.in, &ws, s);
@@ -1070,7 +1081,7 @@ size_t linear_bwd_workspace(const LinearArgs& a, const void* grad_ys, const void
     size_t n = grad_sums_bytes(a);
     if (!copyable(a.dtype, grad_ys, a.out)) n += plane_bytes(a.dtype, a.rows, a.out);
     if (!copyable(a.dtype, xs, a.in)) n += plane_bytes(a.dtype, a.rows, a.in);
-    if (!copyable(a.dtype, weight, a.in))
+    if (!copyable(a.dtype, weight, a.in) && !few_rows(a))
         n += plane_bytes(a.dtype, (int64_t)a.experts * a.out, a.in);
     return n;
 }
@@ -1081,9 +1092,12 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
     char* ws = static_cast<char*>(workspace);
     float* sums = reinterpret_cast<float*>(ws);
     ws += grad_sums_bytes(a);
-    const Planes gy = prepare(a.dtype, grad_ys, a.rows, a.out, &ws, s);
+    Planes gy{};
+    if (grad_weight || !few_rows(a)) gy = prepare(a.dtype, grad_ys, a.rows, a.out, &ws, s);
     CUtensorMap ma, mb;
-    if (grad_xs) {
+    if (grad_xs && few_rows(a)) {
+        launch_few_dx(a, grad_ys, weight, grad_xs, s);
+    } else if (grad_xs) {
         const bool pairs = use_pairs(a, a.in);
         const Planes w = prepare(a.dtype, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
         if (!make_map(&ma, a.dtype, gy, 0, kHigh) || !make_map(&mb, a.dtype, w, a.experts, kSlice))

@@ -258,96 +258,111 @@ __global__ void __launch_bounds__(kRowThreads)
     zero_rows<Word, kLanes>(xs, words, checked_kept(offsets, a.experts, n, a.d_status), n);
 }
 
-constexpr int kChoices = 4;  // of a token's rows in flight
-
-// y[t] = sum over j of w[t, j] * ys[slots[t, j]], j ascending.
-template <typename T, int kVec, int kLanes, int kItems>
+// y[t] = sum over j of w[t, j] * ys[slots[t, j]], j ascending.  kChoices of a
+// token's rows and kTokens tokens are in flight.
+template <typename T, int kVec, int kLanes, int kItems, int kChoices, int kTokens>
 __global__ void __launch_bounds__(kRowThreads)
     k_combine(RowArgs a, const T* __restrict__ ys, const int32_t* __restrict__ slots,
               const float* __restrict__ weights, T* __restrict__ y, int64_t ldy) {
     constexpr int kGroups = kRowThreads / kLanes;
-    const int64_t n = a.tokens * a.topk;
-    for (int64_t t = (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes; t < a.tokens;
-         t += (int64_t)gridDim.x * kGroups)
+    const int64_t n = a.tokens * a.topk, step = (int64_t)gridDim.x * kGroups;
+    for (int64_t t0 = (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes; t0 < a.tokens;
+         t0 += step * kTokens)
         for (int c0 = threadIdx.x % kLanes * kVec; c0 < a.channels;
              c0 += kLanes * kVec * kItems) {
-            float sum[kItems][kVec] = {};
+            float sum[kTokens][kItems][kVec] = {};
             for (int j0 = 0; j0 < a.topk; j0 += kChoices) {
-                int64_t s[kChoices];
-                float w[kChoices];
-                RawVec<T, kVec> raw[kChoices][kItems];
+                int64_t s[kTokens][kChoices];
+                float w[kTokens][kChoices];
+                RawVec<T, kVec> raw[kTokens][kChoices][kItems];
 #pragma unroll
-                for (int q = 0; q < kChoices; ++q) {
-                    const int64_t p = t * a.topk + j0 + q;
-                    s[q] = j0 + q < a.topk ? checked_slot(slots[p], n, a.d_status) : -1;
-                    w[q] = weights && s[q] >= 0 ? weights[p] : 1.f;
-                }
+                for (int u = 0; u < kTokens; ++u)
 #pragma unroll
-                for (int q = 0; q < kChoices; ++q)
-#pragma unroll
-                    for (int i = 0; i < kItems; ++i) {
-                        const int c = c0 + i * kLanes * kVec;
-                        if (s[q] >= 0 && c < a.channels)
-                            raw[q][i] = load_raw<T, kVec>(ys + s[q] * a.channels + c);
+                    for (int q = 0; q < kChoices; ++q) {
+                        const int64_t t = t0 + u * step, p = t * a.topk + j0 + q;
+                        const bool is = t < a.tokens && j0 + q < a.topk;
+                        s[u][q] = is ? checked_slot(slots[p], n, a.d_status) : -1;
+                        w[u][q] = is && weights ? weights[p] : 1.f;
                     }
 #pragma unroll
-                for (int q = 0; q < kChoices; ++q) {
-                    if (s[q] < 0) continue;
+                for (int u = 0; u < kTokens; ++u)
 #pragma unroll
-                    for (int i = 0; i < kItems; ++i) {
-                        float v[kVec];
-                        unpack<T, kVec>(raw[q][i], v);
+                    for (int q = 0; q < kChoices; ++q)
 #pragma unroll
-                        for (int k = 0; k < kVec; ++k) sum[i][k] += w[q] * v[k];
+                        for (int i = 0; i < kItems; ++i) {
+                            const int c = c0 + i * kLanes * kVec;
+                            if (s[u][q] >= 0 && c < a.channels)
+                                raw[u][q][i] =
+                                    load_raw<T, kVec>(ys + s[u][q] * a.channels + c);
+                        }
+#pragma unroll
+                for (int u = 0; u < kTokens; ++u)
+#pragma unroll
+                    for (int q = 0; q < kChoices; ++q) {
+                        if (s[u][q] < 0) continue;
+#pragma unroll
+                        for (int i = 0; i < kItems; ++i) {
+                            float v[kVec];
+                            unpack<T, kVec>(raw[u][q][i], v);
+#pragma unroll
+                            for (int k = 0; k < kVec; ++k) sum[u][i][k] += w[u][q] * v[k];
+                        }
                     }
-                }
             }
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int c = c0 + i * kLanes * kVec;
-                if (c < a.channels) store_vec<T, kVec>(y + t * ldy + c, sum[i]);
-            }
+            for (int u = 0; u < kTokens; ++u)
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int64_t t = t0 + u * step;
+                    const int c = c0 + i * kLanes * kVec;
+                    if (t < a.tokens && c < a.channels)
+                        store_vec<T, kVec>(y + t * ldy + c, sum[u][i]);
+                }
         }
 }
 
 // Per pair: grad_ys[s] = w grad_y[t] and grad_weights = <grad_y[t], ys[s]>.
 // grad_y[t] is read once for the pairs in flight.
-template <typename T, int kVec, int kLanes, int kItems>
+template <typename T, int kVec, int kLanes, int kItems, int kChoices, int kTokens>
 __global__ void __launch_bounds__(kRowThreads)
     k_combine_bwd(RowArgs a, const T* __restrict__ gy, int64_t ldgy, const T* __restrict__ ys,
                   const int32_t* __restrict__ slots, const float* __restrict__ weights,
                   const int32_t* __restrict__ offsets, T* __restrict__ gys,
                   float* __restrict__ gw) {
-    constexpr int kGroups = kRowThreads / kLanes;
+    constexpr int kGroups = kRowThreads / kLanes, kPairs = kTokens * kChoices;
     __shared__ RowScratch scratch;
     int half = 0;
-    const int64_t n = a.tokens * a.topk;
+    const int64_t n = a.tokens * a.topk, step = (int64_t)gridDim.x * kGroups;
     const int at = threadIdx.x % kLanes;
     // whole rounds: the lanes of a row stay together for its sums
-    for (int64_t t0 = (int64_t)blockIdx.x * kGroups; t0 < a.tokens;
-         t0 += (int64_t)gridDim.x * kGroups) {
-        const int64_t t = t0 + threadIdx.x / kLanes;
+    for (int64_t b0 = (int64_t)blockIdx.x * kGroups; b0 < a.tokens; b0 += step * kTokens) {
+        const int64_t t0 = b0 + threadIdx.x / kLanes;
         for (int j0 = 0; j0 < a.topk; j0 += kChoices) {
-            int64_t s[kChoices];
-            float w[kChoices], dot[kChoices];
+            int64_t s[kPairs];
+            float w[kPairs], dot[kPairs];
 #pragma unroll
-            for (int q = 0; q < kChoices; ++q) {
-                const int64_t p = t * a.topk + j0 + q;
-                s[q] = t < a.tokens && j0 + q < a.topk ? checked_slot(slots[p], n, a.d_status)
-                                                       : -1;
-                w[q] = weights && s[q] >= 0 ? weights[p] : 1.f;
+            for (int q = 0; q < kPairs; ++q) {
+                const int64_t t = t0 + q / kChoices * step;
+                const int j = j0 + q % kChoices;
+                const bool is = t < a.tokens && j < a.topk;
+                s[q] = is ? checked_slot(slots[t * a.topk + j], n, a.d_status) : -1;
+                w[q] = is && weights ? weights[t * a.topk + j] : 1.f;
                 dot[q] = 0.f;
             }
-            for (int c0 = at * kVec; t < a.tokens && c0 < a.channels;
-                 c0 += kLanes * kVec * kItems) {
-                RawVec<T, kVec> rg[kItems], ry[kChoices][kItems];
+            for (int c0 = at * kVec; c0 < a.channels; c0 += kLanes * kVec * kItems) {
+                RawVec<T, kVec> rg[kTokens][kItems], ry[kPairs][kItems];
 #pragma unroll
                 for (int i = 0; i < kItems; ++i) {
                     const int c = c0 + i * kLanes * kVec;
-                    rg[i] = c < a.channels ? load_raw<T, kVec>(gy + t * ldgy + c)
-                                           : RawVec<T, kVec>{};
 #pragma unroll
-                    for (int q = 0; q < kChoices; ++q)
+                    for (int u = 0; u < kTokens; ++u) {
+                        const int64_t t = t0 + u * step;
+                        rg[u][i] = t < a.tokens && c < a.channels
+                                       ? load_raw<T, kVec>(gy + t * ldgy + c)
+                                       : RawVec<T, kVec>{};
+                    }
+#pragma unroll
+                    for (int q = 0; q < kPairs; ++q)
                         ry[q][i] = gw && s[q] >= 0 && c < a.channels
                                        ? load_raw<T, kVec>(ys + s[q] * a.channels + c)
                                        : RawVec<T, kVec>{};
@@ -355,12 +370,11 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
                 for (int i = 0; i < kItems; ++i) {
                     const int c = c0 + i * kLanes * kVec;
-                    float g[kVec];
-                    unpack<T, kVec>(rg[i], g);
 #pragma unroll
-                    for (int q = 0; q < kChoices; ++q) {
+                    for (int q = 0; q < kPairs; ++q) {
                         if (s[q] < 0 || c >= a.channels) continue;
-                        float v[kVec], o[kVec];
+                        float g[kVec], v[kVec], o[kVec];
+                        unpack<T, kVec>(rg[q / kChoices][i], g);
                         unpack<T, kVec>(ry[q][i], v);
 #pragma unroll
                         for (int k = 0; k < kVec; ++k) {
@@ -372,10 +386,13 @@ __global__ void __launch_bounds__(kRowThreads)
                 }
             }
             if (!gw) continue;
-            row_sums<kLanes, kChoices>(dot, scratch, half);
+            row_sums<kLanes, kPairs>(dot, scratch, half);
 #pragma unroll
-            for (int q = 0; q < kChoices; ++q)
-                if (at == q && t < a.tokens && j0 + q < a.topk) gw[t * a.topk + j0 + q] = dot[q];
+            for (int q = 0; q < kPairs; ++q) {
+                const int64_t t = t0 + q / kChoices * step;
+                const int j = j0 + q % kChoices;
+                if (at == q && t < a.tokens && j < a.topk) gw[t * a.topk + j] = dot[q];
+            }
         }
     }
     constexpr int kBytes = kVec * (int)sizeof(T);
@@ -463,8 +480,14 @@ void launch_dispatch(const RowArgs& a, const void* x, int64_t ldx, const int32_t
 
 namespace {
 
-// f(element, form) for rows whose arrays are all readable in 16-byte vectors,
-// or in single elements.
+// Four pairs in flight: kChoices of a token's and kTokens tokens.
+template <int kChoices_>
+struct Flight {
+    static constexpr int kChoices = kChoices_, kTokens = 4 / kChoices_;
+};
+
+// f(element, form, flight) for rows whose arrays are all readable in 16-byte
+// vectors, or in single elements.
 template <typename F>
 void with_rows(const RowArgs& a, std::initializer_list<const void*> arrays, int64_t ld, F&& f) {
     with_dtype(a.dtype, [&](auto t) {
@@ -472,10 +495,18 @@ void with_rows(const RowArgs& a, std::initializer_list<const void*> arrays, int6
         constexpr int kWhole = 16 / (int)sizeof(T);
         bool whole = a.channels % kWhole == 0 && ld % kWhole == 0;
         for (const void* p : arrays) whole = whole && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+        const auto go = [&](auto form) {
+            if (a.topk == 1)
+                f(t, form, Flight<1>{});
+            else if (a.topk == 2)
+                f(t, form, Flight<2>{});
+            else
+                f(t, form, Flight<4>{});
+        };
         if (whole)
-            with_row_form<kWhole>(a.channels / kWhole, [&](auto form) { f(t, form); });
+            with_row_form<kWhole>(a.channels / kWhole, go);
         else
-            with_row_form<1>(a.channels, [&](auto form) { f(t, form); });
+            with_row_form<1>(a.channels, go);
     });
 }
 
@@ -483,10 +514,11 @@ void with_rows(const RowArgs& a, std::initializer_list<const void*> arrays, int6
 
 void launch_combine(const RowArgs& a, const void* ys, const int32_t* slots, const float* weights,
                     void* y, int64_t ldy, cudaStream_t s) {
-    with_rows(a, {ys, y}, ldy, [&](auto t, auto form) {
+    with_rows(a, {ys, y}, ldy, [&](auto t, auto form, auto flight) {
         using T = decltype(t);
         using F = decltype(form);
-        const auto kernel = k_combine<T, F::kVec, F::kLanes, F::kItems>;
+        using P = decltype(flight);
+        const auto kernel = k_combine<T, F::kVec, F::kLanes, F::kItems, P::kChoices, P::kTokens>;
         static const int resident = resident_blocks(kernel, 0);
         kernel<<<row_blocks(a.tokens, kRowThreads / F::kLanes, resident), kRowThreads, 0, s>>>(
             a, static_cast<const T*>(ys), slots, weights, static_cast<T*>(y), ldy);
@@ -496,10 +528,12 @@ void launch_combine(const RowArgs& a, const void* ys, const int32_t* slots, cons
 void launch_combine_bwd(const RowArgs& a, const void* grad_y, int64_t ldgy, const void* ys,
                         const int32_t* slots, const float* weights, const int32_t* offsets,
                         void* grad_ys, float* grad_weights, cudaStream_t s) {
-    with_rows(a, {grad_y, ys, grad_ys}, ldgy, [&](auto t, auto form) {
+    with_rows(a, {grad_y, ys, grad_ys}, ldgy, [&](auto t, auto form, auto flight) {
         using T = decltype(t);
         using F = decltype(form);
-        const auto kernel = k_combine_bwd<T, F::kVec, F::kLanes, F::kItems>;
+        using P = decltype(flight);
+        const auto kernel = k_combine_bwd<T, F::kVec, F::kLanes, F::kItems, P::kChoices,
+                                          P::kTokens>;
         static const int resident = resident_blocks(kernel, 0);
         kernel<<<row_blocks(a.tokens, kRowThreads / F::kLanes, resident), kRowThreads, 0, s>>>(
             a, static_cast<const T*>(grad_y), ldgy, static_cast<const T*>(ys), slots, weights,

@@ -47,13 +47,20 @@ void launch_combine_bwd(const RowArgs& a, const void* grad_y, int64_t ldgy, cons
                         const int32_t* slots, const float* weights, const int32_t* offsets,
                         void* grad_ys, float* grad_weights, cudaStream_t s);
 
-// ---- expert_mma.cu: each returns a gs_status.
+// ---- the experts' products; the launchers of expert_mma.cu return a gs_status
 struct LinearArgs {
     const int32_t* offsets;
     int64_t rows;
     int experts, in, out, dtype;
     int32_t* d_status;
 };
+// ---- expert_few.cu: the products of few rows, bound by reading the weights.
+bool few_rows(const LinearArgs& a);
+void launch_few_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
+                    void* ys, cudaStream_t s);
+void launch_few_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
+                   cudaStream_t s);
+// ---- expert_mma.cu
 size_t linear_fwd_workspace(const LinearArgs& a, const void* xs, const void* weight);
 int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
                       void* ys, void* workspace, cudaStream_t s);
