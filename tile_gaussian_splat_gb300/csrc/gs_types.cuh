@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -151,6 +152,24 @@ int resident_blocks(K kernel, size_t smem) {
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 152;
     return std::max(1, per) * sms;
+}
+
+// f(integral constant): the elements of type T in the widest access of 16, 8,
+// 4 or 2 bytes that divides all the pointers and distances in bytes or-ed
+// together in `all`.
+template <typename T, typename F>
+void with_width(uintptr_t all, F&& f) {
+    constexpr int kSize = (int)sizeof(T);
+    if (all % 16 == 0) return f(std::integral_constant<int, 16 / kSize>{});
+    if (all % 8 == 0) return f(std::integral_constant<int, 8 / kSize>{});
+    if (kSize == 2 && all % 4 == 0) return f(std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 1>{});
+}
+
+// A row pointer and distance, for with_width.
+template <typename T>
+uintptr_t row_bits(const void* p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * sizeof(T));
 }
 
 // Whether rows at distance ld from p can be read in 16-byte vectors.

@@ -358,20 +358,23 @@ __global__ void __launch_bounds__(kSumThreads)
 template <typename T, int kVec, typename F>
 void with_form(int channels, F&& f) {
     const int n = (channels + kVec - 1) / kVec;
-    if constexpr (kVec == 1) {
-        if (n <= 32) return f(Form<1, 8, 4, 4>{});
-        if (n <= 64) return f(Form<1, 8, 8, 2>{});
-        if (n <= 128) return f(Form<1, 32, 4, 4>{});
-        if (n <= 256) return f(Form<1, 32, 8, 2>{});
-        if (n <= 512) return f(Form<1, 128, 4, 4>{});
-        return f(Form<1, 128, 8, 2>{});
+    if constexpr (kVec <= 2) {
+        if (n <= 32) return f(Form<kVec, 8, 4, 4>{});
+        if (n <= 64) return f(Form<kVec, 8, 8, 2>{});
+        if (n <= 96) return f(Form<kVec, 16, 6, 2>{});
+        if (n <= 128) return f(Form<kVec, 16, 8, 2>{});
+        if (n <= 192) return f(Form<kVec, 32, 6, 2>{});
+        if (n <= 256) return f(Form<kVec, 32, 8, 2>{});
+        if (n <= 512) return f(Form<kVec, 128, 4, 4>{});
+        if constexpr (kVec == 1) return f(Form<1, 128, 8, 2>{});
     } else {
         if (n <= 8) return f(Form<kVec, 8, 1, 4>{});
         if (n <= 16) return f(Form<kVec, 8, 2, 2>{});
         if (n <= 32) return f(Form<kVec, 32, 1, 4>{});
         if (n <= 64) return f(Form<kVec, 32, 2, 2>{});
-        if (n <= 128) return f(Form<kVec, 128, 1, 4>{});
-        if constexpr (kVec * 128 < kRegisterChannels) return f(Form<kVec, 128, 2, 2>{});
+        if constexpr (kVec == 8) return f(Form<8, 128, 1, 4>{});
+        if (n <= 128) return f(Form<kVec, 32, 4, 1>{});
+        return f(Form<kVec, 128, 2, 2>{});
     }
 }
 
@@ -391,7 +394,6 @@ void launch_norm_fwd(const NormArgs& n, const void* bias, float eps, void* y, in
                     n.param_dtype, eps};
     with_dtype(n.dtype, [&](auto t) {
         using T = decltype(t);
-        constexpr int kWhole = 16 / (int)sizeof(T);
         if (n.channels > kRegisterChannels) {
             k_norm_fwd_long<T><<<blocks_for(n.rows, 1, 152 * 8), kLongThreads, 0, s>>>(a);
             return;
@@ -403,10 +405,9 @@ void launch_norm_fwd(const NormArgs& n, const void* bias, float eps, void* y, in
             static const int resident = resident_blocks(kernel, 0);
             kernel<<<blocks_for(n.rows, groups, resident), kNormThreads, 0, s>>>(a);
         };
-        if (n.channels % kWhole == 0 && rows_aligned<T>(n.x, n.ldx) && rows_aligned<T>(y, ldy))
-            with_form<T, kWhole>(n.channels, go);
-        else
-            with_form<T, 1>(n.channels, go);
+        with_width<T>(row_bits<T>(n.x, n.ldx) | row_bits<T>(y, ldy) |
+                          (uintptr_t)(n.channels * sizeof(T)),
+                      [&](auto width) { with_form<T, decltype(width)::value>(n.channels, go); });
     });
 }
 
@@ -419,7 +420,6 @@ void launch_norm_bwd(const NormArgs& n, const void* grad_y, int64_t ldgy, const 
     int slices = 0;
     if (n.rows > 0) with_dtype(n.dtype, [&](auto t) {
         using T = decltype(t);
-        constexpr int kWhole = 16 / (int)sizeof(T);
         if (n.channels > kRegisterChannels) {
             if (grad_x)
                 k_norm_bwd_long<T><<<blocks_for(n.rows, 1, 152 * 8), kLongThreads, 0, s>>>(a);
@@ -442,11 +442,10 @@ void launch_norm_bwd(const NormArgs& n, const void* grad_y, int64_t ldgy, const 
                                 std::min(norm_bwd_slices(n.rows, n.channels), resident));
             kernel<<<slices, kNormThreads, smem, s>>>(a);
         };
-        if (n.channels % kWhole == 0 && rows_aligned<T>(n.x, n.ldx) &&
-            rows_aligned<T>(grad_y, ldgy) && (!grad_x || rows_aligned<T>(grad_x, ldgx)))
-            with_form<T, kWhole>(n.channels, go);
-        else
-            with_form<T, 1>(n.channels, go);
+        with_width<T>(row_bits<T>(n.x, n.ldx) | row_bits<T>(grad_y, ldgy) |
+                          (grad_x ? row_bits<T>(grad_x, ldgx) : 0) |
+                          (uintptr_t)(n.channels * sizeof(T)),
+                      [&](auto width) { with_form<T, decltype(width)::value>(n.channels, go); });
     });
     if (params)
         k_norm_params_sum<<<dim3((n.channels + 31) / 32, 2), kSumThreads, 0, s>>>(
