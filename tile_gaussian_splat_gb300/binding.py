@@ -720,11 +720,6 @@ def _linear_shapes(xs, offsets, weight):
     return E, i, o
 
 
-def _aligned(*tensors):
-    """Whether every one of the tensors begins on a 16-byte boundary."""
-    return int(all(t.data_ptr() % 16 == 0 for t in tensors))
-
-
 def gs_expert_linear_fwd(xs, offsets, weight, bias=None, d_status=None, out=None, workspace=None,
                          stream=None):
     """Every expert's product over its sorted rows: xs (rows, in_features),
@@ -739,7 +734,8 @@ def gs_expert_linear_fwd(xs, offsets, weight, bias=None, d_status=None, out=None
     ys = _new((R, o), xs.dtype, xs, stream) if out is None else \
         _same(out, (R, o), xs.dtype, "out")
     L = lib()
-    n_bytes = L.gs_expert_linear_fwd_workspace_size(R, E, i, o, dt, _aligned(xs, weight))
+    aligned = (xs.data_ptr() | weight.data_ptr()) % 16 == 0
+    n_bytes = L.gs_expert_linear_fwd_workspace_size(R, E, i, o, dt, aligned)
     ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
     _check(L.gs_expert_linear_fwd(_ptr(xs), _ptr(offsets), _ptr(weight), _ptr(bias), R, E, i, o,
                                   dt, _ptr(ys), _ptr(ws), n_bytes, _ptr(d_status),
@@ -759,8 +755,8 @@ def gs_expert_linear_bwd(grad_ys, xs, offsets, weight, bias=True, input=True, d_
     gw = _new((E, o, i), xs.dtype, xs, stream)
     gb = _new((E, o), xs.dtype, xs, stream) if bias else None
     L = lib()
-    n_bytes = L.gs_expert_linear_bwd_workspace_size(R, E, i, o, dt,
-                                                    _aligned(grad_ys, xs, weight))
+    aligned = (grad_ys.data_ptr() | xs.data_ptr() | weight.data_ptr()) % 16 == 0
+    n_bytes = L.gs_expert_linear_bwd_workspace_size(R, E, i, o, dt, aligned)
     ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
     _check(L.gs_expert_linear_bwd(_ptr(grad_ys), _ptr(xs), _ptr(offsets), _ptr(weight), R, E, i,
                                   o, dt, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), n_bytes,

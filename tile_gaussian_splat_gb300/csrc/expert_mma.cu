@@ -87,7 +87,7 @@ template <int kBlocks, int kWide>
 struct Shape {
     static constexpr int kTileHigh = kHigh * kBlocks;
     static constexpr int kBytesA = kHigh * kSlice * 2;
-    static constexpr int kPartB = kWide / kBlocks;  // columns of B a block holds
+    static constexpr int kPartB = kWide / kBlocks;  // columns of B a block holds, at most
     static constexpr int kBytesB = kPartB * kSlice * 2;
     static constexpr int kStageBytes = kBytesA + kBytesB;
     static constexpr int kStages = kStageBytes > 32768 ? 4 : 6;
@@ -152,6 +152,14 @@ struct Tile {
 
 __device__ __forceinline__ int64_t share_begin(int64_t total, int groups, int group) {
     return total * group / groups;
+}
+
+// Columns of a tile from n0 on that are computed: those inside the output, in
+// the matrix instruction's steps.
+template <int kBlocks, int kWide>
+__device__ __forceinline__ int tile_columns(int width, int n0) {
+    constexpr int kStep = 16 * kBlocks;
+    return min(kWide, (width - n0 + kStep - 1) / kStep * kStep);
 }
 
 // The tiles of one pair of blocks (or block), in order; every warp of it walks
@@ -358,7 +366,8 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
         Ring<S::kStages> at;
         bool ok = true;
         while (ok && walk.next(c)) {
-            const int n0 = c.n0 + rank * S::kPartB;
+            const int n0 =
+                c.n0 + rank * (tile_columns<kBlocks, kWide>(g.width, c.n0) / kBlocks);
             int sum = c.q0 / c.count, k = c.q0 % c.count;
             for (int q = c.q0; q < c.q1; ++q, at.advance()) {
                 const int row_a = plane_a(g.pairs, sum) * (int)g.rows + c.row0;
@@ -410,8 +419,8 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                 if (turn != ~0u) mbar_wait_limited(&bars.full[i], turn & 1, &none);
             }
     } else if (warp == 1) {
-        constexpr uint32_t word = mma_word(S::kTileHigh, kWide,
-                                           std::is_same<T, __nv_bfloat16>::value, kMnA, kMnB);
+        constexpr uint32_t word0 =
+            mma_word(S::kTileHigh, 0, std::is_same<T, __nv_bfloat16>::value, kMnA, kMnB);
         const uint64_t from_a =
             kMnA ? smem_operand(base, 64 * 128, 1024) : smem_operand(base, 16, 1024);
         const uint64_t from_b = kMnB ? smem_operand(base + S::kBytesA, 64 * 128, 1024)
@@ -424,6 +433,8 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
             if (acc.turn > 0) ok = warp_wait(&bars.acc_empty[acc.stage], (acc.turn + 1) & 1, abort);
             tmem_fence_after();
             const uint32_t d = tmem + acc.stage * kWide;
+            const uint32_t word =
+                word0 | (uint32_t)(tile_columns<kBlocks, kWide>(g.width, c.n0) >> 3) << 17;
             int k = kProduct == kWeightGrad ? c.q0 % c.count : 0;
             for (int q = c.q0; q < c.q1 && ok; ++q, at.advance()) {
                 ok = warp_wait(&bars.full[at.stage], at.turn & 1, abort);
@@ -754,49 +765,61 @@ __global__ void __launch_bounds__(256)
 // the fraction, half types copied.  Reads once, writes once.
 constexpr int kPlaneThreads = 256;
 
-// 2^lanes threads a row (of 8 elements each, at most 32), so that narrow rows
-// leave none idle.
-template <typename T, typename Plane>
+// a = a0 + a1 + a2, the top eight bits of the fraction first.
+__device__ __forceinline__ void split3(float a, uint16_t* p) {
+    const uint32_t a0 = __float_as_uint(a) & 0xffff0000u;
+    // an infinity or NaN is all in the first plane
+    const bool finite = (a0 & 0x7f800000u) != 0x7f800000u;
+    const float r1 = finite ? a - __uint_as_float(a0) : 0.f;
+    const uint32_t a1 = __float_as_uint(r1) & 0xffff0000u;
+    const uint32_t a2 = __float_as_uint(r1 - __uint_as_float(a1));
+    // a NaN whose upper half alone would read as an infinity stays one
+    p[0] = (uint16_t)(a0 >> 16 | (a != a ? 0x40u : 0u));
+    p[1] = (uint16_t)(a1 >> 16);
+    p[2] = (uint16_t)(a2 >> 16);
+}
+
+// 2^lanes threads a row, at most 32, of eight elements each (four 2^lanes
+// apart where rows are not whole vectors, so that reads are contiguous, took
+// 19 us where this takes 15: three planes of 2-byte writes).
+template <typename T, typename Plane, bool kVectors>
 __global__ void __launch_bounds__(kPlaneThreads)
     k_planes(const T* __restrict__ x, int64_t rows, int columns, int pitch, int lanes,
-             bool vectors, Plane* __restrict__ out) {
-    const int c = (blockIdx.x * 32 + (threadIdx.x & ((1 << lanes) - 1))) * 8;
-    const int height = kPlaneThreads >> lanes;
-    if (c >= columns) return;
+             Plane* __restrict__ out) {
+    constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1, kEach = 8;
+    const int at = threadIdx.x & ((1 << lanes) - 1), height = kPlaneThreads >> lanes;
+    const int c0 = (blockIdx.x * 32 + at) * kEach;
+    if (c0 >= pitch) return;
+    const int64_t plane = rows * pitch;
     for (int64_t r = (int64_t)blockIdx.y * height + (threadIdx.x >> lanes); r < rows;
          r += (int64_t)gridDim.y * height) {
-        const T* from = x + r * columns + c;
-        __align__(16) T v[8];
-        if (vectors && c + 8 <= columns) {
+        const T* from = x + r * columns + c0;
+        uint16_t* to = reinterpret_cast<uint16_t*>(out) + r * pitch + c0;
+        __align__(16) T v[kEach];
+        if constexpr (kVectors) {
 #pragma unroll
             for (int i = 0; i < (int)sizeof(T) / 2; ++i)
                 reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(from)[i];
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = c + i < columns ? from[i] : from_f<T>(0.f);
+            for (int i = 0; i < kEach; ++i)
+                v[i] = c0 + i < columns ? from[i] : from_f<T>(0.f);
         }
-        if constexpr (sizeof(T) == 4) {
-            __align__(16) uint16_t p[3][8];
+        __align__(16) uint16_t p[kPlanes][kEach];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t a0 = __float_as_uint(v[i]) & 0xffff0000u;
-                // an infinity or NaN is all in the first plane
-                const bool finite = (a0 & 0x7f800000u) != 0x7f800000u;
-                const float r1 = finite ? v[i] - __uint_as_float(a0) : 0.f;
-                const uint32_t a1 = __float_as_uint(r1) & 0xffff0000u;
-                const uint32_t a2 = __float_as_uint(r1 - __uint_as_float(a1));
-                // a NaN whose upper half alone would read as an infinity stays one
-                p[0][i] = (uint16_t)(a0 >> 16 | (v[i] != v[i] ? 0x40u : 0u));
-                p[1][i] = (uint16_t)(a1 >> 16);
-                p[2][i] = (uint16_t)(a2 >> 16);
+        for (int i = 0; i < kEach; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                uint16_t part[3];
+                split3(v[i], part);
+#pragma unroll
+                for (int k = 0; k < kPlanes; ++k) p[k][i] = part[k];
+            } else {
+                p[0][i] = *reinterpret_cast<const uint16_t*>(&v[i]);
             }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<uint4*>(out + ((int64_t)k * rows + r) * pitch + c) =
-                    *reinterpret_cast<const uint4*>(p[k]);
-        } else {
-            *reinterpret_cast<uint4*>(out + r * pitch + c) = *reinterpret_cast<const uint4*>(v);
         }
+#pragma unroll
+        for (int k = 0; k < kPlanes; ++k)
+            *reinterpret_cast<uint4*>(to + k * plane) = *reinterpret_cast<const uint4*>(p[k]);
     }
 }
 
@@ -848,16 +871,23 @@ Planes prepare(int dtype, const void* x, int64_t rows, int columns, char** works
     const int pitch = (int)ceil_div(columns, 8) * 8, count = dtype == GS_F32 ? 3 : 1;
     void* out = *workspace;
     *workspace += plane_bytes(dtype, rows, columns);
+    // whole vectors of 8 elements, so that the last is whole too
+    const bool vectors = aligned16(x) && columns % 8 == 0;
     int lanes = 0;
-    while (lanes < 5 && (8 << lanes) < columns) ++lanes;
-    const dim3 grid((unsigned)ceil_div(columns, 256),
+    while (lanes < 5 && (8 << lanes) < pitch) ++lanes;
+    const dim3 grid((unsigned)ceil_div(pitch, 256),
                     (unsigned)std::min<int64_t>(ceil_div(rows, kPlaneThreads >> lanes), 152 * 64));
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         using Plane = typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type;
-        k_planes<T, Plane><<<grid, kPlaneThreads, 0, s>>>(
-            static_cast<const T*>(x), rows, columns, pitch, lanes,
-            aligned16(x) && columns * sizeof(T) % 16 == 0, static_cast<Plane*>(out));
+        const T* from = static_cast<const T*>(x);
+        Plane* to = static_cast<Plane*>(out);
+        if (vectors)
+            k_planes<T, Plane, true>
+                <<<grid, kPlaneThreads, 0, s>>>(from, rows, columns, pitch, lanes, to);
+        else
+            k_planes<T, Plane, false>
+                <<<grid, kPlaneThreads, 0, s>>>(from, rows, columns, pitch, lanes, to);
     });
     return Planes{out, rows, columns, pitch, count};
 }
@@ -921,10 +951,22 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int
     return cudaLaunchKernelEx(&config, kernel, a, b, g) == cudaSuccess ? GS_OK : GS_ERR_CUDA;
 }
 
-// Two blocks a tile of 256 x 256 where the output is wide enough and the
-// experts have rows enough on average to fill 256 of them.
-bool use_pairs(const LinearArgs& a, int width) {
-    return width > 128 && a.rows >= (int64_t)256 * a.experts;
+// Whether to use two blocks a tile of 256 x 256, or one a tile of 128 x 256:
+// the less time by this estimate of a unit's walk.  A slice of 256 columns
+// takes two blocks 0.28 us and one 0.36 (bound by its copies), a tile 1.5 us
+// to come out; the last tile of every expert is half full.  (20014 rows of 6
+// experts, 131 wide, make 82 tiles for the 76 pairs and 160 for the 152
+// blocks: 27 us and 19.)
+bool use_pairs(const LinearArgs& a, int width, int depth) {
+    if (width <= 128) return false;
+    const double slices = (double)ceil_div(depth, kSlice) * (a.dtype == GS_F32 ? 6 : 1);
+    const double part = std::min(width, 256) / 256.0;
+    const auto time = [&](int high, int units, double slice) {
+        const int64_t tiles = (a.rows / high + (a.experts + 1) / 2) * ceil_div(width, 256);
+        return ceil_div(tiles, units) * (slices * slice * part + 1.5);
+    };
+    const int sms = sm_count();
+    return time(256, sms / 2, 0.28) < time(128, sms, 0.36);
 }
 
 // Columns of B in one box of a tiled copy.
@@ -1049,7 +1091,7 @@ int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, c
         launch_few_fwd(a, xs, weight, bias, ys, s);
         return GS_OK;
     }
-    const bool pairs = use_pairs(a, a.out);
+    const bool pairs = use_pairs(a, a.out, a.in);
     char* ws = static_cast<char*>(workspace);
     const Planes pa = prepare(a.dtype, xs, a.rows, a.in, &ws, s);
     const Planes pb = prepare(a.dtype, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
@@ -1098,7 +1140,7 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
     if (grad_xs && few_rows(a)) {
         launch_few_dx(a, grad_ys, weight, grad_xs, s);
     } else if (grad_xs) {
-        const bool pairs = use_pairs(a, a.in);
+        const bool pairs = use_pairs(a, a.in, a.out);
         const Planes w = prepare(a.dtype, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
         if (!make_map(&ma, a.dtype, gy, 0, kHigh) || !make_map(&mb, a.dtype, w, a.experts, kSlice))
             return GS_ERR_CUDA;

@@ -14,10 +14,10 @@ namespace {
 
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxUnits = 152 * 16;
+constexpr int kMaxUnits = 152 * 32;
 constexpr int kScanThreads = 256;
 constexpr int kSmallSort = 4096;  // most pairs of the one-block sort
-constexpr int kAhead = 4;  // groups of 32 ids a warp has in flight
+constexpr int kAhead = 8;  // groups of 32 ids a warp has in flight
 
 // Range of pairs of one unit (a warp): whole groups of 32.
 __device__ __forceinline__ void unit_range(int64_t n, int units, int unit, int64_t* i0,
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kSortThreads)
     place_unit(ids, i0, i1, experts, own, order, slots);
 }
 
-// counts[unit][e] = pairs of expert e in the unit's range.
+// counts[e][unit] = pairs of expert e in the unit's range.
 __global__ void __launch_bounds__(kSortThreads)
     k_expert_count(const int32_t* __restrict__ ids, int64_t n, int experts, int units,
                    int32_t* __restrict__ counts) {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kSortThreads)
     unit_range(n, units, unit, &i0, &i1);
     count_unit(ids, i0, i1, experts, own);
     for (int e = threadIdx.x & 31; e < experts; e += 32)
-        counts[(int64_t)unit * experts + e] = own[e];
+        counts[(int64_t)e * units + unit] = own[e];
 }
 
 // Exclusive prefix over the units of one expert's counts (block e), in place,
@@ -159,14 +159,14 @@ __global__ void __launch_bounds__(kScanThreads)
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int u = t * kEach + i;
-        c[i] = u < units ? counts[(int64_t)u * experts + e] : 0;
+        c[i] = u < units ? counts[(int64_t)e * units + u] : 0;
         sum += c[i];
     }
     int32_t run = (int32_t)block_exclusive_scan<kScanThreads>(sum, scratch, &total);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int u = t * kEach + i;
-        if (u < units) counts[(int64_t)u * experts + e] = run;
+        if (u < units) counts[(int64_t)e * units + u] = run;
         run += c[i];
     }
     if (t == 0) totals[e] = (int32_t)total;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kSortThreads)
     if (unit >= units) return;
     int32_t* own = sm + threadIdx.x / 32 * experts;
     for (int e = threadIdx.x & 31; e < experts; e += 32)
-        own[e] = first[e] + counts[(int64_t)unit * experts + e];
+        own[e] = first[e] + counts[(int64_t)e * units + unit];
     int64_t i0, i1;
     unit_range(n, units, unit, &i0, &i1);
     place_unit(ids, i0, i1, experts, own, order, slots);

@@ -224,6 +224,7 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, u
 }
 
 // Instruction word of kind::f16 with float32 accumulators.
+// columns: a multiple of 16 (of 32 with two blocks).
 __device__ __forceinline__ constexpr uint32_t mma_word(int rows, int columns, bool bf16,
                                                        bool a_mn, bool b_mn) {
     return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (a_mn ? 1u << 15 : 0u) |
