@@ -16,7 +16,8 @@ SHAPES = [
     (128, 1, 2, 64, 64, [1]), (127, 2, 5, 131, 259, None), (300, 3, 6, 264, 72, [0, 3, 5]),
     (700, 2, 4, 512, 384, None), (1000, 2, 16, 128, 520, None), (2500, 2, 3, 200, 136, None),
     (900, 1, 64, 96, 48, None), (4000, 2, 2, 256, 256, [1]), (60, 2, 1024, 24, 16, None),
-    (1500, 2, 4, 1032, 40, None), (513, 1, 1, 33, 513, None)]
+    (1500, 2, 4, 1032, 40, None), (513, 1, 1, 33, 513, None),
+    (10000, 2, 3, 136, 520, None), (9000, 2, 5, 512, 384, None), (9001, 2, 7, 385, 640, [1, 4, 6])]
 
 
 def _inputs(g, n, experts, i, o, dtype):
