@@ -16,7 +16,9 @@ namespace {
 constexpr int kFewRows = 8;       // rows that share one reading of the weights
 constexpr int kFewThreads = 128;  // four warps
 constexpr int kFewColumns = 4;    // forward: columns of a warp
-constexpr int kFewDepth = 1024;   // terms staged at a time
+constexpr int kFewDepth = 1024;   // forward: terms staged at a time
+constexpr int kDxThreads = 512;   // input gradient: sixteen warps share the sum over out
+constexpr int kDxDepth = 512;
 
 // The rows of piece `piece` (at most kFewRows of one expert); false beyond the
 // last piece.  Every thread of the block calls it.
@@ -39,8 +41,8 @@ __device__ __forceinline__ bool few_piece(const LinearArgs& g, int32_t* begin, i
 template <typename T>
 __device__ __forceinline__ void zero_tail(T* out, int64_t kept, int64_t rows, int width) {
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    const int64_t stride = (int64_t)gridDim.x * gridDim.y * kFewThreads;
-    for (int64_t i = kept * width + block * kFewThreads + threadIdx.x; i < rows * width;
+    const int64_t stride = (int64_t)gridDim.x * gridDim.y * blockDim.x;
+    for (int64_t i = kept * width + block * blockDim.x + threadIdx.x; i < rows * width;
          i += stride)
         out[i] = from_f<T>(0.f);
 }
@@ -115,14 +117,15 @@ __global__ void __launch_bounds__(kFewThreads)
 }
 
 // grad_xs[r, k] = sum over n of grad_ys[r, n] weight[n, k]: a lane takes kVec
-// columns, the block's warps every fourth n; their sums meet in shared memory.
+// columns, the block's warps every sixteenth n; their sums meet in shared
+// memory.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(kDxThreads)
     k_few_dx(LinearArgs g, const T* __restrict__ gys, const T* __restrict__ weight,
              T* __restrict__ gxs) {
     extern __shared__ int32_t begin[];
-    constexpr int kWarps = kFewThreads / 32;
-    __shared__ __align__(16) float a[kFewDepth][kFewRows];
+    constexpr int kWarps = kDxThreads / 32;
+    __shared__ __align__(16) float a[kDxDepth][kFewRows];
     __shared__ float part[kWarps][32 * kVec];
     int e, row0, rows, kept;
     const bool any = few_piece(g, begin, blockIdx.y, &e, &row0, &rows, &kept);
@@ -132,16 +135,16 @@ __global__ void __launch_bounds__(kFewThreads)
     const int k0 = (blockIdx.x * 32 + lane) * kVec;
     const bool in = k0 < g.in;
     float sum[kFewRows][kVec] = {};
-    for (int n0 = 0; n0 < g.out; n0 += kFewDepth) {
-        const int depth = min(kFewDepth, g.out - n0);
+    for (int n0 = 0; n0 < g.out; n0 += kDxDepth) {
+        const int depth = min(kDxDepth, g.out - n0);
         if (n0 > 0) __syncthreads();
         for (int r = 0; r < kFewRows; ++r)
-            for (int n = threadIdx.x; n < depth; n += kFewThreads)
+            for (int n = threadIdx.x; n < depth; n += kDxThreads)
                 a[n][r] = r < rows ? to_f(gys[(int64_t)(row0 + r) * g.out + n0 + n]) : 0.f;
         __syncthreads();
         const T* w = weight + ((int64_t)e * g.out + n0) * g.in + k0;
         if (in) {
-#pragma unroll 4
+#pragma unroll 8
             for (int n = warp; n < depth; n += kWarps) {
                 float v[kVec];
                 unpack<T, kVec>(load_raw<T, kVec>(w + (int64_t)n * g.in), v);
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
         for (int i = 0; i < kVec; ++i) part[warp][i * 32 + lane] = sum[r][i];
         __syncthreads();
-        for (int i = threadIdx.x; i < 32 * kVec; i += kFewThreads) {
+        for (int i = threadIdx.x; i < 32 * kVec; i += kDxThreads) {
             float v = 0.f;
 #pragma unroll
             for (int q = 0; q < kWarps; ++q) v += part[q][i];
@@ -179,8 +182,14 @@ unsigned few_pieces(const LinearArgs& a) {
 
 }  // namespace
 
-// Up to eight rows an expert on average, or eight in all.
-bool few_rows(const LinearArgs& a) { return a.rows <= 8 * (int64_t)a.experts && a.rows <= 256; }
+// Where the tensor cores take the weights as they lie, up to sixteen rows in
+// all (8 experts of 512 x 512 bf16: 3.8 us against 7.8 for 16 rows, 7.9 and
+// 7.8 for 64).  Where they would first be rewritten, sixteen an expert on
+// average (32 experts of 512 x 512 f32, 512 rows: 29 us and 33; 64 of 1024 x
+// 1024: 118 and 228).
+bool few_rows(const LinearArgs& a, bool as_they_lie) {
+    return as_they_lie ? a.rows <= 16 : a.rows <= 16 * (int64_t)a.experts && a.rows <= 1024;
+}
 
 void launch_few_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
                     void* ys, cudaStream_t s) {
@@ -212,9 +221,9 @@ void launch_few_dx(const LinearArgs& a, const void* grad_ys, const void* weight,
             return dim3((a.in + 32 * vec - 1) / (32 * vec), few_pieces(a));
         };
         if (a.in % kWhole == 0 && rows_aligned<T>(weight, a.in))
-            k_few_dx<T, kWhole><<<grid(kWhole), kFewThreads, smem, s>>>(a, gy, w, gx);
+            k_few_dx<T, kWhole><<<grid(kWhole), kDxThreads, smem, s>>>(a, gy, w, gx);
         else
-            k_few_dx<T, 1><<<grid(1), kFewThreads, smem, s>>>(a, gy, w, gx);
+            k_few_dx<T, 1><<<grid(1), kDxThreads, smem, s>>>(a, gy, w, gx);
     });
 }
 

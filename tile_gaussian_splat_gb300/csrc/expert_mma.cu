@@ -951,22 +951,13 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int
     return cudaLaunchKernelEx(&config, kernel, a, b, g) == cudaSuccess ? GS_OK : GS_ERR_CUDA;
 }
 
-// Whether to use two blocks a tile of 256 x 256, or one a tile of 128 x 256:
-// the less time by this estimate of a unit's walk.  A slice of 256 columns
-// takes two blocks 0.28 us and one 0.36 (bound by its copies), a tile 1.5 us
-// to come out; the last tile of every expert is half full.  (20014 rows of 6
-// experts, 131 wide, make 82 tiles for the 76 pairs and 160 for the 152
-// blocks: 27 us and 19.)
-bool use_pairs(const LinearArgs& a, int width, int depth) {
-    if (width <= 128) return false;
-    const double slices = (double)ceil_div(depth, kSlice) * (a.dtype == GS_F32 ? 6 : 1);
-    const double part = std::min(width, 256) / 256.0;
-    const auto time = [&](int high, int units, double slice) {
-        const int64_t tiles = (a.rows / high + (a.experts + 1) / 2) * ceil_div(width, 256);
-        return ceil_div(tiles, units) * (slices * slice * part + 1.5);
-    };
-    const int sms = sm_count();
-    return time(256, sms / 2, 0.28) < time(128, sms, 0.36);
+// Two blocks a tile of 256 x 256 where those fill every pair of SMs twice, or
+// the product is float32's six; one block a tile of 128 x 256 else.  16
+// experts, 512 -> 1024 bf16: 65536 rows 53 us in pairs and 62 single, 16384
+// 18.6 and 20.3, 8192 12.1 both, 2048 9.1 and 8.1; float32 59 and 62 for 8192.
+bool use_pairs(const LinearArgs& a, int width) {
+    const int64_t tiles = (a.rows / 256 + a.experts / 2) * ceil_div(width, 256);
+    return width > 128 && (a.dtype == GS_F32 || tiles >= sm_count());
 }
 
 // Columns of B in one box of a tiled copy.
@@ -1004,7 +995,7 @@ GradPlan grad_plan(const LinearArgs& a) {
     // slice (of each of a float32 product's six sums), 2 us for an expert's
     // part to come out, and the sums at 5 TB/s (where experts are longer than a
     // slice, so that a cut falls inside one).  16 experts of 8192 rows, 1024
-    // x 512: 9 shares measured 131 us and 18 us of sums, 19 shares 169 and 24.
+    // x 512: 113 us in 9 shares, 130 in 19.
     const double slices = a.rows / (double)kSlice + 0.5 * a.experts;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>((int64_t)slices, 2 * units));
     double best = 0.0;
@@ -1078,7 +1069,7 @@ int with_types(int dtype, F&& f) {
 
 size_t linear_fwd_workspace(const LinearArgs& a, const void* xs, const void* weight) {
     size_t n = 0;
-    if (few_rows(a)) return n;
+    if (few_rows(a, copyable(a.dtype, weight, a.in))) return n;
     if (!copyable(a.dtype, xs, a.in)) n += plane_bytes(a.dtype, a.rows, a.in);
     if (!copyable(a.dtype, weight, a.in))
         n += plane_bytes(a.dtype, (int64_t)a.experts * a.out, a.in);
@@ -1087,11 +1078,11 @@ size_t linear_fwd_workspace(const LinearArgs& a, const void* xs, const void* wei
 
 int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
                       void* ys, void* workspace, cudaStream_t s) {
-    if (few_rows(a)) {
+    if (few_rows(a, copyable(a.dtype, weight, a.in))) {
         launch_few_fwd(a, xs, weight, bias, ys, s);
         return GS_OK;
     }
-    const bool pairs = use_pairs(a, a.out, a.in);
+    const bool pairs = use_pairs(a, a.out);
     char* ws = static_cast<char*>(workspace);
     const Planes pa = prepare(a.dtype, xs, a.rows, a.in, &ws, s);
     const Planes pb = prepare(a.dtype, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
@@ -1110,6 +1101,12 @@ int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, c
 
 namespace {
 
+// The input gradient of few rows: only where the weights would be rewritten
+// (as they lie, the tensor cores were never slower).
+bool few_dx(const LinearArgs& a, const void* weight) {
+    return !copyable(a.dtype, weight, a.in) && few_rows(a, false);
+}
+
 size_t grad_sums_bytes(const LinearArgs& a) {
     const GradPlan p = grad_plan(a);
     const size_t n = (partial_floats(p) + bias_floats(p, a.experts)) * sizeof(float);
@@ -1123,7 +1120,7 @@ size_t linear_bwd_workspace(const LinearArgs& a, const void* grad_ys, const void
     size_t n = grad_sums_bytes(a);
     if (!copyable(a.dtype, grad_ys, a.out)) n += plane_bytes(a.dtype, a.rows, a.out);
     if (!copyable(a.dtype, xs, a.in)) n += plane_bytes(a.dtype, a.rows, a.in);
-    if (!copyable(a.dtype, weight, a.in) && !few_rows(a))
+    if (!copyable(a.dtype, weight, a.in) && !few_dx(a, weight))
         n += plane_bytes(a.dtype, (int64_t)a.experts * a.out, a.in);
     return n;
 }
@@ -1135,12 +1132,12 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
     float* sums = reinterpret_cast<float*>(ws);
     ws += grad_sums_bytes(a);
     Planes gy{};
-    if (grad_weight || !few_rows(a)) gy = prepare(a.dtype, grad_ys, a.rows, a.out, &ws, s);
+    if (grad_weight || !few_dx(a, weight)) gy = prepare(a.dtype, grad_ys, a.rows, a.out, &ws, s);
     CUtensorMap ma, mb;
-    if (grad_xs && few_rows(a)) {
+    if (grad_xs && few_dx(a, weight)) {
         launch_few_dx(a, grad_ys, weight, grad_xs, s);
     } else if (grad_xs) {
-        const bool pairs = use_pairs(a, a.in, a.out);
+        const bool pairs = use_pairs(a, a.in);
         const Planes w = prepare(a.dtype, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
         if (!make_map(&ma, a.dtype, gy, 0, kHigh) || !make_map(&mb, a.dtype, w, a.experts, kSlice))
             return GS_ERR_CUDA;

@@ -55,7 +55,8 @@ struct LinearArgs {
     int32_t* d_status;
 };
 // ---- expert_few.cu: the products of few rows, bound by reading the weights.
-bool few_rows(const LinearArgs& a);
+// as_they_lie: the tensor cores could read the weights in place.
+bool few_rows(const LinearArgs& a, bool as_they_lie);
 void launch_few_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
                     void* ys, cudaStream_t s);
 void launch_few_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
