@@ -16,7 +16,11 @@ constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxUnits = 152 * 32;
 constexpr int kScanThreads = 256;
-constexpr int kSmallSort = 4096;  // most pairs of the one-block sort
+// Most pairs of the one-block sort: 8192 of 16 experts take it 7.8 us and three
+// launches 8.6; 16384 take it 13.0.
+constexpr int kSmallSort = 8192;
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr int kAhead = 8;  // groups of 32 ids a warp has in flight
 
 // Range of pairs of one unit (a warp): whole groups of 32.
@@ -99,23 +103,23 @@ __device__ __forceinline__ void warp_prefix(const int32_t* v, int experts, int32
 }
 
 // The whole sort in one block, for few pairs: one launch in place of three.
-__global__ void __launch_bounds__(kSortThreads)
+__global__ void __launch_bounds__(kSmallThreads)
     k_expert_sort_small(const int32_t* __restrict__ ids, int64_t n, int experts,
                         int32_t* __restrict__ offsets, int32_t* __restrict__ order,
                         int32_t* __restrict__ slots) {
     extern __shared__ int32_t sm[];  // counts [warps][experts], totals, first [experts + 1]
-    int32_t* totals = sm + kSortWarps * experts;
+    int32_t* totals = sm + kSmallWarps * experts;
     int32_t* first = totals + experts;
     const int warp = threadIdx.x / 32;
     int32_t* own = sm + warp * experts;
     int64_t i0, i1;
-    unit_range(n, kSortWarps, warp, &i0, &i1);
+    unit_range(n, kSmallWarps, warp, &i0, &i1);
     count_unit(ids, i0, i1, experts, own);
     __syncthreads();
-    for (int e = threadIdx.x; e < experts; e += kSortThreads) {
+    for (int e = threadIdx.x; e < experts; e += kSmallThreads) {
         int32_t run = 0;
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
+        for (int w = 0; w < kSmallWarps; ++w) {
             const int32_t c = sm[w * experts + e];
             sm[w * experts + e] = run;
             run += c;
@@ -125,8 +129,8 @@ __global__ void __launch_bounds__(kSortThreads)
     __syncthreads();
     if (warp == 0) warp_prefix(totals, experts, first);
     __syncthreads();
-    for (int e = threadIdx.x; e <= experts; e += kSortThreads) offsets[e] = first[e];
-    for (int64_t i = first[experts] + threadIdx.x; i < n; i += kSortThreads) order[i] = -1;
+    for (int e = threadIdx.x; e <= experts; e += kSmallThreads) offsets[e] = first[e];
+    for (int64_t i = first[experts] + threadIdx.x; i < n; i += kSmallThreads) order[i] = -1;
     for (int e = threadIdx.x & 31; e < experts; e += 32) own[e] += first[e];
     place_unit(ids, i0, i1, experts, own, order, slots);
 }
@@ -484,8 +488,13 @@ void launch_expert_sort(const int32_t* ids, int64_t n, int experts, int32_t* off
     const int units = sort_units(n);
     const size_t word = sizeof(int32_t), own = (size_t)kSortWarps * experts * word;
     if (units == 0) {
-        k_expert_sort_small<<<1, kSortThreads, own + (2 * experts + 1) * word, s>>>(
-            ids, n, experts, offsets, order, slots);
+        const auto bytes = [&](int e) { return ((size_t)(kSmallWarps + 2) * e + 1) * word; };
+        static const bool raised =
+            cudaFuncSetAttribute(k_expert_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)bytes(GS_MAX_EXPERTS)) == cudaSuccess;
+        (void)raised;  // a launch that needs it fails without
+        k_expert_sort_small<<<1, kSmallThreads, bytes(experts), s>>>(ids, n, experts, offsets,
+                                                                     order, slots);
         return;
     }
     const int blocks = (units + kSortWarps - 1) / kSortWarps;
