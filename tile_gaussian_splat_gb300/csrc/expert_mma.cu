@@ -14,8 +14,8 @@
 // sums round (1.2e-8 of the result per 16 terms on random data: 3.8e-6 over
 // 5000), so every kRound slices of a0 b0 they are added to a running sum, kept
 // in the other half of tensor memory, and start anew.  (Added to the output
-// itself, that traffic took as long as the products.)  Half-type operands whose rows are not
-// whole 16-byte vectors are copied to rows that are (one plane).
+// itself, that traffic took as long as the products.)  Half-type operands whose
+// rows are not whole 16-byte vectors are copied to rows that are (one plane).
 //
 // Two neighbouring blocks work as one on output tiles of 256 x 256 (each
 // block holds half of the rows of A and of B, so every byte copied into shared
@@ -26,6 +26,9 @@
 // the first block's barrier), one warp of the first block issues the matrix
 // instructions, and eight warps move finished accumulators from tensor memory
 // to the output while the next tile is computed in the other half of it.
+// 16 experts, bf16: 262144 rows, 512 -> 1024, 195 us (1410 TFLOP/s; 147 us
+// without the stores, which is what binds); the input gradient of 131072 rows
+// 85 us (1610 TFLOP/s), their weight gradient 113 us (1215 TFLOP/s).
 //
 // The weight gradient's sums run over an expert's rows, of which there are
 // many for few output tiles.  The rows of all experts, end to end, are cut

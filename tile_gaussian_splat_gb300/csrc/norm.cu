@@ -7,6 +7,9 @@
 // weight and bias are loaded once, the sums of their gradients stay in
 // registers -- and several rows are loaded before the first is used.  Longer
 // rows take one block each and are read again from the cache.
+// Forward, 2073600 rows of 64 of 67 float32 channels: 171 us, 6.3 TB/s (94 % of
+// a copy's rate).  Backward, 921600 x 128 bfloat16: 130 us, 5.5 TB/s, bound by
+// the loads that 12 warps of 161 registers keep in flight.
 #include <algorithm>
 #include <cstdint>
 
@@ -324,29 +327,37 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_params_long(NormBwd a) {
     out[a.channels + c] = sb;
 }
 
-// The slices' partial sums added up: 32 channels of one of the two sums a
-// block, 32 threads a channel (eight took 18 us for 760 slices of 1021
-// channels).
-constexpr int kSumThreads = 1024;
+// The slices' partial sums added up: eight channels of one of the two sums a
+// block, 128 threads a channel, so that a thread meets few slices one after
+// the other (32 threads a channel took 7.5 us for 760 slices of 1021 channels,
+// eight 18 us, these 6.5).
+constexpr int kSumThreads = 1024, kSumChannels = 8;
 
 __global__ void __launch_bounds__(kSumThreads)
     k_norm_params_sum(const float* __restrict__ partial, int slices, int channels,
                       int param_dtype, void* gw, void* gb) {
-    __shared__ float part[32][33];
+    constexpr int kParts = kSumThreads / kSumChannels;
+    __shared__ float part[kSumChannels][kParts + 1];
     void* out = blockIdx.y == 0 ? gw : gb;
     if (!out) return;
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
+    const int c = threadIdx.x % kSumChannels, g = threadIdx.x / kSumChannels;
+    const int channel = blockIdx.x * kSumChannels + c;
     float sum = 0.f;
-    if (c < channels) {
-        const float* p = partial + blockIdx.y * channels + c;
+    if (channel < channels) {
+        const float* p = partial + blockIdx.y * channels + channel;
 #pragma unroll 8
-        for (int i = g; i < slices; i += 32) sum += p[(int64_t)i * 2 * channels];
+        for (int i = g; i < slices; i += kParts) sum += p[(int64_t)i * 2 * channels];
     }
-    part[threadIdx.x % 32][g] = sum;
+    part[c][g] = sum;
     __syncthreads();
-    sum = warp_sum(part[g][threadIdx.x % 32]);
-    const int mine = blockIdx.x * 32 + g;
-    if (threadIdx.x % 32 == 0 && mine < channels) store_any(out, param_dtype, mine, sum);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (warp >= kSumChannels) return;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kParts / 32; ++i) sum += part[warp][i * 32 + lane];
+    sum = warp_sum(sum);
+    const int mine = blockIdx.x * kSumChannels + warp;
+    if (lane == 0 && mine < channels) store_any(out, param_dtype, mine, sum);
 }
 
 // Calls f with the form for rows of `channels` elements.  Few lanes a row
@@ -448,7 +459,8 @@ void launch_norm_bwd(const NormArgs& n, const void* grad_y, int64_t ldgy, const 
                       [&](auto width) { with_form<T, decltype(width)::value>(n.channels, go); });
     });
     if (params)
-        k_norm_params_sum<<<dim3((n.channels + 31) / 32, 2), kSumThreads, 0, s>>>(
+        k_norm_params_sum<<<dim3((n.channels + kSumChannels - 1) / kSumChannels, 2), kSumThreads, 0,
+                            s>>>(
             partial, slices, n.channels, n.param_dtype, grad_weight, grad_bias);
 }
 
