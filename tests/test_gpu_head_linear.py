@@ -59,6 +59,53 @@ def test_no_rows():
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", [5, 600, 30000])
+def test_rows_of_no_expert_only(rows, dtype):
+    """Every pair dropped: zeros whatever the rows hold."""
+    offsets = torch.zeros(4, dtype=torch.int32, device=DEV)
+    nan = lambda *s: torch.full(s, float("nan"), dtype=dtype, device=DEV)
+    w = randn(gen(1), 3, 264, 384, dtype=dtype)
+    ys = gs.gs_expert_linear_fwd(nan(rows, 384), offsets, w, w[:, :, 0].contiguous())
+    assert ys.shape == (rows, 264) and not bool(ys.any())
+    for t in gs.gs_expert_linear_bwd(nan(rows, 264), nan(rows, 384), offsets, w):
+        assert not bool(t.any())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("tokens", [3, 2000])
+def test_captured_in_a_graph(tokens, dtype):
+    """The calls neither synchronise nor allocate on their own: a layer and
+    its backward are captured once and replayed on new inputs."""
+    g = gen(12)
+    ids, offsets, _, _ = routed(12, tokens, 2, 4, 0.1)
+    x, gy = randn(g, tokens, 72, dtype=dtype), randn(g, tokens, 40, dtype=dtype)
+    w = (randn(g, 4, 40, 72) / 72 ** 0.5).to(dtype)
+    p = torch.softmax(randn(g, tokens, 2), 1)
+
+    def layer():
+        n, mean, rstd = gs.gs_layer_norm_fwd(x)
+        off, _, slots = gs.gs_expert_sort(ids, 4)
+        xs = gs.gs_expert_dispatch(n, slots, off)
+        ys = gs.gs_expert_linear_fwd(xs, off, w)
+        y = gs.gs_expert_combine(ys, slots, p)
+        gys, gp = gs.gs_expert_combine_bwd(gy, ys, slots, p, off)
+        gxs, gw, gb = gs.gs_expert_linear_bwd(gys, xs, off, w)
+        gx, _, _ = gs.gs_layer_norm_bwd(gs.gs_expert_combine(gxs, slots), x, None, mean, rstd)
+        return y, gp, gw, gb, gx
+
+    layer()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer()
+    for seed in (1, 2):
+        x.copy_(randn(gen(seed), tokens, 72, dtype=dtype))
+        ids.copy_(routed(seed, tokens, 2, 4, 0.2)[0])
+        graph.replay()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, layer()))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("tokens", [6, 400])
 def test_infinity_and_nan_stay_in_their_rows_and_experts(tokens, dtype):
     g = gen(2)
