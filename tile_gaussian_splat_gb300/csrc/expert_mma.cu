@@ -879,7 +879,7 @@ Planes prepare(int dtype, const void* x, int64_t rows, int columns, char** works
     int lanes = 0;
     while (lanes < 5 && (8 << lanes) < pitch) ++lanes;
     const dim3 grid((unsigned)ceil_div(pitch, 256),
-                    (unsigned)std::min<int64_t>(ceil_div(rows, kPlaneThreads >> lanes), 152 * 64));
+                    (unsigned)std::min<int64_t>(ceil_div(rows, kPlaneThreads >> lanes), 152 * 8));
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         using Plane = typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type;
