@@ -9,7 +9,8 @@ from tile_gaussian_splat_gb300 import binding as gs
 pytestmark = pytest.mark.gpu
 
 SHAPES = [(1, 1), (1, 64), (5, 3), (7, 31), (129, 64), (64, 131), (33, 256), (40, 515),
-          (1000, 1024), (9, 1023), (17, 2050), (6, 5000), (3, 16384), (4099, 24), (2500, 128)]
+          (1000, 1024), (9, 1023), (17, 2050), (6, 5000), (3, 16384), (4099, 24), (2500, 128),
+          (70, 4096), (45, 2047), (31, 1500), (700, 4095), (20, 2048), (9, 3998)]
 
 
 def _params(g, ch, p):
