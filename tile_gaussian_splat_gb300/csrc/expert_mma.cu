@@ -10,12 +10,14 @@
 // float32 operands are first written as three bfloat16 planes, a = a0 + a1 +
 // a2 with eight bits of the fraction each (exact), and a product is six sums,
 // a2 b0 + a0 b2 + a1 b1 + a1 b0 + a0 b1 + a0 b0, small ones first; the terms
-// left out are below 2^-22 of |a b|.  The accumulators cut off where float32
-// sums round (1.2e-8 of the result per 16 terms on random data: 3.8e-6 over
-// 5000), so every kRound slices of a0 b0 they are added to a running sum, kept
-// in the other half of tensor memory, and start anew.  (Added to the output
-// itself, that traffic took as long as the products.)  Half-type operands whose
-// rows are not whole 16-byte vectors are copied to rows that are (one plane).
+// left out are below 2^-22 of |a b|.  Half-type operands whose rows are not
+// whole 16-byte vectors are copied to rows that are (one plane).
+//
+// The accumulators cut off where float32 sums round (1.2e-8 of the result per
+// 16 terms on random data: 3.8e-6 over 5000), always towards zero, so every few
+// slices they are added to a running sum, kept in the other half of tensor
+// memory, and start anew.  (Added to the output itself, that traffic took as
+// long as the products.)
 //
 // Two neighbouring blocks work as one on output tiles of 256 x 256 (each
 // block holds half of the rows of A and of B, so every byte copied into shared
@@ -67,6 +69,15 @@ constexpr int kOutWarps = 8;      // two for each quarter of the tile's rows
 template <int kProduct>
 constexpr int kMmaThreads = 32 * (4 + kOutWarps + (kProduct == kWeightGrad ? 2 : 0));
 constexpr int kAccumulators = 2;
+// Slices summed in an accumulator before they are added to the running sum:
+// of a0 b0 (float32), and of half types over features and over rows.  Over
+// 131072 rows in nine shares, 1024 x 512 bfloat16, 0.39 % of the gradients were
+// not the nearest to the exact sum without rounds (0.05 % of sums in float32),
+// 0.12 % with rounds of 32, 0.064 % of 16 and 0.035 % of 8, in 131, 132, 136
+// and 142 us.  Rounds of 16 cost products over 2048 features 16 % (82 -> 96 us),
+// of 32 nothing there and 7 % over 4096; 32768 positive float16 products came
+// out 1.9e-4 too small on average without rounds and 1.3e-5 with 32.
+constexpr int kRound = 8, kHalfRound = 32, kHalfRowsRound = 16;
 
 struct ProductArgs {
     const int32_t* offsets;
@@ -75,7 +86,8 @@ struct ProductArgs {
     int high, width, depth;  // extents: high of the weight gradient, depth of the others
     int groups;              // weight gradient: shares of the rows
     int pairs;               // sums over plane pairs: 1, or 6 for float32
-    int rounds;              // float32: some sums take several rounds
+    int round;               // slices summed before they are added to the running sum
+    int rounds;              // some sums take several rounds
     int vectors;             // output rows are whole 16-byte vectors
     const void* bias;        // kForward
     void* out;
@@ -118,8 +130,6 @@ constexpr size_t smem_bytes(int experts) {
            sizeof(Bars) +
            2 * sizeof(int32_t) * (size_t)(experts + 1);
 }
-
-constexpr int kRound = 8;  // slices of a0 b0 summed before they are added to the running sum
 
 // Planes of A and B in sum number `sum` of g.pairs, small terms first.
 __device__ __forceinline__ int plane_a(int pairs, int sum) {
@@ -192,7 +202,7 @@ struct Walk {
     __device__ __forceinline__ bool next_round(Tile& c) const {
         const int all = c.count * g.pairs;
         c.q0 = c.q1;
-        c.q1 = g.pairs == 1 ? all : min(all, max(c.q0, all - c.count) + kRound);
+        c.q1 = min(all, max(c.q0, all - c.count) + g.round);
         return c.q0 < all;
     }
 
@@ -363,7 +373,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
     Walk<kProduct, kBlocks, kWide> walk(g, begin, prefix);
     Tile c{};
     // where a running sum takes the second accumulator's place
-    const int accumulators = sizeof(Out) == 4 && g.rounds ? 1 : kAccumulators;
+    const int accumulators = g.rounds ? 1 : kAccumulators;
 
     if (warp == 0) {
         Ring<S::kStages> at;
@@ -543,9 +553,10 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
     } else if (warp >= 4 && warp < 4 + kOutWarps) {
         const int q = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
         constexpr int kSpan = S::kSpan;
-        // half types: the next 32 columns come in while these go out (float32
-        // has six times the products to hide behind and sums to hold)
-        constexpr int kAhead = sizeof(Out) == 4 ? 0 : 1;
+        // half types over features: the next 32 columns come in while these go
+        // out (float32 has six times the products to hide behind, the weight
+        // gradient long sums, and no registers to spare)
+        constexpr int kAhead = sizeof(Out) == 4 || kProduct == kWeightGrad ? 0 : 1;
         float* bias = reinterpret_cast<float*>(staging + S::kStaging) + (warp - 4) * kSpan;
         const int first = (warp - 4) / 4 * kSpan;
         char* mine = staging + (warp - 4) * 32 * 64;
@@ -594,21 +605,18 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                 if (!kAhead) tmem_wait_loads();
                 uint32_t* w = u[b & kAhead];
                 const bool last = c.q1 == c.count * g.pairs;
-                if constexpr (sizeof(Out) == 4) {
-                    const uint32_t sum = from + kWide + b * 32;
-                    if (c.q0 > 0) {
-                        uint32_t was[32];
-                        tmem_load32(sum, was);
-                        tmem_wait_loads();
+                const uint32_t sum = from + kWide + b * 32;
+                if (c.q0 > 0) {
+                    uint32_t was[32];
+                    tmem_load32(sum, was);
+                    tmem_wait_loads();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            w[i] = __float_as_uint(__uint_as_float(was[i]) +
-                                                   __uint_as_float(w[i]));
-                    }
-                    if (!last) {
-                        tmem_store32(sum, w);
-                        tmem_wait_stores();
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        w[i] = __float_as_uint(__uint_as_float(was[i]) + __uint_as_float(w[i]));
+                }
+                if (!last) {
+                    tmem_store32(sum, w);
+                    tmem_wait_stores();
                 }
                 const int left = g.width - c.n0 - n;  // columns from here on
                 if (!last) {
@@ -1047,13 +1055,17 @@ int weight_grad_of(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs
     return launch_weight_grad<T, Out, 1, 128>(a, b, g, p, s);
 }
 
-ProductArgs product_args(const LinearArgs& a, void* out, int width) {
+// depth: terms of a sum, 0 where the caller says how long a tile's part is.
+ProductArgs product_args(const LinearArgs& a, void* out, int width, int depth) {
     ProductArgs g{};
     g.offsets = a.offsets;
     g.rows = a.rows;
     g.experts = a.experts;
     g.width = width;
+    g.depth = depth;
     g.pairs = a.dtype == GS_F32 ? 6 : 1;
+    g.round = a.dtype == GS_F32 ? kRound : kHalfRound;
+    g.rounds = ceil_div(depth, kSlice) > g.round;
     g.vectors = aligned16(out) && (size_t)width * dtype_size(a.dtype) % 16 == 0;
     g.out = out;
     g.d_status = a.d_status;
@@ -1093,9 +1105,7 @@ int launch_linear_fwd(const LinearArgs& a, const void* xs, const void* weight, c
     if (!make_map(&ma, a.dtype, pa, 0, kHigh) ||
         !make_map(&mb, a.dtype, pb, a.experts, box_b(pairs, a.out)))
         return GS_ERR_CUDA;
-    ProductArgs g = product_args(a, ys, a.out);
-    g.depth = a.in;
-    g.rounds = ceil_div(a.in, kSlice) > kRound;
+    ProductArgs g = product_args(a, ys, a.out, a.in);
     g.bias = bias;
     return with_types(a.dtype, [&](auto t, auto o) {
         return launch_rows<decltype(t), decltype(o), kForward>(ma, mb, g, pairs, s);
@@ -1144,9 +1154,7 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
         const Planes w = prepare(a.dtype, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
         if (!make_map(&ma, a.dtype, gy, 0, kHigh) || !make_map(&mb, a.dtype, w, a.experts, kSlice))
             return GS_ERR_CUDA;
-        ProductArgs g = product_args(a, grad_xs, a.in);
-        g.depth = a.out;
-        g.rounds = ceil_div(a.out, kSlice) > kRound;
+        const ProductArgs g = product_args(a, grad_xs, a.in, a.out);
         const int rc = with_types(a.dtype, [&](auto t, auto o) {
             return launch_rows<decltype(t), decltype(o), kInputGrad>(ma, mb, g, pairs, s);
         });
@@ -1157,10 +1165,13 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
     if (!make_map(&ma, a.dtype, gy, 0, kSlice) || !make_map(&mb, a.dtype, x, 0, kSlice))
         return GS_ERR_CUDA;
     const GradPlan p = grad_plan(a);
-    ProductArgs g = product_args(a, grad_weight, a.in);
+    ProductArgs g = product_args(a, grad_weight, a.in, 0);
     g.high = a.out;
-    g.rounds = ceil_div(a.rows, kSlice) > kRound;
     g.groups = p.groups;
+    if (a.dtype != GS_F32) g.round = kHalfRowsRound;
+    // no part of a sum is longer than a share, nor than all the rows
+    g.rounds = std::min(ceil_div(a.rows, kSlice),
+                        ceil_div(a.rows / kSlice + a.experts, p.groups)) > g.round;
     g.bias_grad = grad_bias;
     g.partial = sums;
     g.bias_partial = sums + partial_floats(p);
