@@ -128,9 +128,9 @@ int gs_expert_combine_bwd(const void* grad_y, int64_t ldgy, const void* ys,
                           void* grad_ys, float* grad_weights, int32_t* d_status, void* stream);
 
 /* Bytes of workspace gs_expert_linear_fwd and _bwd need.  aligned != 0: every
- * array begins on a 16-byte boundary.  float32 operands, and rows that are not
- * whole 16-byte vectors, are laid out there for the tensor cores; the backward
- * keeps partial sums there. */
+ * array read begins on a 16-byte boundary; 0: the size serves whichever do not.
+ * float32 operands, and rows that are not whole 16-byte vectors, are laid out
+ * there for the tensor cores; the backward keeps partial sums there. */
 size_t gs_expert_linear_fwd_workspace_size(int64_t rows, int experts, int in_features,
                                            int out_features, int dtype, int aligned);
 size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_features,

@@ -1,0 +1,66 @@
+"""Host side of the feature-head calls on stand-ins for the CUDA runtime
+(fake_runtime.cpp): workspace sizes and launches, without a GPU and the same
+with one."""
+
+import ctypes as ct
+import itertools
+import os
+import re
+import subprocess
+
+import pytest
+
+from conftest import ROOT
+from tile_gaussian_splat_gb300 import binding, build
+
+F32, F16, BF16 = 0, 1, 2
+P = ct.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    build.build()
+    objs = [os.path.join(build.BUILD, "release", os.path.basename(s) + ".o")
+            for s in build.sources()]
+    if not all(os.path.exists(o) for o in objs):
+        build.build(force=True, debug=False)
+    fake = os.path.join(ROOT, "tests", "fake_runtime.cpp")
+    with open(fake) as f:
+        wraps = sorted(set(re.findall(r"__wrap_(\w+)", f.read())))
+    out = str(tmp_path_factory.mktemp("fake") / "libgs_host.so")
+    subprocess.run([build._nvcc(), "-shared", "-cudart", "static", "-Xcompiler", "-fPIC", fake,
+                    *objs, "-o", out, *(f"-Xlinker=--wrap={w}" for w in wraps)], check=True,
+                   capture_output=True)
+    L = ct.CDLL(out)
+    for name, (res, args) in binding.SIGNATURES.items():
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = res, args
+    L.fake_launches.restype = L.fake_blocks.restype = ct.c_int64
+    L.fake_use(0, 0)
+    return L
+
+
+ALIGNED, SHIFTED = 1 << 20, (1 << 20) + 4  # elements of every type begin at both
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("i,o", [(128, 64), (64, 32), (8, 8), (63, 64), (64, 63), (131, 259)])
+def test_the_queried_workspace_is_enough_whichever_array_is_misaligned(lib, i, o, dtype):
+    """`aligned` = 0 says that some array is off a 16-byte boundary, not which;
+    the size it gets serves every case, and that of `aligned` = 1 the aligned
+    one."""
+    for rows, experts in itertools.product(
+            (1, 2, 16, 17, 20, 100, 128, 512, 1000, 1024, 1025, 5000), (1, 2, 8, 64, 1024)):
+        for places in itertools.product((ALIGNED, SHIFTED), repeat=3):
+            whole = all(p == ALIGNED for p in places)
+            gys, xs, w = places
+            n = lib.gs_expert_linear_fwd_workspace_size(rows, experts, i, o, dtype,
+                                                        int(xs == w == ALIGNED))
+            rc = lib.gs_expert_linear_fwd(P(xs), P(ALIGNED), P(w), None, rows, experts, i, o,
+                                          dtype, P(ALIGNED), P(ALIGNED), n, None, None)
+            assert rc == 0, ("forward", rows, experts, places)
+            n = lib.gs_expert_linear_bwd_workspace_size(rows, experts, i, o, dtype, int(whole))
+            rc = lib.gs_expert_linear_bwd(P(gys), P(xs), P(ALIGNED), P(w), rows, experts, i, o,
+                                          dtype, P(ALIGNED), P(ALIGNED), P(ALIGNED), P(ALIGNED),
+                                          n, None, None)
+            assert rc == 0, ("backward", rows, experts, places)

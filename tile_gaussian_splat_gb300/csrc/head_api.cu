@@ -1,5 +1,6 @@
 // C ABI of the feature-head calls (declared in include/gs_head.h): argument
 // checks, workspace layout and launches.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -61,6 +62,11 @@ size_t dtype_size(int dtype) { return dtype == GS_F32 ? 4 : 2; }
 
 bool workspace_ok(const void* p, size_t bytes, size_t need) {
     return need == 0 || (p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && bytes >= need);
+}
+
+// Stands for an array that is read, where only sizes are checked.
+const void* some_array(bool aligned) {
+    return reinterpret_cast<const void*>((uintptr_t)(aligned ? 16 : 2));
 }
 
 size_t sort_counts_bytes(int64_t n, int experts) {
@@ -189,9 +195,12 @@ int gs_expert_combine_bwd(const void* grad_y, int64_t ldgy, const void* ys, cons
 size_t gs_expert_linear_fwd_workspace_size(int64_t rows, int experts, int in_features,
                                            int out_features, int dtype, int aligned) {
     if (!linear_ok(&kSomeOffsets, rows, experts, in_features, out_features, dtype)) return 0;
-    const void* p = reinterpret_cast<const void*>((uintptr_t)(aligned ? 16 : 2));
-    return linear_fwd_workspace(
-        LinearArgs{nullptr, rows, experts, in_features, out_features, dtype, nullptr}, p, p);
+    const LinearArgs a{nullptr, rows, experts, in_features, out_features, dtype, nullptr};
+    const size_t with_weight = linear_fwd_workspace(a, some_array(aligned), some_array(true));
+    if (aligned) return with_weight;
+    // a misaligned weight may choose the kernel of few rows, which needs
+    // nothing; with xs alone misaligned its rows are laid out
+    return std::max(with_weight, linear_fwd_workspace(a, some_array(false), some_array(false)));
 }
 
 int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* weight,
@@ -215,9 +224,11 @@ int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* wei
 size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_features,
                                            int out_features, int dtype, int aligned) {
     if (!linear_ok(&kSomeOffsets, rows, experts, in_features, out_features, dtype)) return 0;
-    const void* p = reinterpret_cast<const void*>((uintptr_t)(aligned ? 16 : 2));
-    return linear_bwd_workspace(
-        LinearArgs{nullptr, rows, experts, in_features, out_features, dtype, nullptr}, p, p, p);
+    const LinearArgs a{nullptr, rows, experts, in_features, out_features, dtype, nullptr};
+    // all off the boundary needs the most: where a misaligned weight is read as
+    // it lies, an aligned one is too
+    const void* p = some_array(aligned);
+    return linear_bwd_workspace(a, p, p, p);
 }
 
 int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* offsets,
