@@ -43,6 +43,9 @@ typedef enum gs_dtype {
 #define GS_MAX_NORM_CHANNELS 16384
 #define GS_MAX_EXPERTS 1024
 #define GS_MAX_TOPK 64
+/* Most rows of the experts' products: the kernels number rows in 32 bits, to
+ * the end of a tile of 256. */
+#define GS_MAX_EXPERT_ROWS 2147483392
 
 /*
  * gs_layer_norm_fwd -- per row of x (rows, channels):
@@ -145,8 +148,8 @@ size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_fea
  * workspace (16-byte aligned): as the size call says, or NULL where that is 0.
  * float32 products keep 24 bits (error as of float32 sums); an infinity in
  * them makes the results it enters infinite or NaN.
- * Limits: 0 <= rows < 2^31 (a third of it for float32), 1 <= in_features,
- * out_features <= 65536.
+ * Limits: 0 <= rows <= GS_MAX_EXPERT_ROWS (a third of it for float32),
+ * 1 <= in_features, out_features <= 65536.
  */
 int gs_expert_linear_fwd(const void* xs, const int32_t* offsets, const void* weight,
                          const void* bias, int64_t rows, int experts, int in_features,

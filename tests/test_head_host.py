@@ -64,3 +64,20 @@ def test_the_queried_workspace_is_enough_whichever_array_is_misaligned(lib, i, o
                                           dtype, P(ALIGNED), P(ALIGNED), P(ALIGNED), P(ALIGNED),
                                           n, None, None)
             assert rc == 0, ("backward", rows, experts, places)
+
+
+@pytest.mark.parametrize("dtype,planes", [(BF16, 1), (F16, 1), (F32, 3)])
+def test_rows_up_to_where_the_kernels_row_numbers_fit(lib, dtype, planes):
+    """Row numbers, and those of the planes of float32, are 32-bit and formed
+    before they are cut to the last row of a tile, up to 256 rows behind it."""
+    most = ((1 << 31) - 256) // planes
+    for rows, code in ((most, 0), (most + 1, 1), ((1 << 31) // planes, 1)):
+        n = lib.gs_expert_linear_fwd_workspace_size(rows, 1, 8, 8, dtype, 1)
+        assert lib.gs_expert_linear_fwd(P(ALIGNED), P(ALIGNED), P(ALIGNED), None, rows, 1, 8, 8,
+                                        dtype, P(ALIGNED), P(ALIGNED), n, None, None) == code
+        n = lib.gs_expert_linear_bwd_workspace_size(rows, 1, 8, 8, dtype, 1)
+        assert lib.gs_expert_linear_bwd(P(ALIGNED), P(ALIGNED), P(ALIGNED), P(ALIGNED), rows, 1, 8,
+                                        8, dtype, P(ALIGNED), P(ALIGNED), P(ALIGNED), P(ALIGNED),
+                                        n, None, None) == code
+        if code:
+            assert n == 0

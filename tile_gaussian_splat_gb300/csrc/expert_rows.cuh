@@ -12,6 +12,7 @@ namespace gs {
 // falling whatever the offsets hold; prefix[e] = pieces of `height` rows of
 // the experts before e, prefix[experts] = all of them.  height 0: every
 // expert is one piece, with rows or without.  Returns prefix[experts].
+// rows + height stays below 2^31 (GS_MAX_EXPERT_ROWS).
 __device__ __forceinline__ int expert_pieces(const int32_t* offsets, int experts, int64_t rows,
                                              int height, int32_t* begin, int32_t* prefix,
                                              int32_t* d_status) {

@@ -47,12 +47,12 @@ bool rows_ok(int64_t tokens, int topk, int experts, int channels, int dtype) {
 }
 
 bool linear_ok(const int32_t* offsets, int64_t rows, int experts, int in, int out, int dtype) {
-    if (rows < 0 || rows >= ((int64_t)1 << 31) || experts < 1 || experts > GS_MAX_EXPERTS)
+    if (rows < 0 || rows > GS_MAX_EXPERT_ROWS || experts < 1 || experts > GS_MAX_EXPERTS)
         return false;
     if (in < 1 || in > kMaxFeatures || out < 1 || out > kMaxFeatures || !dtype_ok(dtype))
         return false;
-    // the three planes of float32 rows are numbered in 32 bits
-    if (dtype == GS_F32 && 3 * rows >= ((int64_t)1 << 31)) return false;
+    // the three planes of float32 rows are numbered on end
+    if (dtype == GS_F32 && 3 * rows > GS_MAX_EXPERT_ROWS) return false;
     return words_ok(offsets);
 }
 
