@@ -81,3 +81,64 @@ def test_rows_up_to_where_the_kernels_row_numbers_fit(lib, dtype, planes):
                                         n, None, None) == code
         if code:
             assert n == 0
+
+
+def _product(lib, rows=4096):
+    n = lib.gs_expert_linear_bwd_workspace_size(rows, 4, 512, 512, BF16, 1)
+    a = P(ALIGNED)
+    return (lib.gs_expert_linear_fwd(a, a, a, None, rows, 4, 512, 512, BF16, a, None, 0, None,
+                                     None),
+            lib.gs_expert_linear_bwd(a, a, a, a, rows, 4, 512, 512, BF16, a, a, a, a, n, None,
+                                     None))
+
+
+def _sort(lib):
+    a = P(ALIGNED)
+    return lib.gs_expert_sort(a, 100, 2, 1024, a, a, a, None, 0, None)
+
+
+ROWS = 1 << 20  # more than any device's resident blocks
+
+
+def _norm(lib, ch=64):
+    a = P(ALIGNED)
+    return lib.gs_layer_norm_fwd(a, ch, None, None, ROWS, ch, F32, F32, 1e-5, a, ch, None, None,
+                                 None)
+
+
+def _dispatch(lib):
+    a = P(ALIGNED)
+    return lib.gs_expert_dispatch(a, 64, a, a, ROWS, 1, 8, 64, F32, a, None, None)
+
+
+def _combine(lib):
+    a = P(ALIGNED)
+    return lib.gs_expert_combine(a, a, None, ROWS, 1, 64, F32, a, 64, None, None)
+
+
+def test_kernels_are_set_up_on_every_device(lib):
+    """A process may use several devices: what is set or found out about one
+    is not taken for another's."""
+    for device in (0, 1, 0, 3):
+        lib.fake_use(device, 0)
+        for _ in range(2):
+            assert _product(lib) == (0, 0) and _sort(lib) == 0
+        for call in (_norm, _dispatch, _combine):
+            assert call(lib) == 0 and lib.fake_blocks() == 2 * (152 - 10 * device)
+    # once a device
+    calls, queries = lib.fake_attribute_calls(), lib.fake_queries()
+    assert _product(lib) == (0, 0) and _sort(lib) == 0 and _norm(lib) == 0
+    assert (lib.fake_attribute_calls(), lib.fake_queries()) == (calls, queries)
+    lib.fake_use(0, 0)
+
+
+def test_a_failed_query_is_asked_again(lib):
+    lib.fake_use(4, 1)  # a device no call has used
+    for call in (_norm, _dispatch, _combine):
+        assert call(lib) == 0 and lib.fake_blocks() > 0  # some number of blocks does
+    assert _product(lib) == (6, 6) and _sort(lib) == 6  # the limit is needed
+    lib.fake_use(4, 0)
+    assert _product(lib) == (0, 0) and _sort(lib) == 0
+    for call in (_norm, _dispatch, _combine):
+        assert call(lib) == 0 and lib.fake_blocks() == 2 * (152 - 40)
+    lib.fake_use(0, 0)

@@ -935,10 +935,13 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int
            cudaStream_t s) {
     const auto kernel = k_product<T, Out, kProduct, kBlocks, kWide>;
     const size_t smem = smem_bytes<kBlocks, kWide>(g.experts);
-    static const bool raised =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem_bytes<kBlocks, kWide>(GS_MAX_EXPERTS)) == cudaSuccess;
-    if (!raised) return GS_ERR_CUDA;
+    static PerDevice raised, resident;
+    if (!raised.get(0, [&] {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)smem_bytes<kBlocks, kWide>(GS_MAX_EXPERTS)) ==
+                   cudaSuccess;
+        }))
+        return GS_ERR_CUDA;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(kBlocks);
     config.blockDim = dim3(kMmaThreads<kProduct>);
@@ -952,13 +955,11 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int
     config.numAttrs = 1;
     // as many pairs as are resident at once (an SM without a partner in its
     // cluster's reach stays free)
-    static const int resident = [&] {
+    const int clusters = resident.get(152 / kBlocks, [&] {
         int n = 0;
-        return cudaOccupancyMaxActiveClusters(&n, kernel, &config) == cudaSuccess && n > 0
-                   ? n
-                   : sm_count() / kBlocks;
-    }();
-    config.gridDim = dim3((unsigned)(std::min<int64_t>(max_items, resident) * kBlocks));
+        return cudaOccupancyMaxActiveClusters(&n, kernel, &config) == cudaSuccess ? n : 0;
+    });
+    config.gridDim = dim3((unsigned)(std::min<int64_t>(max_items, clusters) * kBlocks));
     return cudaLaunchKernelEx(&config, kernel, a, b, g) == cudaSuccess ? GS_OK : GS_ERR_CUDA;
 }
 

@@ -497,10 +497,12 @@ void launch_expert_sort(const int32_t* ids, int64_t n, int experts, int32_t* off
     const size_t word = sizeof(int32_t), own = (size_t)kSortWarps * experts * word;
     if (units == 0) {
         const auto bytes = [&](int e) { return ((size_t)(kSmallWarps + 2) * e + 1) * word; };
-        static const bool raised =
-            cudaFuncSetAttribute(k_expert_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)bytes(GS_MAX_EXPERTS)) == cudaSuccess;
-        (void)raised;  // a launch that needs it fails without
+        static PerDevice raised;
+        raised.get(0, [&] {  // a launch that needs it fails without
+            return cudaFuncSetAttribute(k_expert_sort_small,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)bytes(GS_MAX_EXPERTS)) == cudaSuccess;
+        });
         k_expert_sort_small<<<1, kSmallThreads, bytes(experts), s>>>(ids, n, experts, offsets,
                                                                      order, slots);
         return;
@@ -522,10 +524,12 @@ void launch_dispatch(const RowArgs& a, const void* x, int64_t ldx, const int32_t
         with_row_form<sizeof(Word) >= 8 ? 8 : 1>(words, [&](auto form) {
             using F = decltype(form);
             const auto kernel = k_dispatch<Word, F::kLanes, F::kItems, F::kRows>;
-            static const int resident = resident_blocks(kernel, 0);
-            kernel<<<row_blocks(a.tokens, kRowThreads / F::kLanes, resident), kRowThreads, 0,
-                     s>>>(a, static_cast<const Word*>(x), ldx / per, words, slots, offsets,
-                          static_cast<Word*>(xs));
+            static PerDevice resident;
+            const int blocks = row_blocks(a.tokens, kRowThreads / F::kLanes,
+                                          resident_blocks(resident, kernel, 0));
+            kernel<<<blocks, kRowThreads, 0, s>>>(a, static_cast<const Word*>(x), ldx / per,
+                                                  words, slots, offsets,
+                                                  static_cast<Word*>(xs));
         });
     };
     const auto whole = [&](int bytes) {
@@ -583,8 +587,10 @@ void launch_combine(const RowArgs& a, const void* ys, const int32_t* slots, cons
         using F = decltype(form);
         using P = decltype(flight);
         const auto kernel = k_combine<T, F::kVec, F::kLanes, F::kItems, P::kChoices, P::kTokens>;
-        static const int resident = resident_blocks(kernel, 0);
-        kernel<<<row_blocks(a.tokens, kRowThreads / F::kLanes, resident), kRowThreads, 0, s>>>(
+        static PerDevice resident;
+        const int blocks = row_blocks(a.tokens, kRowThreads / F::kLanes,
+                                      resident_blocks(resident, kernel, 0));
+        kernel<<<blocks, kRowThreads, 0, s>>>(
             a, static_cast<const T*>(ys), slots, weights, static_cast<T*>(y), ldy);
     });
 }
@@ -598,8 +604,10 @@ void launch_combine_bwd(const RowArgs& a, const void* grad_y, int64_t ldgy, cons
         using P = decltype(flight);
         const auto kernel = k_combine_bwd<T, F::kVec, F::kLanes, F::kItems, P::kChoices,
                                           P::kTokens>;
-        static const int resident = resident_blocks(kernel, 0);
-        kernel<<<row_blocks(a.tokens, kRowThreads / F::kLanes, resident), kRowThreads, 0, s>>>(
+        static PerDevice resident;
+        const int blocks = row_blocks(a.tokens, kRowThreads / F::kLanes,
+                                      resident_blocks(resident, kernel, 0));
+        kernel<<<blocks, kRowThreads, 0, s>>>(
             a, static_cast<const T*>(grad_y), ldgy, static_cast<const T*>(ys), slots, weights,
             offsets, static_cast<T*>(grad_ys), grad_weights);
     });

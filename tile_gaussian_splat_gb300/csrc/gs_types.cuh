@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 #include <cuda_bf16.h>
@@ -141,17 +142,42 @@ struct Form {
     static constexpr int kVec = kVec_, kLanes = kLanes_, kItems = kItems_, kRows = kRows_;
 };
 
-// Blocks of a kernel that are resident at once: a walk over the rows in equal
-// shares needs exactly those (a second, part-filled wave costs a whole one).
+// A number found out (or a thing done) once for every device a process uses.
+class PerDevice {
+    static constexpr int kMaxDevices = 64;
+    std::atomic<int> found_[kMaxDevices] = {};
+
+  public:
+    // The current device's: what find() gave, `otherwise` while that is 0 (it
+    // is asked again by the next call).
+    template <typename F>
+    int get(int otherwise, F&& find) {
+        int dev = -1;
+        const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices;
+        int v = known ? found_[dev].load(std::memory_order_acquire) : 0;
+        if (v == 0) {
+            v = find();
+            if (known) found_[dev].store(v, std::memory_order_release);
+            if (v == 0) (void)cudaGetLastError();  // not an error of the launch that follows
+        }
+        return v ? v : otherwise;
+    }
+};
+
+// Blocks of a kernel that are resident at once on the current device: a walk
+// over the rows in equal shares needs exactly those (a second, part-filled wave
+// costs a whole one).
 template <typename K>
-int resident_blocks(K kernel, size_t smem) {
-    int per = 0, dev = 0, sms = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kRowThreads, smem) !=
-            cudaSuccess ||
-        cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 152;
-    return std::max(1, per) * sms;
+int resident_blocks(PerDevice& resident, K kernel, size_t smem) {
+    return resident.get(152, [&] {
+        int per = 0, dev = 0, sms = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kRowThreads, smem) !=
+                cudaSuccess ||
+            cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return 0;
+        return std::max(1, per) * sms;
+    });
 }
 
 // f(integral constant): the elements of type T in the widest access of 16, 8,

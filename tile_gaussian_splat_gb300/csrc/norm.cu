@@ -423,8 +423,9 @@ void launch_norm_fwd(const NormArgs& n, const void* bias, float eps, void* y, in
             using F = decltype(form);
             const int groups = kNormThreads / F::kLanes;
             const auto kernel = k_norm_fwd<T, F::kVec, F::kLanes, F::kItems, F::kRows>;
-            static const int resident = resident_blocks(kernel, 0);
-            kernel<<<blocks_for(n.rows, groups, resident), kNormThreads, 0, s>>>(a);
+            static PerDevice resident;
+            const int blocks = blocks_for(n.rows, groups, resident_blocks(resident, kernel, 0));
+            kernel<<<blocks, kNormThreads, 0, s>>>(a);
         };
         with_width<T>(row_bits<T>(n.x, n.ldx) | row_bits<T>(y, ldy) |
                           (uintptr_t)(n.channels * sizeof(T)),
@@ -457,10 +458,11 @@ void launch_norm_bwd(const NormArgs& n, const void* grad_y, int64_t ldgy, const 
             const int groups = kNormThreads / F::kLanes;
             const size_t smem = params ? (groups - 1) * 2 * n.channels * sizeof(float) : 0;
             const auto kernel = k_norm_bwd<T, F::kVec, F::kLanes, F::kItems, F::kRows>;
-            static const int resident = resident_blocks(
-                kernel, (groups - 1) * 2 * F::kVec * F::kLanes * F::kItems * sizeof(float));
+            static PerDevice resident;
+            const size_t most = (groups - 1) * 2 * F::kVec * F::kLanes * F::kItems * sizeof(float);
             slices = blocks_for(n.rows, groups,
-                                std::min(norm_bwd_slices(n.rows, n.channels), resident));
+                                std::min(norm_bwd_slices(n.rows, n.channels),
+                                         resident_blocks(resident, kernel, most)));
             kernel<<<slices, kNormThreads, smem, s>>>(a);
         };
         with_width<T>(row_bits<T>(n.x, n.ldx) | row_bits<T>(grad_y, ldgy) |
