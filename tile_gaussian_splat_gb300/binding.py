@@ -511,10 +511,14 @@ def _rows(t, what):
 
 def _on(stream, like):
     """The call's stream as a raw handle: `stream`, or the current one of the
-    device that `like` is on."""
+    device that `like` is on, which has to be the current device."""
     if not like.is_cuda:
         _refuse("expected a CUDA tensor")
-    return _raw_stream(like.get_device()) if stream is None else stream.cuda_stream
+    device = like.get_device()
+    if device != torch.cuda.current_device() or \
+            getattr(stream, "device_index", device) != device:
+        _refuse("tensors and stream of the current device expected")
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def _new(shape, dtype, like, stream):
