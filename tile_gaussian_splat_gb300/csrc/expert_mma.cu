@@ -8,9 +8,10 @@
 // matrix instruction as it lies (MN-major), so nothing is transposed.
 //
 // float32 operands are first written as three bfloat16 planes, a = a0 + a1 +
-// a2 with eight bits of the fraction each (exact), and a product is six sums,
+// a2, each the nearest to what is left (exact), and a product is six sums,
 // a2 b0 + a0 b2 + a1 b1 + a1 b0 + a0 b1 + a0 b0, small ones first; the terms
-// left out are below 2^-22 of |a b|.  Half-type operands whose rows are not
+// left out are of either sign and at most 2^-24 of |a b|, half a unit of the
+// last place (planes cut off left out up to 2^-21, always towards zero).  Half-type operands whose rows are not
 // whole 16-byte vectors are copied to rows that are (one plane).
 //
 // The accumulators cut off where float32 sums round (1.2e-8 of the result per
@@ -44,6 +45,7 @@
 // taking all of the sums cost 38 us on 95.  One of them also clears the rows
 // of the next expert in an expert's last slice.
 #include <algorithm>
+#include <cfloat>
 #include <cstdint>
 #include <type_traits>
 
@@ -772,22 +774,24 @@ __global__ void __launch_bounds__(256)
 }
 
 // A (rows x columns) matrix as planes of rows of `pitch` elements (a multiple
-// of 8): float32 as three of bfloat16, each cutting off the next eight bits of
-// the fraction, half types copied.  Reads once, writes once.
+// of 8): float32 as three of bfloat16, half types copied.  Reads once, writes once.
 constexpr int kPlaneThreads = 256;
 
-// a = a0 + a1 + a2, the top eight bits of the fraction first.
+// a = a0 + a1 + a2, each the nearest bfloat16 to what is left: at most 2^-8,
+// then 2^-17 of the power of two below |a|, whose last six bits a2 holds (from
+// |a| of 2^-110 on; below, a2 loses what is under 2^-133).
 __device__ __forceinline__ void split3(float a, uint16_t* p) {
-    const uint32_t a0 = __float_as_uint(a) & 0xffff0000u;
+    const bool finite = fabsf(a) <= FLT_MAX;
+    __nv_bfloat16 a0 = __float2bfloat16_rn(a);
+    // the largest values would round to infinity: cut off
+    if (finite && fabsf(__bfloat162float(a0)) > FLT_MAX) a0 = __float2bfloat16_rz(a);
     // an infinity or NaN is all in the first plane
-    const bool finite = (a0 & 0x7f800000u) != 0x7f800000u;
-    const float r1 = finite ? a - __uint_as_float(a0) : 0.f;
-    const uint32_t a1 = __float_as_uint(r1) & 0xffff0000u;
-    const uint32_t a2 = __float_as_uint(r1 - __uint_as_float(a1));
-    // a NaN whose upper half alone would read as an infinity stays one
-    p[0] = (uint16_t)(a0 >> 16 | (a != a ? 0x40u : 0u));
-    p[1] = (uint16_t)(a1 >> 16);
-    p[2] = (uint16_t)(a2 >> 16);
+    const float r1 = finite ? a - __bfloat162float(a0) : 0.f;
+    const __nv_bfloat16 a1 = __float2bfloat16_rn(r1);
+    const __nv_bfloat16 a2 = __float2bfloat16_rn(r1 - __bfloat162float(a1));
+    p[0] = __bfloat16_as_ushort(a0);
+    p[1] = __bfloat16_as_ushort(a1);
+    p[2] = __bfloat16_as_ushort(a2);
 }
 
 // 2^lanes threads a row, at most 32, of eight elements each (four 2^lanes
