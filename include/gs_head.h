@@ -147,8 +147,7 @@ size_t gs_expert_linear_bwd_workspace_size(int64_t rows, int experts, int in_fea
  * (experts, out_features) or NULL, ys (rows, out_features), all of dtype.
  * workspace (16-byte aligned): as the size call says, or NULL where that is 0.
  * A float32 product is off by at most 2^-24 of it (operands from 2^-110 on) and
- * sums of them are float32 sums; an infinity in them makes the results it
- * enters infinite or NaN.
+ * sums of them are float32 sums; a factor below 2^-133 counts as 0.
  * Limits: 0 <= rows <= GS_MAX_EXPERT_ROWS (a third of it for float32),
  * 1 <= in_features, out_features <= 65536.
  */

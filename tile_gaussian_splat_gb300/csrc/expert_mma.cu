@@ -780,15 +780,18 @@ constexpr int kPlaneThreads = 256;
 // a = a0 + a1 + a2, each the nearest bfloat16 to what is left: at most 2^-8,
 // then 2^-17 of the power of two below |a|, whose last six bits a2 holds (from
 // |a| of 2^-110 on; below, a2 loses what is under 2^-133).
+// An infinity is +-1, 0 and itself: a2 meets b0 alone, which is 0 only where b
+// is (below 2^-133), so every product but that with 0 is infinite, and one of
+// two infinities too, by a2 b0 and a0 b2.  (In a0 it would meet b1 and b2,
+// which are 0 for many b.)  A NaN is in a2 as well.
 __device__ __forceinline__ void split3(float a, uint16_t* p) {
     const bool finite = fabsf(a) <= FLT_MAX;
-    __nv_bfloat16 a0 = __float2bfloat16_rn(a);
+    __nv_bfloat16 a0 = __float2bfloat16_rn(finite ? a : copysignf(1.f, a));
     // the largest values would round to infinity: cut off
     if (finite && fabsf(__bfloat162float(a0)) > FLT_MAX) a0 = __float2bfloat16_rz(a);
-    // an infinity or NaN is all in the first plane
     const float r1 = finite ? a - __bfloat162float(a0) : 0.f;
     const __nv_bfloat16 a1 = __float2bfloat16_rn(r1);
-    const __nv_bfloat16 a2 = __float2bfloat16_rn(r1 - __bfloat162float(a1));
+    const __nv_bfloat16 a2 = __float2bfloat16_rn(finite ? r1 - __bfloat162float(a1) : a);
     p[0] = __bfloat16_as_ushort(a0);
     p[1] = __bfloat16_as_ushort(a1);
     p[2] = __bfloat16_as_ushort(a2);
