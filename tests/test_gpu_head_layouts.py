@@ -33,3 +33,30 @@ def test_one_array_off_any_vector_boundary(rows, experts, dtype):
         refs, slacks = linear_bwd_ref(gys, xs, offsets, w)
         for t, r, s in zip(gs.gs_expert_linear_bwd(gys, xs, offsets, w), refs, slacks):
             check(t, r, s, "gradients")
+
+
+def test_results_of_another_stream_share_no_memory_with_work_under_way():
+    """The current stream still has writes to come into a block that it has
+    freed; a call on another stream returns before them and keeps its result."""
+    g = gen(21)
+    x = randn(g, 1 << 14, 256)
+    want = gs.gs_layer_norm_fwd(x, stats=False)[0].clone()
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        block = torch.empty_like(x)
+        y = z = torch.ones((4096, 4096), device=DEV)
+        for _ in range(40):  # some milliseconds
+            z = (z @ y) * 1e-4
+        block.fill_(9.0)
+        del block
+        got = gs.gs_layer_norm_fwd(x, stats=False, stream=side)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        torch.cuda.current_stream().wait_stream(side)
+        again = got + 0  # and the result is used on the current stream
+        del got
+        gs.gs_layer_norm_fwd(-x, stats=False, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(again, want)

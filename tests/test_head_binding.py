@@ -28,3 +28,43 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     for stream, tensor in ((None, _On(1)), (_On(1), _On(1)), (_On(1), _On(0))):
         with pytest.raises(ValueError, match="device"):
             gs._on(stream, tensor)
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
+    """A block that the current stream freed may still be in use there, so a
+    call on another stream takes none of those; and the caller may go on with
+    the result on the current stream."""
+    now = ["current"]
+    log = []
+
+    class Tensor:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def record_stream(self, stream):
+            log.append((self.stream, stream))
+
+    class Use:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.saved, now[0] = now[0], self.stream
+
+        def __exit__(self, *_):
+            now[0] = self.saved
+
+    class Side:
+        cuda_stream = 99
+
+    like, side = _On(0), Side()
+    like.device = "cuda:0"
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: Tensor(now[0]))
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: now[0])
+    monkeypatch.setattr(gs, "_raw_stream", lambda device: 7)
+    assert gs._new((3,), torch.uint8, like, side).stream is side
+    assert now == ["current"] and log == [(side, "current")]
+    side.cuda_stream = 7  # the current stream itself
+    assert gs._new((3,), torch.uint8, like, side).stream == "current" and len(log) == 1
+    assert gs._new((3,), torch.uint8, like, None).stream == "current"

@@ -522,11 +522,14 @@ def _on(stream, like):
 
 
 def _new(shape, dtype, like, stream):
-    """An output or workspace the call's stream uses: when that is not the
-    current one, the allocator is told."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None and stream.cuda_stream != _raw_stream(like.get_device()):
-        t.record_stream(stream)
+    """An output or workspace of the call, of its stream's memory: a block that
+    the current stream has freed may still be in use there.  The allocator is
+    told that the current stream, where the caller goes on, may use it too."""
+    if stream is None or stream.cuda_stream == _raw_stream(like.get_device()):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
