@@ -1,9 +1,14 @@
 """The binding's own checks of the feature-head calls, without a GPU."""
 
+import subprocess
+import sys
+
 import pytest
 import torch
 
+from conftest import ROOT
 from tile_gaussian_splat_gb300 import binding as gs
+from tile_gaussian_splat_gb300 import build
 
 
 class _On:
@@ -68,3 +73,14 @@ def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
     side.cuda_stream = 7  # the current stream itself
     assert gs._new((3,), torch.uint8, like, side).stream == "current" and len(log) == 1
     assert gs._new((3,), torch.uint8, like, None).stream == "current"
+
+
+def test_imports_where_torch_has_no_cuda():
+    """Sizes and argument checks need no GPU, nor a torch built for one."""
+    build.build()
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda')]:\n"
+            "    delattr(torch._C, name)\n"
+            "from tile_gaussian_splat_gb300 import binding\n"
+            "assert binding.gs_tile_bits(4, 4) == 4\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, capture_output=True)

@@ -467,7 +467,7 @@ def gs_rasterize_bwd_steps(means2d, conics, colors, opacities, backgrounds, mask
 # build no message before they fail and the stream is read as its raw handle.
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # None: a torch without CUDA
 
 
 def _dtype(t, what):
