@@ -27,13 +27,14 @@ class FeatureHead:
     """y = sum over the topk experts e of softmax(router)[e] * (W2[e]
     relu(W1[e] n + b1[e]) + b2[e]), n = the layer norm of a pixel's features.
     forward and backward on one stream, parameters in `params`, their
-    gradients in `grads`."""
+    gradients in `grads`, what the kernels report in `status`."""
 
     def __init__(self, features, hidden, out, experts, topk=2, seed=0, device="cuda:0"):
         g = torch.Generator(device=device).manual_seed(seed)
         mat = lambda *s: torch.randn(s, generator=g, device=device) / s[-1] ** 0.5
         zeros = lambda *s: torch.zeros(s, device=device)
         self.topk, self.experts = topk, experts
+        self.status = gs.new_status(device)
         self.params = dict(
             norm_w=torch.ones(features, device=device), norm_b=zeros(features),
             router=mat(experts, features), w1=mat(experts, hidden, features),
@@ -49,10 +50,11 @@ class FeatureHead:
         weights = torch.softmax(top, 1)
         chosen = torch.where(reached.reshape(-1, 1), ids, -1).to(torch.int32)
         offsets, _, slots = gs.gs_expert_sort(chosen, self.experts)
-        xs = gs.gs_expert_dispatch(rows, slots, offsets)
-        h = gs.gs_expert_linear_fwd(xs, offsets, p["w1"], p["b1"]).relu_()
-        ys = gs.gs_expert_linear_fwd(h, offsets, p["w2"], p["b2"])
-        y = gs.gs_expert_combine(ys, slots, weights)
+        st = self.status
+        xs = gs.gs_expert_dispatch(rows, slots, offsets, d_status=st)
+        h = gs.gs_expert_linear_fwd(xs, offsets, p["w1"], p["b1"], d_status=st).relu_()
+        ys = gs.gs_expert_linear_fwd(h, offsets, p["w2"], p["b2"], d_status=st)
+        y = gs.gs_expert_combine(ys, slots, weights, d_status=st)
         self.kept = (x, mean, rstd, rows, ids, weights, offsets, slots, xs, h, ys)
         return y.reshape(*x.shape[:-1], -1)
 
@@ -62,11 +64,12 @@ class FeatureHead:
         p = self.params
         x, mean, rstd, rows, ids, weights, offsets, slots, xs, h, ys = self.kept
         gy = grad_y.reshape(rows.shape[0], -1)
-        gys, gw = gs.gs_expert_combine_bwd(gy, ys, slots, weights, offsets)
-        gh, g_w2, g_b2 = gs.gs_expert_linear_bwd(gys, h, offsets, p["w2"])
+        st = self.status
+        gys, gw = gs.gs_expert_combine_bwd(gy, ys, slots, weights, offsets, d_status=st)
+        gh, g_w2, g_b2 = gs.gs_expert_linear_bwd(gys, h, offsets, p["w2"], d_status=st)
         gh *= h > 0
-        gxs, g_w1, g_b1 = gs.gs_expert_linear_bwd(gh, xs, offsets, p["w1"])
-        g_rows = gs.gs_expert_combine(gxs, slots)  # the dispatch's adjoint
+        gxs, g_w1, g_b1 = gs.gs_expert_linear_bwd(gh, xs, offsets, p["w1"], d_status=st)
+        g_rows = gs.gs_expert_combine(gxs, slots, d_status=st)  # the dispatch's adjoint
         # softmax over the chosen, then the router's product
         g_top = weights * (gw - (weights * gw).sum(1, keepdim=True))
         g_logits = torch.zeros((rows.shape[0], self.experts), device=rows.device)
@@ -101,10 +104,13 @@ def render(d, scene, colors):
 def render_grad(d, scene, colors, alphas, kept, grad_image):
     """The gradient of the splats' channels."""
     offsets, ids, last = kept
-    return gs.gs_rasterize_bwd(
+    status = gs.new_status(colors.device)
+    grads = gs.gs_rasterize_bwd(
         d["means2d"], d["conics"], colors, d["opacities"], None, None, scene.width, scene.height,
         scene.tile_size, offsets, ids, scene.alpha_cutoff, alphas, last, grad_image,
-        torch.zeros_like(alphas))["grad_colors"]
+        torch.zeros_like(alphas), d_status=status)
+    gs.check_status(status, "render_grad")
+    return grads["grad_colors"]
 
 
 def train(steps=30, features=32, hidden=96, out=8, experts=8, width=96, height=64, rate=0.5,
@@ -131,7 +137,9 @@ def train(steps=30, features=32, hidden=96, out=8, experts=8, width=96, height=6
         losses.append(float((diff * diff).sum() / n))
         grad_image = torch.zeros_like(image)  # no loss on the three colours
         head.backward(2 * diff / n, grad_image[..., 3:])
-        colors -= 20 * rate * render_grad(d, scene, colors, alphas, kept, grad_image)
+        grad_colors = render_grad(d, scene, colors, alphas, kept, grad_image)
+        gs.check_status(head.status, "feature head")  # before anything is updated
+        colors -= 20 * rate * grad_colors
         head.step(rate)
     return losses
 

@@ -20,6 +20,9 @@
  *     place.  Arrays without one are contiguous.
  *   - Outputs do not overlap inputs, and no row of an output another row.
  *   - Results do not depend on the run: no floating-point atomics.
+ *   - d_status receives GS_ERR_TIMEOUT from a product whose wait ran out (two
+ *     seconds on what takes microseconds; part of its output is then
+ *     unwritten).  With NULL nothing tells.
  *   - An index read from a device array (a slot, an offset) that lies outside
  *     its array is treated as -1 or clamped; the range-checking build also
  *     reports GS_ERR_OUT_OF_BOUNDS in d_status.

@@ -465,6 +465,10 @@ def gs_rasterize_bwd_steps(means2d, conics, colors, opacities, backgrounds, mask
 #
 # A call on one token is over in a few microseconds on the GPU, so the checks
 # build no message before they fail and the stream is read as its raw handle.
+#
+# d_status (new_status, check_status) is where the kernels report: without it a
+# wait that ran out (GS_ERR_TIMEOUT) leaves part of an output unwritten and
+# nothing is raised.
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # None: a torch without CUDA
