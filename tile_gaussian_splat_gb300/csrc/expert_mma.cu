@@ -799,9 +799,11 @@ __device__ __forceinline__ void split3(float a, uint16_t* p) {
 
 // 2^lanes threads a row, at most 32, of eight elements each (four 2^lanes
 // apart where rows are not whole vectors, so that reads are contiguous, took
-// 19 us where this takes 15: three planes of 2-byte writes).
+// 19 us where this takes 15: three planes of 2-byte writes).  With whole vectors
+// eight blocks an SM are worth a few spilled registers (242486 x 136 float32:
+// 59 us, 65 with six blocks; odd rows 17 us and 14).
 template <typename T, typename Plane, bool kVectors>
-__global__ void __launch_bounds__(kPlaneThreads)
+__global__ void __launch_bounds__(kPlaneThreads, kVectors ? 8 : 6)
     k_planes(const T* __restrict__ x, int64_t rows, int columns, int pitch, int lanes,
              Plane* __restrict__ out) {
     constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1, kEach = 8;
