@@ -183,10 +183,11 @@ unsigned few_pieces(const LinearArgs& a) {
 }  // namespace
 
 // Where the tensor cores take the weights as they lie, up to sixteen rows in
-// all (8 experts of 512 x 512 bf16: 3.8 us against 7.8 for 16 rows, 7.9 and
-// 7.8 for 64).  Where they would first be rewritten, sixteen an expert on
-// average (32 experts of 512 x 512 f32, 512 rows: 29 us and 33; 64 of 1024 x
-// 1024: 118 and 228).
+// all (8 experts of 512 x 512 bf16: 3.9 us against 7.2 for 16 rows, both 7.2
+// for 64).  Where they would first be rewritten, sixteen an expert on average
+// (32 experts of 512 x 512 f32, 512 rows: 29 us and 33; 64 of 1024 x 1024: 119
+// and 246 for 512 rows, 212 and 247 for 1024, whose sixteen rows an expert read
+// its weights twice).
 bool few_rows(const LinearArgs& a, bool as_they_lie) {
     return as_they_lie ? a.rows <= 16 : a.rows <= 16 * (int64_t)a.experts && a.rows <= 1024;
 }

@@ -29,9 +29,11 @@
 // the first block's barrier), one warp of the first block issues the matrix
 // instructions, and eight warps move finished accumulators from tensor memory
 // to the output while the next tile is computed in the other half of it.
-// 16 experts, bf16: 262144 rows, 512 -> 1024, 195 us (1410 TFLOP/s; 147 us
-// without the stores, which is what binds); the input gradient of 131072 rows
-// 85 us (1610 TFLOP/s), their weight gradient 113 us (1215 TFLOP/s).
+// 16 experts, bf16: 262144 rows, 512 -> 1024, 194 us (1420 TFLOP/s) where the
+// experts have equal shares and 222 us (1240) where a router spreads them and
+// passes follow each other; the stores bind (without them 147 of 195 us).  The
+// input gradient of 131072 rows 94 us (1460 TFLOP/s), their weight gradient 126
+// us (1090), with the bias gradient 143.
 //
 // The weight gradient's sums run over an expert's rows, of which there are
 // many for few output tiles.  The rows of all experts, end to end, are cut
@@ -75,10 +77,10 @@ constexpr int kAccumulators = 2;
 // of a0 b0 (float32), and of half types over features and over rows.  Over
 // 131072 rows in nine shares, 1024 x 512 bfloat16, 0.39 % of the gradients were
 // not the nearest to the exact sum without rounds (0.05 % of sums in float32),
-// 0.12 % with rounds of 32, 0.064 % of 16 and 0.035 % of 8, in 131, 132, 136
-// and 142 us.  Rounds of 16 cost products over 2048 features 16 % (82 -> 96 us),
-// of 32 nothing there and 7 % over 4096; 32768 positive float16 products came
-// out 1.9e-4 too small on average without rounds and 1.3e-5 with 32.
+// 0.12 % with rounds of 32, 0.064 % of 16 and 0.035 % of 8, in 141, 142, 145
+// and 151 us.  Rounds of 16 cost products over 2048 features 16 % (82 -> 96 us),
+// of 32 nothing there and 7 to 10 % over 4096; 32768 positive float16 products
+// came out 1.9e-4 too small on average without rounds and 1.3e-5 with 32.
 constexpr int kRound = 8, kHalfRound = 32, kHalfRowsRound = 16;
 
 struct ProductArgs {
@@ -159,7 +161,7 @@ struct Tile {
     int row0, row1;  // rows of the output (of the sum, for kWeightGrad)
     int m0, n0;      // first row (kWeightGrad only) and column of the tile
     int count;       // 64-term slices of the sum
-    int q0, q1;      // of the slices of all sums over plane pairs, this round's
+    int q0, q1;      // of the slices of all sums over plane pairs, those of one round
     int tile;        // kWeightGrad: which tile of the weight matrix
     bool whole;      // kWeightGrad: all of the expert's rows
     int64_t slot;    // kWeightGrad: where a partial sum goes
@@ -1016,7 +1018,7 @@ GradPlan grad_plan(const LinearArgs& a) {
     // slice (of each of a float32 product's six sums), 2 us for an expert's
     // part to come out, and the sums at 5 TB/s (where experts are longer than a
     // slice, so that a cut falls inside one).  16 experts of 8192 rows, 1024
-    // x 512: 113 us in 9 shares, 130 in 19.
+    // x 512: 126 us in 9 shares, 150 in 19, 170 in 5.
     const double slices = a.rows / (double)kSlice + 0.5 * a.experts;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>((int64_t)slices, 2 * units));
     double best = 0.0;
