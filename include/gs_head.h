@@ -7,6 +7,10 @@
  *   gs_expert_dispatch             rows copied into expert order
  *   gs_expert_combine / _bwd       rows summed back with their weights
  *   gs_expert_linear_fwd / _bwd    every expert's matrix product
+ *   gs_expert_route_fwd / _bwd     the choice of experts, its weights, the
+ *                                  experts' counts and the balance loss
+ *   gs_rows_pack8 / gs_rows_unpack8  rows kept in 8 bits, and back
+ *   gs_expert_linear8_fwd / _bwd   the experts' products of 8-bit rows
  * A row is one pixel's (token's) channels.  No counterpart on the pages of
  * gs_splat.h; the formulas stand at each call.
  *
@@ -49,6 +53,16 @@ typedef enum gs_dtype {
 /* Most rows of the experts' products: the kernels number rows in 32 bits, to
  * the end of a tile of 256. */
 #define GS_MAX_EXPERT_ROWS 2147483392
+
+/* 8-bit rows: an element is q * 2^(byte - 127), q in e4m3 (1.4.3 bits, no
+ * infinity, largest 448) and one byte (e8m0; 255 is a NaN) for each
+ * GS_SCALE_BLOCK channels.  A row's elements take GS_ROW8_BYTES bytes, zeros
+ * behind the last channel, its scale bytes GS_ROW8_SCALES, zeros behind the
+ * last block; rows follow each other.  The elements begin on a 16-byte
+ * boundary, the scale bytes on a 4-byte one. */
+#define GS_SCALE_BLOCK 128
+#define GS_ROW8_BYTES(channels) (((channels) + 15) / 16 * 16)
+#define GS_ROW8_SCALES(channels) (((channels) + 511) / 512 * 4)
 
 /*
  * gs_layer_norm_fwd -- per row of x (rows, channels):
@@ -173,6 +187,100 @@ int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* off
                          int out_features, int dtype, void* grad_xs, void* grad_weight,
                          void* grad_bias, void* workspace, size_t workspace_bytes,
                          int32_t* d_status, void* stream);
+
+/* Bytes of workspace gs_expert_route_fwd needs where counts are asked for. */
+size_t gs_expert_route_workspace_size(int64_t tokens, int experts);
+
+/*
+ * gs_expert_route_fwd -- with p the softmax of a row of logits (tokens,
+ * experts):
+ *   ids[t, j]  the expert of the j-th largest logit (equal ones: the lowest
+ *              expert first; a NaN before every number); a logit of minus
+ *              infinity is not chosen
+ *   weights[t, j] = p[ids[t, j]], divided by their sum over j if renormalise
+ *   counts[e] = how many ids are e;  counts[experts] = tokens that take part
+ *   loss = experts * sum over e of counts[e] / (all counts[e]) * (mean of p[e]
+ *          over the tokens that take part);  0 where none does
+ * keep (tokens bytes, or NULL): a token whose byte is 0 does not take part and
+ * its logits are not looked at; nor does one without a logit above minus
+ * infinity.  What is not chosen has ids -1 (gs_expert_sort drops it) and
+ * weight 0.  Logits of dtype, row distance ldl; ids int32 and weights float32
+ * (tokens, topk).  counts int32 (experts + 1) may be NULL (loss then too, and
+ * no workspace is needed), loss (one float32) may be NULL.
+ * Limits: tokens, topk and experts as gs_expert_sort, topk <= experts.
+ */
+int gs_expert_route_fwd(const void* logits, int64_t ldl, const uint8_t* keep, int64_t tokens,
+                        int topk, int experts, int dtype, int renormalise, int32_t* ids,
+                        float* weights, int32_t* counts, float* loss, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * gs_expert_route_bwd -- the gradient of weights and loss in the logits, for
+ * the choice made (the counts do not change with the logits): with g the
+ * gradient of weights, h[e] = *grad_loss * experts * counts[e] / (all
+ * counts[e]) / counts[experts], sums over the choices j and all experts i
+ *   grad_logits[e] = p[e] (h[e] - sum p[i] h[i])
+ *     + (renormalise)  for e = ids[j]: w[j] (g[j] - sum w g), w the weights
+ *     + (otherwise)    p[e] ((g[j] for e = ids[j]) - sum p[ids[j]] g[j])
+ * and 0 for a token whose first id is -1.  ids, counts: as gs_expert_route_fwd
+ * wrote them.  grad_weights (tokens, topk) and grad_loss (one float32 on the
+ * device) may each be NULL for zeros (counts with grad_loss).
+ */
+int gs_expert_route_bwd(const void* logits, int64_t ldl, const int32_t* ids,
+                        const int32_t* counts, const float* grad_weights, const float* grad_loss,
+                        int64_t tokens, int topk, int experts, int dtype, int renormalise,
+                        void* grad_logits, int64_t ldg, int32_t* d_status, void* stream);
+
+/*
+ * gs_rows_pack8 -- x (rows, channels) of dtype, row distance ldx, as 8-bit
+ * rows: a block's byte is the smallest (at least 0) with |x| <= 448 * 2^(byte
+ * - 127) for its finite elements, q the e4m3 nearest to x * 2^(127 - byte),
+ * ties to even; what is not finite becomes a NaN.
+ * gs_rows_unpack8 -- the values back, rounded to dtype (a finite q beyond the
+ * type becomes its largest finite value).
+ * Limits: rows >= 0, 1 <= channels <= 65536.
+ */
+int gs_rows_pack8(const void* x, int64_t ldx, int64_t rows, int channels, int dtype, uint8_t* q,
+                  uint8_t* scales, void* stream);
+int gs_rows_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int channels,
+                    int dtype, void* y, int64_t ldy, void* stream);
+
+/* Bytes of workspace gs_expert_linear8_fwd and _bwd need.  aligned != 0:
+ * grad_ys begins on a 16-byte boundary. */
+size_t gs_expert_linear8_fwd_workspace_size(int64_t rows, int experts, int in_features,
+                                            int out_features, int dtype);
+size_t gs_expert_linear8_bwd_workspace_size(int64_t rows, int experts, int in_features,
+                                            int out_features, int dtype, int aligned);
+
+/*
+ * gs_expert_linear8_fwd -- gs_expert_linear_fwd of 8-bit rows:
+ *   ys[r] = weight[e] xs[r] + bias[e];  rows of no expert are 0,
+ * xs (rows, in_features) and weight (experts * out_features, in_features) 8-bit
+ * rows with their scales; bias and ys of dtype.  Limits as there.
+ */
+int gs_expert_linear8_fwd(const uint8_t* xs, const uint8_t* xs_scales, const int32_t* offsets,
+                          const uint8_t* weight, const uint8_t* weight_scales, const void* bias,
+                          int64_t rows, int experts, int in_features, int out_features, int dtype,
+                          void* ys, void* workspace, size_t workspace_bytes, int32_t* d_status,
+                          void* stream);
+
+/*
+ * gs_expert_linear8_bwd -- gradients of gs_expert_linear8_fwd in the values of
+ * xs, weight and bias, from rows kept in 8 bits since the forward:
+ *   grad_xs[r] = weight[e]^T grad_ys[r]   (rows of no expert 0)
+ *   grad_weight[e] = sum over the expert's rows of grad_ys[r] xs[r]^T
+ *   grad_bias[e] = sum over the expert's rows of grad_ys[r]
+ * grad_ys and the gradients of dtype, the values of xs and weight rounded to
+ * float16 where that is dtype (as gs_rows_unpack8 does).  grad_xs may be NULL
+ * (weight is then not read), grad_bias may be NULL, and grad_weight where
+ * grad_bias is (xs is then not read).
+ */
+int gs_expert_linear8_bwd(const void* grad_ys, const uint8_t* xs, const uint8_t* xs_scales,
+                          const int32_t* offsets, const uint8_t* weight,
+                          const uint8_t* weight_scales, int64_t rows, int experts,
+                          int in_features, int out_features, int dtype, void* grad_xs,
+                          void* grad_weight, void* grad_bias, void* workspace,
+                          size_t workspace_bytes, int32_t* d_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,277 @@
+"""The experts' products of 8-bit rows (gs_expert_linear8_fwd / _bwd) against
+their 64-bit form.
+
+Every product of two 8-bit elements is exact in float32, so a sum of n of them
+is off by at most the bound of head_util's sums; the gradients' products are
+those of gs_expert_linear_bwd."""
+
+import pytest
+import torch
+
+from head8_util import cut, values_ref
+from head_util import (DEV, TYPES, check, gen, linear_bwd_ref, linear_ref, randn, routed)
+from tile_gaussian_splat_gb300 import binding as gs
+
+pytestmark = pytest.mark.gpu
+
+# (tokens, topk, experts, in, out)
+SHAPES = [(1, 1, 1, 1, 1), (1, 2, 8, 256, 1024), (3, 2, 4, 16, 16), (8, 2, 3, 131, 77),
+          (20, 1, 2, 128, 128), (100, 2, 4, 64, 192), (333, 2, 5, 129, 193), (500, 3, 7, 48, 24),
+          (700, 2, 3, 512, 384), (257, 1, 2, 640, 1000), (1500, 2, 40, 200, 72),
+          (2000, 1, 1, 1030, 260), (4000, 2, 6, 259, 131), (129, 1, 1, 2048, 64)]
+
+
+def _packed(seed, rows, E, i, o, kept):
+    g = gen(seed)
+    x = randn(g, rows, i) * torch.exp(randn(g, rows, 1))
+    x[kept:] = 0
+    w = randn(g, E * o, i) * torch.exp(randn(g, E * o, 1)) / i ** 0.5
+    xq, xs = gs.gs_rows_pack8(x)
+    wq, ws = gs.gs_rows_pack8(w)
+    return xq, xs, wq.reshape(E, o, -1), ws.reshape(E, o, -1)
+
+
+def _values(p, i, dtype=None):
+    out = values_ref(p[0], p[1], i), values_ref(p[2], p[3], i)
+    return out if dtype is None else tuple(cut(v, dtype).to(dtype).double() for v in out)
+
+
+def _check_fwd(p, offsets, i, bias, dtype):
+    st = gs.new_status(DEV)
+    ys = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], i, bias, dtype=dtype,
+                                  d_status=st)
+    gs.check_status(st)
+    x, w = _values(p, i)
+    ref, slack = linear_ref(x, offsets, w, bias)
+    check(ys, ref, slack, "ys")
+    return ys
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("tokens,topk,experts,i,o", SHAPES)
+def test_forward_and_backward(tokens, topk, experts, i, o, dtype):
+    seed = tokens + 7 * i + o
+    _, offsets, _, _ = routed(seed, tokens, topk, experts)
+    R = tokens * topk
+    p = _packed(seed, R, experts, i, o, int(offsets[-1]))
+    g = gen(seed + 1)
+    for bias in (None, randn(g, experts, o, dtype=dtype)):
+        _check_fwd(p, offsets, i, bias, dtype)
+    gys = randn(g, R, o, dtype=dtype)
+    st = gs.new_status(DEV)
+    grads = gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], i, d_status=st)
+    gs.check_status(st)
+    # float16 gradients take the values as float16
+    x, w = _values(p, i, torch.float16 if dtype == torch.float16 else None)
+    refs, slacks = linear_bwd_ref(gys, x, offsets, w)
+    for got, ref, slack, what in zip(grads, refs, slacks, ("grad_xs", "grad_weight", "grad_bias")):
+        check(got, ref, slack, what)
+    none, gw, no = gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], i, bias=False,
+                                            input=False)
+    assert none is None and no is None and torch.equal(gw, grads[1])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_experts_without_rows_and_rows_without_experts(dtype):
+    _, offsets, _, _ = routed(3, 600, 2, 9, drop=0.4, to=[2, 3, 7])
+    kept = int(offsets[-1])
+    p = _packed(3, 1200, 9, 160, 144, 1200)  # the rows behind the last expert's hold numbers
+    ys = _check_fwd(p, offsets, 160, None, dtype)
+    assert not bool(ys[kept:].any())
+    # nor does a NaN there reach a result
+    raw = p[0].view(torch.uint8)
+    raw[kept:] = 0x7f
+    assert torch.equal(ys, gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 160,
+                                                    dtype=dtype))
+    gys = randn(gen(4), 1200, 144, dtype=dtype)
+    gys[kept:] = float("nan")
+    gx, gw, gb = gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], 160)
+    assert not bool(gx[kept:].any())
+    for e in (0, 1, 4, 5, 6, 8):
+        assert not bool(gw[e].any()) and not bool(gb[e].any())
+    x, w = _values(p, 160, torch.float16 if dtype == torch.float16 else None)
+    refs, slacks = linear_bwd_ref(gys[:kept], x[:kept], offsets, w)
+    for got, ref, slack in zip((gx[:kept], gw, gb), refs, slacks):
+        check(got, ref, slack, "gradients")
+
+
+def test_scales_far_apart():
+    """Blocks of a row whose powers of two differ by far more than the
+    elements' own range."""
+    g = gen(21)
+    E, R, i, o = 2, 400, 700, 96
+    powers = torch.tensor([-30, 20, 0, -5, 11, 3], device=DEV)
+    each = torch.exp2(powers.float()).repeat_interleave(128)[:i]
+    x, w = randn(g, R, i) * each, randn(g, E * o, i) * each.flip(0)
+    p = (*gs.gs_rows_pack8(x), *(t.reshape(E, o, -1) for t in gs.gs_rows_pack8(w)))
+    offsets = torch.tensor([0, 150, 400], dtype=torch.int32, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        _check_fwd(p, offsets, i, None, dtype)
+
+
+@pytest.mark.parametrize("rows", [5, 700])
+def test_nan_stays_in_its_row(rows):
+    offsets = torch.tensor([0, 2, rows], dtype=torch.int32, device=DEV)
+    p = _packed(5, rows, 2, 300, 80, rows)
+    clean = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 300)
+    p[0].view(torch.uint8)[3, 140] = 0x7f
+    ys = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 300)
+    others = [r for r in range(rows) if r != 3]
+    assert torch.equal(ys[others], clean[others]) and bool(torch.isnan(ys[3]).all())
+
+
+@pytest.mark.parametrize("rows", [16, 640])
+def test_long_sums_of_one_sign(rows):
+    """32768 positive terms, added up over at most 4096 of them, 32 at a time
+    and each time cut off by less than 2^-23 of the sum (1.5e-5 in all), then
+    once for each of those sums (8 roundings)."""
+    g = gen(6)
+    i, o = 32768, 64
+    x, w = randn(g, rows, i).abs(), randn(g, o, i).abs()
+    p = (*gs.gs_rows_pack8(x), *(t.reshape(1, o, -1) for t in gs.gs_rows_pack8(w)))
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    ys = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], i, dtype=torch.float32)
+    xv, wv = _values(p, i)
+    ref = xv @ wv[0].t()
+    assert float(((ys - ref) / ref).abs().max()) <= 2e-5
+
+
+def test_no_rows():
+    p = _packed(7, 4, 3, 32, 40, 4)
+    offsets = torch.zeros(4, dtype=torch.int32, device=DEV)
+    none = p[0][:0], p[1][:0]
+    assert gs.gs_expert_linear8_fwd(*none, offsets, p[2], p[3], 32).shape == (0, 40)
+    gx, gw, gb = gs.gs_expert_linear8_bwd(torch.empty((0, 40), device=DEV), *none, offsets, p[2],
+                                          p[3], 32)
+    assert gx.shape == (0, 32) and not bool(gw.any()) and not bool(gb.any())
+
+
+def test_offsets_that_lie_are_clamped():
+    p = _packed(8, 50, 3, 64, 40, 50)
+    lies = torch.tensor([-5, 70, 20, 4000], dtype=torch.int32, device=DEV)
+    true = torch.tensor([0, 50, 50, 50], dtype=torch.int32, device=DEV)
+    a = gs.gs_expert_linear8_fwd(p[0], p[1], lies, p[2], p[3], 64)
+    assert torch.equal(a, gs.gs_expert_linear8_fwd(p[0], p[1], true, p[2], p[3], 64))
+
+
+def test_outputs_of_any_alignment_repeat_and_streams():
+    _, offsets, _, _ = routed(9, 900, 2, 4)
+    p = _packed(9, 1800, 4, 192, 136, 1800)
+    whole = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 192)
+    room = torch.zeros(1800 * 136 + 1, dtype=torch.bfloat16, device=DEV)
+    odd = room[1:].reshape(1800, 136)
+    gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 192, out=odd)
+    assert torch.equal(odd, whole) and float(room[0]) == 0
+    gys = randn(gen(9), 1800, 136, dtype=torch.bfloat16)
+    shifted = torch.empty(1800 * 136 + 1, dtype=torch.bfloat16, device=DEV)[1:].reshape(1800, 136)
+    shifted.copy_(gys)
+    grads = gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], 192)
+    again = gs.gs_expert_linear8_bwd(shifted, p[0], p[1], offsets, p[2], p[3], 192)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 192, stream=side)
+    grads2 = gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], 192, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, whole) and all(torch.equal(a, b) for a, b in zip(grads, grads2))
+
+
+def test_gradients_against_differences():
+    """The product is linear in the values of xs and in bias, so differences
+    along them have rounding errors only (float32 over 200 terms, 1e-4)."""
+    _, offsets, _, _ = routed(10, 90, 2, 3)
+    R, i, o = 180, 200, 50
+    p = _packed(10, R, 3, i, o, R)
+    q = _packed(11, R, 3, i, o, R)
+    g = gen(12)
+    gys = randn(g, R, o)
+    gx, gw, gb = gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], i)
+    run = lambda a, w, b=None: gs.gs_expert_linear8_fwd(
+        a[0], a[1], offsets, w[2], w[3], i, b, dtype=torch.float32).double()
+    dot = lambda a, b: float((a.double() * b).sum())
+    x0, x1 = values_ref(p[0], p[1], i), values_ref(q[0], q[1], i)
+    w0, w1 = values_ref(p[2], p[3], i), values_ref(q[2], q[3], i)
+    size = lambda a, b: 1e-4 * float(a.double().norm() * b.norm())
+    diff = dot(gys, run(q, p) - run(p, p))
+    assert abs(diff - dot(gx, x1 - x0)) <= size(gx, x1 - x0)
+    diff = dot(gys, run(p, q) - run(p, p))
+    assert abs(diff - dot(gw, w1 - w0)) <= size(gw, w1 - w0)
+    b = randn(g, 3, o)
+    diff = dot(gys, run(p, p, b) - run(p, p))
+    assert abs(diff - dot(gb, b.double())) <= size(gb, b.double())
+
+
+def test_captured_and_replayed():
+    _, offsets, _, _ = routed(13, 1000, 2, 8)
+    p = _packed(13, 2000, 8, 256, 320, 2000)
+    gys = randn(gen(13), 2000, 320, dtype=torch.bfloat16)
+    run = lambda: (gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 256),
+                   *gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], 256))
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for seed in (1, 2):
+        n = _packed(seed, 2000, 8, 256, 320, 2000)
+        for a, b in zip(p, n):
+            a.view(torch.uint8).copy_(b.view(torch.uint8))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, run()))
+
+
+def test_a_layer_from_the_router_on():
+    """The router's choice, rows packed and dispatched as they are, the
+    products of both layers and the answer; 8-bit rows dispatch as 16-bit ones."""
+    g = gen(30)
+    T, D, H, O, E, k = 700, 96, 144, 24, 6, 2
+    x, logits = randn(g, T, D), randn(g, T, E)
+    keep = torch.rand(T, generator=g, device=DEV) > 0.2
+    w1, w2 = randn(g, E * H, D) / D ** 0.5, randn(g, E * O, H) / H ** 0.5
+    ids, weights, counts, _ = gs.gs_expert_route_fwd(logits, k, keep=keep)
+    offsets, _, slots = gs.gs_expert_sort(ids, E)
+    assert torch.equal(offsets[1:] - offsets[:-1], counts[:E])
+    q, s = gs.gs_rows_pack8(x)
+    xq = gs.gs_expert_dispatch(q.view(torch.float16), slots, offsets).view(q.dtype)
+    xs = gs.gs_expert_dispatch(s.view(torch.float16), slots, offsets).view(s.dtype)
+    p1 = [t.reshape(E, H, -1) for t in gs.gs_rows_pack8(w1)]
+    p2 = [t.reshape(E, O, -1) for t in gs.gs_rows_pack8(w2)]
+    h = gs.gs_expert_linear8_fwd(xq, xs, offsets, *p1, D, dtype=torch.float32).relu_()
+    ys = gs.gs_expert_linear8_fwd(*gs.gs_rows_pack8(h), offsets, *p2, H, dtype=torch.float32)
+    y = gs.gs_expert_combine(ys, slots, weights)
+    # the same in 64 bits, the rounding of h to 8 bits taken over
+    xv = values_ref(q, s, D)
+    hv = values_ref(*gs.gs_rows_pack8(h), H)
+    v1, v2 = values_ref(*p1, D), values_ref(*p2, H)
+    want = torch.zeros((T, O), dtype=torch.float64, device=DEV)
+    for t in range(T):
+        for j in range(k):
+            if int(ids[t, j]) < 0:
+                continue
+            e, r = int(ids[t, j]), int(slots[t, j])
+            ref = torch.relu(v1[e] @ xv[t])
+            assert float((h[r] - ref).abs().max()) <= 1e-5 * float(ref.abs().max())
+            want[t] += weights[t, j].double() * (v2[e] @ hv[r])
+    assert float((y - want).norm()) <= 1e-6 * float(want.norm())
+    assert not bool(y[~keep].any())
+
+
+def test_refusals():
+    p = _packed(14, 20, 2, 64, 32, 20)
+    offsets = torch.tensor([0, 10, 20], dtype=torch.int32, device=DEV)
+    gys = torch.zeros((20, 32), device=DEV)
+    fwd, bwd = gs.gs_expert_linear8_fwd, gs.gs_expert_linear8_bwd
+    for bad in (lambda: fwd(p[0], p[1], offsets, p[2], p[3], 80),
+                lambda: fwd(p[0], p[1], offsets[:2], p[2], p[3], 64),
+                lambda: fwd(p[0], p[1][:10], offsets, p[2], p[3], 64),
+                lambda: fwd(p[0].view(torch.uint8), p[1], offsets, p[2], p[3], 64),
+                lambda: fwd(p[0], p[1], offsets, p[2][0], p[3], 64),
+                lambda: fwd(p[0], p[1], offsets, p[2], p[3], 64, gys[:2]),
+                lambda: fwd(p[0], p[1], offsets, p[2], p[3], 64, dtype=torch.float64),
+                lambda: fwd(p[0], p[1], offsets, p[2], p[3], 64, out=gys),
+                lambda: fwd(p[0].cpu(), p[1].cpu(), offsets, p[2], p[3], 64),
+                lambda: bwd(gys[:19], p[0], p[1], offsets, p[2], p[3], 64),
+                lambda: bwd(gys.double(), p[0], p[1], offsets, p[2], p[3], 64),
+                lambda: bwd(gys, p[0], p[1], offsets, p[2], p[3], 63 + 17)):
+        with pytest.raises(ValueError):
+            bad()

@@ -69,6 +69,16 @@ SIGNATURES = {
     "gs_expert_linear_fwd": (I32, [P, P, P, P, I64, I32, I32, I32, I32, P, P, SZ, P, P]),
     "gs_expert_linear_bwd_workspace_size": (SZ, [I64, I32, I32, I32, I32, I32]),
     "gs_expert_linear_bwd": (I32, [P, P, P, P, I64, I32, I32, I32, I32, P, P, P, P, SZ, P, P]),
+    "gs_expert_route_workspace_size": (SZ, [I64, I32]),
+    "gs_expert_route_fwd": (I32, [P, I64, P, I64, I32, I32, I32, I32, P, P, P, P, P, SZ, P]),
+    "gs_expert_route_bwd": (I32, [P, I64, P, P, P, P, I64, I32, I32, I32, I32, P, I64, P, P]),
+    "gs_rows_pack8": (I32, [P, I64, I64, I32, I32, P, P, P]),
+    "gs_rows_unpack8": (I32, [P, P, I64, I32, I32, P, I64, P]),
+    "gs_expert_linear8_fwd_workspace_size": (SZ, [I64, I32, I32, I32, I32]),
+    "gs_expert_linear8_fwd": (I32, [P, P, P, P, P, P, I64, I32, I32, I32, I32, P, P, SZ, P, P]),
+    "gs_expert_linear8_bwd_workspace_size": (SZ, [I64, I32, I32, I32, I32, I32]),
+    "gs_expert_linear8_bwd": (I32, [P, P, P, P, P, P, I64, I32, I32, I32, I32, P, P, P, P, SZ, P,
+                                    P]),
 }
 
 
@@ -772,4 +782,171 @@ def gs_expert_linear_bwd(grad_ys, xs, offsets, weight, bias=True, input=True, d_
     _check(L.gs_expert_linear_bwd(_ptr(grad_ys), _ptr(xs), _ptr(offsets), _ptr(weight), R, E, i,
                                   o, dt, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), n_bytes,
                                   _ptr(d_status), _on(stream, xs)), "gs_expert_linear_bwd")
+    return gx, gw, gb
+
+
+def gs_expert_route_fwd(logits, topk, keep=None, renormalise=True, balance=True, workspace=None,
+                        stream=None):
+    """The choice of experts for logits (tokens, experts): (ids int32 (tokens,
+    topk), weights float32 (tokens, topk), counts int32 (experts + 1,), loss
+    float32 (1,)), the last two None without balance.  keep bool (tokens,):
+    the tokens that take part (None: all); the others' ids are -1.  counts'
+    last element is how many tokens take part."""
+    dt = _dtype(logits, "logits")
+    if logits.dim() != 2:
+        _refuse("logits: (tokens, experts) expected")
+    T, E = logits.shape
+    lp, ldl = _rows(logits, "logits")
+    if keep is not None and (keep.dtype not in (torch.bool, torch.uint8) or keep.shape != (T,)):
+        _refuse("keep: bool (tokens,) expected")
+    if not 0 < topk <= E:
+        _refuse("topk: at least one choice and at most every expert expected")
+    ids = _new((T, topk), torch.int32, logits, stream)
+    weights = _new((T, topk), torch.float32, logits, stream)
+    counts = loss = ws = None
+    n_bytes = 0
+    L = lib()
+    if balance:
+        counts = _new((E + 1,), torch.int32, logits, stream)
+        loss = _new((1,), torch.float32, logits, stream)
+        n_bytes = L.gs_expert_route_workspace_size(T, E)
+        ws = _workspace(workspace, n_bytes, logits, stream)
+    _check(L.gs_expert_route_fwd(lp, ldl, _ptr(keep), T, topk, E, dt, int(renormalise), _ptr(ids),
+                                 _ptr(weights), _ptr(counts), _ptr(loss), _ptr(ws), n_bytes,
+                                 _on(stream, logits)), "gs_expert_route_fwd")
+    return ids, weights, counts, loss
+
+
+def gs_expert_route_bwd(logits, ids, counts=None, grad_weights=None, grad_loss=None,
+                        renormalise=True, d_status=None, out=None, stream=None):
+    """The gradient in the logits of gs_expert_route_fwd's weights
+    (grad_weights float32 (tokens, topk)) and loss (grad_loss, one float32 on
+    the device), each None for zeros; counts are needed with grad_loss."""
+    dt = _dtype(logits, "logits")
+    if logits.dim() != 2 or ids.dim() != 2 or ids.dtype != torch.int32 or \
+            ids.shape[0] != logits.shape[0]:
+        _refuse("logits (tokens, experts) and ids int32 (tokens, topk) expected")
+    T, E = logits.shape
+    k = ids.shape[1]
+    lp, ldl = _rows(logits, "logits")
+    if grad_weights is not None:
+        _same(grad_weights, ids.shape, torch.float32, "grad_weights")
+    if grad_loss is not None:
+        if grad_loss.numel() != 1 or grad_loss.dtype != torch.float32:
+            _refuse("grad_loss: one float32 expected")
+        if counts is None:
+            _refuse("counts: needed with grad_loss")
+        _same(counts, (E + 1,), torch.int32, "counts")
+    if out is None:
+        grad = _new((T, E), logits.dtype, logits, stream)
+        op, ldo = grad.data_ptr() or None, E
+    else:
+        grad = _same(out, (T, E), logits.dtype, "out")
+        op, ldo = _rows(grad, "out")
+    _check(lib().gs_expert_route_bwd(lp, ldl, _ptr(ids), _ptr(counts), _ptr(grad_weights),
+                                     _ptr(grad_loss), T, k, E, dt, int(renormalise), op, ldo,
+                                     _ptr(d_status), _on(stream, logits)), "gs_expert_route_bwd")
+    return grad
+
+
+# 8-bit rows: q float8_e4m3fn (..., channels rounded up to 16) and scales
+# float8_e8m0fnu (..., a power of two for every 128 channels, rounded up to 4).
+_Q8, _S8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _widths8(channels):
+    return (channels + 15) // 16 * 16, (channels + 511) // 512 * 4
+
+
+def _rows8(q, scales, channels, what):
+    """(pointer to q, pointer to scales) of 8-bit rows of `channels`."""
+    wide, blocks = _widths8(channels)
+    if q.dtype != _Q8 or scales.dtype != _S8 or q.dim() == 0 or q.shape[-1] != wide or \
+            scales.shape != (*q.shape[:-1], blocks):
+        _refuse(f"{what}: float8_e4m3fn (..., {wide}) and float8_e8m0fnu (..., {blocks}) expected")
+    return _ptr(q), _ptr(scales)
+
+
+def gs_rows_pack8(x, stream=None):
+    """The rows of x (..., channels) in 8 bits: (q float8_e4m3fn (..., channels
+    rounded up to 16), scales float8_e8m0fnu (..., one for every 128 channels,
+    rounded up to 4)); zeros behind the last channel and block."""
+    dt = _dtype(x, "x")
+    xp, ldx = _rows(x, "x")
+    ch = x.shape[-1]
+    wide, blocks = _widths8(ch)
+    q = _new((*x.shape[:-1], wide), _Q8, x, stream)
+    scales = _new((*x.shape[:-1], blocks), _S8, x, stream)
+    _check(lib().gs_rows_pack8(xp, ldx, x.numel() // ch if ch else 0, ch, dt, _ptr(q),
+                               _ptr(scales), _on(stream, x)), "gs_rows_pack8")
+    return q, scales
+
+
+def gs_rows_unpack8(q, scales, channels, dtype=torch.bfloat16, out=None, stream=None):
+    """The values (..., channels) of gs_rows_pack8's rows, rounded to dtype."""
+    qp, sp = _rows8(q, scales, channels, "q, scales")
+    shape = (*q.shape[:-1], channels)
+    if out is None:
+        y = _new(shape, dtype, q, stream)
+        yp, ldy = y.data_ptr() or None, channels
+    else:
+        y = _same(out, shape, dtype, "out")
+        yp, ldy = _rows(y, "out")
+    _check(lib().gs_rows_unpack8(qp, sp, q.numel() // q.shape[-1] if channels else 0, channels,
+                                 _dtype(y, "dtype"), yp, ldy, _on(stream, q)), "gs_rows_unpack8")
+    return y
+
+
+def _linear8_shapes(xs, offsets, weight, channels):
+    E = _experts(offsets)
+    if weight.dim() != 3 or weight.shape[0] != E or xs.dim() != 2 or channels < 1:
+        _refuse("xs (rows, ...) and weight (experts, out_features, ...) expected")
+    return xs.shape[0], E, weight.shape[1]
+
+
+def gs_expert_linear8_fwd(xs, xs_scales, offsets, weight, weight_scales, in_features, bias=None,
+                          dtype=torch.bfloat16, d_status=None, out=None, workspace=None,
+                          stream=None):
+    """gs_expert_linear_fwd of 8-bit rows (gs_rows_pack8): xs (rows, ...),
+    weight (experts, out_features, ...) of in_features channels, bias
+    (experts, out_features) of dtype or None.  Returns ys (rows,
+    out_features) of dtype."""
+    R, E, o = _linear8_shapes(xs, offsets, weight, in_features)
+    xp, xsp = _rows8(xs, xs_scales, in_features, "xs")
+    wp, wsp = _rows8(weight, weight_scales, in_features, "weight")
+    if bias is not None:
+        _same(bias, (E, o), dtype, "bias")
+    ys = _new((R, o), dtype, xs, stream) if out is None else _same(out, (R, o), dtype, "out")
+    dt = _dtype(ys, "dtype")
+    L = lib()
+    n_bytes = L.gs_expert_linear8_fwd_workspace_size(R, E, in_features, o, dt)
+    ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
+    _check(L.gs_expert_linear8_fwd(xp, xsp, _ptr(offsets), wp, wsp, _ptr(bias), R, E, in_features,
+                                   o, dt, _ptr(ys), _ptr(ws), n_bytes, _ptr(d_status),
+                                   _on(stream, xs)), "gs_expert_linear8_fwd")
+    return ys
+
+
+def gs_expert_linear8_bwd(grad_ys, xs, xs_scales, offsets, weight, weight_scales, in_features,
+                          bias=True, input=True, d_status=None, workspace=None, stream=None):
+    """Gradients of gs_expert_linear8_fwd in the values of its 8-bit rows:
+    (grad_xs, grad_weight, grad_bias) of grad_ys' type, the first None without
+    `input`, the last None without `bias`."""
+    dt = _dtype(grad_ys, "grad_ys")
+    R, E, o = _linear8_shapes(xs, offsets, weight, in_features)
+    xp, xsp = _rows8(xs, xs_scales, in_features, "xs")
+    wp, wsp = _rows8(weight, weight_scales, in_features, "weight")
+    _same(grad_ys, (R, o), grad_ys.dtype, "grad_ys")
+    t = grad_ys.dtype
+    gx = _new((R, in_features), t, grad_ys, stream) if input else None
+    gw = _new((E, o, in_features), t, grad_ys, stream)
+    gb = _new((E, o), t, grad_ys, stream) if bias else None
+    L = lib()
+    n_bytes = L.gs_expert_linear8_bwd_workspace_size(R, E, in_features, o, dt,
+                                                     grad_ys.data_ptr() % 16 == 0)
+    ws = _workspace(workspace, n_bytes, grad_ys, stream) if n_bytes else None
+    _check(L.gs_expert_linear8_bwd(_ptr(grad_ys), xp, xsp, _ptr(offsets), wp, wsp, R, E,
+                                   in_features, o, dt, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws),
+                                   n_bytes, _ptr(d_status), _on(stream, grad_ys)),
+           "gs_expert_linear8_bwd")
     return gx, gw, gb

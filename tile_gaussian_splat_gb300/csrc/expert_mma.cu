@@ -54,6 +54,7 @@
 #include <cuda.h>
 
 #include "expert_rows.cuh"
+#include "expert_tiles.cuh"
 #include "gs_device.cuh"
 #include "gs_head_internal.h"
 #include "gs_mma.cuh"
@@ -65,9 +66,7 @@ namespace {
 
 enum Product { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 
-constexpr int kHigh = 128;        // rows of an output tile
 constexpr int kSlice = 64;        // terms of the sum per stage: 128 bytes
-constexpr int kOutWarps = 8;      // two for each quarter of the tile's rows
 // Warps: 0 copies, 1 issues products, 2 and 3 (and two after the output warps)
 // help with the weight gradient, from 4 on they write the output.
 template <int kProduct>
@@ -89,7 +88,7 @@ struct ProductArgs {
     int experts;
     int high, width, depth;  // extents: high of the weight gradient, depth of the others
     int groups;              // weight gradient: shares of the rows
-    int pairs;               // sums over plane pairs: 1, or 6 for float32
+    int pairs;               // sums over plane pairs: 1, for float32 6 (3 with 8-bit rows)
     int round;               // slices summed before they are added to the running sum
     int rounds;              // some sums take several rounds
     int vectors;             // output rows are whole 16-byte vectors
@@ -135,25 +134,16 @@ constexpr size_t smem_bytes(int experts) {
            2 * sizeof(int32_t) * (size_t)(experts + 1);
 }
 
-// Planes of A and B in sum number `sum` of g.pairs, small terms first.
+// Planes of A and B in sum number `sum` of g.pairs, small terms first (three
+// pairs: B has one plane).
 __device__ __forceinline__ int plane_a(int pairs, int sum) {
+    if (pairs == 3) return 2 - sum;
     return 0x001102 >> 4 * (6 - pairs + sum) & 15;  // 2, 0, 1, 1, 0, 0
 }
 __device__ __forceinline__ int plane_b(int pairs, int sum) {
+    if (pairs == 3) return 0;
     return 0x010120 >> 4 * (6 - pairs + sum) & 15;  // 0, 2, 1, 0, 1, 0
 }
-
-// A place in a ring of kCount stages, and how often it has gone round.
-template <int kCount>
-struct Ring {
-    uint32_t stage = 0, turn = 0;
-    __device__ __forceinline__ void advance(int count = kCount) {
-        if ((int)++stage == count) {
-            stage = 0;
-            ++turn;
-        }
-    }
-};
 
 // One output tile, or one expert's part of it (kWeightGrad).
 struct Tile {
@@ -169,14 +159,6 @@ struct Tile {
 
 __device__ __forceinline__ int64_t share_begin(int64_t total, int groups, int group) {
     return total * group / groups;
-}
-
-// Columns of a tile from n0 on that are computed: those inside the output, in
-// the matrix instruction's steps.
-template <int kBlocks, int kWide>
-__device__ __forceinline__ int tile_columns(int width, int n0) {
-    constexpr int kStep = 16 * kBlocks;
-    return min(kWide, (width - n0 + kStep - 1) / kStep * kStep);
 }
 
 // The tiles of one pair of blocks (or block), in order; every warp of it walks
@@ -252,81 +234,6 @@ struct Walk {
         return next_round(c);
     }
 };
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Eight results of the output's type in 16 (half types) or 32 bytes.
-template <typename Out>
-__device__ __forceinline__ void pack8(const float* f, uint4* v) {
-    if constexpr (sizeof(Out) == 4) {
-        v[0] = uint4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                     __float_as_uint(f[3])};
-        v[1] = uint4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
-                     __float_as_uint(f[7])};
-    } else {
-        v[0] = uint4{pack2<Out>(f[0], f[1]), pack2<Out>(f[2], f[3]), pack2<Out>(f[4], f[5]),
-                     pack2<Out>(f[6], f[7])};
-    }
-}
-
-// 32 rows x 64 bytes of output held one row a lane (four 16-byte vectors),
-// turned through shared memory so that four lanes write one row's 64
-// contiguous bytes (or, where rows of the output are not whole vectors, single
-// elements).  valid_rows of the rows and `left` of a row's elements are inside
-// the output.
-template <typename Out>
-__device__ __forceinline__ void write_block(char* staging, const uint4* v, Out* out,
-                                            int64_t pitch, int valid_rows, int left,
-                                            bool vectors) {
-    const int lane = threadIdx.x & 31;
-    constexpr int kVec = 16 / sizeof(Out), kRow = 64 / sizeof(Out);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(staging + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = v[j];
-    __syncwarp();
-    if (vectors) {
-        const int j = lane & 3;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + lane / 4;
-            const uint4 x =
-                *reinterpret_cast<const uint4*>(staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4));
-            if (r < valid_rows && j * kVec < left)
-                *reinterpret_cast<uint4*>(out + r * pitch + j * kVec) = x;
-        }
-    } else {
-        const int e = lane % kRow, j = e / kVec;
-        for (int r = lane / kRow; r < min(32, valid_rows); r += 32 / kRow) {
-            const Out x = *reinterpret_cast<const Out*>(
-                staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4) + e % kVec * sizeof(Out));
-            if (e < left) out[r * pitch + e] = x;
-        }
-    }
-    __syncwarp();
-}
-
-// By the output warps: n elements from `out` on are 0; `at` and `stride`: this
-// thread's place among all of them.
-template <typename Out>
-__device__ __forceinline__ void zero_range(Out* out, int64_t n, int64_t at, int64_t stride,
-                                           bool vectors) {
-    if (vectors)
-        for (int64_t i = at; i < n * (int64_t)sizeof(Out) / 16; i += stride)
-            reinterpret_cast<uint4*>(out)[i] = uint4{0, 0, 0, 0};
-    else
-        for (int64_t i = at; i < n; i += stride) out[i] = from_f<Out>(0.f);
-}
 
 // T: type of the planes; Out: of the output and of bias.
 template <typename T, typename Out, int kProduct, int kBlocks, int kWide>
@@ -845,36 +752,12 @@ __global__ void __launch_bounds__(kPlaneThreads, kVectors ? 8 : 6)
     }
 }
 
-// cuTensorMapEncodeTiled, found through the runtime (the library does not
-// link the driver).
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // An operand as the tiled copies read it.
 struct Planes {
     const void* base;
     int64_t rows;  // of one plane
     int columns, pitch, count;
 };
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether rows of `columns` elements from p on can be copied as they lie.
 bool copyable(int dtype, const void* p, int columns) {
@@ -933,45 +816,13 @@ bool make_map(CUtensorMap* map, int dtype, const Planes& p, int experts, int box
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 152;
-    return n;
-}
-
 template <typename T, typename Out, int kProduct, int kBlocks, int kWide>
 int launch(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g, int64_t max_items,
            cudaStream_t s) {
-    const auto kernel = k_product<T, Out, kProduct, kBlocks, kWide>;
-    const size_t smem = smem_bytes<kBlocks, kWide>(g.experts);
     static PerDevice raised, resident;
-    if (!raised.get(0, [&] {
-            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)smem_bytes<kBlocks, kWide>(GS_MAX_EXPERTS)) ==
-                   cudaSuccess;
-        }))
-        return GS_ERR_CUDA;
-    cudaLaunchConfig_t config = {};
-    config.gridDim = dim3(kBlocks);
-    config.blockDim = dim3(kMmaThreads<kProduct>);
-    config.dynamicSmemBytes = smem;
-    config.stream = s;
-    cudaLaunchAttribute cluster = {};
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = kBlocks;
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    config.attrs = &cluster;
-    config.numAttrs = 1;
-    // as many pairs as are resident at once (an SM without a partner in its
-    // cluster's reach stays free)
-    const int clusters = resident.get(152 / kBlocks, [&] {
-        int n = 0;
-        return cudaOccupancyMaxActiveClusters(&n, kernel, &config) == cudaSuccess ? n : 0;
-    });
-    config.gridDim = dim3((unsigned)(std::min<int64_t>(max_items, clusters) * kBlocks));
-    return cudaLaunchKernelEx(&config, kernel, a, b, g) == cudaSuccess ? GS_OK : GS_ERR_CUDA;
+    return launch_walk<kBlocks>(raised, resident, k_product<T, Out, kProduct, kBlocks, kWide>,
+                                kMmaThreads<kProduct>, smem_bytes<kBlocks, kWide>(g.experts),
+                                smem_bytes<kBlocks, kWide>(GS_MAX_EXPERTS), max_items, s, a, b, g);
 }
 
 // Two blocks a tile of 256 x 256 where those fill every pair of SMs twice, or
@@ -997,6 +848,10 @@ int launch_rows(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& g
     return launch<T, Out, kProduct, 1, 128>(a, b, g, pieces, s);
 }
 
+// Sums over plane pairs: the planes of float32 gradients meet one plane of
+// 8-bit rows.
+int plane_pairs(const LinearArgs& a) { return a.dtype != GS_F32 ? 1 : a.packed ? 3 : 6; }
+
 // How the weight gradient is cut up.
 struct GradPlan {
     bool pairs;
@@ -1015,7 +870,7 @@ GradPlan grad_plan(const LinearArgs& a) {
     // Shares: more of them occupy more units and fill the last round of them
     // better, but each leaves partial sums (two tiles an item, written and
     // read).  The least time by this estimate of a unit's walk: 0.35 us a
-    // slice (of each of a float32 product's six sums), 2 us for an expert's
+    // slice (of each of a float32 product's sums), 2 us for an expert's
     // part to come out, and the sums at 5 TB/s (where experts are longer than a
     // slice, so that a cut falls inside one).  16 experts of 8192 rows, 1024
     // x 512: 126 us in 9 shares, 150 in 19, 170 in 5.
@@ -1024,7 +879,7 @@ GradPlan grad_plan(const LinearArgs& a) {
     double best = 0.0;
     for (int64_t g = 1; g <= most; ++g) {
         const int64_t items = g * p.tiles;
-        const double walk = slices / g * 0.35 * (a.dtype == GS_F32 ? 6 : 1) +
+        const double walk = slices / g * 0.35 * plane_pairs(a) +
                             2.0 * (a.experts / (double)g + 1);
         const double inside = std::max(0.0, 1.0 - a.experts / slices);
         const double sums = g > 1 ? 3.0 + inside * 16.0 * items * p.high * p.wide / 5e6 : 0.0;
@@ -1075,7 +930,7 @@ ProductArgs product_args(const LinearArgs& a, void* out, int width, int depth) {
     g.experts = a.experts;
     g.width = width;
     g.depth = depth;
-    g.pairs = a.dtype == GS_F32 ? 6 : 1;
+    g.pairs = plane_pairs(a);
     g.round = a.dtype == GS_F32 ? kRound : kHalfRound;
     g.rounds = ceil_div(depth, kSlice) > g.round;
     g.vectors = aligned16(out) && (size_t)width * dtype_size(a.dtype) % 16 == 0;
@@ -1132,6 +987,28 @@ bool few_dx(const LinearArgs& a, const void* weight) {
     return !copyable(a.dtype, weight, a.in) && few_rows(a, false);
 }
 
+// The gradients of weight and bias from the rows' planes, of map_dtype.
+int launch_grad_of_weight(const LinearArgs& a, int map_dtype, const Planes& gy, const Planes& x,
+                          void* grad_weight, void* grad_bias, float* sums, cudaStream_t s) {
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, map_dtype, gy, 0, kSlice) || !make_map(&mb, map_dtype, x, 0, kSlice))
+        return GS_ERR_CUDA;
+    const GradPlan p = grad_plan(a);
+    ProductArgs g = product_args(a, grad_weight, a.in, 0);
+    g.high = a.out;
+    g.groups = p.groups;
+    if (a.dtype != GS_F32) g.round = kHalfRowsRound;
+    // no part of a sum is longer than a share, nor than all the rows
+    g.rounds = std::min(ceil_div(a.rows, kSlice),
+                        ceil_div(a.rows / kSlice + a.experts, p.groups)) > g.round;
+    g.bias_grad = grad_bias;
+    g.partial = sums;
+    g.bias_partial = sums + partial_floats(p);
+    return with_types(a.dtype, [&](auto t, auto o) {
+        return weight_grad_of<decltype(t), decltype(o)>(ma, mb, g, p, s);
+    });
+}
+
 size_t grad_sums_bytes(const LinearArgs& a) {
     const GradPlan p = grad_plan(a);
     const size_t n = (partial_floats(p) + bias_floats(p, a.experts)) * sizeof(float);
@@ -1174,22 +1051,81 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
     }
     if (!grad_weight) return GS_OK;
     const Planes x = prepare(a.dtype, xs, a.rows, a.in, &ws, s);
-    if (!make_map(&ma, a.dtype, gy, 0, kSlice) || !make_map(&mb, a.dtype, x, 0, kSlice))
+    return launch_grad_of_weight(a, a.dtype, gy, x, grad_weight, grad_bias, sums, s);
+}
+
+namespace {
+
+// 8-bit rows as rows of half types: bfloat16 holds every value of theirs.
+constexpr int plane_dtype(int dtype) { return dtype == GS_F16 ? GS_F16 : GS_BF16; }
+
+size_t unpacked_bytes(int64_t rows, int columns) { return plane_bytes(GS_BF16, rows, columns); }
+
+Planes unpacked(int dtype, Rows8 x, int64_t rows, int columns, char** workspace, cudaStream_t s) {
+    const int pitch = (int)ceil_div(columns, 8) * 8;
+    void* out = *workspace;
+    *workspace += unpacked_bytes(rows, columns);
+    launch_unpack8(x.q, x.scales, rows, columns, dtype, out, pitch, s);
+    return Planes{out, rows, columns, pitch, 1};
+}
+
+}  // namespace
+
+size_t linear8_fwd_workspace(const LinearArgs& a) {
+    return unpacked_bytes(a.rows, a.in) + unpacked_bytes((int64_t)a.experts * a.out, a.in);
+}
+
+int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* bias, void* ys,
+                       void* workspace, cudaStream_t s) {
+    LinearArgs halves = a;
+    halves.dtype = GS_BF16;
+    const bool pairs = use_pairs(halves, a.out);
+    char* ws = static_cast<char*>(workspace);
+    const Planes pa = unpacked(GS_BF16, xs, a.rows, a.in, &ws, s);
+    const Planes pb = unpacked(GS_BF16, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, GS_BF16, pa, 0, kHigh) ||
+        !make_map(&mb, GS_BF16, pb, a.experts, box_b(pairs, a.out)))
         return GS_ERR_CUDA;
-    const GradPlan p = grad_plan(a);
-    ProductArgs g = product_args(a, grad_weight, a.in, 0);
-    g.high = a.out;
-    g.groups = p.groups;
-    if (a.dtype != GS_F32) g.round = kHalfRowsRound;
-    // no part of a sum is longer than a share, nor than all the rows
-    g.rounds = std::min(ceil_div(a.rows, kSlice),
-                        ceil_div(a.rows / kSlice + a.experts, p.groups)) > g.round;
-    g.bias_grad = grad_bias;
-    g.partial = sums;
-    g.bias_partial = sums + partial_floats(p);
-    return with_types(a.dtype, [&](auto t, auto o) {
-        return weight_grad_of<decltype(t), decltype(o)>(ma, mb, g, p, s);
+    ProductArgs g = product_args(halves, ys, a.out, a.in);
+    g.vectors = aligned16(ys) && (size_t)a.out * dtype_size(a.dtype) % 16 == 0;
+    g.bias = bias;
+    int rc = GS_OK;
+    with_dtype(a.dtype, [&](auto o) {
+        rc = launch_rows<__nv_bfloat16, decltype(o), kForward>(ma, mb, g, pairs, s);
     });
+    return rc;
+}
+
+size_t linear8_bwd_workspace(const LinearArgs& a, const void* grad_ys) {
+    size_t n = grad_sums_bytes(a);
+    if (!copyable(a.dtype, grad_ys, a.out)) n += plane_bytes(a.dtype, a.rows, a.out);
+    return n + unpacked_bytes(a.rows, a.in) + unpacked_bytes((int64_t)a.experts * a.out, a.in);
+}
+
+int launch_linear8_bwd(const LinearArgs& a, const void* grad_ys, Rows8 xs, Rows8 weight,
+                       void* grad_xs, void* grad_weight, void* grad_bias, void* workspace,
+                       cudaStream_t s) {
+    const int planes = plane_dtype(a.dtype);
+    char* ws = static_cast<char*>(workspace);
+    float* sums = reinterpret_cast<float*>(ws);
+    ws += grad_sums_bytes(a);
+    const Planes gy = prepare(a.dtype, grad_ys, a.rows, a.out, &ws, s);
+    if (grad_xs) {
+        const bool pairs = use_pairs(a, a.in);
+        const Planes w = unpacked(planes, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
+        CUtensorMap ma, mb;
+        if (!make_map(&ma, planes, gy, 0, kHigh) || !make_map(&mb, planes, w, a.experts, kSlice))
+            return GS_ERR_CUDA;
+        const ProductArgs g = product_args(a, grad_xs, a.in, a.out);
+        const int rc = with_types(a.dtype, [&](auto t, auto o) {
+            return launch_rows<decltype(t), decltype(o), kInputGrad>(ma, mb, g, pairs, s);
+        });
+        if (rc != GS_OK) return rc;
+    }
+    if (!grad_weight) return GS_OK;
+    const Planes x = unpacked(planes, xs, a.rows, a.in, &ws, s);
+    return launch_grad_of_weight(a, planes, gy, x, grad_weight, grad_bias, sums, s);
 }
 
 }  // namespace gs

@@ -1,0 +1,178 @@
+// What the tensor-core products share: the walk over stages, the columns of a
+// tile that are computed, finished results on their way to the output, and the
+// host's side of tiled copies and launches.
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+
+#include <cuda.h>
+
+#include "gs_device.cuh"
+#include "gs_mma.cuh"
+#include "gs_types.cuh"
+
+namespace gs {
+
+constexpr int kHigh = 128;        // rows of an output tile
+constexpr int kOutWarps = 8;      // two for each quarter of the tile's rows
+
+// A place in a ring of kCount stages, and how often it has gone round.
+template <int kCount>
+struct Ring {
+    uint32_t stage = 0, turn = 0;
+    __device__ __forceinline__ void advance(int count = kCount) {
+        if ((int)++stage == count) {
+            stage = 0;
+            ++turn;
+        }
+    }
+};
+
+// Columns of a tile from n0 on that are computed: those inside the output, in
+// the matrix instruction's steps.
+template <int kBlocks, int kWide>
+__device__ __forceinline__ int tile_columns(int width, int n0) {
+    constexpr int kStep = 16 * kBlocks;
+    return min(kWide, (width - n0 + kStep - 1) / kStep * kStep);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight results of the output's type in 16 (half types) or 32 bytes.
+template <typename Out>
+__device__ __forceinline__ void pack8(const float* f, uint4* v) {
+    if constexpr (sizeof(Out) == 4) {
+        v[0] = uint4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                     __float_as_uint(f[3])};
+        v[1] = uint4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                     __float_as_uint(f[7])};
+    } else {
+        v[0] = uint4{pack2<Out>(f[0], f[1]), pack2<Out>(f[2], f[3]), pack2<Out>(f[4], f[5]),
+                     pack2<Out>(f[6], f[7])};
+    }
+}
+
+// 32 rows x 64 bytes of output held one row a lane (four 16-byte vectors),
+// turned through shared memory so that four lanes write one row's 64
+// contiguous bytes (or, where rows of the output are not whole vectors, single
+// elements).  valid_rows of the rows and `left` of a row's elements are inside
+// the output.
+template <typename Out>
+__device__ __forceinline__ void write_block(char* staging, const uint4* v, Out* out,
+                                            int64_t pitch, int valid_rows, int left,
+                                            bool vectors) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kVec = 16 / sizeof(Out), kRow = 64 / sizeof(Out);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(staging + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = v[j];
+    __syncwarp();
+    if (vectors) {
+        const int j = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + lane / 4;
+            const uint4 x =
+                *reinterpret_cast<const uint4*>(staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4));
+            if (r < valid_rows && j * kVec < left)
+                *reinterpret_cast<uint4*>(out + r * pitch + j * kVec) = x;
+        }
+    } else {
+        const int e = lane % kRow, j = e / kVec;
+        for (int r = lane / kRow; r < min(32, valid_rows); r += 32 / kRow) {
+            const Out x = *reinterpret_cast<const Out*>(
+                staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4) + e % kVec * sizeof(Out));
+            if (e < left) out[r * pitch + e] = x;
+        }
+    }
+    __syncwarp();
+}
+
+// By the output warps: n elements from `out` on are 0; `at` and `stride`: this
+// thread's place among all of them.
+template <typename Out>
+__device__ __forceinline__ void zero_range(Out* out, int64_t n, int64_t at, int64_t stride,
+                                           bool vectors) {
+    if (vectors)
+        for (int64_t i = at; i < n * (int64_t)sizeof(Out) / 16; i += stride)
+            reinterpret_cast<uint4*>(out)[i] = uint4{0, 0, 0, 0};
+    else
+        for (int64_t i = at; i < n; i += stride) out[i] = from_f<Out>(0.f);
+}
+
+// cuTensorMapEncodeTiled, found through the runtime (the library does not
+// link the driver).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+inline int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 152;
+    return n;
+}
+
+// Launches `kernel` as a walk over at most max_items tiles: as many clusters of
+// kBlocks as are resident at once (an SM without a partner in its cluster's
+// reach stays free).  raised, resident: the kernel's own.  most_smem: the
+// largest dynamic shared memory it is launched with.
+template <int kBlocks, typename K, typename... A>
+int launch_walk(PerDevice& raised, PerDevice& resident, K kernel, int threads, size_t smem,
+                size_t most_smem, int64_t max_items, cudaStream_t s, const A&... args) {
+    if (!raised.get(0, [&] {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)most_smem) == cudaSuccess;
+        }))
+        return GS_ERR_CUDA;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(kBlocks);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = s;
+    cudaLaunchAttribute cluster = {};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = kBlocks;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    config.attrs = &cluster;
+    config.numAttrs = 1;
+    const int clusters = resident.get(152 / kBlocks, [&] {
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, kernel, &config) == cudaSuccess ? n : 0;
+    });
+    config.gridDim = dim3((unsigned)(std::min<int64_t>(max_items, clusters) * kBlocks));
+    return cudaLaunchKernelEx(&config, kernel, args...) == cudaSuccess ? GS_OK : GS_ERR_CUDA;
+}
+
+}  // namespace gs

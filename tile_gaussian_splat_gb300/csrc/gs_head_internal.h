@@ -47,12 +47,34 @@ void launch_combine_bwd(const RowArgs& a, const void* grad_y, int64_t ldgy, cons
                         const int32_t* slots, const float* weights, const int32_t* offsets,
                         void* grad_ys, float* grad_weights, cudaStream_t s);
 
+// ---- route.cu
+struct RouteArgs {
+    const void* logits;
+    int64_t ld, tokens;
+    int topk, experts, dtype, renormalise;
+};
+constexpr int kMaxRouteBlocks = 152 * 8;  // blocks that leave partial sums
+size_t route_workspace(int64_t tokens, int experts);
+// counts and loss may be null (loss where counts is).
+void launch_route_fwd(const RouteArgs& a, const uint8_t* keep, int32_t* ids, float* weights,
+                      int32_t* counts, float* loss, void* workspace, cudaStream_t s);
+void launch_route_bwd(const RouteArgs& a, const int32_t* ids, const int32_t* counts,
+                      const float* grad_weights, const float* grad_loss, void* grad, int64_t ldg,
+                      int32_t* d_status, cudaStream_t s);
+
+// ---- rows8.cu: rows of GS_ROW8_BYTES and scales of GS_ROW8_SCALES bytes
+void launch_pack8(const void* x, int64_t ldx, int64_t rows, int channels, int dtype, uint8_t* q,
+                  uint8_t* scales, cudaStream_t s);
+void launch_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int channels,
+                    int dtype, void* y, int64_t ldy, cudaStream_t s);
+
 // ---- the experts' products; the launchers of expert_mma.cu return a gs_status
 struct LinearArgs {
     const int32_t* offsets;
     int64_t rows;
     int experts, in, out, dtype;
     int32_t* d_status;
+    bool packed = false;  // xs and weight are 8-bit rows
 };
 // ---- expert_few.cu: the products of few rows, bound by reading the weights.
 // as_they_lie: the tensor cores could read the weights in place.
@@ -71,5 +93,16 @@ size_t linear_bwd_workspace(const LinearArgs& a, const void* grad_ys, const void
 int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
                       const void* weight, void* grad_xs, void* grad_weight, void* grad_bias,
                       void* workspace, cudaStream_t s);
+// The same of 8-bit rows (a.packed).
+struct Rows8 {
+    const uint8_t *q, *scales;
+};
+size_t linear8_fwd_workspace(const LinearArgs& a);
+int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* bias, void* ys,
+                       void* workspace, cudaStream_t s);
+size_t linear8_bwd_workspace(const LinearArgs& a, const void* grad_ys);
+int launch_linear8_bwd(const LinearArgs& a, const void* grad_ys, Rows8 xs, Rows8 weight,
+                       void* grad_xs, void* grad_weight, void* grad_bias, void* workspace,
+                       cudaStream_t s);
 
 }  // namespace gs

@@ -207,6 +207,15 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
         "r"(v[30]), "r"(v[31]), "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_stores() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -249,6 +258,36 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
             "l"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
             : "memory");
 }
+
+// Instruction word of kind::mxf8f6f4, e4m3 operands (K-major) with powers of
+// two for every 32 terms of a row, float32 accumulators.  To be added: columns
+// >> 3 at bit 17 (columns as mma_word's), and which byte of the words of powers
+// is taken at bits 4 (B's) and 29 (A's).
+__device__ __forceinline__ constexpr uint32_t mma_word_e4m3(int rows) {
+    return 1u << 23 | (uint32_t)(rows >> 4) << 24;
+}
+
+// 32 terms; power_a, power_b: the first column of the rows' words in tensor
+// memory, row r at lane r % 32 (of every quarter of the lanes) and column r / 32.
+template <int kBlocks>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t word,
+                                         uint32_t power_a, uint32_t power_b, bool accumulate) {
+    if constexpr (kBlocks == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], "
+            "p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate), "r"(power_a), "r"(power_b)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], "
+            "p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate), "r"(power_a), "r"(power_b)
+            : "memory");
+}
+
 // Arrives on `bar` (in every one of the blocks) once all products issued so
 // far by this thread are done.
 template <int kBlocks>

@@ -69,6 +69,33 @@ const void* some_array(bool aligned) {
     return reinterpret_cast<const void*>((uintptr_t)(aligned ? 16 : 2));
 }
 
+// 8-bit rows and their scales.
+bool rows8_ok(const void* q, const void* scales) {
+    return q && (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && words_ok(scales);
+}
+
+bool channels8_ok(int64_t rows, int channels, int dtype) {
+    return rows >= 0 && channels >= 1 && channels <= kMaxFeatures && dtype_ok(dtype);
+}
+
+bool route_ok(int64_t tokens, int topk, int experts, int dtype) {
+    return pairs_ok(tokens, topk, experts) && topk <= experts && dtype_ok(dtype);
+}
+
+// Gradients of weight and bias that are sums over nothing.
+int zero_sums(const LinearArgs& a, void* grad_weight, void* grad_bias, cudaStream_t s) {
+    const size_t row = (size_t)a.experts * a.out * dtype_size(a.dtype);
+    if ((grad_weight && cudaMemsetAsync(grad_weight, 0, row * a.in, s) != cudaSuccess) ||
+        (grad_bias && cudaMemsetAsync(grad_bias, 0, row, s) != cudaSuccess))
+        return GS_ERR_CUDA;
+    return GS_OK;
+}
+
+LinearArgs linear8_args(const int32_t* offsets, int64_t rows, int experts, int in, int out,
+                        int dtype, int32_t* d_status) {
+    return LinearArgs{offsets, rows, experts, in, out, dtype, d_status, true};
+}
+
 size_t sort_counts_bytes(int64_t n, int experts) {
     return align_up((size_t)sort_units(n) * experts * sizeof(int32_t));
 }
@@ -248,16 +275,140 @@ int gs_expert_linear_bwd(const void* grad_ys, const void* xs, const int32_t* off
     const LinearArgs a{offsets, rows, experts, in_features, out_features, dtype, d_status};
     if (!workspace_ok(workspace, workspace_bytes, linear_bwd_workspace(a, grad_ys, xs, weight)))
         return GS_ERR_WORKSPACE;
-    if (rows == 0) {  // sums over nothing
-        const size_t row = (size_t)experts * out_features * dtype_size(dtype);
-        if ((grad_weight && cudaMemsetAsync(grad_weight, 0, row * in_features, s) != cudaSuccess) ||
-            (grad_bias && cudaMemsetAsync(grad_bias, 0, row, s) != cudaSuccess))
-            return GS_ERR_CUDA;
-        return GS_OK;
-    }
+    if (rows == 0) return zero_sums(a, grad_weight, grad_bias, s);
     if (!grad_xs && !grad_weight) return GS_OK;
     const int rc = launch_linear_bwd(a, grad_ys, xs, weight, grad_xs, grad_weight, grad_bias,
                                      workspace, s);
+    return rc == GS_OK ? check_launch() : rc;
+}
+
+size_t gs_expert_route_workspace_size(int64_t tokens, int experts) {
+    if (!pairs_ok(tokens, 1, experts)) return 0;
+    return align_up(route_workspace(tokens, experts));
+}
+
+int gs_expert_route_fwd(const void* logits, int64_t ldl, const uint8_t* keep, int64_t tokens,
+                        int topk, int experts, int dtype, int renormalise, int32_t* ids,
+                        float* weights, int32_t* counts, float* loss, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    if (!route_ok(tokens, topk, experts, dtype)) return GS_ERR_INVALID_ARG;
+    if ((counts && !words_ok(counts)) || (loss && (!words_ok(loss) || !counts)))
+        return GS_ERR_INVALID_ARG;
+    if (tokens > 0 && (!array_ok(logits, dtype) || ldl < experts || !words_ok(ids) ||
+                       !words_ok(weights)))
+        return GS_ERR_INVALID_ARG;
+    if (counts && !workspace_ok(workspace, workspace_bytes,
+                                gs_expert_route_workspace_size(tokens, experts)))
+        return GS_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tokens == 0) {
+        if ((counts && cudaMemsetAsync(counts, 0, (experts + 1) * sizeof(int32_t), s) !=
+                           cudaSuccess) ||
+            (loss && cudaMemsetAsync(loss, 0, sizeof(float), s) != cudaSuccess))
+            return GS_ERR_CUDA;
+        return GS_OK;
+    }
+    launch_route_fwd(RouteArgs{logits, ldl, tokens, topk, experts, dtype, renormalise}, keep, ids,
+                     weights, counts, loss, workspace, s);
+    return check_launch();
+}
+
+int gs_expert_route_bwd(const void* logits, int64_t ldl, const int32_t* ids,
+                        const int32_t* counts, const float* grad_weights, const float* grad_loss,
+                        int64_t tokens, int topk, int experts, int dtype, int renormalise,
+                        void* grad_logits, int64_t ldg, int32_t* d_status, void* stream) {
+    if (!route_ok(tokens, topk, experts, dtype)) return GS_ERR_INVALID_ARG;
+    if (tokens == 0) return GS_OK;
+    if (!array_ok(logits, dtype) || ldl < experts || !words_ok(ids) ||
+        (grad_weights && !words_ok(grad_weights)) ||
+        (grad_loss && (!words_ok(grad_loss) || !words_ok(counts))) ||
+        !array_ok(grad_logits, dtype) || ldg < experts)
+        return GS_ERR_INVALID_ARG;
+    launch_route_bwd(RouteArgs{logits, ldl, tokens, topk, experts, dtype, renormalise}, ids,
+                     counts, grad_weights, grad_loss, grad_logits, ldg, d_status,
+                     static_cast<cudaStream_t>(stream));
+    return check_launch();
+}
+
+int gs_rows_pack8(const void* x, int64_t ldx, int64_t rows, int channels, int dtype, uint8_t* q,
+                  uint8_t* scales, void* stream) {
+    if (!channels8_ok(rows, channels, dtype)) return GS_ERR_INVALID_ARG;
+    if (rows == 0) return GS_OK;
+    if (!array_ok(x, dtype) || ldx < channels || !rows8_ok(q, scales)) return GS_ERR_INVALID_ARG;
+    launch_pack8(x, ldx, rows, channels, dtype, q, scales, static_cast<cudaStream_t>(stream));
+    return check_launch();
+}
+
+int gs_rows_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int channels,
+                    int dtype, void* y, int64_t ldy, void* stream) {
+    if (!channels8_ok(rows, channels, dtype)) return GS_ERR_INVALID_ARG;
+    if (rows == 0) return GS_OK;
+    if (!rows8_ok(q, scales) || !array_ok(y, dtype) || ldy < channels) return GS_ERR_INVALID_ARG;
+    launch_unpack8(q, scales, rows, channels, dtype, y, ldy, static_cast<cudaStream_t>(stream));
+    return check_launch();
+}
+
+size_t gs_expert_linear8_fwd_workspace_size(int64_t rows, int experts, int in_features,
+                                            int out_features, int dtype) {
+    if (!linear_ok(&kSomeOffsets, rows, experts, in_features, out_features, dtype)) return 0;
+    return linear8_fwd_workspace(
+        linear8_args(nullptr, rows, experts, in_features, out_features, dtype, nullptr));
+}
+
+int gs_expert_linear8_fwd(const uint8_t* xs, const uint8_t* xs_scales, const int32_t* offsets,
+                          const uint8_t* weight, const uint8_t* weight_scales, const void* bias,
+                          int64_t rows, int experts, int in_features, int out_features, int dtype,
+                          void* ys, void* workspace, size_t workspace_bytes, int32_t* d_status,
+                          void* stream) {
+    if (!linear_ok(offsets, rows, experts, in_features, out_features, dtype))
+        return GS_ERR_INVALID_ARG;
+    if (rows == 0) return GS_OK;
+    if (!rows8_ok(xs, xs_scales) || !rows8_ok(weight, weight_scales) ||
+        (bias && !array_ok(bias, dtype)) || !array_ok(ys, dtype))
+        return GS_ERR_INVALID_ARG;
+    const LinearArgs a =
+        linear8_args(offsets, rows, experts, in_features, out_features, dtype, d_status);
+    if (!workspace_ok(workspace, workspace_bytes, linear8_fwd_workspace(a)))
+        return GS_ERR_WORKSPACE;
+    const int rc = launch_linear8_fwd(a, Rows8{xs, xs_scales}, Rows8{weight, weight_scales}, bias,
+                                      ys, workspace, static_cast<cudaStream_t>(stream));
+    return rc == GS_OK ? check_launch() : rc;
+}
+
+size_t gs_expert_linear8_bwd_workspace_size(int64_t rows, int experts, int in_features,
+                                            int out_features, int dtype, int aligned) {
+    if (!linear_ok(&kSomeOffsets, rows, experts, in_features, out_features, dtype)) return 0;
+    return linear8_bwd_workspace(
+        linear8_args(nullptr, rows, experts, in_features, out_features, dtype, nullptr),
+        some_array(aligned));
+}
+
+int gs_expert_linear8_bwd(const void* grad_ys, const uint8_t* xs, const uint8_t* xs_scales,
+                          const int32_t* offsets, const uint8_t* weight,
+                          const uint8_t* weight_scales, int64_t rows, int experts,
+                          int in_features, int out_features, int dtype, void* grad_xs,
+                          void* grad_weight, void* grad_bias, void* workspace,
+                          size_t workspace_bytes, int32_t* d_status, void* stream) {
+    if (!linear_ok(offsets, rows, experts, in_features, out_features, dtype))
+        return GS_ERR_INVALID_ARG;
+    if (rows > 0 && !array_ok(grad_ys, dtype)) return GS_ERR_INVALID_ARG;
+    if (rows > 0 && grad_xs && (!array_ok(grad_xs, dtype) || !rows8_ok(weight, weight_scales)))
+        return GS_ERR_INVALID_ARG;
+    if (grad_weight &&
+        (!array_ok(grad_weight, dtype) || (rows > 0 && !rows8_ok(xs, xs_scales))))
+        return GS_ERR_INVALID_ARG;
+    if (grad_bias && (!array_ok(grad_bias, dtype) || !grad_weight)) return GS_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const LinearArgs a =
+        linear8_args(offsets, rows, experts, in_features, out_features, dtype, d_status);
+    if (!workspace_ok(workspace, workspace_bytes, linear8_bwd_workspace(a, grad_ys)))
+        return GS_ERR_WORKSPACE;
+    if (rows == 0)
+        return zero_sums(a, grad_weight, grad_bias, s);
+    if (!grad_xs && !grad_weight) return GS_OK;
+    const int rc = launch_linear8_bwd(a, grad_ys, Rows8{xs, xs_scales},
+                                      Rows8{weight, weight_scales}, grad_xs, grad_weight,
+                                      grad_bias, workspace, s);
     return rc == GS_OK ? check_launch() : rc;
 }
 

@@ -1,0 +1,579 @@
+// The router of the expert head: every token's choice of experts from its
+// logits, the choices' weights, the experts' counts and the balance loss, and
+// their gradient in the logits.
+//
+// Both directions read each row of logits once, so they are bound by memory
+// bandwidth.  kLanes lanes share a row; a lane owns the same experts of every
+// row it meets, so the sums of probabilities behind the balance loss stay in
+// registers until the end and are then added up in a fixed order.  The choice
+// is topk rounds of a maximum over (value, lowest index): each lane keeps its
+// logits as unsigned words in the order of the values, 0 where there is
+// nothing to choose.
+#include <algorithm>
+#include <cstdint>
+
+#include "gs_device.cuh"
+#include "gs_head_internal.h"
+#include "gs_types.cuh"
+
+namespace gs {
+
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kWarps = kRowThreads / 32;
+
+// Logits as words in the order of the values: 0 = not to be chosen (minus
+// infinity), a NaN above everything, both zeros the same.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    if (v != v) return kAll;
+    if (v == -INFINITY) return 0;
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);  // kAll: a NaN
+}
+
+template <int kLanes>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+
+// The largest key and the lowest index that has it, over a row's lanes.
+template <int kLanes>
+__device__ __forceinline__ void group_best(uint32_t& key, int& index) {
+    if constexpr (kLanes == 32) {
+        const uint32_t top = __reduce_max_sync(kAll, key);
+        index = (int)__reduce_min_sync(kAll, key == top ? (uint32_t)index : kAll);
+        key = top;
+    } else {
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) {
+            const uint32_t k = __shfl_xor_sync(kAll, key, o);
+            const int i = __shfl_xor_sync(kAll, index, o);
+            if (k > key || (k == key && i < index)) {
+                key = k;
+                index = i;
+            }
+        }
+    }
+}
+
+struct RouteFwd {
+    const void* logits;
+    const uint8_t* keep;
+    int32_t *ids, *counts;      // counts: or null
+    float *weights, *loss;      // loss: or null
+    float* partial;             // (blocks, experts + 1): sums of probabilities
+    int32_t* part_counts;       // (blocks, experts + 1)
+    float* totals;              // experts + 1
+    uint32_t* ticket;
+    int64_t ld, tokens;
+    int topk, experts, renormalise;
+};
+
+// loss = experts * sum over e of share_e * mean probability_e, by one warp in
+// a fixed order.
+__device__ __forceinline__ float balance(const float* sums, const int32_t* counts, int experts) {
+    const int lane = threadIdx.x & 31;
+    float dot = 0.f;
+    int pairs = 0;
+    for (int e = lane; e < experts; e += 32) {
+        const int c = __ldcg(counts + e);
+        dot += __ldcg(sums + e) * (float)c;
+        pairs += c;
+    }
+    dot = warp_sum(dot);
+    pairs = __reduce_add_sync(kAll, pairs);
+    const int taking = __ldcg(counts + experts);
+    return pairs > 0 ? (float)experts * (dot / ((float)taking * (float)pairs)) : 0.f;
+}
+
+// kVec elements per access, kLanes lanes a row, kItems accesses a lane and
+// row, kRows rows of a lane in flight.
+template <typename T, int kVec, int kLanes, int kItems, int kRows>
+__global__ void __launch_bounds__(kRowThreads) k_route_fwd(RouteFwd a) {
+    constexpr int kGroups = kRowThreads / kLanes;
+    constexpr int kSlots = 64 / kLanes < 8 ? 64 / kLanes : 8;  // choices a lane holds
+    extern __shared__ int32_t shared[];
+    int32_t* count = shared;                                          // experts + 1
+    float* sums = reinterpret_cast<float*>(shared + a.experts + 1);   // kWarps x experts
+    const bool tally = a.counts;
+    const int at = threadIdx.x % kLanes;
+    if (tally) {
+        if (blockIdx.x == 0 && threadIdx.x == 0 && gridDim.x > 1) *a.ticket = 0;
+        for (int e = threadIdx.x; e <= a.experts; e += kRowThreads) count[e] = 0;
+        __syncthreads();
+    }
+    float sum[kItems][kVec] = {};
+    int taking = 0;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step * kRows) {
+        RawVec<T, kVec> raw[kRows][kItems];
+        bool keep[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
+            keep[u] = r < a.tokens && (!a.keep || a.keep[r]);
+            const T* x = static_cast<const T*>(a.logits) + r * a.ld + at * kVec;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                raw[u][i] = keep[u] && (i * kLanes + at) * kVec < a.experts
+                                ? load_raw<T, kVec>(x + i * kLanes * kVec)
+                                : RawVec<T, kVec>{};
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
+            uint32_t key[kItems][kVec];
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                float v[kVec];
+                unpack<T, kVec>(raw[u][i], v);
+                const bool in = keep[u] && (i * kLanes + at) * kVec < a.experts;
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) key[i][j] = in ? order_key(v[j]) : 0;
+            }
+            int id[kSlots];
+            float e[kSlots];
+            float top = 0.f;
+            bool any = false;
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                id[s] = -1;
+                e[s] = 0.f;
+                for (int l = 0; l < kLanes; ++l) {
+                    const int round = s * kLanes + l;
+                    if (round >= a.topk) break;
+                    uint32_t best = 0;
+                    int index = 0x7fffffff;
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j)
+                            if (key[i][j] > best) {
+                                best = key[i][j];
+                                index = (i * kLanes + at) * kVec + j;
+                            }
+                    group_best<kLanes>(best, index);
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j)
+                            if (index == (i * kLanes + at) * kVec + j) key[i][j] = 0;
+                    if (round == 0) {
+                        any = best > 0;
+                        top = key_value(best);
+                    }
+                    if (at == l && best > 0) {
+                        id[s] = index;
+                        e[s] = expf(key_value(best) - top);
+                    }
+                }
+                if ((s + 1) * kLanes >= a.topk) break;
+            }
+            float all = 0.f, chosen = 0.f;
+            float p[kItems][kVec];
+            if (tally || !a.renormalise) {
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    float v[kVec];
+                    unpack<T, kVec>(raw[u][i], v);
+                    const bool in = any && (i * kLanes + at) * kVec < a.experts;
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) {
+                        p[i][j] = in ? expf(v[j] - top) : 0.f;
+                        all += p[i][j];
+                    }
+                }
+                all = group_sum<kLanes>(all);
+            }
+            if (tally && any) {
+                const float each = 1.0f / all;
+#pragma unroll
+                for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) sum[i][j] += p[i][j] * each;
+                taking += at == 0;
+            }
+            if (a.renormalise) {
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) chosen += s * kLanes < a.topk ? e[s] : 0.f;
+                chosen = group_sum<kLanes>(chosen);
+            } else {
+                chosen = all;
+            }
+            if (r >= a.tokens) continue;
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                const int round = s * kLanes + at;
+                if (round < a.topk) {
+                    a.ids[r * a.topk + round] = id[s];
+                    a.weights[r * a.topk + round] = id[s] >= 0 ? e[s] / chosen : 0.f;
+                    if (tally && id[s] >= 0) atomicAdd(count + id[s], 1);
+                }
+            }
+        }
+    }
+    if (!tally) return;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+#pragma unroll
+            for (int o = kLanes; o < 32; o <<= 1)
+                sum[i][j] += __shfl_xor_sync(kAll, sum[i][j], o);
+            const int c = (i * kLanes + at) * kVec + j;
+            if ((threadIdx.x & 31) < kLanes && c < a.experts)
+                sums[threadIdx.x / 32 * a.experts + c] = sum[i][j];
+        }
+    taking = __reduce_add_sync(kAll, taking);
+    if ((threadIdx.x & 31) == 0) atomicAdd(count + a.experts, taking);
+    __syncthreads();
+    const bool alone = gridDim.x == 1;
+    float* total = alone ? a.totals : a.partial + (int64_t)blockIdx.x * (a.experts + 1);
+    int32_t* counts = alone ? a.counts : a.part_counts + (int64_t)blockIdx.x * (a.experts + 1);
+    for (int e = threadIdx.x; e <= a.experts; e += kRowThreads) {
+        float v = 0.f;
+        if (e < a.experts)
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += sums[w * a.experts + e];
+        if (!alone || a.loss) total[e] = v;
+        counts[e] = count[e];
+    }
+    if (!alone || !a.loss) return;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const float loss = balance(a.totals, a.counts, a.experts);
+        if (threadIdx.x == 0) *a.loss = loss;
+    }
+}
+
+// The blocks' sums and counts added up, eight columns a block and 128 threads
+// a column; the last block to finish then has the loss.
+constexpr int kSumThreads = 1024, kSumColumns = 8;
+
+__global__ void __launch_bounds__(kSumThreads) k_route_sum(RouteFwd a, int blocks) {
+    constexpr int kParts = kSumThreads / kSumColumns;
+    __shared__ float part[kSumColumns][kParts + 1];
+    __shared__ int32_t parts[kSumColumns][kParts + 1];
+    __shared__ bool last;
+    const int c = threadIdx.x % kSumColumns, g = threadIdx.x / kSumColumns;
+    const int column = blockIdx.x * kSumColumns + c, columns = a.experts + 1;
+    float sum = 0.f;
+    int32_t count = 0;
+    if (column < columns) {
+#pragma unroll 4
+        for (int i = g; i < blocks; i += kParts) {
+            sum += a.partial[(int64_t)i * columns + column];
+            count += a.part_counts[(int64_t)i * columns + column];
+        }
+    }
+    part[c][g] = sum;
+    parts[c][g] = count;
+    __syncthreads();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int mine = blockIdx.x * kSumColumns + warp;
+    if (warp < kSumColumns && mine < columns) {
+        sum = 0.f;
+        count = 0;
+#pragma unroll
+        for (int i = 0; i < kParts / 32; ++i) {
+            sum += part[warp][i * 32 + lane];
+            count += parts[warp][i * 32 + lane];
+        }
+        sum = warp_sum(sum);
+        count = __reduce_add_sync(kAll, count);
+        if (lane == 0) {
+            a.totals[mine] = sum;
+            a.counts[mine] = count;
+        }
+    }
+    if (!a.loss) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) + 1 == gridDim.x;
+    __syncthreads();
+    if (!last || threadIdx.x >= 32) return;
+    __threadfence();
+    const float loss = balance(a.totals, a.counts, a.experts);
+    if (threadIdx.x == 0) *a.loss = loss;
+}
+
+struct RouteBwd {
+    const void* logits;
+    const int32_t *ids, *counts;     // counts: or null
+    const float *grad_weights, *grad_loss;  // each or null
+    void* grad;
+    int32_t* d_status;
+    int64_t ld, ldg, tokens;
+    int topk, experts, renormalise;
+};
+
+// With p the softmax of a row, h_e = grad_loss * experts * share_e / tokens
+// that take part, and g_j the gradient of the weight of choice j:
+//   renormalised:  d_j = w_j (g_j - sum w g), w the softmax over the chosen
+//   otherwise:     d_j = p_j g_j, and D = sum of d_j
+//   grad_e = p_e (h_e - sum p h - D) + the d_j of the choices that are e
+template <typename T, int kVec, int kLanes, int kItems, int kRows>
+__global__ void __launch_bounds__(kRowThreads) k_route_bwd(RouteBwd a) {
+    constexpr int kGroups = kRowThreads / kLanes;
+    constexpr int kSlots = 64 / kLanes < 8 ? 64 / kLanes : 8;
+    const int at = threadIdx.x % kLanes;
+    float h[kItems][kVec] = {};
+    if (a.grad_loss) {
+        int pairs = 0;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const int c = (i * kLanes + at) * kVec + j;
+                const int n = c < a.experts ? a.counts[c] : 0;
+                pairs += n;
+                h[i][j] = (float)n;
+            }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) pairs += __shfl_xor_sync(kAll, pairs, o);
+        const float scale = pairs > 0 ? *a.grad_loss * (float)a.experts /
+                                            ((float)pairs * (float)a.counts[a.experts])
+                                      : 0.f;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) h[i][j] *= scale;
+    }
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step * kRows) {
+        RawVec<T, kVec> raw[kRows][kItems];
+        int id[kRows][kSlots];
+        float g[kRows][kSlots];
+        bool take[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                const int round = s * kLanes + at;
+                id[u][s] = -1;
+                g[u][s] = 0.f;
+                if (r < a.tokens && round < a.topk) {
+                    id[u][s] = a.ids[r * a.topk + round];
+                    if (id[u][s] < -1 || id[u][s] >= a.experts) {
+                        GS_BOUNDS_REPORT(a.d_status);
+                        id[u][s] = -1;
+                    }
+                    if (a.grad_weights && id[u][s] >= 0)
+                        g[u][s] = a.grad_weights[r * a.topk + round];
+                }
+            }
+            // the first choice tells whether the row takes part
+            take[u] = __shfl_sync(kAll, id[u][0], 0, kLanes) >= 0;
+            const T* x = static_cast<const T*>(a.logits) + r * a.ld + at * kVec;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                raw[u][i] = take[u] && (i * kLanes + at) * kVec < a.experts
+                                ? load_raw<T, kVec>(x + i * kLanes * kVec)
+                                : RawVec<T, kVec>{};
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
+            float p[kItems][kVec];
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                unpack<T, kVec>(raw[u][i], p[i]);
+                const bool in = (i * kLanes + at) * kVec < a.experts;
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    if (!in) p[i][j] = -INFINITY;
+                    top = fmaxf(top, p[i][j]);
+                }
+            }
+            top = group_max<kLanes>(top);
+            float all = 0.f, dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    p[i][j] = expf(p[i][j] - top);
+                    all += p[i][j];
+                    dot += p[i][j] * h[i][j];
+                }
+            all = group_sum<kLanes>(all);
+            dot = a.grad_loss ? group_sum<kLanes>(dot) / all : 0.f;
+            // the choices' exponentials, from their own logits
+            float e[kSlots];
+            float chosen = 0.f, mean = 0.f;
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                e[s] = 0.f;
+                if (s * kLanes >= a.topk) continue;
+                if (take[u] && id[u][s] >= 0)
+                    e[s] = expf(to_f(static_cast<const T*>(a.logits)[r * a.ld + id[u][s]]) - top);
+                chosen += e[s];
+                mean += e[s] * g[u][s];
+            }
+            mean = group_sum<kLanes>(mean);
+            chosen = a.renormalise ? group_sum<kLanes>(chosen) : all;
+            mean /= chosen;  // renormalised: sum w g; otherwise D
+            const float each = 1.0f / all, down = dot + (a.renormalise ? 0.f : mean);
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) p[i][j] *= each * (h[i][j] - down);
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                if (s * kLanes >= a.topk) break;
+                const float d =
+                    e[s] / chosen * (a.renormalise ? g[u][s] - mean : g[u][s]);
+                for (int l = 0; l < kLanes; ++l) {
+                    if (s * kLanes + l >= a.topk) break;
+                    const int index = __shfl_sync(kAll, id[u][s], l, kLanes);
+                    const float add = __shfl_sync(kAll, d, l, kLanes);
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j)
+                            if (index == (i * kLanes + at) * kVec + j) p[i][j] += add;
+                }
+            }
+            if (r >= a.tokens) continue;
+            T* out = static_cast<T*>(a.grad) + r * a.ldg + at * kVec;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                if (!take[u])
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) p[i][j] = 0.f;
+                if ((i * kLanes + at) * kVec < a.experts)
+                    store_vec<T, kVec>(out + i * kLanes * kVec, p[i]);
+            }
+        }
+    }
+}
+
+// Calls f with the form for rows of `experts` elements.
+template <typename T, int kVec, typename F>
+void with_route_form(int experts, F&& f) {
+    const int n = (experts + kVec - 1) / kVec;
+    if constexpr (kVec > 1) {
+        if (n <= 2) return f(Form<kVec, 2, 1, 2>{});
+        if (n <= 4) return f(Form<kVec, 4, 1, 2>{});
+        if (n <= 8) return f(Form<kVec, 8, 1, 2>{});
+        if (n <= 16) return f(Form<kVec, 8, 2, 2>{});
+        if (n <= 32) return f(Form<kVec, 32, 1, 2>{});
+        if (n <= 64) return f(Form<kVec, 32, 2, 1>{});
+        if (n <= 128) return f(Form<kVec, 32, 4, 1>{});
+        if constexpr (kVec == 4) return f(Form<4, 32, 8, 1>{});
+    } else {
+        if (n <= 4) return f(Form<1, 4, 1, 4>{});
+        if (n <= 8) return f(Form<1, 4, 2, 2>{});
+        if (n <= 16) return f(Form<1, 8, 2, 2>{});
+        if (n <= 32) return f(Form<1, 8, 4, 2>{});
+        if (n <= 64) return f(Form<1, 8, 8, 1>{});
+        if (n <= 128) return f(Form<1, 32, 4, 1>{});
+        if (n <= 256) return f(Form<1, 32, 8, 1>{});
+        if (n <= 512) return f(Form<1, 32, 16, 1>{});
+        return f(Form<1, 32, 32, 1>{});
+    }
+}
+
+// Whole 16-byte vectors, or single elements.
+template <typename T, typename F>
+void with_route_width(uintptr_t all, F&& f) {
+    if (all % 16 == 0) return f(std::integral_constant<int, 16 / (int)sizeof(T)>{});
+    return f(std::integral_constant<int, 1>{});
+}
+
+int route_blocks(int64_t tokens, int groups, int cap) {
+    return (int)std::min<int64_t>((tokens + groups - 1) / groups, cap);
+}
+
+size_t align_words(size_t words) { return (words + 63) / 64 * 64; }
+
+}  // namespace
+
+size_t route_workspace(int64_t tokens, int experts) {
+    const size_t columns = experts + 1;
+    // a block takes two rows or more
+    const size_t blocks = (size_t)std::min<int64_t>(std::max<int64_t>(tokens, 1), kMaxRouteBlocks);
+    return 4 * (64 + align_words(columns) + 2 * align_words(blocks * columns));
+}
+
+void launch_route_fwd(const RouteArgs& n, const uint8_t* keep, int32_t* ids, float* weights,
+                      int32_t* counts, float* loss, void* workspace, cudaStream_t s) {
+    RouteFwd a{};
+    a.logits = n.logits;
+    a.keep = keep;
+    a.ids = ids;
+    a.counts = counts;
+    a.weights = weights;
+    a.loss = loss;
+    a.ld = n.ld;
+    a.tokens = n.tokens;
+    a.topk = n.topk;
+    a.experts = n.experts;
+    a.renormalise = n.renormalise;
+    const size_t columns = n.experts + 1;
+    with_dtype(n.dtype, [&](auto t) {
+        using T = decltype(t);
+        const auto go = [&](auto form) {
+            using F = decltype(form);
+            const int groups = kRowThreads / F::kLanes;
+            const auto kernel = k_route_fwd<T, F::kVec, F::kLanes, F::kItems, F::kRows>;
+            const auto smem = [&](int experts) {
+                return counts ? ((size_t)experts + 1) * 4 + (size_t)kWarps * experts * 4 : 0;
+            };
+            static PerDevice resident;
+            const int most = F::kVec * F::kLanes * F::kItems;
+            const int blocks = route_blocks(
+                n.tokens, groups,
+                std::min(kMaxRouteBlocks,
+                         resident_blocks(resident, kernel,
+                                         ((size_t)most + 1) * 4 + (size_t)kWarps * most * 4)));
+            if (counts) {
+                uint32_t* w = static_cast<uint32_t*>(workspace);
+                a.ticket = w;
+                a.totals = reinterpret_cast<float*>(w + 64);
+                a.partial = a.totals + align_words(columns);
+                a.part_counts = reinterpret_cast<int32_t*>(a.partial + align_words(blocks * columns));
+            }
+            kernel<<<blocks, kRowThreads, smem(n.experts), s>>>(a);
+            if (counts && blocks > 1)
+                k_route_sum<<<(unsigned)((columns + kSumColumns - 1) / kSumColumns), kSumThreads, 0,
+                              s>>>(a, blocks);
+        };
+        with_route_width<T>(row_bits<T>(n.logits, n.ld) | (uintptr_t)(n.experts * sizeof(T)),
+                            [&](auto width) {
+                                with_route_form<T, decltype(width)::value>(n.experts, go);
+                            });
+    });
+}
+
+void launch_route_bwd(const RouteArgs& n, const int32_t* ids, const int32_t* counts,
+                      const float* grad_weights, const float* grad_loss, void* grad, int64_t ldg,
+                      int32_t* d_status, cudaStream_t s) {
+    const RouteBwd a{n.logits, ids,  counts, grad_weights, grad_loss, grad,         d_status,
+                     n.ld,     ldg, n.tokens, n.topk,      n.experts, n.renormalise};
+    with_dtype(n.dtype, [&](auto t) {
+        using T = decltype(t);
+        const auto go = [&](auto form) {
+            using F = decltype(form);
+            const auto kernel = k_route_bwd<T, F::kVec, F::kLanes, F::kItems, F::kRows>;
+            static PerDevice resident;
+            const int blocks = route_blocks(n.tokens, kRowThreads / F::kLanes,
+                                            resident_blocks(resident, kernel, 0));
+            kernel<<<blocks, kRowThreads, 0, s>>>(a);
+        };
+        with_route_width<T>(row_bits<T>(n.logits, n.ld) | row_bits<T>(grad, ldg) |
+                                (uintptr_t)(n.experts * sizeof(T)),
+                            [&](auto width) {
+                                with_route_form<T, decltype(width)::value>(n.experts, go);
+                            });
+    });
+}
+
+}  // namespace gs
