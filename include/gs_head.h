@@ -245,10 +245,8 @@ int gs_rows_pack8(const void* x, int64_t ldx, int64_t rows, int channels, int dt
 int gs_rows_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int channels,
                     int dtype, void* y, int64_t ldy, void* stream);
 
-/* Bytes of workspace gs_expert_linear8_fwd and _bwd need.  aligned != 0:
- * grad_ys begins on a 16-byte boundary. */
-size_t gs_expert_linear8_fwd_workspace_size(int64_t rows, int experts, int in_features,
-                                            int out_features, int dtype);
+/* Bytes of workspace gs_expert_linear8_bwd needs.  aligned != 0: grad_ys begins
+ * on a 16-byte boundary. */
 size_t gs_expert_linear8_bwd_workspace_size(int64_t rows, int experts, int in_features,
                                             int out_features, int dtype, int aligned);
 
@@ -261,8 +259,7 @@ size_t gs_expert_linear8_bwd_workspace_size(int64_t rows, int experts, int in_fe
 int gs_expert_linear8_fwd(const uint8_t* xs, const uint8_t* xs_scales, const int32_t* offsets,
                           const uint8_t* weight, const uint8_t* weight_scales, const void* bias,
                           int64_t rows, int experts, int in_features, int out_features, int dtype,
-                          void* ys, void* workspace, size_t workspace_bytes, int32_t* d_status,
-                          void* stream);
+                          void* ys, int32_t* d_status, void* stream);
 
 /*
  * gs_expert_linear8_bwd -- gradients of gs_expert_linear8_fwd in the values of

@@ -74,8 +74,7 @@ SIGNATURES = {
     "gs_expert_route_bwd": (I32, [P, I64, P, P, P, P, I64, I32, I32, I32, I32, P, I64, P, P]),
     "gs_rows_pack8": (I32, [P, I64, I64, I32, I32, P, P, P]),
     "gs_rows_unpack8": (I32, [P, P, I64, I32, I32, P, I64, P]),
-    "gs_expert_linear8_fwd_workspace_size": (SZ, [I64, I32, I32, I32, I32]),
-    "gs_expert_linear8_fwd": (I32, [P, P, P, P, P, P, I64, I32, I32, I32, I32, P, P, SZ, P, P]),
+    "gs_expert_linear8_fwd": (I32, [P, P, P, P, P, P, I64, I32, I32, I32, I32, P, P, P]),
     "gs_expert_linear8_bwd_workspace_size": (SZ, [I64, I32, I32, I32, I32, I32]),
     "gs_expert_linear8_bwd": (I32, [P, P, P, P, P, P, I64, I32, I32, I32, I32, P, P, P, P, SZ, P,
                                     P]),
@@ -905,8 +904,7 @@ def _linear8_shapes(xs, offsets, weight, channels):
 
 
 def gs_expert_linear8_fwd(xs, xs_scales, offsets, weight, weight_scales, in_features, bias=None,
-                          dtype=torch.bfloat16, d_status=None, out=None, workspace=None,
-                          stream=None):
+                          dtype=torch.bfloat16, d_status=None, out=None, stream=None):
     """gs_expert_linear_fwd of 8-bit rows (gs_rows_pack8): xs (rows, ...),
     weight (experts, out_features, ...) of in_features channels, bias
     (experts, out_features) of dtype or None.  Returns ys (rows,
@@ -917,13 +915,9 @@ def gs_expert_linear8_fwd(xs, xs_scales, offsets, weight, weight_scales, in_feat
     if bias is not None:
         _same(bias, (E, o), dtype, "bias")
     ys = _new((R, o), dtype, xs, stream) if out is None else _same(out, (R, o), dtype, "out")
-    dt = _dtype(ys, "dtype")
-    L = lib()
-    n_bytes = L.gs_expert_linear8_fwd_workspace_size(R, E, in_features, o, dt)
-    ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
-    _check(L.gs_expert_linear8_fwd(xp, xsp, _ptr(offsets), wp, wsp, _ptr(bias), R, E, in_features,
-                                   o, dt, _ptr(ys), _ptr(ws), n_bytes, _ptr(d_status),
-                                   _on(stream, xs)), "gs_expert_linear8_fwd")
+    _check(lib().gs_expert_linear8_fwd(xp, xsp, _ptr(offsets), wp, wsp, _ptr(bias), R, E,
+                                       in_features, o, _dtype(ys, "dtype"), _ptr(ys),
+                                       _ptr(d_status), _on(stream, xs)), "gs_expert_linear8_fwd")
     return ys
 
 

@@ -1071,32 +1071,6 @@ Planes unpacked(int dtype, Rows8 x, int64_t rows, int columns, char** workspace,
 
 }  // namespace
 
-size_t linear8_fwd_workspace(const LinearArgs& a) {
-    return unpacked_bytes(a.rows, a.in) + unpacked_bytes((int64_t)a.experts * a.out, a.in);
-}
-
-int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* bias, void* ys,
-                       void* workspace, cudaStream_t s) {
-    LinearArgs halves = a;
-    halves.dtype = GS_BF16;
-    const bool pairs = use_pairs(halves, a.out);
-    char* ws = static_cast<char*>(workspace);
-    const Planes pa = unpacked(GS_BF16, xs, a.rows, a.in, &ws, s);
-    const Planes pb = unpacked(GS_BF16, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
-    CUtensorMap ma, mb;
-    if (!make_map(&ma, GS_BF16, pa, 0, kHigh) ||
-        !make_map(&mb, GS_BF16, pb, a.experts, box_b(pairs, a.out)))
-        return GS_ERR_CUDA;
-    ProductArgs g = product_args(halves, ys, a.out, a.in);
-    g.vectors = aligned16(ys) && (size_t)a.out * dtype_size(a.dtype) % 16 == 0;
-    g.bias = bias;
-    int rc = GS_OK;
-    with_dtype(a.dtype, [&](auto o) {
-        rc = launch_rows<__nv_bfloat16, decltype(o), kForward>(ma, mb, g, pairs, s);
-    });
-    return rc;
-}
-
 size_t linear8_bwd_workspace(const LinearArgs& a, const void* grad_ys) {
     size_t n = grad_sums_bytes(a);
     if (!copyable(a.dtype, grad_ys, a.out)) n += plane_bytes(a.dtype, a.rows, a.out);

@@ -97,9 +97,10 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
 struct Rows8 {
     const uint8_t *q, *scales;
 };
-size_t linear8_fwd_workspace(const LinearArgs& a);
+// ---- expert_mma8.cu
 int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* bias, void* ys,
-                       void* workspace, cudaStream_t s);
+                       cudaStream_t s);
+// ---- expert_mma.cu
 size_t linear8_bwd_workspace(const LinearArgs& a, const void* grad_ys);
 int launch_linear8_bwd(const LinearArgs& a, const void* grad_ys, Rows8 xs, Rows8 weight,
                        void* grad_xs, void* grad_weight, void* grad_bias, void* workspace,

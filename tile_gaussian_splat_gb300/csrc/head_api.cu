@@ -348,18 +348,10 @@ int gs_rows_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int c
     return check_launch();
 }
 
-size_t gs_expert_linear8_fwd_workspace_size(int64_t rows, int experts, int in_features,
-                                            int out_features, int dtype) {
-    if (!linear_ok(&kSomeOffsets, rows, experts, in_features, out_features, dtype)) return 0;
-    return linear8_fwd_workspace(
-        linear8_args(nullptr, rows, experts, in_features, out_features, dtype, nullptr));
-}
-
 int gs_expert_linear8_fwd(const uint8_t* xs, const uint8_t* xs_scales, const int32_t* offsets,
                           const uint8_t* weight, const uint8_t* weight_scales, const void* bias,
                           int64_t rows, int experts, int in_features, int out_features, int dtype,
-                          void* ys, void* workspace, size_t workspace_bytes, int32_t* d_status,
-                          void* stream) {
+                          void* ys, int32_t* d_status, void* stream) {
     if (!linear_ok(offsets, rows, experts, in_features, out_features, dtype))
         return GS_ERR_INVALID_ARG;
     if (rows == 0) return GS_OK;
@@ -368,10 +360,8 @@ int gs_expert_linear8_fwd(const uint8_t* xs, const uint8_t* xs_scales, const int
         return GS_ERR_INVALID_ARG;
     const LinearArgs a =
         linear8_args(offsets, rows, experts, in_features, out_features, dtype, d_status);
-    if (!workspace_ok(workspace, workspace_bytes, linear8_fwd_workspace(a)))
-        return GS_ERR_WORKSPACE;
     const int rc = launch_linear8_fwd(a, Rows8{xs, xs_scales}, Rows8{weight, weight_scales}, bias,
-                                      ys, workspace, static_cast<cudaStream_t>(stream));
+                                      ys, static_cast<cudaStream_t>(stream));
     return rc == GS_OK ? check_launch() : rc;
 }
 
