@@ -7,6 +7,7 @@
 #include "expert_rows.cuh"
 #include "gs_device.cuh"
 #include "gs_head_internal.h"
+#include "gs_rows8.cuh"
 #include "gs_types.cuh"
 
 namespace gs {
@@ -116,6 +117,102 @@ __global__ void __launch_bounds__(kFewThreads)
     }
 }
 
+// The same of 8-bit rows: sixteen elements of a weight row an access, of one
+// block of 128, whose power of two their sum takes.
+template <int kRows>
+__device__ __forceinline__ void few8_terms(const float (*x)[kFewDepth], const uint8_t* const* w,
+                                           const uint8_t* const* powers, int depth,
+                                           float (*sum)[kFewRows]) {
+    for (int k = (threadIdx.x & 31) * 16; k < depth; k += 32 * 16) {
+        float v[kFewColumns][16];
+#pragma unroll
+        for (int n = 0; n < kFewColumns; ++n) {
+            const uint4 q = *reinterpret_cast<const uint4*>(w[n] + k);
+            const float size = scale_of(powers[n][k / GS_SCALE_BLOCK]);
+            unpack8_e4m3(uint2{q.x, q.y}, v[n]);
+            unpack8_e4m3(uint2{q.z, q.w}, v[n] + 8);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[n][i] *= size;
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(&x[r][k + i]);
+#pragma unroll
+                for (int n = 0; n < kFewColumns; ++n) {
+                    sum[n][r] = fmaf(a.x, v[n][i], sum[n][r]);
+                    sum[n][r] = fmaf(a.y, v[n][i + 1], sum[n][r]);
+                    sum[n][r] = fmaf(a.z, v[n][i + 2], sum[n][r]);
+                    sum[n][r] = fmaf(a.w, v[n][i + 3], sum[n][r]);
+                }
+            }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kFewThreads)
+    k_few8_fwd(LinearArgs g, Rows8 xs, Rows8 weight, const T* __restrict__ bias,
+               T* __restrict__ ys) {
+    extern __shared__ int32_t begin[];
+    __shared__ __align__(16) float x[kFewRows][kFewDepth];
+    int e, row0, rows, kept;
+    const bool any = few_piece(g, begin, blockIdx.y, &e, &row0, &rows, &kept);
+    zero_tail(ys, kept, g.rows, g.out);
+    if (!any) return;
+    const int lane = threadIdx.x & 31;
+    const int n0 = (blockIdx.x * (kFewThreads / 32) + threadIdx.x / 32) * kFewColumns;
+    const int pitch = GS_ROW8_BYTES(g.in), scale_pitch = GS_ROW8_SCALES(g.in);
+    const uint8_t *w[kFewColumns], *powers[kFewColumns];
+#pragma unroll
+    for (int n = 0; n < kFewColumns; ++n) {
+        const int64_t row = (int64_t)e * g.out + min(n0 + n, g.out - 1);
+        w[n] = weight.q + row * pitch;
+        powers[n] = weight.scales + row * scale_pitch;
+    }
+    float sum[kFewColumns][kFewRows] = {};
+    for (int k0 = 0; k0 < g.in; k0 += kFewDepth) {
+        const int depth = min(kFewDepth, pitch - k0);  // zeros behind the last channel
+        if (k0 > 0) __syncthreads();
+        for (int r = 0; r < rows; ++r) {
+            const int64_t row = row0 + r;
+            for (int k = threadIdx.x * 8; k < depth; k += kFewThreads * 8) {
+                float v[8];
+                unpack8_e4m3(*reinterpret_cast<const uint2*>(xs.q + row * pitch + k0 + k), v);
+                const float size =
+                    scale_of(xs.scales[row * scale_pitch + (k0 + k) / GS_SCALE_BLOCK]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[r][k + i] = v[i] * size;
+            }
+        }
+        __syncthreads();
+        if (rows == 1)
+            few8_terms<1>(x, w, powers, depth, sum);
+        else if (rows == 2)
+            few8_terms<2>(x, w, powers, depth, sum);
+        else if (rows <= 4)
+            few8_terms<4>(x, w, powers, depth, sum);
+        else
+            few8_terms<8>(x, w, powers, depth, sum);
+#pragma unroll
+        for (int n = 0; n < kFewColumns; ++n) {
+            w[n] += kFewDepth;
+            powers[n] += kFewDepth / GS_SCALE_BLOCK;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kFewRows; ++r) {
+        if (r >= rows) break;
+#pragma unroll
+        for (int n = 0; n < kFewColumns; ++n) {
+            float v = warp_sum(sum[n][r]);
+            if (lane != n || n0 + n >= g.out) continue;
+            if (bias) v += to_f(bias[(int64_t)e * g.out + n0 + n]);
+            ys[(int64_t)(row0 + r) * g.out + n0 + n] = from_f<T>(v);
+        }
+    }
+}
+
 // grad_xs[r, k] = sum over n of grad_ys[r, n] weight[n, k]: a lane takes kVec
 // columns, the block's warps every sixteenth n; their sums meet in shared
 // memory.
@@ -207,6 +304,17 @@ void launch_few_fwd(const LinearArgs& a, const void* xs, const void* weight, con
             k_few_fwd<T, kWhole><<<grid, kFewThreads, smem, s>>>(a, x, w, b, y);
         else
             k_few_fwd<T, 1><<<grid, kFewThreads, smem, s>>>(a, x, w, b, y);
+    });
+}
+
+void launch_few8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* bias, void* ys,
+                     cudaStream_t s) {
+    const int columns = kFewColumns * kFewThreads / 32;
+    const dim3 grid((a.out + columns - 1) / columns, few_pieces(a));
+    with_dtype(a.dtype, [&](auto t) {
+        using T = decltype(t);
+        k_few8_fwd<T><<<grid, kFewThreads, 2 * sizeof(int32_t) * (a.experts + 1), s>>>(
+            a, xs, weight, static_cast<const T*>(bias), static_cast<T*>(ys));
     });
 }
 

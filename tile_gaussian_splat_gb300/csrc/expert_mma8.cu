@@ -9,13 +9,13 @@
 // of 32 channels: four in turn take the same byte.)
 //
 // In every block a warp copies slices of 128 channels into a ring of
-// shared-memory stages (tiled bulk copies), four warps read the rows' words of
-// powers and write them to tensor memory (each to its own quarter of the lanes:
-// the instruction wants them in all four), one warp of the first block issues
-// the matrix instructions, and eight warps move finished accumulators to the
-// output while the next tile is computed in the other ones.  The second
-// accumulators leave no room for the powers beside 256 columns each, so tiles
-// are 192 columns wide.
+// shared-memory stages (tiled bulk copies), another the rows' words of powers,
+// in the order of tensor memory, one warp of the first block issues the copies
+// of those words into tensor memory and the matrix instructions, and eight or
+// twelve warps move finished accumulators to the output (with the bias that a
+// warp laid out before) while the next tile is computed in the other ones.
+// The second accumulators leave no room for the powers beside 256 columns
+// each, so tiles are 192 columns wide.
 #include <algorithm>
 #include <cstdint>
 
@@ -32,19 +32,24 @@ namespace gs {
 
 namespace {
 
-constexpr int kDeep = 128;          // channels a stage: 128 bytes
-constexpr int kGroup = 4;           // stages a word of powers serves
+constexpr int kDeep = 256;          // channels a slice: two boxes of 128 bytes a row
+constexpr int kHalf = kDeep / 2;
+constexpr int kGroup = 2;           // slices a word of powers serves
 constexpr int kAccumulators = 2;
-// Warps: 0 copies, 1 issues products, 2, 3, 12 and 13 write powers (the
-// quarters 2, 3, 0 and 1 of the lanes), 4 to 11 write the output.
-constexpr int kThreads = 32 * 14;
+constexpr int kSpan = 64;           // columns an output warp writes
+// Warps: 0 copies rows, 1 issues products, 2 copies powers, 3 the bias, from 4
+// on they write the output.
+template <int kWide>
+constexpr int kOutputs = 4 * kWide / kSpan;
+template <int kWide>
+constexpr int kThreads = 32 * (4 + kOutputs<kWide>);
 // Columns of tensor memory: the accumulators, then the powers of kBuffers
-// groups, those of A in four columns and those of B, a column for 32 of its
-// rows, from the eighth on.
-constexpr int kColumns = 512, kPowers = 16, kBuffers = 4, kPowersB = 8;
+// groups, those of A's rows in four columns and those of B's, 128 rows in four.
+constexpr int kColumns = 512, kBuffers = 4, kPowersB = 4;
+constexpr int kChunk = 512;         // bytes of 128 rows' words
 // Slices summed in an accumulator before they are added to the running sum: as
 // many instructions as a round of half types over features.
-constexpr int kRound = 32;
+constexpr int kRound = 16;
 static_assert(kRound % kGroup == 0, "a round begins with a word of powers");
 
 struct Product8Args {
@@ -59,38 +64,42 @@ struct Product8Args {
     int32_t* d_status;
 };
 
-template <int kBlocks, int kWide>
+// kSlots, kStages: slices of A and of B in shared memory; kRowBytes: of the boxes
+// the output leaves in, 64 or 128.
+template <int kBlocks_, int kWide_, int kSlots_, int kStages_, int kRowBytes_>
 struct Shape8 {
+    static constexpr int kBlocks = kBlocks_, kWide = kWide_, kSlots = kSlots_;
+    static constexpr int kStages = kStages_, kRowBytes = kRowBytes_;
     static constexpr int kTileHigh = kHigh * kBlocks;
     static constexpr int kBytesA = kHigh * kDeep;
     static constexpr int kPartB = kWide / kBlocks;
     static constexpr int kBytesB = kPartB * kDeep;
-    static constexpr int kStageBytes = kBytesA + kBytesB;
-    static constexpr int kStages = 6;
-    static constexpr int kStaging = kOutWarps * 32 * 64;
-    static constexpr int kSpan = kWide / (kOutWarps / 4);  // columns an output warp writes
-    static constexpr int kBias = kOutWarps * kSpan * 4;
-    static_assert(kStageBytes % 1024 == 0, "swizzled rows begin on 1024 bytes");
+    static constexpr int kChunksB = (kWide + 127) / 128;
+    static constexpr int kPowers = 4 * (1 + kChunksB);  // columns of a buffer
+    static constexpr int kPowerBytes = (1 + kChunksB) * kChunk;
+    static constexpr int kStaging = kOutputs<kWide> * 32 * kRowBytes;
+    static constexpr int kBias = kAccumulators * kWide * 4;
+    static_assert(kPartB * kHalf % 1024 == 0, "swizzled rows begin on 1024 bytes");
     static_assert(kAccumulators * kWide + kBuffers * kPowers <= kColumns, "tensor memory");
-    static_assert(kWide / 32 <= kPowers - kPowersB, "powers of B");
 };
 
 struct Bars8 {
-    // of the first block: a stage's data, a buffer's powers are there (in all
-    // blocks), the accumulators may be overwritten
-    uint64_t full[6], powers_full[kBuffers], acc_empty[kAccumulators];
-    // of each block: a stage, a buffer of powers may be overwritten, the
-    // accumulators are finished
-    uint64_t empty[6], powers_empty[kBuffers], acc_full[kAccumulators], drain;
+    // of the first block: a slice of A or B, a buffer's words of powers are
+    // there (in all blocks), the accumulators may be overwritten
+    uint64_t full_a[4], full_b[4], words_full[kBuffers], acc_empty[kAccumulators];
+    // of each block: a slice may be overwritten, powers are in tensor memory,
+    // a buffer of them may be overwritten, the accumulators are finished, a
+    // tile's bias is there, and may be overwritten
+    uint64_t empty_a[4], empty_b[4], powers_full[kBuffers], powers_empty[kBuffers], acc_full[kAccumulators], bias_full[kAccumulators],
+        bias_empty[kAccumulators], drain;
     uint32_t tmem;
     int abort;
 };
 
-template <int kBlocks, int kWide>
+template <typename S>
 constexpr size_t smem_bytes8(int experts) {
-    using S = Shape8<kBlocks, kWide>;
-    return 1024 + (size_t)S::kStages * S::kStageBytes + S::kStaging + S::kBias + sizeof(Bars8) +
-           2 * sizeof(int32_t) * (size_t)(experts + 1);
+    return 1024 + S::kSlots * S::kBytesA + S::kStages * S::kBytesB + S::kStaging + kBuffers * S::kPowerBytes +
+           S::kBias + sizeof(Bars8) + 2 * sizeof(int32_t) * (size_t)(experts + 1);
 }
 
 struct Tile8 {
@@ -98,39 +107,61 @@ struct Tile8 {
     int row0, row1;  // rows of the output
     int n0;          // first column
     int q0, q1;      // slices of one round
+    bool first, final;  // of the tiles that share their slices of A
 };
 
 // The tiles of one pair of blocks (or block), in order; every warp of it walks
-// the same ones: item = (piece of an expert's rows, column tile).
-template <int kBlocks, int kWide>
+// the same ones: an equal share of the items (piece of an expert's rows, column
+// tile), column tiles of a piece on end.  They share the slices of A, which stay
+// in shared memory, where kSlots hold them all.
+// (Where a tile is follows from the one before: a division and a search of the
+// experts for each took a third of a tile's time, in every warp.)
+template <typename S>
 struct Walk8 {
-    using S = Shape8<kBlocks, kWide>;
-    const Product8Args& g;
-    const int32_t *begin, *prefix;
-    int64_t item, items;
-    int step, across, count;
+    const int32_t* begin;
+    int64_t left;                      // items to come
+    int across, count, experts;
+    int column = 0, expert = 0, row0 = 0;  // of the next tile
+    bool fresh = true;
 
-    __device__ __forceinline__ Walk8(const Product8Args& g_, const int32_t* begin_,
-                                     const int32_t* prefix_)
-        : g(g_), begin(begin_), prefix(prefix_) {
-        item = blockIdx.x / kBlocks;
-        step = gridDim.x / kBlocks;
-        across = (g.width + kWide - 1) / kWide;
+    __device__ __forceinline__ Walk8(const Product8Args& g, const int32_t* begin_,
+                                     const int32_t* prefix)
+        : begin(begin_), experts(g.experts) {
+        across = (g.width + S::kWide - 1) / S::kWide;
         count = (g.depth + kDeep - 1) / kDeep;
-        items = (int64_t)prefix[g.experts] * across;
+        const int64_t items = (int64_t)prefix[g.experts] * across;
+        const int shares = gridDim.x / S::kBlocks, share = blockIdx.x / S::kBlocks;
+        const int64_t item = items * share / shares;
+        left = items * (share + 1) / shares - item;
+        if (left <= 0) return;
+        const int piece = (int)(item / across);
+        column = (int)(item - (int64_t)piece * across);
+        expert = expert_of(prefix, experts, piece);
+        row0 = begin[expert] + (piece - prefix[expert]) * S::kTileHigh;
     }
 
     // c: as the call before left it (q1 = count before the first).
     __device__ __forceinline__ bool next(Tile8& c) {
         if (c.q1 == count) {
-            if (item >= items) return false;
-            const int piece = (int)(item / across);
-            c.n0 = (int)(item - (int64_t)piece * across) * kWide;
-            c.expert = expert_of(prefix, g.experts, piece);
-            c.row0 = begin[c.expert] + (piece - prefix[c.expert]) * S::kTileHigh;
-            c.row1 = min(begin[c.expert + 1], c.row0 + S::kTileHigh);
+            if (left <= 0) return false;
+            --left;
+            c.n0 = column * S::kWide;
+            c.expert = expert;
+            c.row0 = row0;
+            c.row1 = min(begin[expert + 1], row0 + S::kTileHigh);
             c.q1 = 0;
-            item += step;
+            c.first = fresh || count > S::kSlots;
+            fresh = ++column == across;
+            c.final = fresh || left == 0 || count > S::kSlots;
+            if (fresh) {
+                column = 0;
+                row0 += S::kTileHigh;
+                if (row0 >= begin[expert + 1]) {
+                    do ++expert;
+                    while (expert < experts && begin[expert] == begin[expert + 1]);
+                    row0 = begin[expert];
+                }
+            }
         }
         c.q0 = c.q1;
         c.q1 = min(count, c.q0 + kRound);
@@ -138,15 +169,25 @@ struct Walk8 {
     }
 };
 
-template <typename Out, int kBlocks, int kWide>
-__global__ void __launch_bounds__(kThreads, 1)
+// The slices of A in order, a slot for each: `at` of the first of a tile.
+template <int kSlots>
+struct Slots {
+    uint32_t at = 0;
+    __device__ __forceinline__ uint32_t slot(int q) const { return (at + q) % kSlots; }
+    __device__ __forceinline__ uint32_t turn(int q) const { return (at + q) / kSlots; }
+};
+
+template <typename Out, typename S>
+__global__ void __launch_bounds__(kThreads<S::kWide>, 1)
     k_product8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-               const __grid_constant__ Product8Args g) {
-    using S = Shape8<kBlocks, kWide>;
+               const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Product8Args g) {
+    constexpr int kBlocks = S::kBlocks, kWide = S::kWide;
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    char* staging = smem + S::kStages * S::kStageBytes;
-    Bars8& bars = *reinterpret_cast<Bars8*>(staging + S::kStaging + S::kBias);
+    char* staging = smem + S::kSlots * S::kBytesA + S::kStages * S::kBytesB;
+    char* words = staging + S::kStaging;
+    float* biases = reinterpret_cast<float*>(words + kBuffers * S::kPowerBytes);
+    Bars8& bars = *reinterpret_cast<Bars8*>(biases + kAccumulators * kWide);
     int32_t* begin = reinterpret_cast<int32_t*>(&bars + 1);
     int32_t* prefix = begin + g.experts + 1;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -155,17 +196,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
         tma_prefetch(&map_a);
         tma_prefetch(&map_b);
+        if (g.vectors) tma_prefetch(&map_out);
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(&bars.full_a[i], 1);
+            mbar_init(&bars.empty_a[i], 1);
+        }
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 1);
+            mbar_init(&bars.full_b[i], 1);
+            mbar_init(&bars.empty_b[i], 1);
         }
         for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(&bars.powers_full[i], 4 * kBlocks);
+            mbar_init(&bars.words_full[i], kBlocks);
+            mbar_init(&bars.powers_full[i], 1);
             mbar_init(&bars.powers_empty[i], 1);
         }
         for (int i = 0; i < kAccumulators; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], kOutWarps * kBlocks);
+            mbar_init(&bars.acc_empty[i], kOutputs<kWide> * kBlocks);
+            mbar_init(&bars.bias_full[i], 1);
+            mbar_init(&bars.bias_empty[i], kOutputs<kWide>);
         }
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
@@ -179,9 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kBlocks == 2) cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = bars.tmem, base = smem_u32(smem);
+    const uint32_t base_b = base + S::kSlots * S::kBytesA;
     const uint32_t powers = tmem + kAccumulators * kWide;
     volatile int* abort = &bars.abort;
-    Walk8<kBlocks, kWide> walk(g, begin, prefix);
+    Walk8<S> walk(g, begin, prefix);
     Tile8 c{};
     c.q1 = walk.count;
     // where a running sum takes the second accumulator's place
@@ -189,37 +239,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         Ring<S::kStages> at;
+        Slots<S::kSlots> slots;
+        uint32_t loaded = 0;  // slices of A
         bool ok = true;
+        const auto bar = [&](uint64_t* b) { return kBlocks == 2 ? mbar_at(b, 0) : smem_u32(b); };
         while (ok && walk.next(c)) {
             const int n0 =
                 c.n0 + rank * (tile_columns<kBlocks, kWide>(g.width, c.n0) / kBlocks);
             for (int q = c.q0; q < c.q1; ++q, at.advance()) {
-                ok = at.turn == 0 || warp_wait(&bars.empty[at.stage], (at.turn + 1) & 1, abort);
+                // a last slice of up to 128 channels is one box
+                const int boxes = g.depth - q * kDeep > kHalf ? 2 : 1;
+                if (c.first) {
+                    const uint32_t slot = slots.slot(q), turn = slots.turn(q);
+                    ok = turn == 0 || warp_wait(&bars.empty_a[slot], (turn + 1) & 1, abort);
+                    if (!ok) break;
+                    const uint32_t full = bar(&bars.full_a[slot]);
+                    if (elect_one()) {
+                        if (rank == 0)
+                            mbar_expect_tx(&bars.full_a[slot], boxes * S::kBytesA / 2 * kBlocks);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d<kBlocks>(base + slot * S::kBytesA + i * S::kBytesA / 2,
+                                                 &map_a, q * kDeep + i * kHalf,
+                                                 c.row0 + rank * kHigh, full);
+                    }
+                    ++loaded;
+                }
+                ok = at.turn == 0 || warp_wait(&bars.empty_b[at.stage], (at.turn + 1) & 1, abort);
                 if (!ok) break;
-                const uint32_t a = base + at.stage * S::kStageBytes;
-                const uint32_t full = kBlocks == 2 ? mbar_at(&bars.full[at.stage], 0)
-                                                   : smem_u32(&bars.full[at.stage]);
+                const uint32_t full = bar(&bars.full_b[at.stage]);
                 if (elect_one()) {
                     if (rank == 0)
-                        mbar_expect_tx(&bars.full[at.stage], S::kStageBytes * kBlocks);
-                    tma_load_2d<kBlocks>(a, &map_a, q * kDeep, c.row0 + rank * kHigh, full);
-                    tma_load_3d<kBlocks>(a + S::kBytesA, &map_b, q * kDeep, n0, c.expert, full);
+                        mbar_expect_tx(&bars.full_b[at.stage], boxes * S::kBytesB / 2 * kBlocks);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_3d<kBlocks>(base_b + at.stage * S::kBytesB + i * S::kBytesB / 2,
+                                             &map_b, q * kDeep + i * kHalf, n0, c.expert, full);
                 }
                 __syncwarp();
             }
+            if (c.final && c.q1 == walk.count) slots.at += walk.count;
         }
-        if (!ok && rank == 0)  // let the copies in flight land before the blocks go
+        if (!ok && rank == 0) {  // let the copies in flight land before the blocks go
+            int none = 0;
             for (int i = 0; i < S::kStages; ++i) {
                 // stages [stage, ...) were last filled one turn ago
                 const uint32_t turn = i < (int)at.stage ? at.turn : at.turn - 1;
-                int none = 0;
-                if (turn != ~0u) mbar_wait_limited(&bars.full[i], turn & 1, &none);
+                if (turn != ~0u) mbar_wait_limited(&bars.full_b[i], turn & 1, &none);
             }
+            for (uint32_t i = loaded > S::kSlots ? loaded - S::kSlots : 0; i < loaded; ++i)
+                mbar_wait_limited(&bars.full_a[i % S::kSlots], i / S::kSlots & 1, &none);
+        }
     } else if (warp == 1) {
         constexpr uint32_t word0 = mma_word_e4m3(S::kTileHigh);
         const uint64_t from_a = smem_operand(base, 16, 1024);
-        const uint64_t from_b = smem_operand(base + S::kBytesA, 16, 1024);
+        const uint64_t from_b = smem_operand(base_b, 16, 1024);
         Ring<S::kStages> at;
+        Slots<S::kSlots> slots;
         Ring<kAccumulators> acc;
         Ring<kBuffers> buffer;
         bool ok = rank == 0;
@@ -235,27 +309,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tmem_fence_after();
                 }
-                ok = warp_wait(&bars.full[at.stage], at.turn & 1, abort);
+                const uint32_t slot = slots.slot(q);
+                if (c.first) ok = warp_wait(&bars.full_a[slot], slots.turn(q) & 1, abort);
                 if (!ok) break;
-                const uint64_t da = from_a + at.stage * (S::kStageBytes >> 4);
-                const uint64_t db = from_b + at.stage * (S::kStageBytes >> 4);
-                const uint32_t from = powers + buffer.stage * kPowers;
-                const uint32_t byte = q % kGroup;
+                ok = warp_wait(&bars.full_b[at.stage], at.turn & 1, abort);
+                if (!ok) break;
+                const uint64_t da = from_a + slot * (S::kBytesA >> 4);
+                const uint64_t db = from_b + at.stage * (S::kBytesB >> 4);
+                const uint32_t from = powers + buffer.stage * S::kPowers;
                 const bool last = q % kGroup == kGroup - 1 || q + 1 == c.q1;
-                if (elect_one()) {
+                // 32 channels an instruction, four in turn with the same byte
+                const uint32_t turned = word | (uint32_t)(q % kGroup) << 5 |
+                                        (uint32_t)(q % kGroup) << 30;
+                const auto product = [&](int j) {
+                    constexpr int kJumpA = S::kBytesA / 2 >> 4, kJumpB = S::kBytesB / 2 >> 4;
+                    mma_e4m3<kBlocks>(d, da + j / 4 * kJumpA + j % 4 * (32 >> 4),
+                                      db + j / 4 * kJumpB + j % 4 * (32 >> 4),
+                                      turned | (uint32_t)(j / 4) << 4 | (uint32_t)(j / 4) << 29,
+                                      from, from + kPowersB, q > c.q0 || j > 0);
+                };
+                const int steps = (g.depth - q * kDeep + 31) / 32;
+                if (steps >= kDeep / 32) {
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < kDeep / 32; ++j)
-                        mma_e4m3<kBlocks>(d, da + j * (32 >> 4), db + j * (32 >> 4),
-                                          word | byte << 4 | byte << 29, from, from + kPowersB,
-                                          q > c.q0 || j > 0);
-                    mma_commit<kBlocks>(&bars.empty[at.stage]);
-                    if (last) mma_commit<kBlocks>(&bars.powers_empty[buffer.stage]);
-                    if (q + 1 == c.q1) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
+                        for (int j = 0; j < kDeep / 32; ++j) product(j);
+                        mma_commit<kBlocks>(&bars.empty_b[at.stage]);
+                    }
+                } else if (elect_one()) {
+                    for (int j = 0; j < steps; ++j) product(j);
+                    mma_commit<kBlocks>(&bars.empty_b[at.stage]);
                 }
+                if (c.final && elect_one()) mma_commit<kBlocks>(&bars.empty_a[slot]);
+                if (last && elect_one()) mma_commit<kBlocks>(&bars.powers_empty[buffer.stage]);
+                if (q + 1 == c.q1 && elect_one()) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
                 __syncwarp();
                 if (last) buffer.advance();
             }
             acc.advance(accumulators);
+            if (c.final && c.q1 == walk.count) slots.at += walk.count;
         }
         // nothing is still writing tensor memory when it is freed
         if (rank == 0) {
@@ -264,129 +355,200 @@ __global__ void __launch_bounds__(kThreads, 1)
             int none = 0;
             mbar_wait_limited(&bars.drain, 0, &none);
         }
-    } else if (warp < 4 || warp >= 4 + kOutWarps) {
-        const uint32_t mine = powers + ((uint32_t)((warp & 3) * 32) << 16);
-        Ring<kBuffers> buffer;
+    } else if (warp == 2) {
+        // words of powers, a buffer a group, passed on when the copies of two
+        // more are on their way; the first block's warp has all of them copied
+        // into tensor memory (the warp that issues the products lost a fifth
+        // of its time to that)
+        constexpr int kBehind = 2;
+        static_assert(kBehind < kBuffers, "a buffer that is not passed on is not waited for");
+        Ring<kBuffers> buffer, next;
         bool ok = true;
+        int waiting = 0;
+        // the fence hands the words over to the tensor cores' copies; a release
+        // at cluster scope on top cost 1 us a tile
+        const auto pass_on = [&] {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(&bars.words_full[next.stage], 0);
+            if (rank == 0) {
+                ok = warp_wait(&bars.words_full[next.stage], next.turn & 1, abort);
+                if (!ok) return;
+                tmem_fence_after();
+                const uint32_t chunk = smem_u32(words) + next.stage * S::kPowerBytes;
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < 1 + S::kChunksB; ++j)
+                        tmem_copy_32x16<kBlocks>(powers + next.stage * S::kPowers + j * 4,
+                                                 chunk + j * kChunk);
+                    mma_commit<kBlocks>(&bars.powers_full[next.stage]);
+                }
+                __syncwarp();
+            }
+            next.advance();
+        };
         while (ok && walk.next(c)) {
-            const int row = c.row0 + rank * kHigh + lane;
+            const int row = c.row0 + rank * kHigh + lane, n = c.n0 + lane;
             const uint32_t* a = g.powers_a + (int64_t)row * g.words;
-            const uint32_t* b =
-                g.powers_b + ((int64_t)c.expert * g.width + c.n0 + lane) * g.words;
+            const uint32_t* b = g.powers_b + ((int64_t)c.expert * g.width + n) * g.words;
             for (int q = c.q0; q < c.q1; q += kGroup, buffer.advance()) {
-                uint32_t v[kPowers] = {};
-                const int word = q / kGroup;
-#pragma unroll
-                for (int i = 0; i < kHigh / 32; ++i)
-                    if (row + i * 32 < c.row1) v[i] = a[(int64_t)i * 32 * g.words + word];
-#pragma unroll
-                for (int i = 0; i < kWide / 32; ++i)
-                    if (c.n0 + lane + i * 32 < g.width)
-                        v[kPowersB + i] = b[(int64_t)i * 32 * g.words + word];
                 ok = buffer.turn == 0 ||
                      warp_wait(&bars.powers_empty[buffer.stage], (buffer.turn + 1) & 1, abort);
                 if (!ok) break;
-                tmem_fence_after();
-                tmem_store16(mine + buffer.stage * kPowers, v);
-                tmem_wait_stores();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(&bars.powers_full[buffer.stage], 0);
+                const int word = q / kGroup;
+                // row r's word at 16 (r % 32) + 4 (r / 32): tensor memory's order
+                const uint32_t to =
+                    smem_u32(words) + buffer.stage * S::kPowerBytes + lane * 16;
+#pragma unroll
+                for (int i = 0; i < kHigh / 32; ++i) {
+                    const bool in = row + i * 32 < c.row1;
+                    copy_word(to + i * 4, in ? a + (int64_t)i * 32 * g.words + word : g.powers_a,
+                              in);
+                }
+#pragma unroll
+                for (int i = 0; i < kWide / 32; ++i) {
+                    const bool in = n + i * 32 < g.width;
+                    copy_word(to + (1 + i / 4) * kChunk + i % 4 * 4,
+                              in ? b + (int64_t)i * 32 * g.words + word : g.powers_b, in);
+                }
+                copy_group();
+                if (waiting == kBehind) {
+                    copy_wait<kBehind>();
+                    pass_on();
+                    if (!ok) break;
+                } else {
+                    ++waiting;
+                }
             }
+        }
+        copy_wait<0>();
+        for (; ok && waiting > 0; --waiting) pass_on();
+    } else if (warp == 3) {
+        Ring<kAccumulators> at;
+        bool ok = g.bias != nullptr;
+        while (ok && walk.next(c)) {
+            if (c.q1 < walk.count) continue;  // added to what the last round leaves
+            if (at.turn > 0) ok = warp_wait(&bars.bias_empty[at.stage], (at.turn + 1) & 1, abort);
+            if (!ok) break;
+            const Out* p = static_cast<const Out*>(g.bias) + (int64_t)c.expert * g.width;
+#pragma unroll
+            for (int i = lane; i < kWide; i += 32)
+                biases[at.stage * kWide + i] = c.n0 + i < g.width ? to_f(p[c.n0 + i]) : 0.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.bias_full[at.stage]);
+            at.advance();
         }
     } else {
         const int q = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
-        constexpr int kSpan = S::kSpan;
-        // the next 32 columns come in while these go out (float32 has no
-        // registers to spare)
-        constexpr int kAhead = sizeof(Out) == 4 ? 0 : 1;
-        float* bias = reinterpret_cast<float*>(staging + S::kStaging) + (warp - 4) * kSpan;
         const int first = (warp - 4) / 4 * kSpan;
-        char* mine = staging + (warp - 4) * 32 * 64;
-        Ring<kAccumulators> acc;
+        char* mine = staging + (warp - 4) * 32 * S::kRowBytes;
+        constexpr int kRow = S::kRowBytes / (int)sizeof(Out);  // columns written at a time
+        constexpr int kVectors = S::kRowBytes / 16;
+        Ring<kAccumulators> acc, added;
         bool ok = true;
         for (; ok && walk.next(c); acc.advance(accumulators)) {
             const uint32_t from =
                 tmem + ((uint32_t)(q * 32) << 16) + acc.stage * kWide + first;
-            uint32_t u[1 + kAhead][32];
-            if (g.bias) {
-                const Out* p = static_cast<const Out*>(g.bias) + (int64_t)c.expert * g.width;
-#pragma unroll
-                for (int i = lane; i < kSpan; i += 32) {
-                    const int n = c.n0 + first + i;
-                    bias[i] = n < g.width ? to_f(p[n]) : 0.f;
-                }
-                __syncwarp();
-            }
+            const int row = rank * kHigh + q * 32;  // first row in the tile
+            Out* out = static_cast<Out*>(g.out) + ((int64_t)c.row0 + row) * g.width + c.n0 + first;
+            const int rows = c.row1 - c.row0 - row;
+            const bool last = c.q1 == walk.count, with_bias = last && g.bias;
             ok = warp_wait(&bars.acc_full[acc.stage], acc.turn & 1, abort);
             if (!ok) break;
             tmem_fence_after();
-            if (kAhead) {
-                tmem_load32(from, u[0]);
-                tmem_wait_loads();
+            if (with_bias) {
+                ok = warp_wait(&bars.bias_full[added.stage], added.turn & 1, abort);
+                if (!ok) break;
             }
-            const int row = rank * kHigh + q * 32;  // first row in the tile
-            Out* out = static_cast<Out*>(g.out) + ((int64_t)c.row0 + row) * g.width + c.n0;
-            const int rows = c.row1 - c.row0 - row;
-            const bool last = c.q1 == walk.count;
+            const float* bias = biases + added.stage * kWide + first;
+            uint32_t u[kSpan];
 #pragma unroll
-            for (int b = 0; b < kSpan / 32; ++b) {
-                const int n = first + b * 32;
-                if (b + kAhead < kSpan / 32)
-                    tmem_load32(from + (b + kAhead) * 32, u[(b + 1) & kAhead]);
-                if (!kAhead) tmem_wait_loads();
-                uint32_t* w = u[b & kAhead];
-                const uint32_t sum = from + kWide + b * 32;
-                if (c.q0 > 0) {
+            for (int i = 0; i < kSpan; i += 32) tmem_load32(from + i, u + i);
+            tmem_wait_loads();
+            const uint32_t sum = from + kWide;
+            if (c.q0 > 0) {
+#pragma unroll
+                for (int i = 0; i < kSpan; i += 32) {
                     uint32_t was[32];
-                    tmem_load32(sum, was);
+                    tmem_load32(sum + i, was);
                     tmem_wait_loads();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        w[i] = __float_as_uint(__uint_as_float(was[i]) + __uint_as_float(w[i]));
-                }
-                const int left = g.width - c.n0 - n;  // columns from here on
-                if (!last) {
-                    tmem_store32(sum, w);
-                    tmem_wait_stores();
-                } else if (left > 0) {
-                    constexpr int kRow = 64 / (int)sizeof(Out);  // columns written at a time
-#pragma unroll
-                    for (int h = 0; h < 32 / kRow; ++h) {
-                        uint4 v[4];
-#pragma unroll
-                        for (int i = 0; i < kRow / 8; ++i) {
-                            float f[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                f[j] = __uint_as_float(w[kRow * h + 8 * i + j]);
-                            if (g.bias) {
-                                const float4* p = reinterpret_cast<const float4*>(
-                                    bias + b * 32 + kRow * h + 8 * i);
-                                const float4 lo = p[0], hi = p[1];
-                                f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
-                                f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
-                            }
-                            pack8<Out>(f, v + i * (int)sizeof(Out) / 2);
-                        }
-                        write_block<Out>(mine, v, out + n + kRow * h, g.width, rows,
-                                         left - kRow * h, g.vectors);
-                    }
-                }
-                tmem_wait_loads();
-                if (b + 1 + kAhead == kSpan / 32) {
-                    // the accumulator is read: its next product may begin
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(&bars.acc_empty[acc.stage], 0);
+                    for (int j = 0; j < 32; ++j)
+                        u[i + j] = __float_as_uint(__uint_as_float(was[j]) +
+                                                   __uint_as_float(u[i + j]));
                 }
             }
+            if (!last) {
+#pragma unroll
+                for (int i = 0; i < kSpan; i += 32) tmem_store32(sum + i, u + i);
+                tmem_wait_stores();
+            }
+            // the accumulator is read: its next product may begin
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(&bars.acc_empty[acc.stage], 0);
+            const int left = g.width - c.n0 - first;  // columns from here on
+            // whole rows of whole vectors go out as boxes
+            const bool boxed = g.vectors && rows >= 32;
+            const auto write = [&](auto biased) {
+#pragma unroll
+                for (int b = 0; b < kSpan / kRow; ++b) {
+                    if (b * kRow >= left) break;
+                    uint4 v[kVectors];
+#pragma unroll
+                    for (int i = 0; i < kRow / 8; ++i) {
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(u[b * kRow + 8 * i + j]);
+                        if constexpr (decltype(biased)::value) {
+                            const float4* p =
+                                reinterpret_cast<const float4*>(bias + b * kRow + 8 * i);
+                            const float4 lo = p[0], hi = p[1];
+                            f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
+                            f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+                        }
+                        pack8<Out>(f, v + i * (int)sizeof(Out) / 2);
+                    }
+                    // the box before has left
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+                    if (boxed) {
+#pragma unroll
+                        for (int j = 0; j < kVectors; ++j) {
+                            const int turn = kVectors == 8 ? lane & 7 : lane >> 1 & 3;
+                            *reinterpret_cast<uint4*>(mine + lane * S::kRowBytes +
+                                                      ((j ^ turn) << 4)) = v[j];
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0)
+                            tma_store_2d(&map_out, smem_u32(mine), c.n0 + first + b * kRow,
+                                         c.row0 + row);
+                    } else {
+                        constexpr int kPart = 64 / (int)sizeof(Out);
+#pragma unroll
+                        for (int h = 0; h < kRow / kPart; ++h)
+                            write_block<Out>(mine, v + h * 4, out + b * kRow + h * kPart, g.width,
+                                             rows, left - b * kRow - h * kPart, g.vectors);
+                    }
+                }
+            };
+            if (with_bias)
+                write(std::true_type{});
+            else if (last)
+                write(std::false_type{});
+            if (with_bias) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.bias_empty[added.stage]);
+                added.advance();
+            }
         }
+        if (lane == 0) bulk_wait();
         // rows of no expert are 0
         const int64_t kept = begin[g.experts];
         zero_range(static_cast<Out*>(g.out) + kept * g.width, (g.rows - kept) * g.width,
-                   (int64_t)blockIdx.x * (kOutWarps * 32) + threadIdx.x - 128,
-                   (int64_t)gridDim.x * (kOutWarps * 32), g.vectors);
+                   (int64_t)blockIdx.x * (kOutputs<kWide> * 32) + threadIdx.x - 128,
+                   (int64_t)gridDim.x * (kOutputs<kWide> * 32), g.vectors);
     }
     __syncthreads();
     if (kBlocks == 2) cluster_sync();  // the other block's arrivals and products are over too
@@ -403,7 +565,7 @@ bool make_map8(CUtensorMap* map, const uint8_t* base, int64_t rows, int columns,
     const cuuint64_t pitch = GS_ROW8_BYTES(columns);
     const cuuint64_t dims[3] = {(cuuint64_t)columns, (cuuint64_t)rows, (cuuint64_t)experts};
     const cuuint64_t strides[2] = {pitch, pitch * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {kDeep, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {kHalf, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, experts > 0 ? 3 : 2,
                   const_cast<uint8_t*>(base), dims, strides, box, unit,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -411,26 +573,47 @@ bool make_map8(CUtensorMap* map, const uint8_t* base, int64_t rows, int columns,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Out, int kBlocks, int kWide>
+// The output in boxes of 32 rows x row_bytes, swizzled.
+bool make_out_map(CUtensorMap* map, int dtype, void* ys, int64_t rows, int width, int row_bytes) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const size_t size = dtype_size(dtype);
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, pitch = width * size;
+    const cuuint32_t box[2] = {(cuuint32_t)(row_bytes / size), 32}, unit[2] = {1, 1};
+    return encode(map,
+                  dtype == GS_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                  : dtype == GS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  2, ys, dims, &pitch, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Out, typename S>
 int launch_shape(const LinearArgs& a, Rows8 xs, Rows8 weight, const Product8Args& g,
                  cudaStream_t s) {
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mo{};
+    if (g.vectors && !make_out_map(&mo, a.dtype, g.out, a.rows, a.out, S::kRowBytes))
+        return GS_ERR_CUDA;
     if (!make_map8(&ma, xs.q, a.rows, a.in, 0, kHigh) ||
-        !make_map8(&mb, weight.q, a.out, a.in, a.experts, kWide / kBlocks))
+        !make_map8(&mb, weight.q, a.out, a.in, a.experts, S::kPartB))
         return GS_ERR_CUDA;
     // at most one part-filled tile an expert
-    const int64_t items =
-        (a.rows / (kHigh * kBlocks) + a.experts) * ceil_div(g.width, kWide);
+    const int64_t items = (a.rows / S::kTileHigh + a.experts) * ceil_div(g.width, S::kWide);
     static PerDevice raised, resident;
-    return launch_walk<kBlocks>(raised, resident, k_product8<Out, kBlocks, kWide>, kThreads,
-                                smem_bytes8<kBlocks, kWide>(g.experts),
-                                smem_bytes8<kBlocks, kWide>(GS_MAX_EXPERTS), items, s, ma, mb, g);
+    return launch_walk<S::kBlocks>(raised, resident, k_product8<Out, S>, kThreads<S::kWide>,
+                                   smem_bytes8<S>(g.experts), smem_bytes8<S>(GS_MAX_EXPERTS),
+                                   items, s, ma, mb, mo, g);
 }
 
 }  // namespace
 
 int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* bias, void* ys,
                        cudaStream_t s) {
+    if (few_rows(a, true)) {
+        launch_few8_fwd(a, xs, weight, bias, ys, s);
+        return GS_OK;
+    }
     Product8Args g{};
     g.offsets = a.offsets;
     g.powers_a = reinterpret_cast<const uint32_t*>(xs.scales);
@@ -449,10 +632,12 @@ int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* 
     int rc = GS_OK;
     with_dtype(a.dtype, [&](auto o) {
         using Out = decltype(o);
-        if (a.out > 128 && tiles >= sm_count())
-            rc = launch_shape<Out, 2, 192>(a, xs, weight, g, s);
+        if (a.out <= 128 || tiles < sm_count())
+            rc = launch_shape<Out, Shape8<1, 128, 3, 3, 64>>(a, xs, weight, g, s);
+        else if (a.in <= 2 * kDeep)
+            rc = launch_shape<Out, Shape8<2, 192, 2, 4, 128>>(a, xs, weight, g, s);
         else
-            rc = launch_shape<Out, 1, 128>(a, xs, weight, g, s);
+            rc = launch_shape<Out, Shape8<2, 192, 4, 2, 64>>(a, xs, weight, g, s);
     });
     return rc;
 }

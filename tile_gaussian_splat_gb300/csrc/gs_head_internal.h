@@ -76,11 +76,16 @@ struct LinearArgs {
     int32_t* d_status;
     bool packed = false;  // xs and weight are 8-bit rows
 };
+struct Rows8 {
+    const uint8_t *q, *scales;
+};
 // ---- expert_few.cu: the products of few rows, bound by reading the weights.
 // as_they_lie: the tensor cores could read the weights in place.
 bool few_rows(const LinearArgs& a, bool as_they_lie);
 void launch_few_fwd(const LinearArgs& a, const void* xs, const void* weight, const void* bias,
                     void* ys, cudaStream_t s);
+void launch_few8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* bias, void* ys,
+                     cudaStream_t s);
 void launch_few_dx(const LinearArgs& a, const void* grad_ys, const void* weight, void* grad_xs,
                    cudaStream_t s);
 // ---- expert_mma.cu
@@ -94,9 +99,6 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
                       const void* weight, void* grad_xs, void* grad_weight, void* grad_bias,
                       void* workspace, cudaStream_t s);
 // The same of 8-bit rows (a.packed).
-struct Rows8 {
-    const uint8_t *q, *scales;
-};
 // ---- expert_mma8.cu
 int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* bias, void* ys,
                        cudaStream_t s);

@@ -65,6 +65,12 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// Arrives on a barrier of this block, after which this thread's writes to its
+// shared memory are seen by whoever in the block waited for it.
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Arrives on the barrier at the same place in block `rank` of the cluster.
 // What the arrivals here hand over was written by bulk copies or read from
 // tensor memory, which barriers and fences of their own order: the arrival
@@ -147,6 +153,23 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
             : "memory");
 }
 
+// A box from shared memory to a two-dimensional array (what lies beyond its
+// extents is not written), a group of its own among the thread's bulk copies.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+        "cp.async.bulk.commit_group;" ::"l"(map),
+        "r"(c0), "r"(c1), "r"(src)
+        : "memory");
+}
+// Until the thread's bulk stores have read shared memory, or are over.
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // By one warp of each of the kBlocks (1 or 2) blocks whose products share
 // instructions.
 template <int kBlocks>
@@ -207,20 +230,40 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
         "r"(v[30]), "r"(v[31]), "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
-        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-        "r"(addr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_wait_stores() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_wait_loads() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// 32 x 16 bytes that lie on end in shared memory (of each of the blocks) into
+// four columns of tensor memory: 16 bytes a lane, the same for every quarter of
+// the lanes.  Products issued afterwards by the same thread find them there.
+template <int kBlocks>
+__device__ __forceinline__ void tmem_copy_32x16(uint32_t to, uint32_t smem) {
+    const uint64_t from = (uint64_t)((smem & 0x3ffffu) >> 4) | (uint64_t)(128 >> 4) << 16 |
+                          (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+    if constexpr (kBlocks == 2)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(from)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(from)
+                     : "memory");
+}
+
+// Four bytes from global into shared memory without a register between, zeros
+// where !in (the address is then not read).
+__device__ __forceinline__ void copy_word(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the newest kLeft groups of copies are there.
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 // Shared-memory operand of the matrix instruction: 128-byte rows, swizzled as
