@@ -29,13 +29,11 @@ __device__ __forceinline__ float scale_of(int byte) {
     return byte ? two_to(byte) : __uint_as_float(1u << 22);
 }
 
-// Four values rounded to e4m3 (ties to even); at most 448 in size, or not
-// finite: those become NaN, there is no infinity.
+// Four values rounded to e4m3 (ties to even); at most 448 in size, or NaN.
 __device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float d) {
     uint16_t lo, hi;
-    const auto known = [](float v) { return v - v == 0.f ? v : __uint_as_float(0x7fffffffu); };
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(lo) : "f"(known(a)), "f"(known(b)));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(hi) : "f"(known(c)), "f"(known(d)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(lo) : "f"(a), "f"(b));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(hi) : "f"(c), "f"(d));
     return (uint32_t)lo | (uint32_t)hi << 16;
 }
 

@@ -168,10 +168,10 @@ class PerDevice {
 // over the rows in equal shares needs exactly those (a second, part-filled wave
 // costs a whole one).
 template <typename K>
-int resident_blocks(PerDevice& resident, K kernel, size_t smem) {
+int resident_blocks(PerDevice& resident, K kernel, size_t smem, int threads = kRowThreads) {
     return resident.get(152, [&] {
         int per = 0, dev = 0, sms = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kRowThreads, smem) !=
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) !=
                 cudaSuccess ||
             cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -21,7 +21,16 @@ namespace gs {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kWarps = kRowThreads / 32;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// How many lanes share a row, accesses of kVec elements and accesses a lane; a
+// lane holds up to kSlots choices (a row alone four, 32 lanes' 64 together).
+template <int kVec_, int kLanes_, int kItems_>
+struct Spread {
+    static constexpr int kVec = kVec_, kLanes = kLanes_, kItems = kItems_;
+    static constexpr int kSlots = kLanes == 1 ? 4 : kLanes == 32 ? 2 : 1;
+};
 
 // Logits as words in the order of the values: 0 = not to be chosen (minus
 // infinity), a NaN above everything, both zeros the same.
@@ -73,6 +82,7 @@ struct RouteFwd {
     uint32_t* ticket;
     int64_t ld, tokens;
     int topk, experts, renormalise;
+    int pairs;                  // two choices a token, to be written together
 };
 
 // loss = experts * sum over e of share_e * mean probability_e, by one warp in
@@ -92,12 +102,10 @@ __device__ __forceinline__ float balance(const float* sums, const int32_t* count
     return pairs > 0 ? (float)experts * (dot / ((float)taking * (float)pairs)) : 0.f;
 }
 
-// kVec elements per access, kLanes lanes a row, kItems accesses a lane and
-// row, kRows rows of a lane in flight.
-template <typename T, int kVec, int kLanes, int kItems, int kRows>
-__global__ void __launch_bounds__(kRowThreads) k_route_fwd(RouteFwd a) {
-    constexpr int kGroups = kRowThreads / kLanes;
-    constexpr int kSlots = 64 / kLanes < 8 ? 64 / kLanes : 8;  // choices a lane holds
+template <typename T, typename F>
+__global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
+    constexpr int kVec = F::kVec, kLanes = F::kLanes, kItems = F::kItems, kSlots = F::kSlots;
+    constexpr int kGroups = kThreads / kLanes;
     extern __shared__ int32_t shared[];
     int32_t* count = shared;                                          // experts + 1
     float* sums = reinterpret_cast<float*>(shared + a.experts + 1);   // kWarps x experts
@@ -105,116 +113,118 @@ __global__ void __launch_bounds__(kRowThreads) k_route_fwd(RouteFwd a) {
     const int at = threadIdx.x % kLanes;
     if (tally) {
         if (blockIdx.x == 0 && threadIdx.x == 0 && gridDim.x > 1) *a.ticket = 0;
-        for (int e = threadIdx.x; e <= a.experts; e += kRowThreads) count[e] = 0;
+        for (int e = threadIdx.x; e <= a.experts; e += kThreads) count[e] = 0;
         __syncthreads();
     }
     float sum[kItems][kVec] = {};
     int taking = 0;
     const int64_t step = (int64_t)gridDim.x * kGroups;
-    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step * kRows) {
-        RawVec<T, kVec> raw[kRows][kItems];
-        bool keep[kRows];
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step) {
+        const int64_t r = r0 + threadIdx.x / kLanes;
+        const bool keep = r < a.tokens && (!a.keep || a.keep[r]);
+        const T* x = static_cast<const T*>(a.logits) + r * a.ld + at * kVec;
+        RawVec<T, kVec> raw[kItems];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
-            keep[u] = r < a.tokens && (!a.keep || a.keep[r]);
-            const T* x = static_cast<const T*>(a.logits) + r * a.ld + at * kVec;
+        for (int i = 0; i < kItems; ++i)
+            raw[i] = keep && (i * kLanes + at) * kVec < a.experts
+                         ? load_raw<T, kVec>(x + i * kLanes * kVec)
+                         : RawVec<T, kVec>{};
+        uint32_t key[kItems][kVec];
 #pragma unroll
-            for (int i = 0; i < kItems; ++i)
-                raw[u][i] = keep[u] && (i * kLanes + at) * kVec < a.experts
-                                ? load_raw<T, kVec>(x + i * kLanes * kVec)
-                                : RawVec<T, kVec>{};
+        for (int i = 0; i < kItems; ++i) {
+            float v[kVec];
+            unpack<T, kVec>(raw[i], v);
+            const bool in = keep && (i * kLanes + at) * kVec < a.experts;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) key[i][j] = in ? order_key(v[j]) : 0;
         }
+        int id[kSlots];
+        float e[kSlots];
+        float top = 0.f;
+        bool any = false;
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
-            uint32_t key[kItems][kVec];
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                float v[kVec];
-                unpack<T, kVec>(raw[u][i], v);
-                const bool in = keep[u] && (i * kLanes + at) * kVec < a.experts;
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) key[i][j] = in ? order_key(v[j]) : 0;
-            }
-            int id[kSlots];
-            float e[kSlots];
-            float top = 0.f;
-            bool any = false;
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                id[s] = -1;
-                e[s] = 0.f;
-                for (int l = 0; l < kLanes; ++l) {
-                    const int round = s * kLanes + l;
-                    if (round >= a.topk) break;
-                    uint32_t best = 0;
-                    int index = 0x7fffffff;
-#pragma unroll
-                    for (int i = 0; i < kItems; ++i)
-#pragma unroll
-                        for (int j = 0; j < kVec; ++j)
-                            if (key[i][j] > best) {
-                                best = key[i][j];
-                                index = (i * kLanes + at) * kVec + j;
-                            }
-                    group_best<kLanes>(best, index);
-#pragma unroll
-                    for (int i = 0; i < kItems; ++i)
-#pragma unroll
-                        for (int j = 0; j < kVec; ++j)
-                            if (index == (i * kLanes + at) * kVec + j) key[i][j] = 0;
-                    if (round == 0) {
-                        any = best > 0;
-                        top = key_value(best);
-                    }
-                    if (at == l && best > 0) {
-                        id[s] = index;
-                        e[s] = expf(key_value(best) - top);
-                    }
-                }
-                if ((s + 1) * kLanes >= a.topk) break;
-            }
-            float all = 0.f, chosen = 0.f;
-            float p[kItems][kVec];
-            if (tally || !a.renormalise) {
-#pragma unroll
-                for (int i = 0; i < kItems; ++i) {
-                    float v[kVec];
-                    unpack<T, kVec>(raw[u][i], v);
-                    const bool in = any && (i * kLanes + at) * kVec < a.experts;
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        p[i][j] = in ? expf(v[j] - top) : 0.f;
-                        all += p[i][j];
-                    }
-                }
-                all = group_sum<kLanes>(all);
-            }
-            if (tally && any) {
-                const float each = 1.0f / all;
+        for (int s = 0; s < kSlots; ++s) {
+            id[s] = -1;
+            e[s] = 0.f;
+            for (int l = 0; l < kLanes; ++l) {
+                const int round = s * kLanes + l;
+                if (round >= a.topk) break;
+                uint32_t best = 0;
+                int index = 0x7fffffff;
 #pragma unroll
                 for (int i = 0; i < kItems; ++i)
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) sum[i][j] += p[i][j] * each;
-                taking += at == 0;
-            }
-            if (a.renormalise) {
+                    for (int j = 0; j < kVec; ++j)
+                        if (key[i][j] > best) {
+                            best = key[i][j];
+                            index = (i * kLanes + at) * kVec + j;
+                        }
+                group_best<kLanes>(best, index);
 #pragma unroll
-                for (int s = 0; s < kSlots; ++s) chosen += s * kLanes < a.topk ? e[s] : 0.f;
-                chosen = group_sum<kLanes>(chosen);
-            } else {
-                chosen = all;
-            }
-            if (r >= a.tokens) continue;
+                for (int i = 0; i < kItems; ++i)
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                const int round = s * kLanes + at;
-                if (round < a.topk) {
-                    a.ids[r * a.topk + round] = id[s];
-                    a.weights[r * a.topk + round] = id[s] >= 0 ? e[s] / chosen : 0.f;
-                    if (tally && id[s] >= 0) atomicAdd(count + id[s], 1);
+                    for (int j = 0; j < kVec; ++j)
+                        if (index == (i * kLanes + at) * kVec + j) key[i][j] = 0;
+                if (round == 0) {
+                    any = best > 0;
+                    top = key_value(best);
                 }
+                if (at == l && best > 0) {
+                    id[s] = index;
+                    e[s] = expf(key_value(best) - top);
+                }
+            }
+        }
+        float all = 0.f, chosen = 0.f;
+        float p[kItems][kVec];
+        if (tally || !a.renormalise) {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                float v[kVec];
+                unpack<T, kVec>(raw[i], v);
+                const bool in = any && (i * kLanes + at) * kVec < a.experts;
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    p[i][j] = in ? expf(v[j] - top) : 0.f;
+                    all += p[i][j];
+                }
+            }
+            all = group_sum<kLanes>(all);
+        }
+        if (tally && any) {
+            const float each = 1.0f / all;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) sum[i][j] += p[i][j] * each;
+            taking += at == 0;
+        }
+        if (a.renormalise) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) chosen += e[s];
+            chosen = group_sum<kLanes>(chosen);
+        } else {
+            chosen = all;
+        }
+        if (r >= a.tokens) continue;
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            e[s] = id[s] >= 0 ? e[s] / chosen : 0.f;
+            if (tally && id[s] >= 0) atomicAdd(count + id[s], 1);
+        }
+        const int64_t to = r * a.topk;
+        if constexpr (kLanes == 1)
+            if (a.pairs) {
+                *reinterpret_cast<int2*>(a.ids + to) = int2{id[0], id[1]};
+                *reinterpret_cast<float2*>(a.weights + to) = float2{e[0], e[1]};
+                continue;
+            }
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            const int round = s * kLanes + at;
+            if (round < a.topk) {
+                a.ids[to + round] = id[s];
+                a.weights[to + round] = e[s];
             }
         }
     }
@@ -236,7 +246,7 @@ __global__ void __launch_bounds__(kRowThreads) k_route_fwd(RouteFwd a) {
     const bool alone = gridDim.x == 1;
     float* total = alone ? a.totals : a.partial + (int64_t)blockIdx.x * (a.experts + 1);
     int32_t* counts = alone ? a.counts : a.part_counts + (int64_t)blockIdx.x * (a.experts + 1);
-    for (int e = threadIdx.x; e <= a.experts; e += kRowThreads) {
+    for (int e = threadIdx.x; e <= a.experts; e += kThreads) {
         float v = 0.f;
         if (e < a.experts)
 #pragma unroll
@@ -318,10 +328,10 @@ struct RouteBwd {
 //   renormalised:  d_j = w_j (g_j - sum w g), w the softmax over the chosen
 //   otherwise:     d_j = p_j g_j, and D = sum of d_j
 //   grad_e = p_e (h_e - sum p h - D) + the d_j of the choices that are e
-template <typename T, int kVec, int kLanes, int kItems, int kRows>
-__global__ void __launch_bounds__(kRowThreads) k_route_bwd(RouteBwd a) {
-    constexpr int kGroups = kRowThreads / kLanes;
-    constexpr int kSlots = 64 / kLanes < 8 ? 64 / kLanes : 8;
+template <typename T, typename F>
+__global__ void __launch_bounds__(kThreads) k_route_bwd(RouteBwd a) {
+    constexpr int kVec = F::kVec, kLanes = F::kLanes, kItems = F::kItems, kSlots = F::kSlots;
+    constexpr int kGroups = kThreads / kLanes;
     const int at = threadIdx.x % kLanes;
     float h[kItems][kVec] = {};
     if (a.grad_loss) {
@@ -346,138 +356,131 @@ __global__ void __launch_bounds__(kRowThreads) k_route_bwd(RouteBwd a) {
             for (int j = 0; j < kVec; ++j) h[i][j] *= scale;
     }
     const int64_t step = (int64_t)gridDim.x * kGroups;
-    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step * kRows) {
-        RawVec<T, kVec> raw[kRows][kItems];
-        int id[kRows][kSlots];
-        float g[kRows][kSlots];
-        bool take[kRows];
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step) {
+        const int64_t r = r0 + threadIdx.x / kLanes;
+        const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+        RawVec<T, kVec> raw[kItems];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
+        for (int i = 0; i < kItems; ++i)
+            raw[i] = r < a.tokens && (i * kLanes + at) * kVec < a.experts
+                         ? load_raw<T, kVec>(row + (i * kLanes + at) * kVec)
+                         : RawVec<T, kVec>{};
+        int id[kSlots];
+        float g[kSlots], e[kSlots];
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                const int round = s * kLanes + at;
-                id[u][s] = -1;
-                g[u][s] = 0.f;
-                if (r < a.tokens && round < a.topk) {
-                    id[u][s] = a.ids[r * a.topk + round];
-                    if (id[u][s] < -1 || id[u][s] >= a.experts) {
-                        GS_BOUNDS_REPORT(a.d_status);
-                        id[u][s] = -1;
-                    }
-                    if (a.grad_weights && id[u][s] >= 0)
-                        g[u][s] = a.grad_weights[r * a.topk + round];
+        for (int s = 0; s < kSlots; ++s) {
+            const int round = s * kLanes + at;
+            id[s] = -1;
+            g[s] = e[s] = 0.f;
+            if (r < a.tokens && round < a.topk) {
+                id[s] = a.ids[r * a.topk + round];
+                if (id[s] < -1 || id[s] >= a.experts) {
+                    GS_BOUNDS_REPORT(a.d_status);
+                    id[s] = -1;
                 }
+                if (a.grad_weights && id[s] >= 0) g[s] = a.grad_weights[r * a.topk + round];
             }
-            // the first choice tells whether the row takes part
-            take[u] = __shfl_sync(kAll, id[u][0], 0, kLanes) >= 0;
-            const T* x = static_cast<const T*>(a.logits) + r * a.ld + at * kVec;
+        }
+        // the first choice tells whether the row takes part
+        const bool take = __shfl_sync(kAll, id[0], 0, kLanes) >= 0;
+        float p[kItems][kVec];
+        float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kItems; ++i)
-                raw[u][i] = take[u] && (i * kLanes + at) * kVec < a.experts
-                                ? load_raw<T, kVec>(x + i * kLanes * kVec)
-                                : RawVec<T, kVec>{};
+        for (int i = 0; i < kItems; ++i) {
+            unpack<T, kVec>(raw[i], p[i]);
+            const bool in = (i * kLanes + at) * kVec < a.experts;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                if (!in) p[i][j] = -INFINITY;
+                top = fmaxf(top, p[i][j]);
+            }
+        }
+        top = group_max<kLanes>(top);
+        // the choices' exponentials, from their own logits
+        float chosen = 0.f, mean = 0.f;
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            if (take && id[s] >= 0) e[s] = expf(to_f(row[id[s]]) - top);
+            chosen += e[s];
+            mean += e[s] * g[s];
+        }
+        float all = 0.f, dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                p[i][j] = expf(p[i][j] - top);
+                all += p[i][j];
+                dot += p[i][j] * h[i][j];
+            }
+        all = group_sum<kLanes>(all);
+        const float each = 1.0f / all;
+        dot = a.grad_loss ? group_sum<kLanes>(dot) * each : 0.f;
+        mean = group_sum<kLanes>(mean);
+        chosen = a.renormalise ? group_sum<kLanes>(chosen) : all;
+        mean /= chosen;  // renormalised: sum w g; otherwise D
+        const float down = dot + (a.renormalise ? 0.f : mean);
+        if (a.renormalise) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) g[s] -= mean;
         }
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int64_t r = r0 + u * step + threadIdx.x / kLanes;
-            float p[kItems][kVec];
-            float top = -INFINITY;
+        for (int i = 0; i < kItems; ++i)
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                unpack<T, kVec>(raw[u][i], p[i]);
-                const bool in = (i * kLanes + at) * kVec < a.experts;
+            for (int j = 0; j < kVec; ++j) p[i][j] *= each * (h[i][j] - down);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    if (!in) p[i][j] = -INFINITY;
-                    top = fmaxf(top, p[i][j]);
-                }
+        for (int s = 0; s < kSlots; ++s) {
+            const float d = e[s] / chosen * g[s];
+            for (int l = 0; l < kLanes; ++l) {
+                if (s * kLanes + l >= a.topk) break;
+                const int index = __shfl_sync(kAll, id[s], l, kLanes);
+                const float add = __shfl_sync(kAll, d, l, kLanes);
+#pragma unroll
+                for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j)
+                        if (index == (i * kLanes + at) * kVec + j) p[i][j] += add;
             }
-            top = group_max<kLanes>(top);
-            float all = 0.f, dot = 0.f;
+        }
+        if (r >= a.tokens) continue;
+        T* out = static_cast<T*>(a.grad) + r * a.ldg + at * kVec;
 #pragma unroll
-            for (int i = 0; i < kItems; ++i)
+        for (int i = 0; i < kItems; ++i) {
+            if (!take)
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    p[i][j] = expf(p[i][j] - top);
-                    all += p[i][j];
-                    dot += p[i][j] * h[i][j];
-                }
-            all = group_sum<kLanes>(all);
-            dot = a.grad_loss ? group_sum<kLanes>(dot) / all : 0.f;
-            // the choices' exponentials, from their own logits
-            float e[kSlots];
-            float chosen = 0.f, mean = 0.f;
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                e[s] = 0.f;
-                if (s * kLanes >= a.topk) continue;
-                if (take[u] && id[u][s] >= 0)
-                    e[s] = expf(to_f(static_cast<const T*>(a.logits)[r * a.ld + id[u][s]]) - top);
-                chosen += e[s];
-                mean += e[s] * g[u][s];
-            }
-            mean = group_sum<kLanes>(mean);
-            chosen = a.renormalise ? group_sum<kLanes>(chosen) : all;
-            mean /= chosen;  // renormalised: sum w g; otherwise D
-            const float each = 1.0f / all, down = dot + (a.renormalise ? 0.f : mean);
-#pragma unroll
-            for (int i = 0; i < kItems; ++i)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) p[i][j] *= each * (h[i][j] - down);
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                if (s * kLanes >= a.topk) break;
-                const float d =
-                    e[s] / chosen * (a.renormalise ? g[u][s] - mean : g[u][s]);
-                for (int l = 0; l < kLanes; ++l) {
-                    if (s * kLanes + l >= a.topk) break;
-                    const int index = __shfl_sync(kAll, id[u][s], l, kLanes);
-                    const float add = __shfl_sync(kAll, d, l, kLanes);
-#pragma unroll
-                    for (int i = 0; i < kItems; ++i)
-#pragma unroll
-                        for (int j = 0; j < kVec; ++j)
-                            if (index == (i * kLanes + at) * kVec + j) p[i][j] += add;
-                }
-            }
-            if (r >= a.tokens) continue;
-            T* out = static_cast<T*>(a.grad) + r * a.ldg + at * kVec;
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                if (!take[u])
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) p[i][j] = 0.f;
-                if ((i * kLanes + at) * kVec < a.experts)
-                    store_vec<T, kVec>(out + i * kLanes * kVec, p[i]);
-            }
+                for (int j = 0; j < kVec; ++j) p[i][j] = 0.f;
+            if ((i * kLanes + at) * kVec < a.experts)
+                store_vec<T, kVec>(out + i * kLanes * kVec, p[i]);
         }
     }
 }
 
-// Calls f with the form for rows of `experts` elements.
+// Calls f with how rows of `experts` elements are spread.  A row to a thread
+// needs no exchange between lanes (forward, 921600 rows of 16 float32, two
+// choices: 66 us with four lanes a row); a row of few lanes holds at most a
+// choice a lane, more choices take a whole warp.
 template <typename T, int kVec, typename F>
-void with_route_form(int experts, F&& f) {
+void with_spread(int experts, int topk, F&& f) {
     const int n = (experts + kVec - 1) / kVec;
     if constexpr (kVec > 1) {
-        if (n <= 2) return f(Form<kVec, 2, 1, 2>{});
-        if (n <= 4) return f(Form<kVec, 4, 1, 2>{});
-        if (n <= 8) return f(Form<kVec, 8, 1, 2>{});
-        if (n <= 16) return f(Form<kVec, 8, 2, 2>{});
-        if (n <= 32) return f(Form<kVec, 32, 1, 2>{});
-        if (n <= 64) return f(Form<kVec, 32, 2, 1>{});
-        if (n <= 128) return f(Form<kVec, 32, 4, 1>{});
-        if constexpr (kVec == 4) return f(Form<4, 32, 8, 1>{});
+        if (topk <= 4 && experts <= 8) return f(Spread<kVec, 1, 8 / kVec>{});
+        if (topk <= 4 && experts <= 16) return f(Spread<kVec, 1, 16 / kVec>{});
+        if (topk <= 4 && n <= 4) return f(Spread<kVec, 4, 1>{});
+        if (topk <= 8 && n <= 8) return f(Spread<kVec, 8, 1>{});
+        if (topk <= 8 && n <= 16) return f(Spread<kVec, 8, 2>{});
+        if (n <= 32) return f(Spread<kVec, 32, 1>{});
+        if (n <= 64) return f(Spread<kVec, 32, 2>{});
+        if (n <= 128) return f(Spread<kVec, 32, 4>{});
+        if constexpr (kVec == 4) return f(Spread<4, 32, 8>{});
     } else {
-        if (n <= 4) return f(Form<1, 4, 1, 4>{});
-        if (n <= 8) return f(Form<1, 4, 2, 2>{});
-        if (n <= 16) return f(Form<1, 8, 2, 2>{});
-        if (n <= 32) return f(Form<1, 8, 4, 2>{});
-        if (n <= 64) return f(Form<1, 8, 8, 1>{});
-        if (n <= 128) return f(Form<1, 32, 4, 1>{});
-        if (n <= 256) return f(Form<1, 32, 8, 1>{});
-        if (n <= 512) return f(Form<1, 32, 16, 1>{});
-        return f(Form<1, 32, 32, 1>{});
+        if (topk <= 4 && n <= 8) return f(Spread<1, 1, 8>{});
+        if (topk <= 4 && n <= 16) return f(Spread<1, 1, 16>{});
+        if (topk <= 8 && n <= 32) return f(Spread<1, 8, 4>{});
+        if (topk <= 8 && n <= 64) return f(Spread<1, 8, 8>{});
+        if (n <= 128) return f(Spread<1, 32, 4>{});
+        if (n <= 256) return f(Spread<1, 32, 8>{});
+        if (n <= 512) return f(Spread<1, 32, 16>{});
+        return f(Spread<1, 32, 32>{});
     }
 }
 
@@ -498,7 +501,7 @@ size_t align_words(size_t words) { return (words + 63) / 64 * 64; }
 
 size_t route_workspace(int64_t tokens, int experts) {
     const size_t columns = experts + 1;
-    // a block takes two rows or more
+    // a block takes a row or more
     const size_t blocks = (size_t)std::min<int64_t>(std::max<int64_t>(tokens, 1), kMaxRouteBlocks);
     return 4 * (64 + align_words(columns) + 2 * align_words(blocks * columns));
 }
@@ -517,13 +520,15 @@ void launch_route_fwd(const RouteArgs& n, const uint8_t* keep, int32_t* ids, flo
     a.topk = n.topk;
     a.experts = n.experts;
     a.renormalise = n.renormalise;
+    a.pairs = n.topk == 2 &&
+              ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(weights)) & 7u) == 0;
     const size_t columns = n.experts + 1;
     with_dtype(n.dtype, [&](auto t) {
         using T = decltype(t);
         const auto go = [&](auto form) {
             using F = decltype(form);
-            const int groups = kRowThreads / F::kLanes;
-            const auto kernel = k_route_fwd<T, F::kVec, F::kLanes, F::kItems, F::kRows>;
+            const int groups = kThreads / F::kLanes;
+            const auto kernel = k_route_fwd<T, F>;
             const auto smem = [&](int experts) {
                 return counts ? ((size_t)experts + 1) * 4 + (size_t)kWarps * experts * 4 : 0;
             };
@@ -533,7 +538,8 @@ void launch_route_fwd(const RouteArgs& n, const uint8_t* keep, int32_t* ids, flo
                 n.tokens, groups,
                 std::min(kMaxRouteBlocks,
                          resident_blocks(resident, kernel,
-                                         ((size_t)most + 1) * 4 + (size_t)kWarps * most * 4)));
+                                         ((size_t)most + 1) * 4 + (size_t)kWarps * most * 4,
+                                         kThreads)));
             if (counts) {
                 uint32_t* w = static_cast<uint32_t*>(workspace);
                 a.ticket = w;
@@ -541,14 +547,14 @@ void launch_route_fwd(const RouteArgs& n, const uint8_t* keep, int32_t* ids, flo
                 a.partial = a.totals + align_words(columns);
                 a.part_counts = reinterpret_cast<int32_t*>(a.partial + align_words(blocks * columns));
             }
-            kernel<<<blocks, kRowThreads, smem(n.experts), s>>>(a);
+            kernel<<<blocks, kThreads, smem(n.experts), s>>>(a);
             if (counts && blocks > 1)
                 k_route_sum<<<(unsigned)((columns + kSumColumns - 1) / kSumColumns), kSumThreads, 0,
                               s>>>(a, blocks);
         };
         with_route_width<T>(row_bits<T>(n.logits, n.ld) | (uintptr_t)(n.experts * sizeof(T)),
                             [&](auto width) {
-                                with_route_form<T, decltype(width)::value>(n.experts, go);
+                                with_spread<T, decltype(width)::value>(n.experts, n.topk, go);
                             });
     });
 }
@@ -562,16 +568,16 @@ void launch_route_bwd(const RouteArgs& n, const int32_t* ids, const int32_t* cou
         using T = decltype(t);
         const auto go = [&](auto form) {
             using F = decltype(form);
-            const auto kernel = k_route_bwd<T, F::kVec, F::kLanes, F::kItems, F::kRows>;
+            const auto kernel = k_route_bwd<T, F>;
             static PerDevice resident;
-            const int blocks = route_blocks(n.tokens, kRowThreads / F::kLanes,
-                                            resident_blocks(resident, kernel, 0));
-            kernel<<<blocks, kRowThreads, 0, s>>>(a);
+            const int blocks = route_blocks(n.tokens, kThreads / F::kLanes,
+                                            resident_blocks(resident, kernel, 0, kThreads));
+            kernel<<<blocks, kThreads, 0, s>>>(a);
         };
         with_route_width<T>(row_bits<T>(n.logits, n.ld) | row_bits<T>(grad, ldg) |
                                 (uintptr_t)(n.experts * sizeof(T)),
                             [&](auto width) {
-                                with_route_form<T, decltype(width)::value>(n.experts, go);
+                                with_spread<T, decltype(width)::value>(n.experts, n.topk, go);
                             });
     });
 }

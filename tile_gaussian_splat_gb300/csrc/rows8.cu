@@ -6,7 +6,10 @@
 // their own, and the matrix instruction takes them as they are.  Both ways
 // each byte is read and written once: bound by memory bandwidth.  kLanes lanes
 // of eight elements each share a block (fewer where a row is short), and
-// several blocks are loaded before the first is used.
+// several blocks are loaded before the first is used.  Where a block lies
+// follows from the one before (two 64-bit divisions a block took half of the
+// time).  Rows that begin anywhere are read and written as the aligned vectors
+// that they lie in, turned by the elements they are off.
 #include <algorithm>
 #include <cfloat>
 #include <cstdint>
@@ -21,8 +24,30 @@ namespace gs {
 namespace {
 
 constexpr int kThreads8 = 128;
-constexpr int kEach = 8;       // elements of a lane
+constexpr int kEach = 8;         // elements of a lane
 constexpr int kBlocksAhead = 4;  // blocks of a lane in flight
+
+// The blocks of 128 channels of all rows on end, `step` of them apart.
+struct Place {
+    int64_t row;
+    int block;
+    int64_t row_step;
+    int block_step, blocks;
+    __device__ __forceinline__ Place(int64_t first, int64_t step, int blocks_) : blocks(blocks_) {
+        row = first / blocks;
+        block = (int)(first - row * blocks);
+        row_step = step / blocks;
+        block_step = (int)(step - row_step * blocks);
+    }
+    __device__ __forceinline__ void advance() {
+        row += row_step;
+        block += block_step;
+        if (block >= blocks) {
+            block -= blocks;
+            ++row;
+        }
+    }
+};
 
 struct Pack8 {
     const void* x;
@@ -31,64 +56,152 @@ struct Pack8 {
     int channels, blocks, pitch, scale_pitch;
 };
 
-// Eight elements from p on of which `left` are inside the row (0 beyond).
+// Eight elements as they lie in memory.
+template <typename T>
+struct Eight {
+    static constexpr int kWords = sizeof(T) * 2;
+    uint32_t w[kWords];
+};
+
+// Eight elements from p on, of which `left` are inside the row (0 beyond); all
+// of [begin, end) may be read.
 template <typename T, bool kVectors>
-__device__ __forceinline__ void load8(const T* p, int left, float* v) {
-    constexpr int kVec = 16 / (int)sizeof(T);
+__device__ __forceinline__ Eight<T> load8(const T* p, int left, const T* begin, const T* end) {
+    constexpr int kWords = Eight<T>::kWords, kVec = 16 / (int)sizeof(T);
+    Eight<T> e{};
+    if (left <= 0) return e;
     if constexpr (kVectors) {
 #pragma unroll
-        for (int i = 0; i < kEach / kVec; ++i) {
-            RawVec<T, kVec> raw{};
-            if (i * kVec < left) raw = load_raw<T, kVec>(p + i * kVec);
-            unpack<T, kVec>(raw, v + i * kVec);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) v[i] = i < left ? to_f(p[i]) : 0.f;
+        for (int i = 0; i < kWords / 4; ++i)
+            if (i * kVec < left) {
+                const uint4 v = *reinterpret_cast<const uint4*>(p + i * kVec);
+                e.w[4 * i] = v.x, e.w[4 * i + 1] = v.y, e.w[4 * i + 2] = v.z, e.w[4 * i + 3] = v.w;
+            }
+        return e;
     }
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const int off = (int)(at & 15u);
+    const char* from = reinterpret_cast<const char*>(p) - off;
+    if (left < 8 || from < reinterpret_cast<const char*>(begin) ||
+        from + 4 * kWords + 16 > reinterpret_cast<const char*>(end)) {
+        T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : from_f<T>(0.f);
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e.w[i] = __float_as_uint(to_f(v[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                e.w[i] = (uint32_t)*reinterpret_cast<const uint16_t*>(&v[2 * i]) |
+                         (uint32_t)*reinterpret_cast<const uint16_t*>(&v[2 * i + 1]) << 16;
+        }
+        return e;
+    }
+    uint32_t w[kWords + 4];
+#pragma unroll
+    for (int i = 0; i < kWords / 4 + 1; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from + 16 * i);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+    // off = 8 o3 + 4 o2 + 2 o1
+#pragma unroll
+    for (int i = 0; i < kWords + 2; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < kWords + 1; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+        e.w[i] = sizeof(T) == 2 && (off & 2) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    return e;
+}
+
+template <typename T>
+__device__ __forceinline__ void floats8(const Eight<T>& e, float* v) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(e.w[i]);
+    } else {
+        const T* t = reinterpret_cast<const T*>(e.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f(t[i]);
+    }
+}
+
+// f(lanes a block): rows of up to 32 or 64 channels leave no lane idle.
+template <typename F>
+void with_lanes(int channels, F&& f) {
+    if (channels <= 32) return f(std::integral_constant<int, 4>{});
+    if (channels <= 64) return f(std::integral_constant<int, 8>{});
+    return f(std::integral_constant<int, 16>{});
+}
+
+template <int kLanes>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
 }
 
 template <typename T, int kLanes, bool kVectors>
 __global__ void __launch_bounds__(kThreads8) k_pack8(Pack8 a) {
     constexpr int kGroups = kThreads8 / kLanes;
     const int at = threadIdx.x % kLanes;
-    const int64_t items = a.rows * a.blocks, step = (int64_t)gridDim.x * kGroups;
-    for (int64_t i0 = (int64_t)blockIdx.x * kGroups; i0 < items; i0 += step * kBlocksAhead) {
-        float v[kBlocksAhead][kEach];
+    const T* x = static_cast<const T*>(a.x);
+    const T* end = x + (a.rows - 1) * a.ldx + a.channels;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    Place load((int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes, step, a.blocks), p = load;
+    // a warp's groups end together: they exchange across all lanes
+    const int64_t turns = (a.rows * a.blocks + step - 1) / step;
+    for (int64_t t = 0; t < turns; t += kBlocksAhead) {
+        Eight<T> e[kBlocksAhead];
 #pragma unroll
-        for (int u = 0; u < kBlocksAhead; ++u) {
-            const int64_t item = i0 + u * step + threadIdx.x / kLanes;
-            const int64_t r = item / a.blocks;
-            const int c = (int)(item - r * a.blocks) * GS_SCALE_BLOCK + at * kEach;
-            load8<T, kVectors>(static_cast<const T*>(a.x) + r * a.ldx + c,
-                               item < items ? a.channels - c : 0, v[u]);
+        for (int u = 0; u < kBlocksAhead; ++u, load.advance()) {
+            const int c = load.block * GS_SCALE_BLOCK + at * kEach;
+            e[u] = load8<T, kVectors>(x + load.row * a.ldx + c,
+                                      load.row < a.rows ? a.channels - c : 0, x, end);
         }
 #pragma unroll
-        for (int u = 0; u < kBlocksAhead; ++u) {
-            const int64_t item = i0 + u * step + threadIdx.x / kLanes;
+        for (int u = 0; u < kBlocksAhead; ++u, p.advance()) {
+            float v[kEach];
+            floats8(e[u], v);
             float most = 0.f;
 #pragma unroll
-            for (int j = 0; j < kEach; ++j)
-                most = fmaxf(most, fabsf(v[u][j]) <= FLT_MAX ? fabsf(v[u][j]) : 0.f);
+            for (int j = 0; j < kEach; ++j) most = fmaxf(most, fabsf(v[j]));
+            most = lanes_max<kLanes>(most);
+            // fmaxf passes over a NaN; an infinity is not counted either
+            if (__any_sync(0xffffffffu, most > FLT_MAX)) {
+                most = 0.f;
 #pragma unroll
-            for (int o = kLanes / 2; o; o >>= 1)
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            if (item >= items) continue;
-            const int64_t r = item / a.blocks;
-            const int block = (int)(item - r * a.blocks), c = block * GS_SCALE_BLOCK + at * kEach;
+                for (int j = 0; j < kEach; ++j) {
+                    const bool finite = fabsf(v[j]) <= FLT_MAX;
+                    most = fmaxf(most, finite ? fabsf(v[j]) : 0.f);
+                    if (!finite) v[j] = __uint_as_float(0x7fffffffu);
+                }
+                most = lanes_max<kLanes>(most);
+            }
+            if (p.row >= a.rows) continue;
+            const int c = p.block * GS_SCALE_BLOCK + at * kEach;
             const int power = scale_byte(most);
             const float up = two_to(254 - power);
             if (c < a.pitch) {  // 0 behind the last channel
                 uint2 q;
-                q.x = pack4_e4m3(v[u][0] * up, v[u][1] * up, v[u][2] * up, v[u][3] * up);
-                q.y = pack4_e4m3(v[u][4] * up, v[u][5] * up, v[u][6] * up, v[u][7] * up);
-                *reinterpret_cast<uint2*>(a.q + r * a.pitch + c) = q;
+                q.x = pack4_e4m3(v[0] * up, v[1] * up, v[2] * up, v[3] * up);
+                q.y = pack4_e4m3(v[4] * up, v[5] * up, v[6] * up, v[7] * up);
+                *reinterpret_cast<uint2*>(a.q + p.row * a.pitch + c) = q;
             }
             if (at == 0) {
-                a.scales[r * a.scale_pitch + block] = (uint8_t)power;
-                if (block + 1 == a.blocks)
-                    for (int b = a.blocks; b < a.scale_pitch; ++b)
-                        a.scales[r * a.scale_pitch + b] = 0;
+                uint8_t* to = a.scales + p.row * a.scale_pitch + p.block;
+                // with the zeros behind the last block
+                if (p.block + 1 < a.blocks || a.blocks % 4 == 0) {
+                    *to = (uint8_t)power;
+                } else if (a.blocks % 4 == 1) {
+                    *reinterpret_cast<uint32_t*>(to) = (uint32_t)power;
+                } else if (a.blocks % 4 == 3) {
+                    *reinterpret_cast<uint16_t*>(to) = (uint16_t)power;
+                } else {
+                    to[0] = (uint8_t)power;
+                    *reinterpret_cast<uint16_t*>(to + 1) = 0;
+                }
             }
         }
     }
@@ -101,54 +214,102 @@ struct Unpack8 {
     int channels, blocks, pitch, scale_pitch;
 };
 
-template <typename T, int kLanes, bool kVectors>
+// Eight values times their scales, as T.
+template <typename T>
+__device__ __forceinline__ Eight<T> scaled8(uint2 q, const float* size) {
+    float v[8];
+    unpack8_e4m3(q, v);
+    Eight<T> e;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = cut_to<T>(v[j] * size[j]);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e.w[j] = __float_as_uint(v[j]);
+    } else {
+        T* t = reinterpret_cast<T*>(e.w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = from_f<T>(v[j]);
+    }
+    return e;
+}
+
+template <typename T, int kLanes>
 __global__ void __launch_bounds__(kThreads8) k_unpack8(Unpack8 a) {
     constexpr int kGroups = kThreads8 / kLanes, kVec = 16 / (int)sizeof(T);
     const int at = threadIdx.x % kLanes;
-    const int64_t items = a.rows * a.blocks, step = (int64_t)gridDim.x * kGroups;
-    for (int64_t i0 = (int64_t)blockIdx.x * kGroups; i0 < items; i0 += step * kBlocksAhead) {
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    Place load((int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes, step, a.blocks), p = load;
+    while (p.row < a.rows) {
         uint2 q[kBlocksAhead];
         int power[kBlocksAhead];
 #pragma unroll
-        for (int u = 0; u < kBlocksAhead; ++u) {
-            const int64_t item = i0 + u * step + threadIdx.x / kLanes;
-            const int64_t r = item / a.blocks;
-            const int block = (int)(item - r * a.blocks), c = block * GS_SCALE_BLOCK + at * kEach;
-            const bool in = item < items && c < a.channels;
-            q[u] = in ? *reinterpret_cast<const uint2*>(a.q + r * a.pitch + c) : uint2{0, 0};
-            power[u] = in ? a.scales[r * a.scale_pitch + block] : 0;
+        for (int u = 0; u < kBlocksAhead; ++u, load.advance()) {
+            const int c = load.block * GS_SCALE_BLOCK + at * kEach;
+            const bool in = load.row < a.rows && c < a.channels;
+            q[u] = in ? *reinterpret_cast<const uint2*>(a.q + load.row * a.pitch + c) : uint2{0, 0};
+            power[u] = in ? a.scales[load.row * a.scale_pitch + load.block] : 0;
         }
 #pragma unroll
-        for (int u = 0; u < kBlocksAhead; ++u) {
-            const int64_t item = i0 + u * step + threadIdx.x / kLanes;
-            const int64_t r = item / a.blocks;
-            const int c = (int)(item - r * a.blocks) * GS_SCALE_BLOCK + at * kEach;
-            if (item >= items || c >= a.channels) continue;
-            float v[kEach];
-            unpack8_e4m3(q[u], v);
-            const float size = scale_of(power[u]);
+        for (int u = 0; u < kBlocksAhead; ++u, p.advance()) {
+            const int c = p.block * GS_SCALE_BLOCK + at * kEach;
+            if (p.row >= a.rows || c >= a.channels) continue;
+            const float one = scale_of(power[u]);
+            const float size[8] = {one, one, one, one, one, one, one, one};
+            const Eight<T> e = scaled8<T>(q[u], size);
+            T* y = static_cast<T*>(a.y) + p.row * a.ldy + c;
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) v[j] = cut_to<T>(v[j] * size);
-            T* y = static_cast<T*>(a.y) + r * a.ldy + c;
-            if constexpr (kVectors) {
-#pragma unroll
-                for (int i = 0; i < kEach / kVec; ++i)
-                    if (c + i * kVec < a.channels) store_vec<T, kVec>(y + i * kVec, v + i * kVec);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kEach; ++j)
-                    if (c + j < a.channels) y[j] = from_f<T>(v[j]);
-            }
+            for (int i = 0; i < kEach / kVec; ++i)
+                if (c + i * kVec < a.channels)
+                    reinterpret_cast<uint4*>(y)[i] =
+                        uint4{e.w[4 * i], e.w[4 * i + 1], e.w[4 * i + 2], e.w[4 * i + 3]};
         }
     }
 }
 
-// f(lanes a block): rows of up to 32 or 64 channels leave no lane idle.
-template <typename F>
-void with_lanes(int channels, F&& f) {
-    if (channels <= 32) return f(std::integral_constant<int, 4>{});
-    if (channels <= 64) return f(std::integral_constant<int, 8>{});
-    return f(std::integral_constant<int, 16>{});
+// Rows of y that begin anywhere: a thread has the eight elements of one or two
+// aligned vectors of a row, of which the first and last may lie across its
+// ends.  They take eight bytes of q from two aligned words of eight, and at
+// most two blocks' scales.
+template <typename T>
+__global__ void __launch_bounds__(kThreads8) k_unpack8_any(Unpack8 a, int vectors) {
+    Place p((int64_t)blockIdx.x * kThreads8 + threadIdx.x, (int64_t)gridDim.x * kThreads8, vectors);
+    for (; p.row < a.rows; p.advance()) {
+        T* row = static_cast<T*>(a.y) + p.row * a.ldy;
+        // first channel of this thread: at most 0
+        const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / (int)sizeof(T);
+        const int c = p.block * kEach - off;
+        if (c >= a.channels) continue;
+        const uint8_t* q = a.q + p.row * a.pitch;
+        const int lo = (c >> 3) * 8, turn = (c - lo) * 8;  // eight bytes from lo on, bits off
+        const uint2 w0 = lo >= 0 ? *reinterpret_cast<const uint2*>(q + lo) : uint2{0, 0};
+        const uint2 w1 =
+            lo + 8 < a.pitch ? *reinterpret_cast<const uint2*>(q + lo + 8) : uint2{0, 0};
+        uint32_t w[4] = {w0.x, w0.y, w1.x, w1.y};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) w[i] = turn & 32 ? w[i + 1] : w[i];
+        const uint2 v{__funnelshift_r(w[0], w[1], turn & 31), __funnelshift_r(w[1], w[2], turn & 31)};
+        const uint8_t* s = a.scales + p.row * a.scale_pitch;
+        const int block = max(c, 0) / GS_SCALE_BLOCK;
+        const float here = scale_of(s[block]);
+        const float next = (block + 1) * GS_SCALE_BLOCK < min(c + kEach, a.channels)
+                               ? scale_of(s[block + 1])
+                               : 0.f;
+        float size[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) size[j] = c + j < (block + 1) * GS_SCALE_BLOCK ? here : next;
+        const Eight<T> e = scaled8<T>(v, size);
+        if (c >= 0 && c + kEach <= a.channels) {
+#pragma unroll
+            for (int i = 0; i < Eight<T>::kWords / 4; ++i)
+                reinterpret_cast<uint4*>(row + c)[i] =
+                    uint4{e.w[4 * i], e.w[4 * i + 1], e.w[4 * i + 2], e.w[4 * i + 3]};
+        } else {
+            const T* t = reinterpret_cast<const T*>(e.w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j >= 0 && c + j < a.channels) row[c + j] = t[j];
+        }
+    }
 }
 
 template <typename K>
@@ -157,6 +318,8 @@ int blocks8(PerDevice& resident, K kernel, int64_t items, int lanes) {
     return (int)std::min<int64_t>((items + groups - 1) / groups,
                                   resident_blocks(resident, kernel, 0));
 }
+
+static_assert(kThreads8 == kRowThreads, "resident blocks are asked for of these");
 
 }  // namespace
 
@@ -191,19 +354,19 @@ void launch_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int c
                     GS_ROW8_SCALES(channels)};
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
+        if (!rows_aligned<T>(y, ldy) || channels * sizeof(T) % 16 != 0) {
+            // elements before a row's first in its first vector: at most 16 bytes
+            const int vectors = (channels + 16 / (int)sizeof(T) - 1 + kEach - 1) / kEach;
+            static PerDevice resident;
+            k_unpack8_any<T><<<blocks8(resident, k_unpack8_any<T>, rows * vectors, 1), kThreads8,
+                               0, s>>>(a, vectors);
+            return;
+        }
         with_lanes(channels, [&](auto lanes) {
             constexpr int kLanes = decltype(lanes)::value;
-            const bool vectors = rows_aligned<T>(y, ldy) && channels * sizeof(T) % 16 == 0;
-            const int64_t items = rows * blocks;
-            if (vectors) {
-                const auto kernel = k_unpack8<T, kLanes, true>;
-                static PerDevice resident;
-                kernel<<<blocks8(resident, kernel, items, kLanes), kThreads8, 0, s>>>(a);
-            } else {
-                const auto kernel = k_unpack8<T, kLanes, false>;
-                static PerDevice resident;
-                kernel<<<blocks8(resident, kernel, items, kLanes), kThreads8, 0, s>>>(a);
-            }
+            static PerDevice resident;
+            const auto kernel = k_unpack8<T, kLanes>;
+            kernel<<<blocks8(resident, kernel, rows * blocks, kLanes), kThreads8, 0, s>>>(a);
         });
     });
 }
