@@ -29,10 +29,11 @@ def test_route(lib):
                 dict(dt=3), dict(dt=-1), dict(ids=0), dict(ids=6), dict(w=0), dict(w=1), dict(c=2),
                 dict(l=3), dict(c=0), dict(tokens=1 << 30, topk=2)):
         assert fwd(**bad) == 1, bad
-    assert fwd(ws=0) == 4 and fwd(ws=8) == 4 and fwd(n=16) == 4
+    assert size(8, 8) == 0  # a handful of tokens needs none
+    assert fwd(tokens=9, ws=0) == 4 and fwd(tokens=9, ws=8) == 4 and fwd(tokens=9, n=16) == 4
     assert size(-1, 8) == 0 and size(10, 0) == 0 and size(10, 1025) == 0
-    assert fwd(n=size(4, 8) - 1) == 4
-    assert 0 < size(1, 1) <= size(1000, 8) <= size(10 ** 9, 1024) < 1 << 24
+    assert fwd(tokens=9, n=size(9, 8) - 1) == 4
+    assert 0 < size(9, 1) <= size(1000, 8) <= size(10 ** 9, 1024) < 1 << 24
 
     def bwd(x=8, ldl=8, ids=8, c=8, gw=8, gl=8, tokens=4, topk=2, experts=8, dt=F16, g=8, ldg=8):
         return lib.gs_expert_route_bwd(P(x), ldl, P(ids), P(c), P(gw), P(gl), tokens, topk,

@@ -809,7 +809,7 @@ def gs_expert_route_fwd(logits, topk, keep=None, renormalise=True, balance=True,
         counts = _new((E + 1,), torch.int32, logits, stream)
         loss = _new((1,), torch.float32, logits, stream)
         n_bytes = L.gs_expert_route_workspace_size(T, E)
-        ws = _workspace(workspace, n_bytes, logits, stream)
+        ws = _workspace(workspace, n_bytes, logits, stream) if n_bytes else None
     _check(L.gs_expert_route_fwd(lp, ldl, _ptr(keep), T, topk, E, dt, int(renormalise), _ptr(ids),
                                  _ptr(weights), _ptr(counts), _ptr(loss), _ptr(ws), n_bytes,
                                  _on(stream, logits)), "gs_expert_route_fwd")

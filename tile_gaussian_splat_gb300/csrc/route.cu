@@ -32,17 +32,16 @@ struct Spread {
     static constexpr int kSlots = kLanes == 1 ? 4 : kLanes == 32 ? 2 : 1;
 };
 
-// Logits as words in the order of the values: 0 = not to be chosen (minus
-// infinity), a NaN above everything, both zeros the same.
+// Logits as words in the order of the values: an addition of 0 makes both zeros
+// the same and every NaN the positive one, which is above everything.
 __device__ __forceinline__ uint32_t order_key(float v) {
-    if (v != v) return kAll;
-    if (v == -INFINITY) return 0;
     const uint32_t u = __float_as_uint(v + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);  // kAll: a NaN
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
+constexpr uint32_t kLowest = 0x007fffffu;  // minus infinity: not chosen, nor what is below
 
 template <int kLanes>
 __device__ __forceinline__ float group_max(float v) {
@@ -51,24 +50,19 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
-// The largest key and the lowest index that has it, over a row's lanes.
 template <int kLanes>
-__device__ __forceinline__ void group_best(uint32_t& key, int& index) {
-    if constexpr (kLanes == 32) {
-        const uint32_t top = __reduce_max_sync(kAll, key);
-        index = (int)__reduce_min_sync(kAll, key == top ? (uint32_t)index : kAll);
-        key = top;
-    } else {
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    if constexpr (kLanes == 32) return __reduce_max_sync(kAll, v);
 #pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) {
-            const uint32_t k = __shfl_xor_sync(kAll, key, o);
-            const int i = __shfl_xor_sync(kAll, index, o);
-            if (k > key || (k == key && i < index)) {
-                key = k;
-                index = i;
-            }
-        }
-    }
+    for (int o = kLanes / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+template <int kLanes>
+__device__ __forceinline__ int group_min(int v) {
+    if constexpr (kLanes == 32) return __reduce_min_sync(kAll, v);
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) v = min(v, __shfl_xor_sync(kAll, v, o));
+    return v;
 }
 
 struct RouteFwd {
@@ -86,19 +80,20 @@ struct RouteFwd {
 };
 
 // loss = experts * sum over e of share_e * mean probability_e, by one warp in
-// a fixed order.
-__device__ __forceinline__ float balance(const float* sums, const int32_t* counts, int experts) {
+// a fixed order.  volatile: other blocks' sums, from where they wrote them.
+__device__ __forceinline__ float balance(const volatile float* sums,
+                                         const volatile int32_t* counts, int experts) {
     const int lane = threadIdx.x & 31;
     float dot = 0.f;
     int pairs = 0;
     for (int e = lane; e < experts; e += 32) {
-        const int c = __ldcg(counts + e);
-        dot += __ldcg(sums + e) * (float)c;
+        const int c = counts[e];
+        dot += sums[e] * (float)c;
         pairs += c;
     }
     dot = warp_sum(dot);
     pairs = __reduce_add_sync(kAll, pairs);
-    const int taking = __ldcg(counts + experts);
+    const int taking = counts[experts];
     return pairs > 0 ? (float)experts * (dot / ((float)taking * (float)pairs)) : 0.f;
 }
 
@@ -149,27 +144,29 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
             for (int l = 0; l < kLanes; ++l) {
                 const int round = s * kLanes + l;
                 if (round >= a.topk) break;
-                uint32_t best = 0;
-                int index = 0x7fffffff;
+                uint32_t best = kLowest;
 #pragma unroll
                 for (int i = 0; i < kItems; ++i)
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j)
-                        if (key[i][j] > best) {
-                            best = key[i][j];
-                            index = (i * kLanes + at) * kVec + j;
-                        }
-                group_best<kLanes>(best, index);
+                    for (int j = 0; j < kVec; ++j) best = max(best, key[i][j]);
+                best = group_max<kLanes>(best);
+                int index = 0x7fffffff;  // the lowest that has it
+#pragma unroll
+                for (int i = kItems - 1; i >= 0; --i)
+#pragma unroll
+                    for (int j = kVec - 1; j >= 0; --j)
+                        if (key[i][j] == best) index = (i * kLanes + at) * kVec + j;
+                index = group_min<kLanes>(index);
 #pragma unroll
                 for (int i = 0; i < kItems; ++i)
 #pragma unroll
                     for (int j = 0; j < kVec; ++j)
                         if (index == (i * kLanes + at) * kVec + j) key[i][j] = 0;
                 if (round == 0) {
-                    any = best > 0;
+                    any = best > kLowest;
                     top = key_value(best);
                 }
-                if (at == l && best > 0) {
+                if (at == l && best > kLowest) {
                     id[s] = index;
                     e[s] = expf(key_value(best) - top);
                 }
@@ -244,20 +241,22 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
     if ((threadIdx.x & 31) == 0) atomicAdd(count + a.experts, taking);
     __syncthreads();
     const bool alone = gridDim.x == 1;
-    float* total = alone ? a.totals : a.partial + (int64_t)blockIdx.x * (a.experts + 1);
     int32_t* counts = alone ? a.counts : a.part_counts + (int64_t)blockIdx.x * (a.experts + 1);
     for (int e = threadIdx.x; e <= a.experts; e += kThreads) {
         float v = 0.f;
         if (e < a.experts)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v += sums[w * a.experts + e];
-        if (!alone || a.loss) total[e] = v;
+        if (!alone)
+            a.partial[(int64_t)blockIdx.x * (a.experts + 1) + e] = v;
+        else if (e < a.experts)
+            sums[e] = v;
         counts[e] = count[e];
     }
     if (!alone || !a.loss) return;
     __syncthreads();
     if (threadIdx.x < 32) {
-        const float loss = balance(a.totals, a.counts, a.experts);
+        const float loss = balance(sums, count, a.experts);
         if (threadIdx.x == 0) *a.loss = loss;
     }
 }
@@ -500,6 +499,7 @@ size_t align_words(size_t words) { return (words + 63) / 64 * 64; }
 }  // namespace
 
 size_t route_workspace(int64_t tokens, int experts) {
+    if (tokens <= kThreads / 32) return 0;  // one block, whatever the spread
     const size_t columns = experts + 1;
     // a block takes a row or more
     const size_t blocks = (size_t)std::min<int64_t>(std::max<int64_t>(tokens, 1), kMaxRouteBlocks);

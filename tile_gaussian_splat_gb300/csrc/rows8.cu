@@ -24,8 +24,14 @@ namespace gs {
 namespace {
 
 constexpr int kThreads8 = 128;
-constexpr int kEach = 8;         // elements of a lane
-constexpr int kBlocksAhead = 4;  // blocks of a lane in flight
+constexpr int kEach = 8;  // elements of an access
+
+// kLanes lanes share a block with kItems accesses each (so that what is done
+// once a block is done by few lanes), kAhead blocks of a lane are in flight.
+template <int kLanes_, int kItems_, int kAhead_>
+struct Share {
+    static constexpr int kLanes = kLanes_, kItems = kItems_, kAhead = kAhead_;
+};
 
 // The blocks of 128 channels of all rows on end, `step` of them apart.
 struct Place {
@@ -127,12 +133,12 @@ __device__ __forceinline__ void floats8(const Eight<T>& e, float* v) {
     }
 }
 
-// f(lanes a block): rows of up to 32 or 64 channels leave no lane idle.
+// f(how a block is shared): rows of up to 32 or 64 channels leave no lane idle.
 template <typename F>
-void with_lanes(int channels, F&& f) {
-    if (channels <= 32) return f(std::integral_constant<int, 4>{});
-    if (channels <= 64) return f(std::integral_constant<int, 8>{});
-    return f(std::integral_constant<int, 16>{});
+void with_share(int channels, F&& f) {
+    if (channels <= 32) return f(Share<4, 1, 4>{});
+    if (channels <= 64) return f(Share<8, 1, 4>{});
+    return f(Share<8, 2, 2>{});
 }
 
 template <int kLanes>
@@ -142,65 +148,77 @@ __device__ __forceinline__ float lanes_max(float v) {
     return v;
 }
 
-template <typename T, int kLanes, bool kVectors>
+template <typename T, typename S, bool kVectors>
 __global__ void __launch_bounds__(kThreads8) k_pack8(Pack8 a) {
-    constexpr int kGroups = kThreads8 / kLanes;
-    const int at = threadIdx.x % kLanes;
+    constexpr int kLanes = S::kLanes, kItems = S::kItems, kGroups = kThreads8 / kLanes;
+    const int at = threadIdx.x % kLanes * kEach;
     const T* x = static_cast<const T*>(a.x);
     const T* end = x + (a.rows - 1) * a.ldx + a.channels;
     const int64_t step = (int64_t)gridDim.x * kGroups;
     Place load((int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes, step, a.blocks), p = load;
     // a warp's groups end together: they exchange across all lanes
     const int64_t turns = (a.rows * a.blocks + step - 1) / step;
-    for (int64_t t = 0; t < turns; t += kBlocksAhead) {
-        Eight<T> e[kBlocksAhead];
+    for (int64_t t = 0; t < turns; t += S::kAhead) {
+        Eight<T> e[S::kAhead][kItems];
 #pragma unroll
-        for (int u = 0; u < kBlocksAhead; ++u, load.advance()) {
-            const int c = load.block * GS_SCALE_BLOCK + at * kEach;
-            e[u] = load8<T, kVectors>(x + load.row * a.ldx + c,
-                                      load.row < a.rows ? a.channels - c : 0, x, end);
+        for (int u = 0; u < S::kAhead; ++u, load.advance()) {
+            const int c = load.block * GS_SCALE_BLOCK + at;
+            const T* from = x + load.row * a.ldx + c;
+            const int left = load.row < a.rows ? a.channels - c : 0;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                e[u][i] = load8<T, kVectors>(from + i * kLanes * kEach, left - i * kLanes * kEach,
+                                             x, end);
         }
 #pragma unroll
-        for (int u = 0; u < kBlocksAhead; ++u, p.advance()) {
-            float v[kEach];
-            floats8(e[u], v);
+        for (int u = 0; u < S::kAhead; ++u, p.advance()) {
+            float v[kItems][kEach];
             float most = 0.f;
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) most = fmaxf(most, fabsf(v[j]));
+            for (int i = 0; i < kItems; ++i) {
+                floats8(e[u][i], v[i]);
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) most = fmaxf(most, fabsf(v[i][j]));
+            }
             most = lanes_max<kLanes>(most);
             // fmaxf passes over a NaN; an infinity is not counted either
             if (__any_sync(0xffffffffu, most > FLT_MAX)) {
                 most = 0.f;
 #pragma unroll
-                for (int j = 0; j < kEach; ++j) {
-                    const bool finite = fabsf(v[j]) <= FLT_MAX;
-                    most = fmaxf(most, finite ? fabsf(v[j]) : 0.f);
-                    if (!finite) v[j] = __uint_as_float(0x7fffffffu);
-                }
+                for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j) {
+                        const bool finite = fabsf(v[i][j]) <= FLT_MAX;
+                        most = fmaxf(most, finite ? fabsf(v[i][j]) : 0.f);
+                        if (!finite) v[i][j] = __uint_as_float(0x7fffffffu);
+                    }
                 most = lanes_max<kLanes>(most);
             }
             if (p.row >= a.rows) continue;
-            const int c = p.block * GS_SCALE_BLOCK + at * kEach;
+            const int c = p.block * GS_SCALE_BLOCK + at;
             const int power = scale_byte(most);
             const float up = two_to(254 - power);
-            if (c < a.pitch) {  // 0 behind the last channel
-                uint2 q;
-                q.x = pack4_e4m3(v[0] * up, v[1] * up, v[2] * up, v[3] * up);
-                q.y = pack4_e4m3(v[4] * up, v[5] * up, v[6] * up, v[7] * up);
-                *reinterpret_cast<uint2*>(a.q + p.row * a.pitch + c) = q;
+            uint8_t* to = a.q + p.row * a.pitch + c;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                if (c + i * kLanes * kEach >= a.pitch) break;  // 0 behind the last channel
+                const float* f = v[i];
+                *reinterpret_cast<uint2*>(to + i * kLanes * kEach) =
+                    uint2{pack4_e4m3(f[0] * up, f[1] * up, f[2] * up, f[3] * up),
+                          pack4_e4m3(f[4] * up, f[5] * up, f[6] * up, f[7] * up)};
             }
             if (at == 0) {
-                uint8_t* to = a.scales + p.row * a.scale_pitch + p.block;
+                uint8_t* s = a.scales + p.row * a.scale_pitch + p.block;
                 // with the zeros behind the last block
                 if (p.block + 1 < a.blocks || a.blocks % 4 == 0) {
-                    *to = (uint8_t)power;
+                    *s = (uint8_t)power;
                 } else if (a.blocks % 4 == 1) {
-                    *reinterpret_cast<uint32_t*>(to) = (uint32_t)power;
+                    *reinterpret_cast<uint32_t*>(s) = (uint32_t)power;
                 } else if (a.blocks % 4 == 3) {
-                    *reinterpret_cast<uint16_t*>(to) = (uint16_t)power;
+                    *reinterpret_cast<uint16_t*>(s) = (uint16_t)power;
                 } else {
-                    to[0] = (uint8_t)power;
-                    *reinterpret_cast<uint16_t*>(to + 1) = 0;
+                    s[0] = (uint8_t)power;
+                    *reinterpret_cast<uint16_t*>(s + 1) = 0;
                 }
             }
         }
@@ -214,14 +232,18 @@ struct Unpack8 {
     int channels, blocks, pitch, scale_pitch;
 };
 
-// Eight values times their scales, as T.
+// The largest byte whose block's values, up to 448 * 2^(byte - 127), T holds.
 template <typename T>
+constexpr int kSafeByte = std::is_same<T, __half>::value ? 134 : 246;
+
+// Eight values times their scales, as T; kCut: which may be beyond the type.
+template <typename T, bool kCut>
 __device__ __forceinline__ Eight<T> scaled8(uint2 q, const float* size) {
     float v[8];
     unpack8_e4m3(q, v);
     Eight<T> e;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = cut_to<T>(v[j] * size[j]);
+    for (int j = 0; j < 8; ++j) v[j] = kCut ? cut_to<T>(v[j] * size[j]) : v[j] * size[j];
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) e.w[j] = __float_as_uint(v[j]);
@@ -233,35 +255,52 @@ __device__ __forceinline__ Eight<T> scaled8(uint2 q, const float* size) {
     return e;
 }
 
-template <typename T, int kLanes>
+template <typename T, typename S>
 __global__ void __launch_bounds__(kThreads8) k_unpack8(Unpack8 a) {
-    constexpr int kGroups = kThreads8 / kLanes, kVec = 16 / (int)sizeof(T);
-    const int at = threadIdx.x % kLanes;
+    constexpr int kLanes = S::kLanes, kItems = S::kItems, kGroups = kThreads8 / kLanes;
+    constexpr int kVec = 16 / (int)sizeof(T);
+    const int at = threadIdx.x % kLanes * kEach;
     const int64_t step = (int64_t)gridDim.x * kGroups;
     Place load((int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes, step, a.blocks), p = load;
     while (p.row < a.rows) {
-        uint2 q[kBlocksAhead];
-        int power[kBlocksAhead];
+        uint2 q[S::kAhead][kItems];
+        int power[S::kAhead];
 #pragma unroll
-        for (int u = 0; u < kBlocksAhead; ++u, load.advance()) {
-            const int c = load.block * GS_SCALE_BLOCK + at * kEach;
-            const bool in = load.row < a.rows && c < a.channels;
-            q[u] = in ? *reinterpret_cast<const uint2*>(a.q + load.row * a.pitch + c) : uint2{0, 0};
-            power[u] = in ? a.scales[load.row * a.scale_pitch + load.block] : 0;
+        for (int u = 0; u < S::kAhead; ++u, load.advance()) {
+            const int c = load.block * GS_SCALE_BLOCK + at;
+            const uint8_t* from = a.q + load.row * a.pitch + c;
+            const bool here = load.row < a.rows;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                q[u][i] = here && c + i * kLanes * kEach < a.channels
+                              ? *reinterpret_cast<const uint2*>(from + i * kLanes * kEach)
+                              : uint2{0, 0};
+            power[u] = here ? a.scales[load.row * a.scale_pitch + load.block] : 0;
         }
 #pragma unroll
-        for (int u = 0; u < kBlocksAhead; ++u, p.advance()) {
-            const int c = p.block * GS_SCALE_BLOCK + at * kEach;
-            if (p.row >= a.rows || c >= a.channels) continue;
+        for (int u = 0; u < S::kAhead; ++u, p.advance()) {
+            if (p.row >= a.rows) continue;
+            const int c = p.block * GS_SCALE_BLOCK + at;
+            T* to = static_cast<T*>(a.y) + p.row * a.ldy + c;
             const float one = scale_of(power[u]);
             const float size[8] = {one, one, one, one, one, one, one, one};
-            const Eight<T> e = scaled8<T>(q[u], size);
-            T* y = static_cast<T*>(a.y) + p.row * a.ldy + c;
+            const auto write = [&](auto cut) {
 #pragma unroll
-            for (int i = 0; i < kEach / kVec; ++i)
-                if (c + i * kVec < a.channels)
-                    reinterpret_cast<uint4*>(y)[i] =
-                        uint4{e.w[4 * i], e.w[4 * i + 1], e.w[4 * i + 2], e.w[4 * i + 3]};
+                for (int i = 0; i < kItems; ++i) {
+                    const int left = a.channels - c - i * kLanes * kEach;
+                    const Eight<T> e = scaled8<T, decltype(cut)::value>(q[u][i], size);
+                    uint4* y = reinterpret_cast<uint4*>(to + i * kLanes * kEach);
+#pragma unroll
+                    for (int k = 0; k < kEach / kVec; ++k)
+                        if (k * kVec < left)
+                            y[k] = uint4{e.w[4 * k], e.w[4 * k + 1], e.w[4 * k + 2],
+                                         e.w[4 * k + 3]};
+                }
+            };
+            if (power[u] > kSafeByte<T>)
+                write(std::true_type{});
+            else
+                write(std::false_type{});
         }
     }
 }
@@ -297,7 +336,7 @@ __global__ void __launch_bounds__(kThreads8) k_unpack8_any(Unpack8 a, int vector
         float size[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) size[j] = c + j < (block + 1) * GS_SCALE_BLOCK ? here : next;
-        const Eight<T> e = scaled8<T>(v, size);
+        const Eight<T> e = scaled8<T, true>(v, size);
         if (c >= 0 && c + kEach <= a.channels) {
 #pragma unroll
             for (int i = 0; i < Eight<T>::kWords / 4; ++i)
@@ -330,18 +369,17 @@ void launch_pack8(const void* x, int64_t ldx, int64_t rows, int channels, int dt
                   GS_ROW8_SCALES(channels)};
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        with_lanes(channels, [&](auto lanes) {
-            constexpr int kLanes = decltype(lanes)::value;
-            const bool vectors = rows_aligned<T>(x, ldx) && channels * sizeof(T) % 16 == 0;
+        with_share(channels, [&](auto share) {
+            using S = decltype(share);
             const int64_t items = rows * blocks;
-            if (vectors) {
-                const auto kernel = k_pack8<T, kLanes, true>;
+            if (rows_aligned<T>(x, ldx) && channels * sizeof(T) % 16 == 0) {
+                const auto kernel = k_pack8<T, S, true>;
                 static PerDevice resident;
-                kernel<<<blocks8(resident, kernel, items, kLanes), kThreads8, 0, s>>>(a);
+                kernel<<<blocks8(resident, kernel, items, S::kLanes), kThreads8, 0, s>>>(a);
             } else {
-                const auto kernel = k_pack8<T, kLanes, false>;
+                const auto kernel = k_pack8<T, S, false>;
                 static PerDevice resident;
-                kernel<<<blocks8(resident, kernel, items, kLanes), kThreads8, 0, s>>>(a);
+                kernel<<<blocks8(resident, kernel, items, S::kLanes), kThreads8, 0, s>>>(a);
             }
         });
     });
@@ -362,11 +400,11 @@ void launch_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int c
                                0, s>>>(a, vectors);
             return;
         }
-        with_lanes(channels, [&](auto lanes) {
-            constexpr int kLanes = decltype(lanes)::value;
+        with_share(channels, [&](auto share) {
+            using S = decltype(share);
             static PerDevice resident;
-            const auto kernel = k_unpack8<T, kLanes>;
-            kernel<<<blocks8(resident, kernel, rows * blocks, kLanes), kThreads8, 0, s>>>(a);
+            const auto kernel = k_unpack8<T, S>;
+            kernel<<<blocks8(resident, kernel, rows * blocks, S::kLanes), kThreads8, 0, s>>>(a);
         });
     });
 }
