@@ -640,16 +640,25 @@ __global__ void __launch_bounds__(256)
             const int row = i / (kWide / 4), col = i % (kWide / 4) * 4;
             if (m0 + row >= g.high || n0 + col >= g.width) continue;
             float4 sum{0.f, 0.f, 0.f, 0.f};
-            for (int s = s0; s <= s1; ++s) {
-                if (share_begin(total, g.groups, s) == share_begin(total, g.groups, s + 1))
-                    continue;
-                const float4 v = *reinterpret_cast<const float4*>(
-                    g.partial + (slot(s, s0, tile) * S::kTileHigh + block % kSlabs * kSlab + row) *
-                                    kWide + col);
-                sum.x += v.x;
-                sum.y += v.y;
-                sum.z += v.z;
-                sum.w += v.w;
+            // four shares' parts on their way at once, added in order
+            for (int s = s0; s <= s1; s += 4) {
+                float4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = float4{0.f, 0.f, 0.f, 0.f};
+                    if (s + k <= s1 && share_begin(total, g.groups, s + k) <
+                                           share_begin(total, g.groups, s + k + 1))
+                        v[k] = *reinterpret_cast<const float4*>(
+                            g.partial + (slot(s + k, s0, tile) * S::kTileHigh +
+                                         block % kSlabs * kSlab + row) * kWide + col);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    sum.x += v[k].x;
+                    sum.y += v[k].y;
+                    sum.z += v[k].z;
+                    sum.w += v[k].w;
+                }
             }
             Out* out = static_cast<Out*>(g.out) + ((int64_t)e * g.high + m0 + row) * g.width +
                        n0 + col;
@@ -1062,10 +1071,12 @@ constexpr int plane_dtype(int dtype) { return dtype == GS_F16 ? GS_F16 : GS_BF16
 size_t unpacked_bytes(int64_t rows, int columns) { return plane_bytes(GS_BF16, rows, columns); }
 
 Planes unpacked(int dtype, Rows8 x, int64_t rows, int columns, char** workspace, cudaStream_t s) {
+    // the zeros behind the last column too, up to whole vectors: they lie in
+    // the same block and row of 16 bytes
     const int pitch = (int)ceil_div(columns, 8) * 8;
     void* out = *workspace;
     *workspace += unpacked_bytes(rows, columns);
-    launch_unpack8(x.q, x.scales, rows, columns, dtype, out, pitch, s);
+    launch_unpack8(x.q, x.scales, rows, pitch, dtype, out, pitch, s);
     return Planes{out, rows, columns, pitch, 1};
 }
 

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
                 }
                 if (at == l && best > kLowest) {
                     id[s] = index;
-                    e[s] = expf(key_value(best) - top);
+                    e[s] = __expf(key_value(best) - top);
                 }
             }
         }
@@ -182,14 +182,14 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
                 const bool in = any && (i * kLanes + at) * kVec < a.experts;
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
-                    p[i][j] = in ? expf(v[j] - top) : 0.f;
+                    p[i][j] = in ? __expf(v[j] - top) : 0.f;
                     all += p[i][j];
                 }
             }
             all = group_sum<kLanes>(all);
         }
         if (tally && any) {
-            const float each = 1.0f / all;
+            const float each = __fdividef(1.0f, all);
 #pragma unroll
             for (int i = 0; i < kItems; ++i)
 #pragma unroll
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
         if (r >= a.tokens) continue;
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            e[s] = id[s] >= 0 ? e[s] / chosen : 0.f;
+            e[s] = id[s] >= 0 ? __fdividef(e[s], chosen) : 0.f;
             if (tally && id[s] >= 0) atomicAdd(count + id[s], 1);
         }
         const int64_t to = r * a.topk;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(RouteBwd a) {
         float chosen = 0.f, mean = 0.f;
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            if (take && id[s] >= 0) e[s] = expf(to_f(row[id[s]]) - top);
+            if (take && id[s] >= 0) e[s] = __expf(to_f(row[id[s]]) - top);
             chosen += e[s];
             mean += e[s] * g[s];
         }
@@ -408,16 +408,16 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(RouteBwd a) {
         for (int i = 0; i < kItems; ++i)
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                p[i][j] = expf(p[i][j] - top);
+                p[i][j] = __expf(p[i][j] - top);
                 all += p[i][j];
                 dot += p[i][j] * h[i][j];
             }
         all = group_sum<kLanes>(all);
-        const float each = 1.0f / all;
+        const float each = __fdividef(1.0f, all);
         dot = a.grad_loss ? group_sum<kLanes>(dot) * each : 0.f;
         mean = group_sum<kLanes>(mean);
         chosen = a.renormalise ? group_sum<kLanes>(chosen) : all;
-        mean /= chosen;  // renormalised: sum w g; otherwise D
+        mean = __fdividef(mean, chosen);  // renormalised: sum w g; otherwise D
         const float down = dot + (a.renormalise ? 0.f : mean);
         if (a.renormalise) {
 #pragma unroll
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(RouteBwd a) {
             for (int j = 0; j < kVec; ++j) p[i][j] *= each * (h[i][j] - down);
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            const float d = e[s] / chosen * g[s];
+            const float d = __fdividef(e[s], chosen) * g[s];
             for (int l = 0; l < kLanes; ++l) {
                 if (s * kLanes + l >= a.topk) break;
                 const int index = __shfl_sync(kAll, id[s], l, kLanes);
