@@ -8,7 +8,10 @@ every splat's features.  Only pixels that some splat reaches enter the
 experts.  Every call is one of tile_gaussian_splat_gb300.binding; plain torch
 does the router's small product, its softmax and the updates.
 
-    python examples/feature_head.py [steps]
+With "8" the head is EightBitHead: the library's router with a balance loss,
+and the experts' products of rows kept in 8 bits.
+
+    python examples/feature_head.py [steps] [8]
 """
 
 import os
@@ -86,6 +89,59 @@ class FeatureHead:
             self.params[k] -= rate * g
 
 
+class EightBitHead(FeatureHead):
+    """The same head with rows and weights of the experts' products in 8 bits,
+    forward and backward (what the backward needs of a product is kept in 8
+    bits only), the choice of experts by the library's router, and `balance`
+    times its balance loss added to the loss.  The updates go to the float32
+    parameters, as if the rounding to 8 bits were not there."""
+
+    def __init__(self, *args, balance=0.01, **kwargs):
+        super().__init__(*args, **kwargs)
+        self.balance = torch.full((1,), balance, device=self.status.device)
+
+    def forward(self, x, reached):
+        p, st = self.params, self.status
+        norm, mean, rstd = gs.gs_layer_norm_fwd(x, p["norm_w"], p["norm_b"])
+        rows = norm.reshape(-1, norm.shape[-1])
+        logits = rows @ p["router"].t()
+        ids, weights, counts, self.balance_loss = gs.gs_expert_route_fwd(
+            logits, self.topk, keep=reached.reshape(-1))
+        offsets, _, slots = gs.gs_expert_sort(ids, self.experts)
+        w1, w2 = gs.gs_rows_pack8(p["w1"]), gs.gs_rows_pack8(p["w2"])
+        # 8-bit rows are dispatched as rows of 16-bit elements
+        xs = [gs.gs_expert_dispatch(t.view(torch.float16), slots, offsets, d_status=st).view(t.dtype)
+              for t in gs.gs_rows_pack8(rows)]
+        h = gs.gs_expert_linear8_fwd(*xs, offsets, *w1, rows.shape[1], p["b1"],
+                                     dtype=torch.float32, d_status=st).relu_()
+        h8 = gs.gs_rows_pack8(h)
+        ys = gs.gs_expert_linear8_fwd(*h8, offsets, *w2, h.shape[1], p["b2"], dtype=torch.float32,
+                                      d_status=st)
+        y = gs.gs_expert_combine(ys, slots, weights, d_status=st)
+        self.kept = (x, mean, rstd, rows, logits, ids, weights, counts, offsets, slots, xs, h8, w1,
+                     w2, ys)
+        return y.reshape(*x.shape[:-1], -1)
+
+    def backward(self, grad_y, grad_x):
+        p, st = self.params, self.status
+        (x, mean, rstd, rows, logits, ids, weights, counts, offsets, slots, xs, h8, w1, w2,
+         ys) = self.kept
+        hidden = p["w1"].shape[1]
+        gy = grad_y.reshape(rows.shape[0], -1)
+        gys, gw = gs.gs_expert_combine_bwd(gy, ys, slots, weights, offsets, d_status=st)
+        gh, g_w2, g_b2 = gs.gs_expert_linear8_bwd(gys, *h8, offsets, *w2, hidden, d_status=st)
+        gh *= gs.gs_rows_unpack8(*h8, hidden, torch.float32) > 0
+        gxs, g_w1, g_b1 = gs.gs_expert_linear8_bwd(gh, *xs, offsets, *w1, rows.shape[1],
+                                                   d_status=st)
+        g_rows = gs.gs_expert_combine(gxs, slots, d_status=st)
+        g_logits = gs.gs_expert_route_bwd(logits, ids, counts, gw, self.balance, d_status=st)
+        g_rows += g_logits @ p["router"]
+        _, g_nw, g_nb = gs.gs_layer_norm_bwd(g_rows.reshape(x.shape), x, p["norm_w"], mean, rstd,
+                                             out=grad_x)
+        self.grads = dict(norm_w=g_nw, norm_b=g_nb, router=g_logits.t() @ rows, w1=g_w1, b1=g_b1,
+                          w2=g_w2, b2=g_b2)
+
+
 def render(d, scene, colors):
     """(image (C, H, W, channels), alphas, what the backward needs)."""
     status = gs.new_status(colors.device)
@@ -114,7 +170,7 @@ def render_grad(d, scene, colors, alphas, kept, grad_image):
 
 
 def train(steps=30, features=32, hidden=96, out=8, experts=8, width=96, height=64, rate=0.5,
-          seed=0):
+          seed=0, head_type=FeatureHead):
     """Fits the head and the splats' features to a smooth target image; returns
     the loss of every step."""
     scene = scenes.random_small(seed, C=1, N=600, W=width, H=height, sigma=(1.0, 8.0),
@@ -126,7 +182,7 @@ def train(steps=30, features=32, hidden=96, out=8, experts=8, width=96, height=6
                             indexing="ij")
     k = torch.arange(1, out + 1)
     target = torch.sin(xx[..., None] * k / 2 + yy[..., None]).cuda()[None]
-    head = FeatureHead(features, hidden, out, experts, seed=seed)
+    head = head_type(features, hidden, out, experts, seed=seed)
     losses = []
     for _ in range(steps):
         image, alphas, kept = render(d, scene, colors)
@@ -146,5 +202,6 @@ def train(steps=30, features=32, hidden=96, out=8, experts=8, width=96, height=6
 
 if __name__ == "__main__":
     count = int(sys.argv[1]) if len(sys.argv) > 1 else 30
-    for i, loss in enumerate(train(count)):
+    kind = EightBitHead if "8" in sys.argv[2:] else FeatureHead
+    for i, loss in enumerate(train(count, head_type=kind)):
         print(f"step {i:3d}  loss {loss:.4f}")

@@ -121,6 +121,45 @@ def test_nan_stays_in_its_row(rows):
     assert torch.equal(ys[others], clean[others]) and bool(torch.isnan(ys[3]).all())
 
 
+@pytest.mark.parametrize("rows", [5, 700])
+def test_a_scale_that_is_no_number(rows):
+    """Byte 255: in a row, its answers; in a weight's, that column's."""
+    offsets = torch.tensor([0, rows, rows], dtype=torch.int32, device=DEV)
+    p = _packed(15, rows, 2, 300, 80, rows)
+    clean = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 300)
+    p[1].view(torch.uint8)[2, 1] = 255
+    p[3].view(torch.uint8)[0, 7, 2] = 255
+    p[3].view(torch.uint8)[1, 9, 0] = 255  # of an expert without rows
+    ys = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], 300)
+    bad = torch.zeros_like(ys, dtype=torch.bool)
+    bad[2] = True
+    bad[:, 7] = True
+    assert torch.equal(torch.isnan(ys), bad) and torch.equal(ys[~bad], clean[~bad])
+
+
+def test_two_calls_at_once():
+    """On two streams, without anything that they share."""
+    _, offsets, _, _ = routed(16, 20000, 2, 8)
+    p, q = _packed(16, 40000, 8, 256, 384, 40000), _packed(17, 40000, 8, 256, 384, 40000)
+    gys = randn(gen(16), 40000, 384, dtype=torch.bfloat16)
+
+    def run(r):
+        return (gs.gs_expert_linear8_fwd(r[0], r[1], offsets, r[2], r[3], 256),
+                *gs.gs_expert_linear8_bwd(gys, r[0], r[1], offsets, r[2], r[3], 256))
+
+    want = run(p), run(q)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        for s, r in zip(streams, (p, q)):
+            with torch.cuda.stream(s):
+                got.append(run(r))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
 @pytest.mark.parametrize("rows", [16, 640])
 def test_long_sums_of_one_sign(rows):
     """32768 positive terms, added up over at most 4096 of them, 32 at a time

@@ -152,6 +152,20 @@ def test_ids_that_are_none_are_skipped():
         check(grad, ref, slack, "grad_logits")
 
 
+def test_the_range_checking_build_reports_such_ids():
+    g = gen(10)
+    logits = randn(g, 6, 12)
+    ids = torch.tensor([[3, 4], [3, -1], [-1, -1], [5, 6], [0, 11], [9, 1]], dtype=torch.int32,
+                       device=DEV)
+    with gs.library(gs.LIB_DEBUG_PATH):
+        for bad, code in ((None, 0), (12, 9), (-2, 9)):
+            st = gs.new_status(DEV)
+            if bad is not None:
+                ids[4, 1] = bad
+            gs.gs_expert_route_bwd(logits, ids, None, randn(g, 6, 2), d_status=st)
+            assert int(st.item()) == code
+
+
 def test_gradient_against_differences():
     """Central differences of the forward along random directions that keep
     the choice: 2h = 2e-3, its cubic term h^2 and the forward's rounding (1e-6

@@ -423,6 +423,13 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
         }
         copy_wait<0>();
         for (; ok && waiting > 0; --waiting) pass_on();
+        if (!ok && rank == 0) {  // let the copies into tensor memory end
+            int none = 0;
+            for (int i = 0; i < kBuffers; ++i) {
+                const uint32_t turn = i < (int)next.stage ? next.turn : next.turn - 1;
+                if (turn != ~0u) mbar_wait_limited(&bars.powers_full[i], turn & 1, &none);
+            }
+        }
     } else if (warp == 3) {
         Ring<kAccumulators> at;
         bool ok = g.bias != nullptr;
