@@ -170,7 +170,7 @@ def render_grad(d, scene, colors, alphas, kept, grad_image):
 
 
 def train(steps=30, features=32, hidden=96, out=8, experts=8, width=96, height=64, rate=0.5,
-          seed=0, head_type=FeatureHead):
+          seed=0, head_type=None):
     """Fits the head and the splats' features to a smooth target image; returns
     the loss of every step."""
     scene = scenes.random_small(seed, C=1, N=600, W=width, H=height, sigma=(1.0, 8.0),
@@ -182,7 +182,7 @@ def train(steps=30, features=32, hidden=96, out=8, experts=8, width=96, height=6
                             indexing="ij")
     k = torch.arange(1, out + 1)
     target = torch.sin(xx[..., None] * k / 2 + yy[..., None]).cuda()[None]
-    head = head_type(features, hidden, out, experts, seed=seed)
+    head = (head_type or FeatureHead)(features, hidden, out, experts, seed=seed)
     losses = []
     for _ in range(steps):
         image, alphas, kept = render(d, scene, colors)
@@ -202,6 +202,6 @@ def train(steps=30, features=32, hidden=96, out=8, experts=8, width=96, height=6
 
 if __name__ == "__main__":
     count = int(sys.argv[1]) if len(sys.argv) > 1 else 30
-    kind = EightBitHead if "8" in sys.argv[2:] else FeatureHead
+    kind = EightBitHead if "8" in sys.argv[2:] else None
     for i, loss in enumerate(train(count, head_type=kind)):
         print(f"step {i:3d}  loss {loss:.4f}")

@@ -69,7 +69,7 @@ def test_gradients_of_the_whole_head():
     ref = out.detach()
     # sums of at most 40 float32 terms: a relative 1e-5 is over 20 times their rounding
     assert float((y.double() - ref).norm()) <= 1e-5 * float(ref.norm())
-    assert abs(float(head.balance_loss) - float(balance)) <= 1e-5 * float(balance)
+    assert abs(float(head.balance_loss) - float(balance.detach())) <= 1e-5 * float(balance.detach())
     gy = randn(g, *y.shape) * reached[..., None]
     grad_image = torch.full_like(image, 9.0)
     head.backward(gy, grad_image[..., 3:])
@@ -84,3 +84,30 @@ def test_it_trains():
     ex = _example()
     losses = ex.train(steps=5, head_type=ex.EightBitHead)
     assert len(losses) == 5 and all(v == v for v in losses)
+
+
+@pytest.mark.parametrize("call", ["gs_expert_linear8_fwd", "gs_expert_linear8_bwd",
+                                  "gs_expert_route_bwd"])
+def test_a_reported_error_stops_the_training(call, monkeypatch):
+    from tile_gaussian_splat_gb300 import binding as gs
+
+    ex = _example()
+    made = []
+
+    class Head(ex.EightBitHead):
+        def __init__(self, *args, **kw):
+            super().__init__(*args, **kw)
+            made.append((self, {k: v.clone() for k, v in self.params.items()}))
+
+    def reporting(*args, d_status=None, **kw):
+        out = genuine(*args, d_status=d_status, **kw)
+        if d_status is not None:
+            d_status.fill_(5)  # as a wait that ran out does
+        return out
+
+    genuine = getattr(gs, call)
+    monkeypatch.setattr(gs, call, reporting)
+    with pytest.raises(gs.GsError, match="TIMEOUT"):
+        ex.train(steps=1, head_type=Head)
+    head, before = made[0]
+    assert all(torch.equal(head.params[k], v) for k, v in before.items())

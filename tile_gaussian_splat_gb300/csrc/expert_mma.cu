@@ -581,12 +581,12 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
         Out* out = static_cast<Out*>(g.out);
         if (kProduct != kWeightGrad) {
             const int64_t kept = begin[g.experts];
-            zero_range(out + kept * g.width, (g.rows - kept) * g.width, at, stride, g.vectors);
+            zero_range(out + kept * g.width, (g.rows - kept) * g.width, at, stride);
         } else {
             const int64_t size = (int64_t)g.high * g.width;
             for (int e = 0; e < g.experts; ++e)
                 if (prefix[e] == prefix[e + 1])
-                    zero_range(out + e * size, size, at, stride, g.vectors);
+                    zero_range(out + e * size, size, at, stride);
         }
     }
     __syncthreads();

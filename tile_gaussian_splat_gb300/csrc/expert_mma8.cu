@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
         const int64_t kept = begin[g.experts];
         zero_range(static_cast<Out*>(g.out) + kept * g.width, (g.rows - kept) * g.width,
                    (int64_t)blockIdx.x * (kOutputs<kWide> * 32) + threadIdx.x - 128,
-                   (int64_t)gridDim.x * (kOutputs<kWide> * 32), g.vectors);
+                   (int64_t)gridDim.x * (kOutputs<kWide> * 32));
     }
     __syncthreads();
     if (kBlocks == 2) cluster_sync();  // the other block's arrivals and products are over too
@@ -644,7 +644,7 @@ int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* 
         else if (a.in <= 2 * kDeep)
             rc = launch_shape<Out, Shape8<2, 192, 2, 4, 128>>(a, xs, weight, g, s);
         else
-            rc = launch_shape<Out, Shape8<2, 192, 4, 2, 64>>(a, xs, weight, g, s);
+            rc = launch_shape<Out, Shape8<2, 192, 3, 3, 64>>(a, xs, weight, g, s);
     });
     return rc;
 }

@@ -90,26 +90,33 @@ __device__ __forceinline__ void write_block(char* staging, const uint4* v, Out* 
                 *reinterpret_cast<uint4*>(out + r * pitch + j * kVec) = x;
         }
     } else {
+        // several elements on their way at once (one after the other, 64 odd
+        // float32 columns of a tile took 5000 cycles)
         const int e = lane % kRow, j = e / kVec;
-        for (int r = lane / kRow; r < min(32, valid_rows); r += 32 / kRow) {
+        constexpr int kStep = 32 / kRow;
+#pragma unroll 8
+        for (int i = 0; i < 32 / kStep; ++i) {
+            const int r = i * kStep + lane / kRow;
             const Out x = *reinterpret_cast<const Out*>(
                 staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4) + e % kVec * sizeof(Out));
-            if (e < left) out[r * pitch + e] = x;
+            if (r < valid_rows && e < left) out[r * pitch + e] = x;
         }
     }
     __syncwarp();
 }
 
 // By the output warps: n elements from `out` on are 0; `at` and `stride`: this
-// thread's place among all of them.
+// thread's place among all of them.  Whole vectors between the ends.
 template <typename Out>
-__device__ __forceinline__ void zero_range(Out* out, int64_t n, int64_t at, int64_t stride,
-                                           bool vectors) {
-    if (vectors)
-        for (int64_t i = at; i < n * (int64_t)sizeof(Out) / 16; i += stride)
-            reinterpret_cast<uint4*>(out)[i] = uint4{0, 0, 0, 0};
-    else
-        for (int64_t i = at; i < n; i += stride) out[i] = from_f<Out>(0.f);
+__device__ __forceinline__ void zero_range(Out* out, int64_t n, int64_t at, int64_t stride) {
+    constexpr int kVec = 16 / (int)sizeof(Out);
+    const int off = (int)(reinterpret_cast<uintptr_t>(out) & 15u) / (int)sizeof(Out);
+    const int64_t head = min(n, (int64_t)((kVec - off) % kVec));
+    const int64_t whole = (n - head) / kVec, tail = head + whole * kVec;
+    for (int64_t i = at; i < whole; i += stride)
+        reinterpret_cast<uint4*>(out + head)[i] = uint4{0, 0, 0, 0};
+    for (int64_t i = at; i < head; i += stride) out[i] = from_f<Out>(0.f);
+    for (int64_t i = tail + at; i < n; i += stride) out[i] = from_f<Out>(0.f);
 }
 
 // cuTensorMapEncodeTiled, found through the runtime (the library does not

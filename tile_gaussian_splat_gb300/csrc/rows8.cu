@@ -329,14 +329,15 @@ __global__ void __launch_bounds__(kThreads8) k_unpack8_any(Unpack8 a, int vector
         const uint2 v{__funnelshift_r(w[0], w[1], turn & 31), __funnelshift_r(w[1], w[2], turn & 31)};
         const uint8_t* s = a.scales + p.row * a.scale_pitch;
         const int block = max(c, 0) / GS_SCALE_BLOCK;
-        const float here = scale_of(s[block]);
-        const float next = (block + 1) * GS_SCALE_BLOCK < min(c + kEach, a.channels)
-                               ? scale_of(s[block + 1])
-                               : 0.f;
+        const bool both = (block + 1) * GS_SCALE_BLOCK < min(c + kEach, a.channels);
+        const int p0 = s[block], p1 = both ? s[block + 1] : p0;
+        const float here = scale_of(p0), next = scale_of(p1);
+        const int mine = (block + 1) * GS_SCALE_BLOCK - c;  // elements of the first of them
         float size[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) size[j] = c + j < (block + 1) * GS_SCALE_BLOCK ? here : next;
-        const Eight<T> e = scaled8<T, true>(v, size);
+        for (int j = 0; j < 8; ++j) size[j] = j < mine ? here : next;
+        const Eight<T> e = max(p0, p1) > kSafeByte<T> ? scaled8<T, true>(v, size)
+                                                      : scaled8<T, false>(v, size);
         if (c >= 0 && c + kEach <= a.channels) {
 #pragma unroll
             for (int i = 0; i < Eight<T>::kWords / 4; ++i)
