@@ -37,6 +37,7 @@ constexpr int kHalf = kDeep / 2;
 constexpr int kGroup = 2;           // slices a word of powers serves
 constexpr int kAccumulators = 2;
 constexpr int kSpan = 64;           // columns an output warp writes
+constexpr int kRowBytes = 64;       // of the boxes they leave in
 // Warps: 0 copies rows, 1 issues products, 2 copies powers, 3 the bias, from 4
 // on they write the output.
 template <int kWide>
@@ -64,12 +65,28 @@ struct Product8Args {
     int32_t* d_status;
 };
 
-// kSlots, kStages: slices of A and of B in shared memory; kRowBytes: of the boxes
-// the output leaves in, 64 or 128.
-template <int kBlocks_, int kWide_, int kSlots_, int kStages_, int kRowBytes_>
+struct Bars8 {
+    // of the first block: a slice of A or B, a buffer's words of powers are
+    // there (in all blocks), the accumulators may be overwritten
+    uint64_t full_a[4], full_b[4], words_full[kBuffers], acc_empty[kAccumulators];
+    // of each block: a slice may be overwritten, powers are in tensor memory,
+    // a buffer of them may be overwritten, the accumulators are finished, a
+    // tile's bias is there, and may be overwritten
+    uint64_t empty_a[4], empty_b[4], powers_full[kBuffers], powers_empty[kBuffers],
+        acc_full[kAccumulators], bias_full[kAccumulators], bias_empty[kAccumulators], drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// kSlots, kStages: slices of A and of B in shared memory.  512 channels leave a
+// slot of three for the next piece's first slice, whose 1 to 2 us from memory
+// under the output's writes are else waited for at every piece (262144 rows 512
+// -> 1024: 140 us with 3 and 4, 150 with 2 and 4, 147 with 2 and 5, 152 with 3
+// and 3, 175 with 4 and 2).
+template <int kBlocks_, int kWide_, int kSlots_, int kStages_>
 struct Shape8 {
     static constexpr int kBlocks = kBlocks_, kWide = kWide_, kSlots = kSlots_;
-    static constexpr int kStages = kStages_, kRowBytes = kRowBytes_;
+    static constexpr int kStages = kStages_;
     static constexpr int kTileHigh = kHigh * kBlocks;
     static constexpr int kBytesA = kHigh * kDeep;
     static constexpr int kPartB = kWide / kBlocks;
@@ -79,27 +96,17 @@ struct Shape8 {
     static constexpr int kPowerBytes = (1 + kChunksB) * kChunk;
     static constexpr int kStaging = kOutputs<kWide> * 32 * kRowBytes;
     static constexpr int kBias = kAccumulators * kWide * 4;
+    // most experts whose ranges fit beside the rest
+    static constexpr int kRest = 1024 + kSlots * kBytesA + kStages * kBytesB + kStaging +
+                                 kBuffers * kPowerBytes + kBias + sizeof(Bars8);
+    static constexpr int kExperts = std::min(GS_MAX_EXPERTS, (232448 - kRest) / 8 - 1);
     static_assert(kPartB * kHalf % 1024 == 0, "swizzled rows begin on 1024 bytes");
     static_assert(kAccumulators * kWide + kBuffers * kPowers <= kColumns, "tensor memory");
 };
 
-struct Bars8 {
-    // of the first block: a slice of A or B, a buffer's words of powers are
-    // there (in all blocks), the accumulators may be overwritten
-    uint64_t full_a[4], full_b[4], words_full[kBuffers], acc_empty[kAccumulators];
-    // of each block: a slice may be overwritten, powers are in tensor memory,
-    // a buffer of them may be overwritten, the accumulators are finished, a
-    // tile's bias is there, and may be overwritten
-    uint64_t empty_a[4], empty_b[4], powers_full[kBuffers], powers_empty[kBuffers], acc_full[kAccumulators], bias_full[kAccumulators],
-        bias_empty[kAccumulators], drain;
-    uint32_t tmem;
-    int abort;
-};
-
 template <typename S>
 constexpr size_t smem_bytes8(int experts) {
-    return 1024 + S::kSlots * S::kBytesA + S::kStages * S::kBytesB + S::kStaging + kBuffers * S::kPowerBytes +
-           S::kBias + sizeof(Bars8) + 2 * sizeof(int32_t) * (size_t)(experts + 1);
+    return S::kRest + 2 * sizeof(int32_t) * (size_t)(experts + 1);
 }
 
 struct Tile8 {
@@ -448,9 +455,9 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
     } else {
         const int q = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
         const int first = (warp - 4) / 4 * kSpan;
-        char* mine = staging + (warp - 4) * 32 * S::kRowBytes;
-        constexpr int kRow = S::kRowBytes / (int)sizeof(Out);  // columns written at a time
-        constexpr int kVectors = S::kRowBytes / 16;
+        char* mine = staging + (warp - 4) * 32 * kRowBytes;
+        constexpr int kRow = kRowBytes / (int)sizeof(Out);  // columns written at a time
+        constexpr int kVectors = kRowBytes / 16;
         Ring<kAccumulators> acc, added;
         bool ok = true;
         for (; ok && walk.next(c); acc.advance(accumulators)) {
@@ -521,22 +528,17 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
                     __syncwarp();
                     if (boxed) {
 #pragma unroll
-                        for (int j = 0; j < kVectors; ++j) {
-                            const int turn = kVectors == 8 ? lane & 7 : lane >> 1 & 3;
-                            *reinterpret_cast<uint4*>(mine + lane * S::kRowBytes +
-                                                      ((j ^ turn) << 4)) = v[j];
-                        }
+                        for (int j = 0; j < kVectors; ++j)
+                            *reinterpret_cast<uint4*>(mine + lane * kRowBytes +
+                                                      ((j ^ (lane >> 1 & 3)) << 4)) = v[j];
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                         if (lane == 0)
                             tma_store_2d(&map_out, smem_u32(mine), c.n0 + first + b * kRow,
                                          c.row0 + row);
                     } else {
-                        constexpr int kPart = 64 / (int)sizeof(Out);
-#pragma unroll
-                        for (int h = 0; h < kRow / kPart; ++h)
-                            write_block<Out>(mine, v + h * 4, out + b * kRow + h * kPart, g.width,
-                                             rows, left - b * kRow - h * kPart, g.vectors);
+                        write_block<Out>(mine, v, out + b * kRow, g.width, rows, left - b * kRow,
+                                         g.vectors);
                     }
                 }
             };
@@ -580,19 +582,19 @@ bool make_map8(CUtensorMap* map, const uint8_t* base, int64_t rows, int columns,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The output in boxes of 32 rows x row_bytes, swizzled.
-bool make_out_map(CUtensorMap* map, int dtype, void* ys, int64_t rows, int width, int row_bytes) {
+// The output in boxes of 32 rows x kRowBytes, swizzled.
+bool make_out_map(CUtensorMap* map, int dtype, void* ys, int64_t rows, int width) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
     const size_t size = dtype_size(dtype);
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, pitch = width * size;
-    const cuuint32_t box[2] = {(cuuint32_t)(row_bytes / size), 32}, unit[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / size), 32}, unit[2] = {1, 1};
     return encode(map,
                   dtype == GS_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                   : dtype == GS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                   2, ys, dims, &pitch, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -600,7 +602,7 @@ template <typename Out, typename S>
 int launch_shape(const LinearArgs& a, Rows8 xs, Rows8 weight, const Product8Args& g,
                  cudaStream_t s) {
     CUtensorMap ma, mb, mo{};
-    if (g.vectors && !make_out_map(&mo, a.dtype, g.out, a.rows, a.out, S::kRowBytes))
+    if (g.vectors && !make_out_map(&mo, a.dtype, g.out, a.rows, a.out))
         return GS_ERR_CUDA;
     if (!make_map8(&ma, xs.q, a.rows, a.in, 0, kHigh) ||
         !make_map8(&mb, weight.q, a.out, a.in, a.experts, S::kPartB))
@@ -609,7 +611,7 @@ int launch_shape(const LinearArgs& a, Rows8 xs, Rows8 weight, const Product8Args
     const int64_t items = (a.rows / S::kTileHigh + a.experts) * ceil_div(g.width, S::kWide);
     static PerDevice raised, resident;
     return launch_walk<S::kBlocks>(raised, resident, k_product8<Out, S>, kThreads<S::kWide>,
-                                   smem_bytes8<S>(g.experts), smem_bytes8<S>(GS_MAX_EXPERTS),
+                                   smem_bytes8<S>(g.experts), smem_bytes8<S>(S::kExperts),
                                    items, s, ma, mb, mo, g);
 }
 
@@ -635,16 +637,19 @@ int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* 
     g.bias = bias;
     g.out = ys;
     g.d_status = a.d_status;
+    // Two blocks a tile of 256 x 192 where those fill every pair of SMs twice,
+    // one block a tile of 128 x 128 else (512 -> 1024 bf16: 40000 rows 31 us in
+    // pairs and 33 single, 4000 12.3 and 10.3).
     const int64_t tiles = (a.rows / 256 + a.experts / 2) * ceil_div(a.out, 192);
     int rc = GS_OK;
     with_dtype(a.dtype, [&](auto o) {
         using Out = decltype(o);
         if (a.out <= 128 || tiles < sm_count())
-            rc = launch_shape<Out, Shape8<1, 128, 3, 3, 64>>(a, xs, weight, g, s);
-        else if (a.in <= 2 * kDeep)
-            rc = launch_shape<Out, Shape8<2, 192, 2, 4, 128>>(a, xs, weight, g, s);
+            rc = launch_shape<Out, Shape8<1, 128, 3, 3>>(a, xs, weight, g, s);
+        else if (a.experts <= Shape8<2, 192, 3, 4>::kExperts)
+            rc = launch_shape<Out, Shape8<2, 192, 3, 4>>(a, xs, weight, g, s);
         else
-            rc = launch_shape<Out, Shape8<2, 192, 3, 3, 64>>(a, xs, weight, g, s);
+            rc = launch_shape<Out, Shape8<2, 192, 3, 3>>(a, xs, weight, g, s);
     });
     return rc;
 }
