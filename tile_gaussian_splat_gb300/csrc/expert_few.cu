@@ -118,7 +118,10 @@ __global__ void __launch_bounds__(kFewThreads)
 }
 
 // The same of 8-bit rows: sixteen elements of a weight row an access, of one
-// block of 128, whose power of two their sum takes.
+// block of 128, times its power of two (exact).  2 rows, 256 -> 1024: 5.6 us.  The
+// rule of few_rows holds here too (calls back to back, 8 experts: 8 rows 1024 ->
+// 1024 7.6 us and 9.6 on the tensor cores, 16 rows 256 -> 1024 7.7 and 8.1, 32 rows
+// 10.3 and 8.1).
 template <int kRows>
 __device__ __forceinline__ void few8_terms(const float (*x)[kFewDepth], const uint8_t* const* w,
                                            const uint8_t* const* powers, int depth,
