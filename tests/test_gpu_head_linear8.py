@@ -123,6 +123,21 @@ def test_nan_stays_in_its_row(rows):
     assert torch.equal(ys[others], clean[others]) and bool(torch.isnan(ys[3]).all())
 
 
+@pytest.mark.parametrize("rows", [5, 700, 40000])
+def test_what_lies_behind_the_last_channel_counts_for_nothing(rows):
+    i, o = 259, 200  # rows of 272 bytes and four scales, three of them used
+    offsets = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device=DEV)
+    p = _packed(18, rows, 2, i, o, rows)
+    gys = randn(gen(18), rows, o, dtype=torch.bfloat16)
+    run = lambda: (gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], i),
+                   *gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], i))
+    clean = run()
+    for q, s in ((p[0], p[1]), (p[2], p[3])):
+        q.view(torch.uint8)[..., i:] = 0x7f
+        s.view(torch.uint8)[..., 3:] = 255
+    assert all(torch.equal(a, b) for a, b in zip(run(), clean))
+
+
 @pytest.mark.parametrize("rows", [5, 700])
 def test_a_scale_that_is_no_number(rows):
     """Byte 255: in a row, its answers; in a weight's, that column's."""

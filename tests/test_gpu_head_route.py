@@ -13,7 +13,9 @@ pytestmark = pytest.mark.gpu
 # (tokens, experts, topk)
 SHAPES = [(1, 1, 1), (1, 8, 2), (3, 2, 2), (5, 7, 3), (9, 16, 4), (64, 33, 8), (130, 64, 6),
           (33, 100, 17), (21, 256, 64), (12, 515, 64), (7, 1024, 33), (400, 4, 1), (2000, 20, 5),
-          (257, 12, 12), (3001, 32, 32), (17, 130, 64)]
+          (257, 12, 12), (3001, 32, 32), (17, 130, 64), (40, 9, 4),
+          (50, 31, 4), (50, 31, 5), (60, 63, 8), (60, 64, 16), (60, 64, 17), (33, 128, 16),
+          (33, 127, 9), (30, 256, 32), (30, 250, 33), (20, 512, 9), (500, 8, 8), (70, 16, 16)]
 
 
 def _check_fwd(logits, topk, keep=None, renormalise=True):

@@ -134,8 +134,9 @@ __device__ __forceinline__ void few8_terms(const float (*x)[kFewDepth], const ui
             const float size = scale_of(powers[n][k / GS_SCALE_BLOCK]);
             unpack8_e4m3(uint2{q.x, q.y}, v[n]);
             unpack8_e4m3(uint2{q.z, q.w}, v[n] + 8);
+            // whatever lies behind the last channel
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[n][i] *= size;
+            for (int i = 0; i < 16; ++i) v[n][i] = k + i < depth ? v[n][i] * size : 0.f;
         }
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
@@ -175,17 +176,17 @@ __global__ void __launch_bounds__(kFewThreads)
     }
     float sum[kFewColumns][kFewRows] = {};
     for (int k0 = 0; k0 < g.in; k0 += kFewDepth) {
-        const int depth = min(kFewDepth, pitch - k0);  // zeros behind the last channel
+        const int depth = min(kFewDepth, g.in - k0), whole = min(kFewDepth, pitch - k0);
         if (k0 > 0) __syncthreads();
         for (int r = 0; r < rows; ++r) {
             const int64_t row = row0 + r;
-            for (int k = threadIdx.x * 8; k < depth; k += kFewThreads * 8) {
+            for (int k = threadIdx.x * 8; k < whole; k += kFewThreads * 8) {
                 float v[8];
                 unpack8_e4m3(*reinterpret_cast<const uint2*>(xs.q + row * pitch + k0 + k), v);
                 const float size =
                     scale_of(xs.scales[row * scale_pitch + (k0 + k) / GS_SCALE_BLOCK]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[r][k + i] = v[i] * size;
+                for (int i = 0; i < 8; ++i) x[r][k + i] = k + i < depth ? v[i] * size : 0.f;
             }
         }
         __syncthreads();

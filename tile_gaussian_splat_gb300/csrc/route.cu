@@ -31,11 +31,12 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 // How many lanes share a row, accesses of kVec elements and accesses a lane; a
-// lane holds up to kSlots choices (a row alone four, 32 lanes' 64 together).
+// lane holds up to kSlots choices (32 lanes all that there can be).
 template <int kVec_, int kLanes_, int kItems_>
 struct Spread {
     static constexpr int kVec = kVec_, kLanes = kLanes_, kItems = kItems_;
-    static constexpr int kSlots = kLanes == 1 ? 4 : kLanes == 32 ? 2 : 1;
+    static constexpr int kSlots = kLanes == 1 ? 4 : 2;
+    static constexpr int kChoices = kLanes * kSlots;
 };
 
 // Logits as words in the order of the values: an addition of 0 makes both zeros
@@ -467,33 +468,40 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(RouteBwd a) {
     }
 }
 
-// Calls f with how rows of `experts` elements are spread.  A row to a thread
-// needs no exchange between lanes (forward, 921600 rows of 16 float32, two
-// choices: 37 us in all, 52 with four lanes a row); a row of few lanes holds at
-// most a choice a lane, more choices take a whole warp.
-template <typename T, int kVec, typename F>
+// Calls f with how rows of `experts` elements are spread: sixteen elements a lane
+// keep what is done once a row, and exchanged between lanes, small beside what is
+// done for each element, and many rows in flight.  Forward, 460800 rows of 32
+// float32 and 230400 of 64 bfloat16: 31 and 38 us, 49 and 47 with eight lanes; 921600
+// of 16 float32 in a thread each 33, in two lanes 33, in four 43.  The gradient's
+// rows are written too, which wants neighbours: two lanes at least (921600 of 16
+// float32: 31 us, a thread each 43; 900000 of 7 float16 18.5 and 22.6), single
+// elements eight a lane up to 64 (460800 of 31: 35.5 us, sixteen a lane 47).
+template <typename T, int kVec, bool kBackward, typename F>
 void with_spread(int experts, int topk, F&& f) {
-    const int n = (experts + kVec - 1) / kVec;
-    if constexpr (kVec > 1) {
-        if (topk <= 4 && experts <= 8) return f(Spread<kVec, 1, 8 / kVec>{});
-        if (topk <= 4 && experts <= 16) return f(Spread<kVec, 1, 16 / kVec>{});
-        if (topk <= 4 && n <= 4) return f(Spread<kVec, 4, 1>{});
-        if (topk <= 8 && n <= 8) return f(Spread<kVec, 8, 1>{});
-        if (topk <= 8 && n <= 16) return f(Spread<kVec, 8, 2>{});
-        if (n <= 32) return f(Spread<kVec, 32, 1>{});
-        if (n <= 64) return f(Spread<kVec, 32, 2>{});
-        if (n <= 128) return f(Spread<kVec, 32, 4>{});
-        if constexpr (kVec == 4) return f(Spread<4, 32, 8>{});
+    const auto fits = [&](auto spread, int most) {
+        return experts <= most && topk <= decltype(spread)::kChoices;
+    };
+    constexpr int k8 = 8 / kVec, k16 = 16 / kVec, k32 = 32 / kVec;
+    if constexpr (!kBackward) {
+        if (fits(Spread<kVec, 1, k8>{}, 8)) return f(Spread<kVec, 1, k8>{});
+        if (fits(Spread<kVec, 1, k16>{}, 16)) return f(Spread<kVec, 1, k16>{});
     } else {
-        if (topk <= 4 && n <= 8) return f(Spread<1, 1, 8>{});
-        if (topk <= 4 && n <= 16) return f(Spread<1, 1, 16>{});
-        if (topk <= 8 && n <= 32) return f(Spread<1, 8, 4>{});
-        if (topk <= 8 && n <= 64) return f(Spread<1, 8, 8>{});
-        if (n <= 128) return f(Spread<1, 32, 4>{});
-        if (n <= 256) return f(Spread<1, 32, 8>{});
-        if (n <= 512) return f(Spread<1, 32, 16>{});
-        return f(Spread<1, 32, 32>{});
+        if constexpr (kVec < 8)
+            if (fits(Spread<kVec, 2, 4 / kVec>{}, 8)) return f(Spread<kVec, 2, 4 / kVec>{});
+        if (fits(Spread<kVec, 2, k8>{}, 16)) return f(Spread<kVec, 2, k8>{});
     }
+    if constexpr (kBackward && kVec == 1) {
+        if (fits(Spread<1, 4, 8>{}, 32)) return f(Spread<1, 4, 8>{});
+        if (fits(Spread<1, 8, 8>{}, 64)) return f(Spread<1, 8, 8>{});
+    } else {
+        if (fits(Spread<kVec, 2, k16>{}, 32)) return f(Spread<kVec, 2, k16>{});
+        if (fits(Spread<kVec, 4, k16>{}, 64)) return f(Spread<kVec, 4, k16>{});
+    }
+    if (fits(Spread<kVec, 8, k16>{}, 128)) return f(Spread<kVec, 8, k16>{});
+    if (fits(Spread<kVec, 16, k16>{}, 256)) return f(Spread<kVec, 16, k16>{});
+    if (fits(Spread<kVec, 32, k8>{}, 256)) return f(Spread<kVec, 32, k8>{});
+    if (fits(Spread<kVec, 32, k16>{}, 512)) return f(Spread<kVec, 32, k16>{});
+    return f(Spread<kVec, 32, k32>{});
 }
 
 // Whole 16-byte vectors, or single elements.
@@ -567,7 +575,7 @@ void launch_route_fwd(const RouteArgs& n, const uint8_t* keep, int32_t* ids, flo
         };
         with_route_width<T>(row_bits<T>(n.logits, n.ld) | (uintptr_t)(n.experts * sizeof(T)),
                             [&](auto width) {
-                                with_spread<T, decltype(width)::value>(n.experts, n.topk, go);
+                                with_spread<T, decltype(width)::value, false>(n.experts, n.topk, go);
                             });
     });
 }
@@ -590,7 +598,7 @@ void launch_route_bwd(const RouteArgs& n, const int32_t* ids, const int32_t* cou
         with_route_width<T>(row_bits<T>(n.logits, n.ld) | row_bits<T>(grad, ldg) |
                                 (uintptr_t)(n.experts * sizeof(T)),
                             [&](auto width) {
-                                with_spread<T, decltype(width)::value>(n.experts, n.topk, go);
+                                with_spread<T, decltype(width)::value, true>(n.experts, n.topk, go);
                             });
     });
 }
