@@ -85,9 +85,10 @@ struct Product8Args {
 };
 
 struct Bars8 {
-    // of the first block: a slice of A or B, a buffer's words of powers are
-    // there (in all blocks), the accumulators may be overwritten
-    uint64_t full_a[4], full_b[4], words_full[kBuffers], acc_empty[kAccumulators];
+    // of the first block: a slice of B, and of A where it comes with it, a
+    // buffer's words of powers are there (in all blocks), the accumulators may
+    // be overwritten
+    uint64_t full[4], words_full[kBuffers], acc_empty[kAccumulators];
     // of each block: a slice may be overwritten, powers are in tensor memory,
     // a buffer of them may be overwritten, the accumulators are finished, a
     // tile's bias is there, and may be overwritten
@@ -223,12 +224,9 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
         tma_prefetch(&map_a);
         tma_prefetch(&map_b);
         if (g.vectors) tma_prefetch(&map_out);
-        for (int i = 0; i < S::kSlots; ++i) {
-            mbar_init(&bars.full_a[i], 1);
-            mbar_init(&bars.empty_a[i], 1);
-        }
+        for (int i = 0; i < S::kSlots; ++i) mbar_init(&bars.empty_a[i], 1);
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&bars.full_b[i], 1);
+            mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty_b[i], 1);
         }
         for (int i = 0; i < kBuffers; ++i) {
@@ -266,36 +264,28 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
     if (warp == 0) {
         Ring<S::kStages> at;
         Slots<S::kSlots> slots;
-        uint32_t loaded = 0;  // slices of A
         bool ok = true;
-        const auto bar = [&](uint64_t* b) { return kBlocks == 2 ? mbar_at(b, 0) : smem_u32(b); };
         while (ok && walk.next(c)) {
             const int n0 =
                 c.n0 + rank * (tile_columns<kBlocks, kWide>(g.width, c.n0) / kBlocks);
             for (int q = c.q0; q < c.q1; ++q, at.advance()) {
                 // a last slice of up to 128 channels is one box
                 const int boxes = g.depth - q * kDeep > kHalf ? 2 : 1;
-                if (c.first) {
-                    const uint32_t slot = slots.slot(q), turn = slots.turn(q);
-                    ok = turn == 0 || warp_wait(&bars.empty_a[slot], (turn + 1) & 1, abort);
-                    if (!ok) break;
-                    const uint32_t full = bar(&bars.full_a[slot]);
-                    if (elect_one()) {
-                        if (rank == 0)
-                            mbar_expect_tx(&bars.full_a[slot], boxes * S::kBytesA / 2 * kBlocks);
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d<kBlocks>(base + slot * S::kBytesA + i * S::kBytesA / 2,
-                                                 &map_a, q * kDeep + i * kHalf,
-                                                 c.row0 + rank * kHigh, full);
-                    }
-                    ++loaded;
-                }
-                ok = at.turn == 0 || warp_wait(&bars.empty_b[at.stage], (at.turn + 1) & 1, abort);
+                const uint32_t slot = slots.slot(q), turn = slots.turn(q);
+                if (c.first && turn > 0) ok = warp_wait(&bars.empty_a[slot], (turn + 1) & 1, abort);
+                if (ok && at.turn > 0)
+                    ok = warp_wait(&bars.empty_b[at.stage], (at.turn + 1) & 1, abort);
                 if (!ok) break;
-                const uint32_t full = bar(&bars.full_b[at.stage]);
+                const uint32_t full = kBlocks == 2 ? mbar_at(&bars.full[at.stage], 0)
+                                                   : smem_u32(&bars.full[at.stage]);
                 if (elect_one()) {
                     if (rank == 0)
-                        mbar_expect_tx(&bars.full_b[at.stage], boxes * S::kBytesB / 2 * kBlocks);
+                        mbar_expect_tx(&bars.full[at.stage],
+                                       boxes * kBlocks *
+                                           (S::kBytesB / 2 + (c.first ? S::kBytesA / 2 : 0)));
+                    for (int i = 0; i < boxes && c.first; ++i)
+                        tma_load_2d<kBlocks>(base + slot * S::kBytesA + i * S::kBytesA / 2, &map_a,
+                                             q * kDeep + i * kHalf, c.row0 + rank * kHigh, full);
                     for (int i = 0; i < boxes; ++i)
                         tma_load_3d<kBlocks>(base_b + at.stage * S::kBytesB + i * S::kBytesB / 2,
                                              &map_b, q * kDeep + i * kHalf, n0, c.expert, full);
@@ -304,16 +294,13 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
             }
             if (c.final && c.q1 == walk.count) slots.at += walk.count;
         }
-        if (!ok && rank == 0) {  // let the copies in flight land before the blocks go
-            int none = 0;
+        if (!ok && rank == 0)  // let the copies in flight land before the blocks go
             for (int i = 0; i < S::kStages; ++i) {
                 // stages [stage, ...) were last filled one turn ago
                 const uint32_t turn = i < (int)at.stage ? at.turn : at.turn - 1;
-                if (turn != ~0u) mbar_wait_limited(&bars.full_b[i], turn & 1, &none);
+                int none = 0;
+                if (turn != ~0u) mbar_wait_limited(&bars.full[i], turn & 1, &none);
             }
-            for (uint32_t i = loaded > S::kSlots ? loaded - S::kSlots : 0; i < loaded; ++i)
-                mbar_wait_limited(&bars.full_a[i % S::kSlots], i / S::kSlots & 1, &none);
-        }
     } else if (warp == 1) {
         constexpr uint32_t word0 = mma_word_e4m3(S::kTileHigh);
         const uint64_t from_a = smem_operand(base, 16, 1024);
@@ -336,9 +323,7 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
                     tmem_fence_after();
                 }
                 const uint32_t slot = slots.slot(q);
-                if (c.first) ok = warp_wait(&bars.full_a[slot], slots.turn(q) & 1, abort);
-                if (!ok) break;
-                ok = warp_wait(&bars.full_b[at.stage], at.turn & 1, abort);
+                ok = warp_wait(&bars.full[at.stage], at.turn & 1, abort);
                 if (!ok) break;
                 const uint64_t da = from_a + slot * (S::kBytesA >> 4);
                 const uint64_t db = from_b + at.stage * (S::kBytesB >> 4);
@@ -355,19 +340,18 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
                                       from, from + kPowersB, q > c.q0 || j > 0);
                 };
                 const int steps = (g.depth - q * kDeep + 31) / 32;
-                if (steps >= kDeep / 32) {
-                    if (elect_one()) {
+                if (elect_one()) {
+                    if (steps >= kDeep / 32) {
 #pragma unroll
                         for (int j = 0; j < kDeep / 32; ++j) product(j);
-                        mma_commit<kBlocks>(&bars.empty_b[at.stage]);
+                    } else {
+                        for (int j = 0; j < steps; ++j) product(j);
                     }
-                } else if (elect_one()) {
-                    for (int j = 0; j < steps; ++j) product(j);
                     mma_commit<kBlocks>(&bars.empty_b[at.stage]);
+                    if (c.final) mma_commit<kBlocks>(&bars.empty_a[slot]);
+                    if (last) mma_commit<kBlocks>(&bars.powers_empty[buffer.stage]);
+                    if (q + 1 == c.q1) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
                 }
-                if (c.final && elect_one()) mma_commit<kBlocks>(&bars.empty_a[slot]);
-                if (last && elect_one()) mma_commit<kBlocks>(&bars.powers_empty[buffer.stage]);
-                if (q + 1 == c.q1 && elect_one()) mma_commit<kBlocks>(&bars.acc_full[acc.stage]);
                 __syncwarp();
                 if (last) buffer.advance();
             }

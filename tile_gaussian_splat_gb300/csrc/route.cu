@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
     float* sums = reinterpret_cast<float*>(shared + a.experts + 1);   // kWarps x experts
     const bool tally = a.counts;
     const int at = threadIdx.x % kLanes;
+    cudaTriggerProgrammaticLaunchCompletion();  // k_route_sum may come up, and wait
     if (tally) {
         if (blockIdx.x == 0 && threadIdx.x == 0 && gridDim.x > 1) *a.ticket = 0;
         for (int e = threadIdx.x; e <= a.experts; e += kThreads) count[e] = 0;
@@ -128,16 +129,26 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
     float sum[kItems][kVec] = {};
     int taking = 0;
     const int64_t step = (int64_t)gridDim.x * kGroups;
-    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step) {
-        const int64_t r = r0 + threadIdx.x / kLanes;
-        const bool keep = r < a.tokens && (!a.keep || a.keep[r]);
+    // the next row comes in while this one is worked on
+    RawVec<T, kVec> ahead[kItems];
+    bool keep_ahead;
+    const auto load = [&](int64_t r) {
+        keep_ahead = r < a.tokens && (!a.keep || a.keep[r]);
         const T* x = static_cast<const T*>(a.logits) + r * a.ld + at * kVec;
-        RawVec<T, kVec> raw[kItems];
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
-            raw[i] = keep && (i * kLanes + at) * kVec < a.experts
-                         ? load_raw<T, kVec>(x + i * kLanes * kVec)
-                         : RawVec<T, kVec>{};
+            ahead[i] = keep_ahead && (i * kLanes + at) * kVec < a.experts
+                           ? load_raw<T, kVec>(x + i * kLanes * kVec)
+                           : RawVec<T, kVec>{};
+    };
+    load((int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes);
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step) {
+        const int64_t r = r0 + threadIdx.x / kLanes;
+        const bool keep = keep_ahead;
+        RawVec<T, kVec> raw[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) raw[i] = ahead[i];
+        load(r + step);
         uint32_t key[kItems][kVec];
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
@@ -276,7 +287,8 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(RouteFwd a) {
 }
 
 // The blocks' sums and counts added up, eight columns a block and 128 threads
-// a column; the last block to finish then has the loss.
+// a column; the last block to finish then has the loss.  Launched while the
+// blocks are still at work, so that it is there when they end (2 us).
 constexpr int kSumThreads = 1024, kSumColumns = 8;
 
 __global__ void __launch_bounds__(kSumThreads) k_route_sum(RouteFwd a, int blocks) {
@@ -286,6 +298,7 @@ __global__ void __launch_bounds__(kSumThreads) k_route_sum(RouteFwd a, int block
     __shared__ bool last;
     const int c = threadIdx.x % kSumColumns, g = threadIdx.x / kSumColumns;
     const int column = blockIdx.x * kSumColumns + c, columns = a.experts + 1;
+    cudaGridDependencySynchronize();
     float sum = 0.f;
     int32_t count = 0;
     if (column < columns) {
@@ -369,31 +382,45 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(RouteBwd a) {
             for (int j = 0; j < kVec; ++j) h[i][j] *= scale;
     }
     const int64_t step = (int64_t)gridDim.x * kGroups;
+    // the next row and its choices come in while this one is worked on
+    RawVec<T, kVec> ahead[kItems];
+    int id_ahead[kSlots];
+    float g_ahead[kSlots];
+    const auto load = [&](int64_t r) {
+        const T* x = static_cast<const T*>(a.logits) + r * a.ld + at * kVec;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+            ahead[i] = r < a.tokens && (i * kLanes + at) * kVec < a.experts
+                           ? load_raw<T, kVec>(x + i * kLanes * kVec)
+                           : RawVec<T, kVec>{};
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            const int round = s * kLanes + at;
+            const bool in = r < a.tokens && round < a.topk;
+            id_ahead[s] = in ? a.ids[r * a.topk + round] : -1;
+            g_ahead[s] = in && a.grad_weights ? a.grad_weights[r * a.topk + round] : 0.f;
+        }
+    };
+    load((int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes);
     for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.tokens; r0 += step) {
         const int64_t r = r0 + threadIdx.x / kLanes;
         const T* row = static_cast<const T*>(a.logits) + r * a.ld;
         RawVec<T, kVec> raw[kItems];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i)
-            raw[i] = r < a.tokens && (i * kLanes + at) * kVec < a.experts
-                         ? load_raw<T, kVec>(row + (i * kLanes + at) * kVec)
-                         : RawVec<T, kVec>{};
+        for (int i = 0; i < kItems; ++i) raw[i] = ahead[i];
         int id[kSlots];
         float g[kSlots], e[kSlots];
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            const int round = s * kLanes + at;
-            id[s] = -1;
-            g[s] = e[s] = 0.f;
-            if (r < a.tokens && round < a.topk) {
-                id[s] = a.ids[r * a.topk + round];
-                if (id[s] < -1 || id[s] >= a.experts) {
-                    GS_BOUNDS_REPORT(a.d_status);
-                    id[s] = -1;
-                }
-                if (a.grad_weights && id[s] >= 0) g[s] = a.grad_weights[r * a.topk + round];
+            id[s] = id_ahead[s];
+            if (id[s] < -1 || id[s] >= a.experts) {
+                GS_BOUNDS_REPORT(a.d_status);
+                id[s] = -1;
             }
+            g[s] = id[s] >= 0 ? g_ahead[s] : 0.f;
+            e[s] = 0.f;
         }
+        load(r + step);
         // the first choice tells whether the row takes part
         const bool take = __shfl_sync(kAll, id[0], 0, kLanes) >= 0;
         float p[kItems][kVec];
@@ -569,9 +596,18 @@ void launch_route_fwd(const RouteArgs& n, const uint8_t* keep, int32_t* ids, flo
                 a.part_counts = reinterpret_cast<int32_t*>(a.partial + align_words(blocks * columns));
             }
             kernel<<<blocks, kThreads, smem(n.experts), s>>>(a);
-            if (counts && blocks > 1)
-                k_route_sum<<<(unsigned)((columns + kSumColumns - 1) / kSumColumns), kSumThreads, 0,
-                              s>>>(a, blocks);
+            if (counts && blocks > 1) {
+                cudaLaunchConfig_t config = {};
+                config.gridDim = dim3((unsigned)((columns + kSumColumns - 1) / kSumColumns));
+                config.blockDim = dim3(kSumThreads);
+                config.stream = s;
+                cudaLaunchAttribute early = {};
+                early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+                early.val.programmaticStreamSerializationAllowed = 1;
+                config.attrs = &early;
+                config.numAttrs = 1;
+                (void)cudaLaunchKernelEx(&config, k_route_sum, a, blocks);
+            }
         };
         with_route_width<T>(row_bits<T>(n.logits, n.ld) | (uintptr_t)(n.experts * sizeof(T)),
                             [&](auto width) {
