@@ -860,8 +860,9 @@ def _widths8(channels):
 def _rows8(q, scales, channels, what):
     """(pointer to q, pointer to scales) of 8-bit rows of `channels`."""
     wide, blocks = _widths8(channels)
-    if q.dtype != _Q8 or scales.dtype != _S8 or q.dim() == 0 or q.shape[-1] != wide or \
-            scales.shape != (*q.shape[:-1], blocks):
+    shape = q.shape
+    if q.dtype is not _Q8 or scales.dtype is not _S8 or not shape or shape[-1] != wide or \
+            scales.shape != shape[:-1] + (blocks,):
         _refuse(f"{what}: float8_e4m3fn (..., {wide}) and float8_e8m0fnu (..., {blocks}) expected")
     return _ptr(q), _ptr(scales)
 
@@ -898,9 +899,10 @@ def gs_rows_unpack8(q, scales, channels, dtype=torch.bfloat16, out=None, stream=
 
 def _linear8_shapes(xs, offsets, weight, channels):
     E = _experts(offsets)
-    if weight.dim() != 3 or weight.shape[0] != E or xs.dim() != 2 or channels < 1:
+    w, x = weight.shape, xs.shape
+    if len(w) != 3 or w[0] != E or len(x) != 2 or channels < 1:
         _refuse("xs (rows, ...) and weight (experts, out_features, ...) expected")
-    return xs.shape[0], E, weight.shape[1]
+    return x[0], E, w[1]
 
 
 def gs_expert_linear8_fwd(xs, xs_scales, offsets, weight, weight_scales, in_features, bias=None,

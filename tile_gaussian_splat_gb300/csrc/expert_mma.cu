@@ -619,6 +619,13 @@ __global__ void __launch_bounds__(256)
         while (share_begin(total, g.groups, s + 1) <= pos) ++s;
         return s;
     };
+    // shares without a slice there are only where there are more shares than
+    // slices (asked of every share for every sum, two 64-bit divisions each took
+    // as long as the sums)
+    const bool gaps = total < g.groups;
+    const auto empty = [&](int s) {
+        return gaps && share_begin(total, g.groups, s) == share_begin(total, g.groups, s + 1);
+    };
     // an expert's part in share s, of the shares s0 .. that it lies in
     const auto slot = [&](int s, int s0, int tile) {
         return ((int64_t)s * tiles + tile) * 2 + (s == s0 ? 1 : 0);
@@ -646,8 +653,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     v[k] = float4{0.f, 0.f, 0.f, 0.f};
-                    if (s + k <= s1 && share_begin(total, g.groups, s + k) <
-                                           share_begin(total, g.groups, s + k + 1))
+                    if (s + k <= s1 && !empty(s + k))
                         v[k] = *reinterpret_cast<const float4*>(
                             g.partial + (slot(s + k, s0, tile) * S::kTileHigh +
                                          block % kSlabs * kSlab + row) * kWide + col);
@@ -680,7 +686,7 @@ __global__ void __launch_bounds__(256)
         const int s0 = share_of(prefix[e]), s1 = share_of((int64_t)prefix[e + 1] - 1);
         const int row = m % S::kTileHigh, tile0 = m / S::kTileHigh * across;
         for (int s = s0; s <= s1; ++s) {
-            if (share_begin(total, g.groups, s) == share_begin(total, g.groups, s + 1)) continue;
+            if (empty(s)) continue;
             for (int n = tile0; n < tile0 + across; ++n) {
                 const int64_t at = s0 == s1 ? 2 * (int64_t)g.groups * tiles + e * tiles + n
                                             : slot(s, s0, n);
