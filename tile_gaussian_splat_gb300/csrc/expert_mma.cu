@@ -1076,13 +1076,16 @@ constexpr int plane_dtype(int dtype) { return dtype == GS_F16 ? GS_F16 : GS_BF16
 
 size_t unpacked_bytes(int64_t rows, int columns) { return plane_bytes(GS_BF16, rows, columns); }
 
-Planes unpacked(int dtype, Rows8 x, int64_t rows, int columns, char** workspace, cudaStream_t s) {
+// offsets: x are weights, of which only experts that have rows are needed.
+Planes unpacked(int dtype, Rows8 x, int64_t rows, int columns, const int32_t* offsets, int experts,
+                char** workspace, cudaStream_t s) {
     // the zeros behind the last column too, up to whole vectors: they lie in
     // the same block and row of 16 bytes
     const int pitch = (int)ceil_div(columns, 8) * 8;
     void* out = *workspace;
     *workspace += unpacked_bytes(rows, columns);
-    launch_unpack8(x.q, x.scales, rows, pitch, dtype, out, pitch, s);
+    launch_unpack8(x.q, x.scales, offsets ? rows / experts : rows, pitch, dtype, out, pitch, s,
+                   offsets, experts);
     return Planes{out, rows, columns, pitch, 1};
 }
 
@@ -1104,7 +1107,8 @@ int launch_linear8_bwd(const LinearArgs& a, const void* grad_ys, Rows8 xs, Rows8
     const Planes gy = prepare(a.dtype, grad_ys, a.rows, a.out, &ws, s);
     if (grad_xs) {
         const bool pairs = use_pairs(a, a.in);
-        const Planes w = unpacked(planes, weight, (int64_t)a.experts * a.out, a.in, &ws, s);
+        const Planes w = unpacked(planes, weight, (int64_t)a.experts * a.out, a.in, a.offsets,
+                                  a.experts, &ws, s);
         CUtensorMap ma, mb;
         if (!make_map(&ma, planes, gy, 0, kHigh) || !make_map(&mb, planes, w, a.experts, kSlice))
             return GS_ERR_CUDA;
@@ -1115,7 +1119,7 @@ int launch_linear8_bwd(const LinearArgs& a, const void* grad_ys, Rows8 xs, Rows8
         if (rc != GS_OK) return rc;
     }
     if (!grad_weight) return GS_OK;
-    const Planes x = unpacked(planes, xs, a.rows, a.in, &ws, s);
+    const Planes x = unpacked(planes, xs, a.rows, a.in, nullptr, 0, &ws, s);
     return launch_grad_of_weight(a, planes, gy, x, grad_weight, grad_bias, sums, s);
 }
 

@@ -65,8 +65,11 @@ void launch_route_bwd(const RouteArgs& a, const int32_t* ids, const int32_t* cou
 // ---- rows8.cu: rows of GS_ROW8_BYTES and scales of GS_ROW8_SCALES bytes
 void launch_pack8(const void* x, int64_t ldx, int64_t rows, int channels, int dtype, uint8_t* q,
                   uint8_t* scales, cudaStream_t s);
+// With offsets: `rows` rows for each of the experts, of which those without rows
+// of their own are left out (y aligned and its rows whole 16-byte vectors).
 void launch_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int channels,
-                    int dtype, void* y, int64_t ldy, cudaStream_t s);
+                    int dtype, void* y, int64_t ldy, cudaStream_t s,
+                    const int32_t* offsets = nullptr, int experts = 0);
 
 // ---- the experts' products; the launchers of expert_mma.cu return a gs_status
 struct LinearArgs {

@@ -234,6 +234,7 @@ struct Unpack8 {
     void* y;
     int64_t ldy, rows;
     int channels, blocks, pitch, scale_pitch;
+    const int32_t* used;  // or null: `rows` rows for every expert, those with rows of x
 };
 
 // The largest byte whose block's values, up to 448 * 2^(byte - 127), T holds.
@@ -265,6 +266,14 @@ __global__ void __launch_bounds__(kThreads8) k_unpack8(Unpack8 a) {
     constexpr int kVec = 16 / (int)sizeof(T);
     const int at = threadIdx.x % kLanes * kEach;
     const int64_t step = (int64_t)gridDim.x * kGroups;
+    if (a.used) {
+        // an expert without rows is not looked at; offsets that fall or lie
+        // outside are cut where they are used, which leaves no more of them
+        if (a.used[blockIdx.y + 1] <= a.used[blockIdx.y]) return;
+        a.q += blockIdx.y * a.rows * a.pitch;
+        a.scales += blockIdx.y * a.rows * a.scale_pitch;
+        a.y = static_cast<T*>(a.y) + blockIdx.y * a.rows * a.ldy;
+    }
     Place load((int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes, step, a.blocks), p = load;
     while (p.row < a.rows) {
         uint2 q[S::kAhead][kItems];
@@ -391,10 +400,11 @@ void launch_pack8(const void* x, int64_t ldx, int64_t rows, int channels, int dt
 }
 
 void launch_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int channels,
-                    int dtype, void* y, int64_t ldy, cudaStream_t s) {
+                    int dtype, void* y, int64_t ldy, cudaStream_t s, const int32_t* offsets,
+                    int experts) {
     const int blocks = (channels + GS_SCALE_BLOCK - 1) / GS_SCALE_BLOCK;
     const Unpack8 a{q, scales, y, ldy, rows, channels, blocks, GS_ROW8_BYTES(channels),
-                    GS_ROW8_SCALES(channels)};
+                    GS_ROW8_SCALES(channels), offsets};
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         if (!rows_aligned<T>(y, ldy) || channels * sizeof(T) % 16 != 0) {
@@ -409,7 +419,11 @@ void launch_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int c
             using S = decltype(share);
             static PerDevice resident;
             const auto kernel = k_unpack8<T, S>;
-            kernel<<<blocks8(resident, kernel, rows * blocks, S::kLanes), kThreads8, 0, s>>>(a);
+            const int all = blocks8(resident, kernel, rows * blocks, S::kLanes);
+            // which experts have rows is not known here: each has the blocks for
+            // its part, at least some where few have any
+            const int each = offsets ? std::min(all, std::max(all / experts, 32)) : all;
+            kernel<<<dim3(each, offsets ? experts : 1), kThreads8, 0, s>>>(a);
         });
     });
 }
