@@ -193,6 +193,32 @@ def test_long_sums_of_one_sign(rows):
     assert float(((ys - ref) / ref).abs().max()) <= 2e-5
 
 
+def test_offsets_beyond_32_bits():
+    rows, i, o = 2 ** 21 + 700, 1040, 1032  # 2.18e9 elements in and 2.16e9 out
+    last = 150
+    offsets = torch.tensor([0, 1000, rows - last, rows], dtype=torch.int32, device=DEV)
+    g = gen(40)
+    x = torch.zeros((rows, i), dtype=torch.bfloat16, device=DEV)
+    x[:9], x[-last:] = randn(g, 9, i).bfloat16(), randn(g, last, i).bfloat16()
+    xq, xs = gs.gs_rows_pack8(x)
+    del x
+    wq, ws = (t.reshape(3, o, -1) for t in gs.gs_rows_pack8(randn(g, 3 * o, i) / i ** 0.5))
+    ys = gs.gs_expert_linear8_fwd(xq, xs, offsets, wq, ws, i)
+    xv, wv = values_ref(xq[-last:], xs[-last:], i), values_ref(wq, ws, i)
+    tail = torch.tensor([0, 0, 0, last], dtype=torch.int32, device=DEV)
+    ref, slack = linear_ref(xv, tail, wv, None)
+    check(ys[-last:], ref, slack, "ys")
+    assert not bool(ys[9:1000].any()) and not bool(ys[2 ** 20:2 ** 20 + 1000].any())
+    gys = ys.zero_()
+    gys[-last:] = randn(g, last, o, dtype=torch.bfloat16)
+    gx, gw, gb = gs.gs_expert_linear8_bwd(gys, xq, xs, offsets, wq, ws, i)
+    refs, slacks = linear_bwd_ref(gys[-last:], xv, tail, wv)
+    check(gx[-last:], refs[0], slacks[0], "grad_xs")
+    check(gw, refs[1], slacks[1], "grad_weight")
+    check(gb, refs[2], slacks[2], "grad_bias")
+    assert not bool(gx[:1000].any()) and not bool(gx[2 ** 20:2 ** 20 + 1000].any())
+
+
 def test_no_rows():
     p = _packed(7, 4, 3, 32, 40, 4)
     offsets = torch.zeros(4, dtype=torch.int32, device=DEV)

@@ -133,6 +133,20 @@ def test_nan_and_infinity_stay_in_their_row():
     assert bool(torch.isfinite(grad[others]).all()) and bool(torch.isnan(grad[4]).all())
 
 
+@pytest.mark.parametrize("dtype,bits", [(torch.float32, -0x400000), (torch.float16, -0x200),
+                                        (torch.bfloat16, -0x40)])
+@pytest.mark.parametrize("experts", [8, 12, 33, 200])
+def test_a_nan_comes_first_whatever_its_sign(experts, dtype, bits):
+    logits = randn(gen(experts), 9, experts, dtype=dtype)
+    raw = logits.view({4: torch.int32, 2: torch.int16}[dtype.itemsize])
+    raw[2, 5] = bits  # a NaN with its sign bit set
+    logits[3, 1] = float("inf")
+    logits[3, 6], logits[3, 2] = float("nan"), float("nan")
+    assert bool(torch.isnan(logits[2, 5]))
+    ids = gs.gs_expert_route_fwd(logits, 3)[0]
+    assert int(ids[2, 0]) == 5 and ids[3].tolist() == [2, 6, 1]
+
+
 def test_no_tokens():
     logits = torch.empty((0, 8), device=DEV)
     ids, weights, counts, loss = gs.gs_expert_route_fwd(logits, 2)
@@ -242,6 +256,12 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(ids[-5:], r[0])
     check(weights[-5:], r[1], r[2], "weights")
     assert bool((ids[:-5] == torch.tensor([0, 1], device=DEV)).all())
+    gw = randn(gen(15), T, 2)
+    out = torch.full_like(wide, 3.0)
+    grad = gs.gs_expert_route_bwd(logits, ids, None, gw, out=out[:, 3:11])
+    ref, slack = route_bwd_ref(logits[-5:], ids[-5:], None, gw[-5:], None, True)
+    check(grad[-5:], ref, slack, "grad_logits")
+    assert bool((out[:, :3] == 3).all()) and bool((out[:, 11:] == 3).all())
 
 
 def test_refusals():

@@ -19,7 +19,7 @@
 // other accumulators.  Those leave no room for the powers beside 256 columns
 // each, so tiles are 192 columns wide.
 //
-// 262144 rows, 16 experts, 512 -> 1024, bfloat16 out: 140 us (1960 TFLOP/s, 4.9
+// 262144 rows, 16 experts, 512 -> 1024, bfloat16 out: 137 us (2010 TFLOP/s, 5.0
 // TB/s; the bytes alone take 100 us); 65536 rows 1024 -> 1024, float16 out: 68 us
 // (2010 TFLOP/s).  Nothing is saturated (tensor pipe 46 %, memory 59 %, shared
 // memory below 50 %): without the output the first takes 105 us, without the
@@ -30,7 +30,8 @@
 // warps 218 us; with the bias read ahead and arrivals that do not wait for the
 // writes to global memory 157 (a release at cluster scope, one a tile, cost 35 us
 // for the bias and 35 for the powers); slices of 256 channels, A kept, boxes, no
-// division a tile 147; a third slice of A 140.  Not kept: whole 32-byte sectors
+// division a tile 147; a third slice of A 140; its slices on the barrier of B's 137.
+// Not kept: whole 32-byte sectors
 // stored from registers (178 against 159 at that step), prefetches of the next
 // piece's A into the L2 (155 against 147).  Two warps that issue in turn are
 // unsound as long as each waits only for its own tiles' slices: a barrier's

@@ -11,10 +11,10 @@
 // it: each lane keeps its logits as unsigned words in the order of the values, 0
 // where there is nothing to choose.
 //
-// 921600 rows of 16 float32, two choices: 28 us and 5 for the sums (floor 10; four
-// lanes a row 66 us, with IEEE divisions and expf 43), 22 without the balance.
-// Gradient, 131072 rows of 64 bfloat16, four choices: 16.4 us (floor 5.5; 20 with
-// IEEE divisions and expf).  100003 rows of 7 float16 of 9: 9 us.
+// 921600 rows of 16 float32, two choices: 27 us (floor 10; without the next row on
+// its way 33, with IEEE divisions and expf 49, with four lanes a row 66).  Gradient,
+// the same rows: 27 us (floor 19); 230400 of 64 bfloat16, four choices 20.5 us (floor
+// 9.7), forward 35.
 #include <algorithm>
 #include <cstdint>
 
