@@ -207,6 +207,20 @@ def test_gradient_against_differences():
         assert abs(diff - want) <= 2e-3 * float(grad.norm() * v.norm())
 
 
+@pytest.mark.parametrize("experts,topk", [(8, 2), (40, 4), (300, 12)])
+def test_gradients_that_have_most_in_common(experts, topk):
+    """Renormalised weights sum to one, so an offset of all their gradients
+    drops out: 1000 beside differences of 1 costs the rounding of the
+    differences (2^-24 of 1000 each) and not that of sums of 1000."""
+    g = gen(experts)
+    logits = randn(g, 200, experts)
+    ids = gs.gs_expert_route_fwd(logits, topk)[0]
+    gw = 1000 + randn(g, 200, topk)
+    grad = gs.gs_expert_route_bwd(logits, ids, None, gw)
+    ref, slack = route_bwd_ref(logits, ids, None, gw - gw[:, :1], None, True)
+    check(grad, ref, slack, "grad_logits")
+
+
 def test_many_tokens_repeat_and_other_streams():
     g = gen(12)
     logits = randn(g, 300001, 16)

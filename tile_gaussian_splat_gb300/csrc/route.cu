@@ -423,6 +423,13 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(RouteBwd a) {
         load(r + step);
         // the first choice tells whether the row takes part
         const bool take = __shfl_sync(kAll, id[0], 0, kLanes) >= 0;
+        // renormalised weights sum to one: what all gradients have in common
+        // drops out, and before it is multiplied loses nothing of the rest
+        if (a.renormalise) {
+            const float common = __shfl_sync(kAll, g[0], 0, kLanes);
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) g[s] = id[s] >= 0 ? g[s] - common : 0.f;
+        }
         float p[kItems][kVec];
         float top = -INFINITY;
 #pragma unroll
