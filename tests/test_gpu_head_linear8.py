@@ -21,7 +21,7 @@ SHAPES = [(1, 1, 1, 1, 1), (1, 2, 8, 256, 1024), (3, 2, 4, 16, 16), (8, 2, 3, 13
           (2000, 1, 1, 1030, 260), (4000, 2, 6, 259, 131), (129, 1, 1, 2048, 64),
           (20000, 2, 4, 300, 200), (6000, 2, 16, 128, 1000), (1300, 1, 2, 4200, 9000),
           (30000, 1, 300, 128, 256), (9000, 1, 3, 700, 800), (8000, 1, 2, 512, 520),
-          (12000, 1, 900, 1100, 200)]
+          (12000, 1, 900, 1100, 200), (700, 2, 3, 202, 130), (20000, 2, 2, 66, 250)]
 
 
 def _packed(seed, rows, E, i, o, kept):

@@ -91,7 +91,7 @@ struct ProductArgs {
     int pairs;               // sums over plane pairs: 1, for float32 6 (3 with 8-bit rows)
     int round;               // slices summed before they are added to the running sum
     int rounds;              // some sums take several rounds
-    int vectors;             // output rows are whole 16-byte vectors
+    int access;              // bytes at which the output's rows can be written
     const void* bias;        // kForward
     void* out;
     void* bias_grad;         // kWeightGrad, or null
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                         for (int i = 0; i < 4; ++i)
                             v[i] = uint4{w[16 * h + 4 * i], w[16 * h + 4 * i + 1],
                                          w[16 * h + 4 * i + 2], w[16 * h + 4 * i + 3]};
-                        write_block<float>(mine, v, part + n + 16 * h, kWide, rows, 16, true);
+                        write_block<float>(mine, v, part + n + 16 * h, kWide, rows, 16, 16);
                     }
                 } else if (left > 0) {
                     constexpr int kRow = 64 / (int)sizeof(Out);  // columns written at a time
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                             pack8<Out>(f, v + i * (int)sizeof(Out) / 2);
                         }
                         write_block<Out>(mine, v, out + n + kRow * h, g.width, rows,
-                                         left - kRow * h, g.vectors);
+                                         left - kRow * h, g.access);
                     }
                 }
                 tmem_wait_loads();
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(256)
             Out* out = static_cast<Out*>(g.out) + ((int64_t)e * g.high + m0 + row) * g.width +
                        n0 + col;
             const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-            if (g.vectors) {
+            if (g.access >= 4 * (int)sizeof(Out)) {
                 store_vec<Out, 4>(out, v);
             } else {
                 for (int j = 0; j < min(4, g.width - n0 - col); ++j) out[j] = from_f<Out>(v[j]);
@@ -948,7 +948,8 @@ ProductArgs product_args(const LinearArgs& a, void* out, int width, int depth) {
     g.pairs = plane_pairs(a);
     g.round = a.dtype == GS_F32 ? kRound : kHalfRound;
     g.rounds = ceil_div(depth, kSlice) > g.round;
-    g.vectors = aligned16(out) && (size_t)width * dtype_size(a.dtype) % 16 == 0;
+    const int size = (int)dtype_size(a.dtype);
+    g.access = access_bytes(out, (size_t)width * size, size);
     g.out = out;
     g.d_status = a.d_status;
     return g;

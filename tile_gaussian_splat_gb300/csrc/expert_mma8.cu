@@ -79,7 +79,7 @@ struct Product8Args {
     int64_t rows;
     int experts, width, depth, words;
     int rounds;   // sums take several rounds
-    int vectors;  // output rows are whole 16-byte vectors
+    int access;   // bytes at which the output's rows can be written
     const void* bias;
     void* out;
     int32_t* d_status;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
     if (warp == 0 && lane == 0) {
         tma_prefetch(&map_a);
         tma_prefetch(&map_b);
-        if (g.vectors) tma_prefetch(&map_out);
+        if (g.access == 16) tma_prefetch(&map_out);
         for (int i = 0; i < S::kSlots; ++i) mbar_init(&bars.empty_a[i], 1);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&bars.full[i], 1);
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
             if (lane == 0) mbar_arrive_at(&bars.acc_empty[acc.stage], 0);
             const int left = g.width - c.n0 - first;  // columns from here on
             // whole rows of whole vectors go out as boxes
-            const bool boxed = g.vectors && rows >= 32;
+            const bool boxed = g.access == 16 && rows >= 32;
             const auto write = [&](auto biased) {
 #pragma unroll
                 for (int b = 0; b < kSpan / kRow; ++b) {
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
                                          c.row0 + row);
                     } else {
                         write_block<Out>(mine, v, out + b * kRow, g.width, rows, left - b * kRow,
-                                         g.vectors);
+                                         g.access);
                     }
                 }
             };
@@ -606,7 +606,7 @@ template <typename Out, typename S>
 int launch_shape(const LinearArgs& a, Rows8 xs, Rows8 weight, const Product8Args& g,
                  cudaStream_t s) {
     CUtensorMap ma, mb, mo{};
-    if (g.vectors && !make_out_map(&mo, a.dtype, g.out, a.rows, a.out))
+    if (g.access == 16 && !make_out_map(&mo, a.dtype, g.out, a.rows, a.out))
         return GS_ERR_CUDA;
     if (!make_map8(&ma, xs.q, a.rows, a.in, 0, kHigh) ||
         !make_map8(&mb, weight.q, a.out, a.in, a.experts, S::kPartB))
@@ -637,7 +637,8 @@ int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* 
     g.depth = a.in;
     g.words = GS_ROW8_SCALES(a.in) / 4;
     g.rounds = ceil_div(a.in, kDeep) > kRound;
-    g.vectors = aligned16(ys) && (size_t)a.out * dtype_size(a.dtype) % 16 == 0;
+    const int size = (int)dtype_size(a.dtype);
+    g.access = access_bytes(ys, (size_t)a.out * size, size);
     g.bias = bias;
     g.out = ys;
     g.d_status = a.d_status;

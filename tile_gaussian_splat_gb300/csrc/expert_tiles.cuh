@@ -64,44 +64,59 @@ __device__ __forceinline__ void pack8(const float* f, uint4* v) {
     }
 }
 
+// 32 rows x 64 bytes of output from shared memory (write_block's order), a Word an
+// access, several on their way at once (one after the other, 64 odd float32
+// columns of a tile took 5000 cycles).
+template <typename Word>
+__device__ __forceinline__ void write_words(const char* staging, char* out, int64_t pitch_bytes,
+                                            int valid_rows, int left_bytes) {
+    constexpr int kWords = 64 / (int)sizeof(Word), kStep = 32 / kWords;
+    const int lane = threadIdx.x & 31;
+    const int byte = lane % kWords * (int)sizeof(Word), j = byte / 16;
+#pragma unroll 8
+    for (int i = 0; i < 32 / kStep; ++i) {
+        const int r = i * kStep + lane / kWords;
+        const Word x = *reinterpret_cast<const Word*>(
+            staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4) + byte % 16);
+        if (r < valid_rows && byte < left_bytes)
+            *reinterpret_cast<Word*>(out + r * pitch_bytes + byte) = x;
+    }
+}
+
+// The widest access of up to 16 bytes, and not below an element, for rows of
+// `bytes` bytes on end from p on.
+inline int access_bytes(const void* p, size_t bytes, int element) {
+    int access = 16;
+    while (access > element && (reinterpret_cast<uintptr_t>(p) | bytes) % access) access /= 2;
+    return access;
+}
+
 // 32 rows x 64 bytes of output held one row a lane (four 16-byte vectors),
-// turned through shared memory so that four lanes write one row's 64
-// contiguous bytes (or, where rows of the output are not whole vectors, single
-// elements).  valid_rows of the rows and `left` of a row's elements are inside
-// the output.
+// turned through shared memory so that neighbouring lanes write a row's 64
+// contiguous bytes, `access` bytes each (16 down to an element: 60000 rows of 8-bit
+// products, 512 -> 1004, 1002 and 1001 bfloat16, 50, 68 and 84 us, 90 an element
+// each).  valid_rows of the rows and `left` of a row's elements are inside the
+// output.
 template <typename Out>
 __device__ __forceinline__ void write_block(char* staging, const uint4* v, Out* out,
                                             int64_t pitch, int valid_rows, int left,
-                                            bool vectors) {
+                                            int access) {
     const int lane = threadIdx.x & 31;
-    constexpr int kVec = 16 / sizeof(Out), kRow = 64 / sizeof(Out);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         *reinterpret_cast<uint4*>(staging + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = v[j];
     __syncwarp();
-    if (vectors) {
-        const int j = lane & 3;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + lane / 4;
-            const uint4 x =
-                *reinterpret_cast<const uint4*>(staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4));
-            if (r < valid_rows && j * kVec < left)
-                *reinterpret_cast<uint4*>(out + r * pitch + j * kVec) = x;
-        }
-    } else {
-        // several elements on their way at once (one after the other, 64 odd
-        // float32 columns of a tile took 5000 cycles)
-        const int e = lane % kRow, j = e / kVec;
-        constexpr int kStep = 32 / kRow;
-#pragma unroll 8
-        for (int i = 0; i < 32 / kStep; ++i) {
-            const int r = i * kStep + lane / kRow;
-            const Out x = *reinterpret_cast<const Out*>(
-                staging + r * 64 + ((j ^ (r >> 1 & 3)) << 4) + e % kVec * sizeof(Out));
-            if (r < valid_rows && e < left) out[r * pitch + e] = x;
-        }
-    }
+    char* to = reinterpret_cast<char*>(out);
+    const int64_t pitch_bytes = pitch * (int)sizeof(Out);
+    const int left_bytes = left * (int)sizeof(Out);
+    if (access == 16)
+        write_words<uint4>(staging, to, pitch_bytes, valid_rows, left_bytes);
+    else if (access == 8)
+        write_words<uint2>(staging, to, pitch_bytes, valid_rows, left_bytes);
+    else if (access == 4)
+        write_words<uint32_t>(staging, to, pitch_bytes, valid_rows, left_bytes);
+    else if constexpr (sizeof(Out) == 2)
+        write_words<uint16_t>(staging, to, pitch_bytes, valid_rows, left_bytes);
     __syncwarp();
 }
 
