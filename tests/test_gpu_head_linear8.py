@@ -113,6 +113,23 @@ def test_scales_far_apart():
 
 
 @pytest.mark.parametrize("rows", [5, 700])
+def test_values_at_the_end_of_float32(rows):
+    """float32's largest value is kept as 2^128; times small weights it is finite."""
+    g = gen(50)
+    x, w = randn(g, rows, 200), randn(g, 96, 200) * 2.0 ** -30
+    x[1, 3], x[2, 150], x[3, 7] = 3.4e38, -torch.finfo(torch.float32).max, 2.0 ** 127
+    w[5] *= 2.0 ** -90  # blocks whose powers lie far apart
+    p = (*gs.gs_rows_pack8(x), *(t.reshape(1, 96, -1) for t in gs.gs_rows_pack8(w)))
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    _check_fwd(p, offsets, 200, None, torch.float32)
+    _check_fwd(p, offsets, 200, None, torch.bfloat16)
+    # and the other way about
+    q = (*gs.gs_rows_pack8(w[:rows] if rows < 96 else w.repeat(8, 1)[:rows]),
+         *(t.reshape(1, -1, t.shape[-1]) for t in gs.gs_rows_pack8(x[:5])))
+    _check_fwd(q, offsets, 200, None, torch.float32)
+
+
+@pytest.mark.parametrize("rows", [5, 700])
 def test_nan_stays_in_its_row(rows):
     offsets = torch.tensor([0, 2, rows], dtype=torch.int32, device=DEV)
     p = _packed(5, rows, 2, 300, 80, rows)

@@ -137,6 +137,9 @@ __device__ __forceinline__ void few8_terms(const float (*x)[kFewDepth], const ui
             // whatever lies behind the last channel
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[n][i] = k + i < depth ? v[n][i] * size : 0.f;
+            if (powers[n][k / GS_SCALE_BLOCK] > kSafeByte<float>)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[n][i] = cut_to<float>(v[n][i]);
         }
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
@@ -186,7 +189,8 @@ __global__ void __launch_bounds__(kFewThreads)
                 const float size =
                     scale_of(xs.scales[row * scale_pitch + (k0 + k) / GS_SCALE_BLOCK]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[r][k + i] = k + i < depth ? v[i] * size : 0.f;
+                for (int i = 0; i < 8; ++i)
+                    x[r][k + i] = k + i < depth ? cut_to<float>(v[i] * size) : 0.f;
             }
         }
         __syncthreads();

@@ -63,4 +63,8 @@ __device__ __forceinline__ float cut_to(float v) {
     return fabsf(v) > kMost ? copysignf(kMost, v) : v;
 }
 
+// The largest byte whose block's values, up to 448 * 2^(byte - 127), T holds.
+template <typename T>
+constexpr int kSafeByte = std::is_same<T, __half>::value ? 134 : 246;
+
 }  // namespace gs

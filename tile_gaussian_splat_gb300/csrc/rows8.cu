@@ -237,10 +237,6 @@ struct Unpack8 {
     const int32_t* used;  // or null: `rows` rows for every expert, those with rows of x
 };
 
-// The largest byte whose block's values, up to 448 * 2^(byte - 127), T holds.
-template <typename T>
-constexpr int kSafeByte = std::is_same<T, __half>::value ? 134 : 246;
-
 // Eight values times their scales, as T; kCut: which may be beyond the type.
 template <typename T, bool kCut>
 __device__ __forceinline__ Eight<T> scaled8(uint2 q, const float* size) {
