@@ -112,6 +112,29 @@ def test_scales_far_apart():
         _check_fwd(p, offsets, i, None, dtype)
 
 
+@pytest.mark.parametrize("i", [512, 1700, 4352])
+def test_every_block_of_channels_meets_its_own_powers(i):
+    """Rows that two blocks of threads share, every power another one: a word of
+    powers that came too late would leave its buffer's last ones.  Blocks of one
+    value, so that all sums are whole multiples of 2^-4 below 2^17: exact."""
+    g = gen(60 + i)
+    E, R, o, n = 3, 40000, 520, (i + 127) // 128
+    power = lambda rows: torch.randint(-2, 3, (rows, n), generator=g, device=DEV)
+    spread = lambda p: torch.exp2(p.float()).repeat_interleave(128, 1)[:, :i]
+    a, b = power(R), power(E * o)
+    p = (*gs.gs_rows_pack8(spread(a)),
+         *(t.reshape(E, o, -1) for t in gs.gs_rows_pack8(spread(b))))
+    offsets = torch.tensor([0, 13001, 26002, R], dtype=torch.int32, device=DEV)
+    wide = torch.full((n,), 128.0, dtype=torch.float64, device=DEV)
+    wide[-1] = i - 128 * (n - 1)
+    x, w = torch.exp2(a.double()) * wide, torch.exp2(b.double()).reshape(E, o, n)
+    want = torch.cat([x[lo:hi] @ w[e].t() for e, (lo, hi) in
+                      enumerate(zip(offsets.tolist(), offsets.tolist()[1:]))])
+    for _ in range(5):
+        ys = gs.gs_expert_linear8_fwd(p[0], p[1], offsets, p[2], p[3], i, dtype=torch.float32)
+        assert torch.equal(ys.double(), want)
+
+
 @pytest.mark.parametrize("rows", [5, 700])
 def test_values_at_the_end_of_float32(rows):
     """float32's largest value is kept as 2^128; times small weights it is finite."""

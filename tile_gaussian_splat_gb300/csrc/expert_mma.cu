@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                 if (kProduct == kWeightGrad) {
                     if (lane < kBlocks) mbar_arrive_at(&bars.landed[at.stage], lane);
                     if (c.row1 - c.row0 < (k + 1) * kSlice) {
-                        ok = warp_wait(&bars.cleared, cut++ & 1, abort);
+                        ok = warp_wait<kBlocks == 2>(&bars.cleared, cut++ & 1, abort);
                         if (!ok) break;
                     }
                     __syncwarp();

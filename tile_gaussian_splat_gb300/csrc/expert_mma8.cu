@@ -28,12 +28,12 @@
 // wait that is over 40), and slices of A that come late from memory behind the
 // output's writes.  Steps: powers written to tensor memory from registers by four
 // warps 218 us; with the bias read ahead and arrivals that do not wait for the
-// writes to global memory 157 (a release at cluster scope, one a tile, cost 35 us
-// for the bias and 35 for the powers); slices of 256 channels, A kept, boxes, no
-// division a tile 147; a third slice of A 140; its slices on the barrier of B's 137.
-// Not kept: whole 32-byte sectors
-// stored from registers (178 against 159 at that step), prefetches of the next
-// piece's A into the L2 (155 against 147).  Two warps that issue in turn are
+// writes to global memory 157 (a release at cluster scope by one warp, one a tile,
+// cost 35 us for the bias and 35 for the powers, which need it); slices of 256
+// channels, A kept, boxes, no division a tile 147; a third slice of A 140; its
+// slices on the barrier of B's 137.  Not kept: whole 32-byte sectors stored from
+// registers (178 against 159 at that step), prefetches of the next piece's A into
+// the L2 (155 against 147).  Two warps that issue in turn are
 // unsound as long as each waits only for its own tiles' slices: a barrier's
 // parity then stands for two phases.
 #include <algorithm>
@@ -58,8 +58,8 @@ constexpr int kGroup = 2;           // slices a word of powers serves
 constexpr int kAccumulators = 2;
 constexpr int kSpan = 64;           // columns an output warp writes
 constexpr int kRowBytes = 64;       // of the boxes they leave in
-// Warps: 0 copies rows, 1 issues products, 2 copies powers, 3 the bias, from 4
-// on they write the output.
+// Warps: 0 copies rows, 1 issues products (of a second block: copies powers with
+// 2), 2 copies powers, 3 the bias, from 4 on they write the output.
 template <int kWide>
 constexpr int kOutputs = 4 * kWide / kSpan;
 template <int kWide>
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
                 int none = 0;
                 if (turn != ~0u) mbar_wait_limited(&bars.full[i], turn & 1, &none);
             }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         constexpr uint32_t word0 = mma_word_e4m3(S::kTileHigh);
         const uint64_t from_a = smem_operand(base, 16, 1024);
         const uint64_t from_b = smem_operand(base_b, 16, 1024);
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
         Slots<S::kSlots> slots;
         Ring<kAccumulators> acc;
         Ring<kBuffers> buffer;
-        bool ok = rank == 0;
+        bool ok = true;
         while (ok && walk.next(c)) {
             if (acc.turn > 0) ok = warp_wait(&bars.acc_empty[acc.stage], (acc.turn + 1) & 1, abort);
             tmem_fence_after();
@@ -360,42 +360,39 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
             if (c.final && c.q1 == walk.count) slots.at += walk.count;
         }
         // nothing is still writing tensor memory when it is freed
-        if (rank == 0) {
-            if (elect_one()) mma_commit<kBlocks>(&bars.drain);
-            __syncwarp();
-            int none = 0;
-            mbar_wait_limited(&bars.drain, 0, &none);
-        }
-    } else if (warp == 2) {
-        // words of powers, a buffer a group, passed on when the copies of two
-        // more are on their way; the first block's warp has all of them copied
-        // into tensor memory (the warp that issues the products lost a fifth
-        // of its time to that)
+        if (elect_one()) mma_commit<kBlocks>(&bars.drain);
+        __syncwarp();
+        int none = 0;
+        mbar_wait_limited(&bars.drain, 0, &none);
+    } else if (warp == 2 || (warp == 1 && rank != 0)) {
+        // words of powers, a buffer a group; the first block's warp has all of
+        // them copied into tensor memory when the copies of two more groups are
+        // on their way (the warp that issues the products lost a fifth of its
+        // time to that).  The second block's words are read by the first one's
+        // instructions: they are fenced for those and released at cluster scope,
+        // which takes as long as a tile, so two warps do it in turn, each with
+        // half of the buffers (262144 rows 512 -> 1024: 149 us, 186 with one).
         constexpr int kBehind = 2;
         static_assert(kBehind < kBuffers, "a buffer that is not passed on is not waited for");
         Ring<kBuffers> buffer, next;
         bool ok = true;
         int waiting = 0;
-        // the fence hands the words over to the tensor cores' copies; a release
-        // at cluster scope on top cost 1 us a tile
         const auto pass_on = [&] {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(&bars.words_full[next.stage], 0);
-            if (rank == 0) {
-                ok = warp_wait(&bars.words_full[next.stage], next.turn & 1, abort);
-                if (!ok) return;
-                tmem_fence_after();
-                const uint32_t chunk = smem_u32(words) + next.stage * S::kPowerBytes;
-                if (elect_one()) {
+            if (lane == 0) mbar_arrive(&bars.words_full[next.stage]);
+            ok = warp_wait<kBlocks == 2>(&bars.words_full[next.stage], next.turn & 1, abort);
+            if (!ok) return;
+            tmem_fence_after();
+            const uint32_t chunk = smem_u32(words) + next.stage * S::kPowerBytes;
+            if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 1 + S::kChunksB; ++j)
-                        tmem_copy_32x16<kBlocks>(powers + next.stage * S::kPowers + j * 4,
-                                                 chunk + j * kChunk);
-                    mma_commit<kBlocks>(&bars.powers_full[next.stage]);
-                }
-                __syncwarp();
+                for (int j = 0; j < 1 + S::kChunksB; ++j)
+                    tmem_copy_32x16<kBlocks>(powers + next.stage * S::kPowers + j * 4,
+                                             chunk + j * kChunk);
+                mma_commit<kBlocks>(&bars.powers_full[next.stage]);
             }
+            __syncwarp();
             next.advance();
         };
         while (ok && walk.next(c)) {
@@ -403,6 +400,7 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
             const uint32_t* a = g.powers_a + (int64_t)row * g.words;
             const uint32_t* b = g.powers_b + ((int64_t)c.expert * g.width + n) * g.words;
             for (int q = c.q0; q < c.q1; q += kGroup, buffer.advance()) {
+                if (rank != 0 && (buffer.stage & 1) != (warp & 1)) continue;
                 ok = buffer.turn == 0 ||
                      warp_wait(&bars.powers_empty[buffer.stage], (buffer.turn + 1) & 1, abort);
                 if (!ok) break;
@@ -423,7 +421,12 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
                               in ? b + (int64_t)i * 32 * g.words + word : g.powers_b, in);
                 }
                 copy_group();
-                if (waiting == kBehind) {
+                if (rank != 0) {
+                    copy_wait<0>();
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_release_at(&bars.words_full[buffer.stage], 0);
+                } else if (waiting == kBehind) {
                     copy_wait<kBehind>();
                     pass_on();
                     if (!ok) break;

@@ -20,14 +20,26 @@ __device__ __forceinline__ uint64_t now_ns() {
     return t;
 }
 
+// kCluster: what threads of the other block released (mbar_release_at) is seen
+// after the wait too, not only what this block's did.
+template <bool kCluster>
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if constexpr (kCluster)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
     return done != 0;
 }
 
@@ -35,11 +47,12 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
 // block that gave up) or the limit has passed.  The clock is looked at every
 // 256 polls only: reading the global timer takes as long as a slice's
 // products.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity,
                                                   volatile int* abort) {
     uint64_t start = 0;
     for (uint32_t polls = 1;; ++polls) {
-        if (mbar_try(bar, parity)) return true;
+        if (mbar_try<kCluster>(bar, parity)) return true;
         if (polls % 256) continue;
         if (*abort) return false;
         const uint64_t now = now_ns();
@@ -52,8 +65,9 @@ __device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity
 }
 
 // The same for a whole warp, with one answer.
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait_limited(bar, parity, abort));
+    return __all_sync(0xffffffffu, mbar_wait_limited<kCluster>(bar, parity, abort));
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -72,10 +86,10 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // Arrives on the barrier at the same place in block `rank` of the cluster.
-// What the arrivals here hand over was written by bulk copies or read from
-// tensor memory, which barriers and fences of their own order: the arrival
-// releases nothing else.  (A release at cluster scope waits for the thread's
-// stores to global memory: 1 us a slice, twice the whole kernel's time.)
+// What such arrivals hand to the other block was written by bulk copies or read
+// from tensor memory, which barriers and fences of their own order: the arrival
+// releases nothing else.  (A release at cluster scope takes 1 us beside other
+// traffic, longer than a slice's products.)
 __device__ __forceinline__ void mbar_arrive_at(uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
@@ -85,7 +99,8 @@ __device__ __forceinline__ void mbar_arrive_at(uint64_t* bar, uint32_t rank) {
 }
 
 // The same, after which this warp's writes to its own shared memory are seen
-// by whoever waited for it.
+// by whoever in the cluster waited for it (with kCluster): for what threads of
+// one block write and the other block's instructions read.
 __device__ __forceinline__ void mbar_release_at(uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
