@@ -267,10 +267,11 @@ int gs_expert_linear8_fwd(const uint8_t* xs, const uint8_t* xs_scales, const int
  *   grad_xs[r] = weight[e]^T grad_ys[r]   (rows of no expert 0)
  *   grad_weight[e] = sum over the expert's rows of grad_ys[r] xs[r]^T
  *   grad_bias[e] = sum over the expert's rows of grad_ys[r]
- * grad_ys and the gradients of dtype, the values of xs and weight rounded to
- * float16 where that is dtype (as gs_rows_unpack8 does).  grad_xs may be NULL
- * (weight is then not read), grad_bias may be NULL, and grad_weight where
- * grad_bias is (xs is then not read).
+ * grad_ys and the gradients of dtype.  With float16 a value of xs (of weight) is
+ * taken exactly where its block's byte is at most 22 below the largest of the
+ * experts' rows (of the weights of experts that have rows), else to within 2^-39
+ * of the largest value.  grad_xs may be NULL (weight is then not read), grad_bias
+ * may be NULL, and grad_weight where grad_bias is (xs is then not read).
  */
 int gs_expert_linear8_bwd(const void* grad_ys, const uint8_t* xs, const uint8_t* xs_scales,
                           const int32_t* offsets, const uint8_t* weight,

@@ -135,6 +135,83 @@ def test_every_block_of_channels_meets_its_own_powers(i):
         assert torch.equal(ys.double(), want)
 
 
+@pytest.mark.parametrize("rows,i,o", [(9, 300, 40), (700, 400, 96), (30000, 512, 520)])
+@pytest.mark.parametrize("high,low", [(18, 18), (-20, -20), (18, -4), (100, 100), (-110, -120),
+                                      (18, -20), (60, -60)])
+def test_float16_gradients_of_values_beyond_float16(high, low, rows, i, o):
+    """Blocks around 2^high and 2^low, gradients that bring the sums back into
+    float16 where it has such: each value counts exactly, or to within 2^-39 of
+    the largest (the lowest bytes' of all)."""
+    g = gen(70 + high + low)
+    E = 4
+    offsets = torch.tensor([0, rows // 3, rows // 3, rows - 2, rows - 1], dtype=torch.int32,
+                           device=DEV)
+    at = torch.arange(i, device=DEV) // 128 % 2
+    each = torch.exp2(torch.where(at == 0, high, low).double()).float()
+    p = (*gs.gs_rows_pack8(randn(g, rows, i) * each),
+         *(t.reshape(E, o, -1) for t in gs.gs_rows_pack8(randn(g, E * o, i) * each)))
+    size = 2.0 ** max(min(-high, 8), -12)
+    gys = (randn(g, rows, o) * size).half()
+    run = lambda: gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], i)
+    grads = run()
+    x, w = _values(p, i)
+    refs, slacks = linear_bwd_ref(gys, x, offsets, w)
+    count = gys.double().abs()
+    beyond = (2.0 ** -39 * w.abs().max() * count.sum(1, keepdim=True),
+              2.0 ** -39 * x.abs().max() * torch.stack(
+                  [count[a:b].sum(0) for a, b in zip(offsets.tolist(), offsets.tolist()[1:])]
+              )[..., None], 0.0)
+    most = torch.finfo(torch.float16).max
+    for got, ref, slack, more in zip(grads, refs, slacks, beyond):
+        held = ref.abs() + slack + more <= most
+        none = torch.zeros((), dtype=torch.float64, device=DEV)
+        check(torch.where(held, got, 0), torch.where(held, ref, none),
+              torch.where(held, slack + more, none), "gradients")
+        over = ref.abs() - slack - more >= 2 * most
+        assert bool((got[over].double() == ref[over].sign() * float("inf")).all())
+    # nor do powers count that no expert uses, nor what stands for no number
+    p[1].view(torch.uint8)[rows - 1:] = 254
+    p[3].view(torch.uint8)[1] = 254
+    p[3].view(torch.uint8)[..., (i + 127) // 128:] = 254
+    assert all(torch.equal(a, b) for a, b in zip(run(), grads))
+    p[3].view(torch.uint8)[0, 3, 0] = 255
+    assert torch.equal(run()[1], grads[1]) and torch.equal(run()[0][rows // 3:],
+                                                           grads[0][rows // 3:])
+
+
+def test_float16_gradients_captured_and_at_once():
+    """The powers that the operands have in common are of the call's own data:
+    of a replay's, and of either of two streams'."""
+    _, offsets, _, _ = routed(90, 3000, 2, 8)
+    a, b = _packed(90, 6000, 8, 256, 320, 6000), _packed(91, 6000, 8, 256, 320, 6000)
+    for t in (b[1], b[3]):
+        t.view(torch.uint8).sub_(40)
+    gys = randn(gen(90), 6000, 320, dtype=torch.float16)
+    run = lambda r: gs.gs_expert_linear8_bwd(gys, r[0], r[1], offsets, r[2], r[3], 256)
+    want = run(a), run(b)
+    assert not torch.equal(want[0][1], want[1][1])
+    p = tuple(t.clone() for t in a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(p)
+    for r, w in ((b, want[1]), (a, want[0]), (b, want[1])):
+        for t, u in zip(p, r):
+            t.view(torch.uint8).copy_(u.view(torch.uint8))
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(out, w))
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s, r in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                got.append(run(r))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[i % 2]))
+
+
 @pytest.mark.parametrize("rows", [5, 700])
 def test_values_at_the_end_of_float32(rows):
     """float32's largest value is kept as 2^128; times small weights it is finite."""

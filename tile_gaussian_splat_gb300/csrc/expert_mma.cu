@@ -58,6 +58,7 @@
 #include "gs_device.cuh"
 #include "gs_head_internal.h"
 #include "gs_mma.cuh"
+#include "gs_rows8.cuh"
 #include "gs_types.cuh"
 
 namespace gs {
@@ -92,6 +93,7 @@ struct ProductArgs {
     int round;               // slices summed before they are added to the running sum
     int rounds;              // some sums take several rounds
     int access;              // bytes at which the output's rows can be written
+    const int32_t* tops;     // or null: sums are multiples of 2^(top_of - 134) (float16)
     const void* bias;        // kForward
     void* out;
     void* bias_grad;         // kWeightGrad, or null
@@ -234,6 +236,14 @@ struct Walk {
         return next_round(c);
     }
 };
+
+// By a whole warp: what sums are multiples of: planes of 8-bit rows in float16 leave a common
+// power of two out.  (Sums are below 2^63: times 2^-126 they are 0 in float16.)
+template <typename Out>
+__device__ __forceinline__ float unit_of(const ProductArgs& g) {
+    if (!std::is_same<Out, __half>::value || !g.tops) return 1.f;
+    return two_to(max(top_of(g.tops) - 7, 1));
+}
 
 // T: type of the planes; Out: of the output and of bias.
 template <typename T, typename Out, int kProduct, int kBlocks, int kWide>
@@ -471,6 +481,7 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
         float* bias = reinterpret_cast<float*>(staging + S::kStaging) + (warp - 4) * kSpan;
         const int first = (warp - 4) / 4 * kSpan;
         char* mine = staging + (warp - 4) * 32 * 64;
+        const float unit = kProduct == kForward ? 1.f : unit_of<Out>(g);
         Ring<kAccumulators> acc;
         bool ok = true;
         for (; ok && walk.next(c); acc.advance(accumulators)) {
@@ -551,8 +562,12 @@ __global__ void __launch_bounds__(kMmaThreads<kProduct>, 1)
                         for (int i = 0; i < kRow / 8; ++i) {
                             float f[8];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
+                            for (int j = 0; j < 8; ++j) {
                                 f[j] = __uint_as_float(w[kRow * h + 8 * i + j]);
+                                if constexpr (kProduct != kForward &&
+                                              std::is_same<Out, __half>::value)
+                                    f[j] *= unit;
+                            }
                             if (kProduct == kForward && g.bias) {
                                 const float4* p = reinterpret_cast<const float4*>(
                                     bias + b * 32 + kRow * h + 8 * i);
@@ -631,6 +646,7 @@ __global__ void __launch_bounds__(256)
         return ((int64_t)s * tiles + tile) * 2 + (s == s0 ? 1 : 0);
     };
     int block = blockIdx.x;
+    const float unit = unit_of<Out>(g);
     const int cut_blocks = (g.groups - 1) * tiles * kSlabs;
     if (block < cut_blocks) {
         const int cut = block / (tiles * kSlabs) + 1, tile = block / kSlabs % tiles;
@@ -668,7 +684,7 @@ __global__ void __launch_bounds__(256)
             }
             Out* out = static_cast<Out*>(g.out) + ((int64_t)e * g.high + m0 + row) * g.width +
                        n0 + col;
-            const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+            const float v[4] = {sum.x * unit, sum.y * unit, sum.z * unit, sum.w * unit};
             if (g.access >= 4 * (int)sizeof(Out)) {
                 store_vec<Out, 4>(out, v);
             } else {
@@ -1003,9 +1019,10 @@ bool few_dx(const LinearArgs& a, const void* weight) {
     return !copyable(a.dtype, weight, a.in) && few_rows(a, false);
 }
 
-// The gradients of weight and bias from the rows' planes, of map_dtype.
+// The gradients of weight and bias from the rows' planes, of map_dtype.  tops: of x.
 int launch_grad_of_weight(const LinearArgs& a, int map_dtype, const Planes& gy, const Planes& x,
-                          void* grad_weight, void* grad_bias, float* sums, cudaStream_t s) {
+                          const int32_t* tops, void* grad_weight, void* grad_bias, float* sums,
+                          cudaStream_t s) {
     CUtensorMap ma, mb;
     if (!make_map(&ma, map_dtype, gy, 0, kSlice) || !make_map(&mb, map_dtype, x, 0, kSlice))
         return GS_ERR_CUDA;
@@ -1017,6 +1034,7 @@ int launch_grad_of_weight(const LinearArgs& a, int map_dtype, const Planes& gy, 
     // no part of a sum is longer than a share, nor than all the rows
     g.rounds = std::min(ceil_div(a.rows, kSlice),
                         ceil_div(a.rows / kSlice + a.experts, p.groups)) > g.round;
+    g.tops = tops;
     g.bias_grad = grad_bias;
     g.partial = sums;
     g.bias_partial = sums + partial_floats(p);
@@ -1067,33 +1085,40 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
     }
     if (!grad_weight) return GS_OK;
     const Planes x = prepare(a.dtype, xs, a.rows, a.in, &ws, s);
-    return launch_grad_of_weight(a, a.dtype, gy, x, grad_weight, grad_bias, sums, s);
+    return launch_grad_of_weight(a, a.dtype, gy, x, nullptr, grad_weight, grad_bias, sums, s);
 }
 
 namespace {
 
 // 8-bit rows as rows of half types: bfloat16 holds every value of theirs.
+// float16 takes the elements as multiples of a power of two that all of the rows
+// (of the weights) have in common, by which the sums are multiplied: the largest
+// byte's lie just within it, those of up to 22 bytes below are exact, and what is
+// smaller is off by at most 2^-25 there, 2^-39 of the largest.
 constexpr int plane_dtype(int dtype) { return dtype == GS_F16 ? GS_F16 : GS_BF16; }
 
 size_t unpacked_bytes(int64_t rows, int columns) { return plane_bytes(GS_BF16, rows, columns); }
 
+// At the front of the workspace, of float16: what launch_top_bytes leaves.
+size_t tops_bytes(int dtype) { return dtype == GS_F16 ? 2 * kTopParts * sizeof(int32_t) : 0; }
+
 // offsets: x are weights, of which only experts that have rows are needed.
 Planes unpacked(int dtype, Rows8 x, int64_t rows, int columns, const int32_t* offsets, int experts,
-                char** workspace, cudaStream_t s) {
+                const int32_t* tops, char** workspace, cudaStream_t s) {
     // the zeros behind the last column too, up to whole vectors: they lie in
     // the same block and row of 16 bytes
     const int pitch = (int)ceil_div(columns, 8) * 8;
     void* out = *workspace;
     *workspace += unpacked_bytes(rows, columns);
     launch_unpack8(x.q, x.scales, offsets ? rows / experts : rows, pitch, dtype, out, pitch, s,
-                   offsets, experts);
+                   offsets, experts, tops);
     return Planes{out, rows, columns, pitch, 1};
 }
 
 }  // namespace
 
 size_t linear8_bwd_workspace(const LinearArgs& a, const void* grad_ys) {
-    size_t n = grad_sums_bytes(a);
+    size_t n = tops_bytes(a.dtype) + grad_sums_bytes(a);
     if (!copyable(a.dtype, grad_ys, a.out)) n += plane_bytes(a.dtype, a.rows, a.out);
     return n + unpacked_bytes(a.rows, a.in) + unpacked_bytes((int64_t)a.experts * a.out, a.in);
 }
@@ -1103,25 +1128,31 @@ int launch_linear8_bwd(const LinearArgs& a, const void* grad_ys, Rows8 xs, Rows8
                        cudaStream_t s) {
     const int planes = plane_dtype(a.dtype);
     char* ws = static_cast<char*>(workspace);
+    int32_t* tops = a.dtype == GS_F16 ? reinterpret_cast<int32_t*>(ws) : nullptr;
+    ws += tops_bytes(a.dtype);
     float* sums = reinterpret_cast<float*>(ws);
     ws += grad_sums_bytes(a);
     const Planes gy = prepare(a.dtype, grad_ys, a.rows, a.out, &ws, s);
+    if (tops)
+        launch_top_bytes(a, grad_weight ? xs.scales : nullptr, grad_xs ? weight.scales : nullptr,
+                         tops, s);
     if (grad_xs) {
         const bool pairs = use_pairs(a, a.in);
         const Planes w = unpacked(planes, weight, (int64_t)a.experts * a.out, a.in, a.offsets,
-                                  a.experts, &ws, s);
+                                  a.experts, tops ? tops + kTopParts : nullptr, &ws, s);
         CUtensorMap ma, mb;
         if (!make_map(&ma, planes, gy, 0, kHigh) || !make_map(&mb, planes, w, a.experts, kSlice))
             return GS_ERR_CUDA;
-        const ProductArgs g = product_args(a, grad_xs, a.in, a.out);
+        ProductArgs g = product_args(a, grad_xs, a.in, a.out);
+        g.tops = tops ? tops + kTopParts : nullptr;
         const int rc = with_types(a.dtype, [&](auto t, auto o) {
             return launch_rows<decltype(t), decltype(o), kInputGrad>(ma, mb, g, pairs, s);
         });
         if (rc != GS_OK) return rc;
     }
     if (!grad_weight) return GS_OK;
-    const Planes x = unpacked(planes, xs, a.rows, a.in, nullptr, 0, &ws, s);
-    return launch_grad_of_weight(a, planes, gy, x, grad_weight, grad_bias, sums, s);
+    const Planes x = unpacked(planes, xs, a.rows, a.in, nullptr, 0, tops, &ws, s);
+    return launch_grad_of_weight(a, planes, gy, x, tops, grad_weight, grad_bias, sums, s);
 }
 
 }  // namespace gs

@@ -66,10 +66,12 @@ void launch_route_bwd(const RouteArgs& a, const int32_t* ids, const int32_t* cou
 void launch_pack8(const void* x, int64_t ldx, int64_t rows, int channels, int dtype, uint8_t* q,
                   uint8_t* scales, cudaStream_t s);
 // With offsets: `rows` rows for each of the experts, of which those without rows
-// of their own are left out (y aligned and its rows whole 16-byte vectors).
+// of their own are left out.  With tops (float16): as multiples of 2^(top_of - 134).
+// (Either: y aligned and its rows whole 16-byte vectors.)
 void launch_unpack8(const uint8_t* q, const uint8_t* scales, int64_t rows, int channels,
                     int dtype, void* y, int64_t ldy, cudaStream_t s,
-                    const int32_t* offsets = nullptr, int experts = 0);
+                    const int32_t* offsets = nullptr, int experts = 0,
+                    const int32_t* tops = nullptr);
 
 // ---- the experts' products; the launchers of expert_mma.cu return a gs_status
 struct LinearArgs {
@@ -82,6 +84,12 @@ struct LinearArgs {
 struct Rows8 {
     const uint8_t *q, *scales;
 };
+// ---- rows8.cu: the largest scale byte of the rows' blocks, then of the weights',
+// of those that the products use and that are numbers (0 for a null), as the
+// largest of kTopParts words each
+constexpr int kTopParts = 128;
+void launch_top_bytes(const LinearArgs& a, const uint8_t* xs, const uint8_t* weight,
+                      int32_t* tops, cudaStream_t s);
 // ---- expert_few.cu: the products of few rows, bound by reading the weights.
 // as_they_lie: the tensor cores could read the weights in place.
 bool few_rows(const LinearArgs& a, bool as_they_lie);

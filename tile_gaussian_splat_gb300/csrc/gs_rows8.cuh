@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/gs_head.h"
+#include "gs_head_internal.h"
 
 namespace gs {
 
@@ -66,5 +67,14 @@ __device__ __forceinline__ float cut_to(float v) {
 // The largest byte whose block's values, up to 448 * 2^(byte - 127), T holds.
 template <typename T>
 constexpr int kSafeByte = std::is_same<T, __half>::value ? 134 : 246;
+
+// By a whole warp: the largest byte of all, from what the blocks of k_top_bytes
+// found in their parts.
+__device__ __forceinline__ int top_of(const int32_t* parts) {
+    int top = 0;
+#pragma unroll
+    for (int i = 0; i < kTopParts / 32; ++i) top = max(top, parts[i * 32 + (threadIdx.x & 31)]);
+    return __reduce_max_sync(0xffffffffu, top);
+}
 
 }  // namespace gs
