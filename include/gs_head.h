@@ -267,11 +267,14 @@ int gs_expert_linear8_fwd(const uint8_t* xs, const uint8_t* xs_scales, const int
  *   grad_xs[r] = weight[e]^T grad_ys[r]   (rows of no expert 0)
  *   grad_weight[e] = sum over the expert's rows of grad_ys[r] xs[r]^T
  *   grad_bias[e] = sum over the expert's rows of grad_ys[r]
- * grad_ys and the gradients of dtype.  With float16 a value of xs (of weight) is
- * taken exactly where its block's byte is at most 22 below the largest of the
- * experts' rows (of the weights of experts that have rows), else to within 2^-39
- * of the largest value.  grad_xs may be NULL (weight is then not read), grad_bias
- * may be NULL, and grad_weight where grad_bias is (xs is then not read).
+ * grad_ys and the gradients of dtype.  With float32 and bfloat16 a value of xs or
+ * weight is taken as bfloat16 holds it: exactly where its block's byte is 3 to
+ * 246, as the type's largest, 255 * 2^120, from 2^128 on, and in steps of 2^-133
+ * below 2^-126.  With float16 a value of xs (of weight) is taken exactly where
+ * its block's byte is at most 22 below the largest of the experts' rows (of the
+ * weights of experts that have rows), else to within 2^-39 of the largest value.
+ * grad_xs may be NULL (weight is then not read), grad_bias may be NULL, and
+ * grad_weight where grad_bias is (xs is then not read).
  */
 int gs_expert_linear8_bwd(const void* grad_ys, const uint8_t* xs, const uint8_t* xs_scales,
                           const int32_t* offsets, const uint8_t* weight,

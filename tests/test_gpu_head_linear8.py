@@ -229,6 +229,35 @@ def test_values_at_the_end_of_float32(rows):
     _check_fwd(q, offsets, 200, None, torch.float32)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("rows", [5, 700])
+def test_gradients_at_the_ends_of_bfloat16(rows, dtype):
+    """Other gradients than float16's take the values as bfloat16 holds them:
+    from 2^128 on (what float32's largest is kept as) its largest, below 2^-126
+    in steps of 2^-133, which the lowest three bytes' values are finer than."""
+    g = gen(51)
+    i, o = 300, 96
+    offsets = torch.tensor([0, 2, rows], dtype=torch.int32, device=DEV)
+    x, w = randn(g, rows, i), randn(g, 2 * o, i)
+    x[1, 3], x[2, 150], x[3, 290], w[5, 7] = 3.4e38, -3.4e38, 2.0 ** 127, -3.4e38
+    low = (*gs.gs_rows_pack8(randn(g, rows, i) * 2.0 ** -121),
+           *(t.reshape(2, o, -1) for t in gs.gs_rows_pack8(randn(g, 2 * o, i) * 2.0 ** -121)))
+    for t in (low[1], low[3]):  # bytes 0 to 4
+        t.view(torch.uint8).copy_(torch.randint(0, 5, t.shape, generator=g, device=DEV))
+    high = (*gs.gs_rows_pack8(x), *(t.reshape(2, o, -1) for t in gs.gs_rows_pack8(w)))
+    assert int(high[1].view(torch.uint8).max()) == 247
+    for p, size in ((high, 2.0 ** -60), (low, 2.0 ** 110)):
+        gys = (randn(g, rows, o) * size).to(dtype)
+        exact = _values(p, i)
+        held = _values(p, i, torch.bfloat16)
+        assert not any(torch.equal(a, b) for a, b in zip(exact, held))
+        refs, slacks = linear_bwd_ref(gys, held[0], offsets, held[1])
+        grads = gs.gs_expert_linear8_bwd(gys, p[0], p[1], offsets, p[2], p[3], i)
+        for got, ref, slack, what in zip(grads, refs, slacks, ("xs", "weight", "bias")):
+            assert float(ref.abs().max()) > 1e-20
+            check(got, ref, slack, what)
+
+
 @pytest.mark.parametrize("rows", [5, 700])
 def test_nan_stays_in_its_row(rows):
     offsets = torch.tensor([0, 2, rows], dtype=torch.int32, device=DEV)

@@ -1090,7 +1090,9 @@ int launch_linear_bwd(const LinearArgs& a, const void* grad_ys, const void* xs,
 
 namespace {
 
-// 8-bit rows as rows of half types: bfloat16 holds every value of theirs.
+// 8-bit rows as rows of half types: bfloat16 holds the values of bytes 3 to 246
+// (4 bits from 2^-133 to 448 * 2^119); above it is cut to its largest, as
+// gs_rows_unpack8 does, below what is finer than 2^-133 is rounded.
 // float16 takes the elements as multiples of a power of two that all of the rows
 // (of the weights) have in common, by which the sums are multiplied: the largest
 // byte's lie just within it, those of up to 22 bytes below are exact, and what is
