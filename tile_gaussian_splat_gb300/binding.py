@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as ct
+import functools
 import os
 
 import torch
@@ -522,15 +523,25 @@ def _rows(t, what):
     return t.data_ptr() or None, ld
 
 
-def _on(stream, like):
+@functools.cache
+def _devices():
+    return torch.cuda.device_count()
+
+
+def _on(stream, like, *others):
     """The call's stream as a raw handle: `stream`, or the current one of the
-    device that `like` is on, which has to be the current device."""
+    device that `like` is on, which has to be the current device and that of
+    the call's other tensors (or None)."""
     if not like.is_cuda:
         _refuse("expected a CUDA tensor")
     device = like.get_device()
     if device != torch.cuda.current_device() or \
             getattr(stream, "device_index", device) != device:
         _refuse("tensors and stream of the current device expected")
+    if _devices() > 1:  # else every CUDA tensor is on the one there is
+        for t in others:
+            if t is not None and t.get_device() != device:
+                _refuse("tensors and stream of the current device expected")
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
@@ -591,7 +602,8 @@ def gs_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stats=True,
         rstd = _new(shape[:-1], torch.float32, x, stream)
     _check(lib().gs_layer_norm_fwd(xp, ldx, _ptr(weight), _ptr(bias),
                                    x.numel() // ch if ch else 0, ch, dt, _DTYPES[p], eps, yp, ldy,
-                                   _ptr(mean), _ptr(rstd), _on(stream, x)), "gs_layer_norm_fwd")
+                                   _ptr(mean), _ptr(rstd), _on(stream, x, weight, bias, out)),
+           "gs_layer_norm_fwd")
     return y, mean, rstd
 
 
@@ -628,7 +640,8 @@ def gs_layer_norm_bwd(grad_y, x, weight, mean, rstd, out=None, params=True, para
         ws = _workspace(workspace, n_bytes, x, stream)
     _check(L.gs_layer_norm_bwd(gp, ldg, xp, ldx, _ptr(weight), _ptr(mean), _ptr(rstd), rows, ch,
                                dt, _DTYPES[p], op, ldo, _ptr(gw), _ptr(gb), _ptr(ws), n_bytes,
-                               _on(stream, x)), "gs_layer_norm_bwd")
+                               _on(stream, x, grad_y, weight, mean, rstd, out, ws)),
+           "gs_layer_norm_bwd")
     return gx, gw, gb
 
 
@@ -649,7 +662,7 @@ def gs_expert_sort(expert_ids, experts, workspace=None, stream=None):
     n_bytes = L.gs_expert_sort_workspace_size(T, k, experts)
     ws = _workspace(workspace, n_bytes, expert_ids, stream) if n_bytes else None
     _check(L.gs_expert_sort(_ptr(expert_ids), T, k, experts, _ptr(offsets), _ptr(order),
-                            _ptr(slots), _ptr(ws), n_bytes, _on(stream, expert_ids)),
+                            _ptr(slots), _ptr(ws), n_bytes, _on(stream, expert_ids, ws)),
            "gs_expert_sort")
     return offsets, order, slots
 
@@ -685,7 +698,8 @@ def gs_expert_dispatch(x, slots, offsets, d_status=None, out=None, stream=None):
     xs = _new((T * k, ch), x.dtype, x, stream) if out is None else \
         _same(out, (T * k, ch), x.dtype, "out")
     _check(lib().gs_expert_dispatch(xp, ldx, _ptr(slots), _ptr(offsets), T, k, E, ch, dt,
-                                    _ptr(xs), _ptr(d_status), _on(stream, x)),
+                                    _ptr(xs), _ptr(d_status),
+                                    _on(stream, x, slots, offsets, d_status, out)),
            "gs_expert_dispatch")
     return xs
 
@@ -706,7 +720,8 @@ def gs_expert_combine(ys, slots, weights=None, d_status=None, out=None, stream=N
         y = _same(out, (T, ch), ys.dtype, "out")
         yp, ldy = _rows(y, "out")
     _check(lib().gs_expert_combine(_ptr(ys), _ptr(slots), _pair_weights(weights, slots), T, k, ch,
-                                   dt, yp, ldy, _ptr(d_status), _on(stream, ys)),
+                                   dt, yp, ldy, _ptr(d_status),
+                                   _on(stream, ys, slots, weights, d_status, out)),
            "gs_expert_combine")
     return y
 
@@ -725,7 +740,8 @@ def gs_expert_combine_bwd(grad_y, ys, slots, weights, offsets, d_status=None, st
     gw = _new((T, k), torch.float32, ys, stream) if weights is not None else None
     _check(lib().gs_expert_combine_bwd(gp, ldg, _ptr(ys), _ptr(slots),
                                        _pair_weights(weights, slots), _ptr(offsets), T, k, E, ch,
-                                       dt, _ptr(gys), _ptr(gw), _ptr(d_status), _on(stream, ys)),
+                                       dt, _ptr(gys), _ptr(gw), _ptr(d_status),
+                                       _on(stream, ys, grad_y, slots, weights, offsets, d_status)),
            "gs_expert_combine_bwd")
     return gys, gw
 
@@ -759,7 +775,8 @@ def gs_expert_linear_fwd(xs, offsets, weight, bias=None, d_status=None, out=None
     ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
     _check(L.gs_expert_linear_fwd(_ptr(xs), _ptr(offsets), _ptr(weight), _ptr(bias), R, E, i, o,
                                   dt, _ptr(ys), _ptr(ws), n_bytes, _ptr(d_status),
-                                  _on(stream, xs)), "gs_expert_linear_fwd")
+                                  _on(stream, xs, offsets, weight, bias, d_status, out, ws)),
+           "gs_expert_linear_fwd")
     return ys
 
 
@@ -780,7 +797,9 @@ def gs_expert_linear_bwd(grad_ys, xs, offsets, weight, bias=True, input=True, d_
     ws = _workspace(workspace, n_bytes, xs, stream) if n_bytes else None
     _check(L.gs_expert_linear_bwd(_ptr(grad_ys), _ptr(xs), _ptr(offsets), _ptr(weight), R, E, i,
                                   o, dt, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), n_bytes,
-                                  _ptr(d_status), _on(stream, xs)), "gs_expert_linear_bwd")
+                                  _ptr(d_status),
+                                  _on(stream, xs, grad_ys, offsets, weight, d_status, ws)),
+           "gs_expert_linear_bwd")
     return gx, gw, gb
 
 
@@ -812,7 +831,7 @@ def gs_expert_route_fwd(logits, topk, keep=None, renormalise=True, balance=True,
         ws = _workspace(workspace, n_bytes, logits, stream) if n_bytes else None
     _check(L.gs_expert_route_fwd(lp, ldl, _ptr(keep), T, topk, E, dt, int(renormalise), _ptr(ids),
                                  _ptr(weights), _ptr(counts), _ptr(loss), _ptr(ws), n_bytes,
-                                 _on(stream, logits)), "gs_expert_route_fwd")
+                                 _on(stream, logits, keep, ws)), "gs_expert_route_fwd")
     return ids, weights, counts, loss
 
 
@@ -844,7 +863,10 @@ def gs_expert_route_bwd(logits, ids, counts=None, grad_weights=None, grad_loss=N
         op, ldo = _rows(grad, "out")
     _check(lib().gs_expert_route_bwd(lp, ldl, _ptr(ids), _ptr(counts), _ptr(grad_weights),
                                      _ptr(grad_loss), T, k, E, dt, int(renormalise), op, ldo,
-                                     _ptr(d_status), _on(stream, logits)), "gs_expert_route_bwd")
+                                     _ptr(d_status),
+                                     _on(stream, logits, ids, counts, grad_weights, grad_loss,
+                                         d_status, out)),
+           "gs_expert_route_bwd")
     return grad
 
 
@@ -893,7 +915,8 @@ def gs_rows_unpack8(q, scales, channels, dtype=torch.bfloat16, out=None, stream=
         y = _same(out, shape, dtype, "out")
         yp, ldy = _rows(y, "out")
     _check(lib().gs_rows_unpack8(qp, sp, q.numel() // q.shape[-1] if channels else 0, channels,
-                                 _dtype(y, "dtype"), yp, ldy, _on(stream, q)), "gs_rows_unpack8")
+                                 _dtype(y, "dtype"), yp, ldy, _on(stream, q, scales, out)),
+           "gs_rows_unpack8")
     return y
 
 
@@ -919,7 +942,9 @@ def gs_expert_linear8_fwd(xs, xs_scales, offsets, weight, weight_scales, in_feat
     ys = _new((R, o), dtype, xs, stream) if out is None else _same(out, (R, o), dtype, "out")
     _check(lib().gs_expert_linear8_fwd(xp, xsp, _ptr(offsets), wp, wsp, _ptr(bias), R, E,
                                        in_features, o, _dtype(ys, "dtype"), _ptr(ys),
-                                       _ptr(d_status), _on(stream, xs)), "gs_expert_linear8_fwd")
+                                       _ptr(d_status),
+                                       _on(stream, xs, xs_scales, offsets, weight, weight_scales,
+                                           bias, d_status, out)), "gs_expert_linear8_fwd")
     return ys
 
 
@@ -943,6 +968,8 @@ def gs_expert_linear8_bwd(grad_ys, xs, xs_scales, offsets, weight, weight_scales
     ws = _workspace(workspace, n_bytes, grad_ys, stream) if n_bytes else None
     _check(L.gs_expert_linear8_bwd(_ptr(grad_ys), xp, xsp, _ptr(offsets), wp, wsp, R, E,
                                    in_features, o, dt, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws),
-                                   n_bytes, _ptr(d_status), _on(stream, grad_ys)),
+                                   n_bytes, _ptr(d_status),
+                                   _on(stream, grad_ys, xs, xs_scales, offsets, weight,
+                                       weight_scales, d_status, ws)),
            "gs_expert_linear8_bwd")
     return gx, gw, gb
