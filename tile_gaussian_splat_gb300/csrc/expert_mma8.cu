@@ -19,11 +19,13 @@
 // other accumulators.  Those leave no room for the powers beside 256 columns
 // each, so tiles are 192 columns wide.
 //
-// 262144 rows, 16 experts, 512 -> 1024, bfloat16 out: 137 us (2010 TFLOP/s, 5.0
-// TB/s; the bytes alone take 100 us); 65536 rows 1024 -> 1024, float16 out: 68 us
-// (2010 TFLOP/s).  Nothing is saturated (tensor pipe 46 %, memory 59 %, shared
-// memory below 50 %): without the output the first takes 105 us, without the
-// products 133, without both 93.  What is left is the issuing warp's own time,
+// 262144 rows, 16 experts, 512 -> 1024, bfloat16 out: 143 us (1920 TFLOP/s, 4.8
+// TB/s; the bytes alone take 100 us), float32 229 (178); 65536 rows 1024 -> 1024,
+// bfloat16, float16 and float32 out: 72, 76 and 87 us.  Nothing is saturated (131072
+// of the first: tensor pipe 37 %, memory 49 %, L2 44 %, issue 46 %); 512 threads
+// leave 128 registers each, 32 bytes short (float32 52).  At 137 us, before the
+// release below, it took 105 without the output, 133 without the products and 93
+// without both.  What is left is the issuing warp's own time,
 // 2000 cycles a tile beside 1536 of products (an instruction 42, a commit 90, a
 // wait that is over 40), and slices of A that come late from memory behind the
 // output's writes.  Steps: powers written to tensor memory from registers by four
@@ -31,7 +33,8 @@
 // writes to global memory 157 (a release at cluster scope by one warp, one a tile,
 // cost 35 us for the bias and 35 for the powers, which need it); slices of 256
 // channels, A kept, boxes, no division a tile 147; a third slice of A 140; its
-// slices on the barrier of B's 137.  Not kept: whole 32-byte sectors stored from
+// slices on the barrier of B's 137; the second block's powers released at cluster
+// scope 143.  Not kept: whole 32-byte sectors stored from
 // registers (178 against 159 at that step), prefetches of the next piece's A into
 // the L2 (155 against 147).  Two warps that issue in turn are
 // unsound as long as each waits only for its own tiles' slices: a barrier's
@@ -102,8 +105,8 @@ struct Bars8 {
 // kSlots, kStages: slices of A and of B in shared memory.  512 channels leave a
 // slot of three for the next piece's first slice, whose 1 to 2 us from memory
 // under the output's writes are else waited for at every piece (262144 rows 512
-// -> 1024: 140 us with 3 and 4, 150 with 2 and 4, 147 with 2 and 5, 152 with 3
-// and 3, 175 with 4 and 2).
+// -> 1024, at that step: 140 us with 3 and 4, 150 with 2 and 4, 147 with 2 and 5,
+// 152 with 3 and 3, 175 with 4 and 2).
 template <int kBlocks_, int kWide_, int kSlots_, int kStages_>
 struct Shape8 {
     static constexpr int kBlocks = kBlocks_, kWide = kWide_, kSlots = kSlots_;
@@ -371,7 +374,11 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
         // time to that).  The second block's words are read by the first one's
         // instructions: they are fenced for those and released at cluster scope,
         // which takes as long as a tile, so two warps do it in turn, each with
-        // half of the buffers (262144 rows 512 -> 1024: 149 us, 186 with one).
+        // half of the buffers (262144 rows 512 -> 1024: 143 us, 180 with one; 155
+        // with copies of the next words on their way, which the release waits for
+        // too; 142 with one release for two buffers).  Written from the first
+        // block instead, with no more than a fence for the tensor cores' copies,
+        // some words came too late.
         constexpr int kBehind = 2;
         static_assert(kBehind < kBuffers, "a buffer that is not passed on is not waited for");
         Ring<kBuffers> buffer, next;
@@ -646,7 +653,7 @@ int launch_linear8_fwd(const LinearArgs& a, Rows8 xs, Rows8 weight, const void* 
     g.out = ys;
     g.d_status = a.d_status;
     // Two blocks a tile of 256 x 192 where those fill every pair of SMs twice,
-    // one block a tile of 128 x 128 else (512 -> 1024 bf16: 40000 rows 31 us in
+    // one block a tile of 128 x 128 else (512 -> 1024 bf16: 40000 rows 33 us in
     // pairs and 33 single, 4000 12.3 and 10.3).
     const int64_t tiles = (a.rows / 256 + a.experts / 2) * ceil_div(a.out, 192);
     int rc = GS_OK;

@@ -94,7 +94,7 @@ inline int access_bytes(const void* p, size_t bytes, int element) {
 // 32 rows x 64 bytes of output held one row a lane (four 16-byte vectors),
 // turned through shared memory so that neighbouring lanes write a row's 64
 // contiguous bytes, `access` bytes each (16 down to an element: 60000 rows of 8-bit
-// products, 512 -> 1004, 1002 and 1001 bfloat16, 50, 68 and 84 us, 90 an element
+// products, 512 -> 1004, 1002 and 1001 bfloat16, 60, 69 and 83 us, 90 an element
 // each).  valid_rows of the rows and `left` of a row's elements are inside the
 // output.
 template <typename Out>

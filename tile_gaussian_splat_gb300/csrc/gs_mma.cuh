@@ -89,7 +89,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // What such arrivals hand to the other block was written by bulk copies or read
 // from tensor memory, which barriers and fences of their own order: the arrival
 // releases nothing else.  (A release at cluster scope takes 1 us beside other
-// traffic, longer than a slice's products.)
+// traffic and waits for the warp's copies on their way.)
 __device__ __forceinline__ void mbar_arrive_at(uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"

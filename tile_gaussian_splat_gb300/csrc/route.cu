@@ -3,7 +3,9 @@
 // their gradient in the logits.
 //
 // Both directions read each row of logits once, so memory bandwidth is their
-// floor; what bounds them is the instructions a row takes.  kLanes lanes share a
+// floor; what bounds them is the instructions a row takes, in the few warps that
+// 70 to 120 registers a thread leave on an SM (forward, 16 float32: issue 65 %,
+// warps 21 %, DRAM 33 %; gradient 69, 35 and 44 %).  kLanes lanes share a
 // row (up to 16 experts a thread has it alone and exchanges nothing); a lane owns
 // the same experts of every row it meets, so the sums of probabilities behind the
 // balance loss stay in registers until the end and are then added up in a fixed
@@ -11,10 +13,10 @@
 // it: each lane keeps its logits as unsigned words in the order of the values, 0
 // where there is nothing to choose.
 //
-// 921600 rows of 16 float32, two choices: 27 us (floor 10; without the next row on
-// its way 33, with IEEE divisions and expf 49, with four lanes a row 66).  Gradient,
-// the same rows: 27 us (floor 19); 230400 of 64 bfloat16, four choices 20.5 us (floor
-// 9.7), forward 35.
+// 921600 rows of 16 float32, two choices: 27 us (floor 11; without the next row on
+// its way 33, before that with IEEE divisions and expf 49, with four lanes a row
+// 66).  Gradient, the same rows: 30 us (floor 19); 230400 of 64 bfloat16, four
+// choices 24 us (floor 9.7), forward 36 (floor 5.4).
 #include <algorithm>
 #include <cstdint>
 
@@ -49,7 +51,10 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 // exp(v) by the hardware's power of two: off by about (2 + |v|) 2^-23 of it, 0
-// below 2^-126.
+// below 2^-126.  The small probabilities are off the most: weights of logits three
+// apart by 1e-6 at most, 4e-8 of their norm, where expf and IEEE divisions for the
+// choices alone leave 6e-7 and 4e-8, and take 32 us for the forward's 27 and 33 for
+// the gradient's 30.
 __device__ __forceinline__ float exp_approx(float v) {
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * 1.44269504f));
@@ -504,9 +509,10 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(RouteBwd a) {
 
 // Calls f with how rows of `experts` elements are spread: sixteen elements a lane
 // keep what is done once a row, and exchanged between lanes, small beside what is
-// done for each element, and many rows in flight.  Forward, 460800 rows of 32
-// float32 and 230400 of 64 bfloat16: 31 and 38 us, 49 and 47 with eight lanes; 921600
-// of 16 float32 in a thread each 33, in two lanes 33, in four 43.  The gradient's
+// done for each element, and many rows in flight.  Measured before the next row
+// came in ahead (since then 27, 36 and 27 us): forward, 460800 rows of 32 float32
+// and 230400 of 64 bfloat16, 31 and 38 us, 49 and 47 with eight lanes; 921600 of 16
+// float32 in a thread each 33, in two lanes 33, in four 43.  The gradient's
 // rows are written too, which wants neighbours: two lanes at least (921600 of 16
 // float32: 31 us, a thread each 43; 900000 of 7 float16 18.5 and 22.6), single
 // elements eight a lane up to 64 (460800 of 31: 35.5 us, sixteen a lane 47).

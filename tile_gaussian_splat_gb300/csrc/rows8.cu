@@ -10,10 +10,10 @@
 // follows from the one before (two 64-bit divisions a block took half of the
 // time).  Rows that begin anywhere are read and written as the aligned vectors
 // that they lie in, turned by the elements they are off.
-// 921600 rows of 128 bfloat16: 55 us there, 55 back, 6.4 TB/s (96 % of a copy's
-// rate; with eight elements a lane 72 and 70, bound by the instructions).  16383
-// rows of 1021 float16: 15 and 17 us, bound by instructions (element by element
-// 22 and 53).
+// 921600 rows of 128 bfloat16: 54 us there, 56 back by themselves, 6.4 TB/s (96 % of
+// a copy's rate; with eight elements a lane 72 and 70, bound by the instructions),
+// 58 and 65 among others with all data in memory.  16383 rows of 1021 float16: 17 us
+// either way, bound by instructions (element by element 22 and 53).
 #include <algorithm>
 #include <cfloat>
 #include <cstdint>
