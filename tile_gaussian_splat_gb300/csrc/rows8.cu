@@ -380,9 +380,9 @@ __global__ void __launch_bounds__(kThreads8) k_unpack8_any(Unpack8 a, int vector
 // xs' rows and of the weights of experts that have rows (each null: not wanted),
 // what every block of threads found in tops (top_of).  A row a thread: a byte for
 // 128 elements, small beside what unpacks them, which is launched while this is
-// at work.  The gradients of 131072 rows, 512 -> 1024, take 280 us, 275 without it
+// at work.  The gradients of 131072 rows, 512 -> 1024, take 277 us, 272 without it
 // (285 with one maximum for all, set to 0 before), those of 20014 rows 259 -> 131
-// 70 and 68.
+// 71 and 68, those of 921600 rows 128 -> 64 228 and 218 (238 a word at a time).
 constexpr int kTopThreads = 256;
 
 __global__ void __launch_bounds__(kTopThreads)
@@ -403,29 +403,39 @@ __global__ void __launch_bounds__(kTopThreads)
     // bytes behind the last block count for nothing
     const uint32_t last = 0xffffffffu >> (words * 4 - blocks) * 8;
     const int64_t first = (int64_t)blockIdx.x * kTopThreads + threadIdx.x;
-    const int64_t step = (int64_t)kTopParts * kTopThreads;
-    const auto of_row = [&](const uint32_t* p, int most) {
-        for (int w = 0; w < words; ++w) {
-            uint32_t v = p[w] & (w + 1 == words ? last : 0xffffffffu);
-            v &= ~__vcmpeq4(v, 0xffffffffu);
-            v = __vmaxu4(v, v >> 16);
-            v = __vmaxu4(v, v >> 8);
-            most = max(most, (int)(v & 255u));
-        }
-        return most;
+    constexpr int64_t kStep = (int64_t)kTopParts * kTopThreads;
+    // the largest of every byte of the words of rows [r, end) that are used,
+    // eight of them on their way at once
+    const auto largest = [&](const uint32_t* p, int64_t r, int64_t end, auto used) {
+        uint32_t most = 0;
+        for (; r < end; r += 8 * kStep)
+            for (int w = 0; w < words; ++w) {
+                uint32_t v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int64_t row = r + k * kStep;
+                    v[k] = row < end && used(row) ? p[row * words + w] : 0;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    v[k] &= w + 1 == words ? last : 0xffffffffu;
+                    most = __vmaxu4(most, v[k] & ~__vcmpeq4(v[k], 0xffffffffu));
+                }
+            }
+        most = __vmaxu4(most, most >> 16);
+        return __vmaxu4(most, most >> 8) & 255u;
     };
-    int most[2] = {0, 0};
-    if (xs)
-        for (int64_t r = begin + first; r < kept; r += step) most[0] = of_row(xs + r * words, most[0]);
+    uint32_t most[2] = {0, 0};
+    if (xs) most[0] = largest(xs, begin + first, kept, [](int64_t) { return true; });
     if (weight)
-        for (int64_t r = first; r < (int64_t)experts * out; r += step) {
-            const int e = (int)(r / out);
-            if (offsets[e + 1] > offsets[e]) most[1] = of_row(weight + r * words, most[1]);
-        }
+        most[1] = largest(weight, first, (int64_t)experts * out, [&](int64_t row) {
+            const int e = (int)((uint32_t)row / (uint32_t)out);
+            return offsets[e + 1] > offsets[e];
+        });
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int top = __reduce_max_sync(0xffffffffu, most[i]);
-        if ((threadIdx.x & 31) == 0) atomicMax(found + i, top);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, most[i]);
+        if ((threadIdx.x & 31) == 0) atomicMax(found + i, (int)top);
     }
     __syncthreads();
     if (threadIdx.x < 2) tops[threadIdx.x * kTopParts + blockIdx.x] = found[threadIdx.x];
