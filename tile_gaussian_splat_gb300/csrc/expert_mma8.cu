@@ -374,11 +374,10 @@ __global__ void __launch_bounds__(kThreads<S::kWide>, 1)
         // time to that).  The second block's words are read by the first one's
         // instructions: they are fenced for those and released at cluster scope,
         // which takes as long as a tile, so two warps do it in turn, each with
-        // half of the buffers (262144 rows 512 -> 1024: 143 us, 180 with one; 155
-        // with copies of the next words on their way, which the release waits for
-        // too; 142 with one release for two buffers).  Written from the first
-        // block instead, with no more than a fence for the tensor cores' copies,
-        // some words came too late.
+        // half of the buffers (262144 rows 512 -> 1024: 143 us, 180 with one; 153
+        // with one that releases two buffers together; 155 with copies of the next
+        // words on their way, which the release waits for too; 166 with all words
+        // written from the first block into the second's shared memory).
         constexpr int kBehind = 2;
         static_assert(kBehind < kBuffers, "a buffer that is not passed on is not waited for");
         Ring<kBuffers> buffer, next;
